@@ -75,6 +75,13 @@ typedef enum {
   SSM_DISC_BILINEAR = 3
 } ssm_bbar_mode;
 
+/* ssm_group_norm_fwd: the function of the affine result ... */
+typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1 } ssm_activation;
+
+/* ... and where silu(z) multiplies: nowhere (z NULL), the input before the
+ * statistics, or the output. */
+typedef enum { SSM_GATE_NONE = 0, SSM_GATE_BEFORE = 1, SSM_GATE_AFTER = 2 } ssm_gate;
+
 typedef enum {
   SSM_OK = 0,
   SSM_E_NULL = 1,        /* a required pointer is NULL                         */
@@ -321,6 +328,131 @@ int ssm_ssd_fwd_noalloc(const void* x, const void* dt, const float* A, const voi
 
 /* Bytes of the static scratch that ssm_ssd_fwd_noalloc uses (per GPU). */
 int64_t ssm_ssd_scratch_bytes(void);
+
+/*
+ * The Mamba-2 mixer over packed prompts: the depthwise causal convolution and
+ * silu of the x, B and C channels, and the scan with a scalar A per head, as
+ * the block diagram has them between its projections ("State-space models",
+ * section "Mamba: selection"; recurrence as for ssm_ssd_fwd).  Rows are
+ * tokens, channels are innermost, and every row tensor has a row stride in
+ * elements, so xbc, dt and z can be slices of the input projection's rows.
+ *
+ *   in_t     row t of xbc;  inputs before the sequence: conv_state, or zero
+ *   [x|B|C]  = silu(conv_bias + sum_{k<W} conv_weight_k in_{t-(W-1)+k})
+ *   dt_t     = softplus(dt_raw_t + dt_bias)   (or without the softplus)
+ *   h_t[p,n] = exp(dt_t A_h) h_{t-1}[p,n] + dt_t x_t[h,p] B_t[g,n]
+ *   y_t[h,p] = (sum_n C_t[g,n] h_t[p,n] + D_h x_t[h,p]) (* silu(z_t[h,p]))
+ *
+ *  xbc          [tokens, nheads * headdim + 2 * ngroups * dstate] io_dtype:
+ *               x of every head, B of every group, C of every group
+ *  dt           [tokens, nheads] io_dtype, raw step
+ *  z            [tokens, nheads * headdim] io_dtype or NULL (no gate)
+ *  conv_weight  [channels, width] float32;  conv_bias [channels] or NULL
+ *  A            [nheads] float32 (negative);  Dskip, dt_bias [nheads] or NULL
+ *  cu_seqlens   [nseq + 1] int32, device: sequence s is rows
+ *               [cu_seqlens[s], cu_seqlens[s + 1]), possibly none; rows of no
+ *               sequence are not read and their y is left as it was
+ *  slots        [nseq] int32, device, or NULL (sequence s has slot s): the
+ *               sequence's slot in the two states.  A slot outside
+ *               [0, nslots) marks padding: the sequence is skipped and its y
+ *               left as it was.  No slot may appear twice.
+ *  has_state    [nseq] bytes, device, or NULL: nonzero where the sequence
+ *               continues from its slot's states, zero (NULL: everywhere)
+ *               where it starts from zeros
+ *  conv_state   [nslots, channels, width - 1] float32, oldest input first
+ *  ssm_state    [nslots, nheads, headdim, dstate] float32
+ *               Both are read and written in place; an empty sequence leaves
+ *               what it starts from.  Both NULL: nothing is carried (slots
+ *               and has_state then NULL too).
+ *  y            [tokens, nheads * headdim] io_dtype
+ *  workspace    ssm_conv_ssd_workspace_size(...) bytes of device memory,
+ *               16-byte aligned, owned by the caller; its contents on entry do
+ *               not matter; calls sharing it must not run concurrently
+ * headdim and dstate are 1..256, width 1..4 (SSM_E_UNSUPPORTED otherwise),
+ * tokens below 2^31.  A float32 or bf16 tensor needs the alignment of its
+ * elements only.  Offsets outside [0, tokens] or out of order are clamped into
+ * it: the sequences they describe are wrong, no other memory is touched.
+ * Outputs must not overlap inputs; slices of one buffer's rows with disjoint
+ * columns do not.  Results do not vary from run to run.  A non-finite input
+ * makes what depends on it non-finite (an infinity may become a NaN), and
+ * leaves earlier tokens and other sequences as they are.
+ */
+int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_t dt_stride,
+                     const void* z, int64_t z_stride, const float* conv_weight,
+                     const float* conv_bias, const float* A, const float* Dskip,
+                     const float* dt_bias, int dt_softplus, const int32_t* cu_seqlens,
+                     const int32_t* slots, const uint8_t* has_state, float* conv_state,
+                     float* ssm_state, void* y, int64_t y_stride, void* workspace,
+                     int64_t workspace_bytes, int64_t tokens, int64_t nseq, int64_t nslots,
+                     int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
+                     int64_t width, int io_dtype, void* hip_stream);
+
+/* Bytes of workspace ssm_conv_ssd_fwd needs (-1 if an extent is out of
+ * range).  Host-only, enqueues nothing. */
+int64_t ssm_conv_ssd_workspace_size(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim,
+                                    int64_t ngroups, int64_t dstate, int io_dtype);
+
+/*
+ * One token for every entry of a batch: ssm_conv_ssd_fwd with sequences of one
+ * row each, all of them continuing from their slots.  Row i of xbc, dt, z and y
+ * belongs to slot slots[i] (NULL: i); a slot outside [0, nslots) marks an
+ * entry that a padded batch leaves empty, which is skipped.  No slot may
+ * appear twice.  Layouts, types and errors as above; no workspace.
+ */
+int ssm_conv_ssd_update(const void* xbc, int64_t xbc_stride, const void* dt, int64_t dt_stride,
+                        const void* z, int64_t z_stride, const float* conv_weight,
+                        const float* conv_bias, const float* A, const float* Dskip,
+                        const float* dt_bias, int dt_softplus, const int32_t* slots,
+                        float* conv_state, float* ssm_state, void* y, int64_t y_stride,
+                        int64_t batch, int64_t nslots, int64_t nheads, int64_t headdim,
+                        int64_t ngroups, int64_t dstate, int64_t width, int io_dtype,
+                        void* hip_stream);
+
+/*
+ * Norm over groups of a row's channels (channels innermost), with the gate and
+ * the activation around it: what the Mamba-2 block puts between the scan and
+ * its output projection.  Per row and group of channels / ngroups channels:
+ *
+ *   v = x * silu(z)            (gate SSM_GATE_BEFORE) or x
+ *   m = mean(v) if center, else 0
+ *   n = (v - m) / sqrt(mean((v - m)^2) + eps)
+ *   a = weight * n + bias;  a = silu(a) for SSM_ACT_SILU
+ *   y = a * silu(z)            (gate SSM_GATE_AFTER) or a
+ *
+ *  x, z, y       [rows, channels] io_dtype with row strides in elements; z is
+ *                NULL exactly when the gate is SSM_GATE_NONE
+ *  weight, bias  [channels] float32 or NULL (1, 0)
+ * A group has at most 32768 channels (SSM_E_UNSUPPORTED otherwise).  y must
+ * not overlap an input.  Arithmetic in float32.
+ */
+int ssm_group_norm_fwd(const void* x, int64_t x_stride, const void* z, int64_t z_stride,
+                       const float* weight, const float* bias, float eps, int center,
+                       int activation, int gate, void* y, int64_t y_stride, int64_t rows,
+                       int64_t channels, int64_t ngroups, int io_dtype, void* hip_stream);
+
+/*
+ * Gradients of ssm_group_norm_fwd for the loss sum(dy * y), from its inputs
+ * (nothing of the forward is kept):
+ *  dx, dz           [rows, channels] io_dtype with row strides; dz exactly
+ *                   when z is given
+ *  dweight, dbias   [channels] float32 or NULL (not computed); sums over the
+ *                   rows in a fixed order, so results do not vary from run to
+ *                   run
+ *  workspace        ssm_group_norm_bwd_workspace_size(...) bytes, 16-byte
+ *                   aligned, owned by the caller; contents on entry do not
+ *                   matter; calls sharing it must not run concurrently
+ * Outputs must not overlap inputs or each other.
+ */
+int ssm_group_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                       const void* z, int64_t z_stride, const float* weight, const float* bias,
+                       float eps, int center, int activation, int gate, void* dx,
+                       int64_t dx_stride, void* dz, int64_t dz_stride, float* dweight,
+                       float* dbias, void* workspace, int64_t workspace_bytes, int64_t rows,
+                       int64_t channels, int64_t ngroups, int io_dtype, void* hip_stream);
+
+/* Bytes of workspace ssm_group_norm_bwd needs (-1 if an extent is out of
+ * range). */
+int64_t ssm_group_norm_bwd_workspace_size(int64_t rows, int64_t channels, int64_t ngroups);
 
 /*
  * Time-invariant path: y = K * u + D u, the causal convolution of every

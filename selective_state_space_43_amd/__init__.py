@@ -38,15 +38,30 @@ Entry points carry the C names:
          checkpoints feed ssm_selective_scan_bwd
   causal_conv1d_fn(x, weight, bias=None, state_in=None, silu=True) -> out,
       differentiable through ssm_causal_conv1d_bwd
+  ssm_conv_ssd_fwd(xbc, dt, conv_weight, A, cu_seqlens, headdim, ngroups,
+                   conv_bias=None, D=None, z=None, dt_bias=None, dt_softplus=True,
+                   slots=None, has_state=None, conv_state=None, ssm_state=None,
+                   y=None, workspace=None) -> y
+      the Mamba-2 mixer's convolution and scan over packed prompts (rows are
+      tokens), the states of each sequence read and written at its slot
+  ssm_conv_ssd_update(xbc, dt, conv_state, ssm_state, conv_weight, A, ngroups,
+                      ..., slots=None, y=None) -> y       (one token a sequence)
+  ssm_group_norm_fwd(x, weight, ngroups, bias=None, z=None, eps=1e-5,
+                     center=False, activation="none", gate="none", y=None) -> y
+  ssm_group_norm_bwd(dy, x, weight, ngroups, ...) -> dict of gradients
+      the norm over groups of a row's channels, with its gate or activation
+  group_norm_fn(x, weight, ngroups, ...) -> y, differentiable
 
 Layouts: u, delta, z, y [batch, dim, L]; B, C [batch, dstate, L]; A
 [dim, dstate]; D, delta_bias [dim]; h0 / final_state / state
-[batch, dim, dstate].  Sequence tensors are torch.bfloat16 or torch.float32
+[batch, dim, dstate]; the mixer's tensors are [rows, channels] with any row
+stride.  Sequence tensors are torch.bfloat16 or torch.float32
 (one dtype for all of them); everything else is float32.
 """
 from __future__ import annotations
 
-from ._lib import (SSM_BBAR_DELTA_B, SSM_BBAR_ZOH_EXACT, SSM_DTYPE_BF16, SSM_DTYPE_F32,
+from ._lib import (SSM_ACT_NONE, SSM_ACT_SILU, SSM_GATE_AFTER, SSM_GATE_BEFORE, SSM_GATE_NONE,
+                   SSM_BBAR_DELTA_B, SSM_BBAR_ZOH_EXACT, SSM_DTYPE_BF16, SSM_DTYPE_F32,
                    SelscanError, library_path, lib, ssm_abi_version, ssm_last_error,
                    ssm_status_str)
 from .binding import (ssm_causal_conv1d_bwd, ssm_causal_conv1d_fwd, ssm_causal_conv1d_update,
@@ -55,7 +70,10 @@ from .binding import (ssm_causal_conv1d_bwd, ssm_causal_conv1d_fwd, ssm_causal_c
                       ssm_selective_scan_bwd, ssm_ssd_fwd, ssm_ssd_fwd_noalloc,
                       ssm_ssd_scratch_bytes, ssm_ssd_workspace_size,
                       ssm_selective_scan_bwd_workspace_size, ssm_selective_scan_fwd,
-                      ssm_state_update, selective_scan_fn, causal_conv1d_fn)
+                      ssm_state_update, selective_scan_fn, causal_conv1d_fn,
+                      ssm_conv_ssd_fwd, ssm_conv_ssd_update, ssm_conv_ssd_workspace_size,
+                      ssm_group_norm_fwd, ssm_group_norm_bwd, ssm_group_norm_bwd_workspace_size,
+                      group_norm_fn)
 
 __all__ = [
     "ssm_selective_scan_fwd", "ssm_state_update", "ssm_lti_kernel", "ssm_lti_conv",
@@ -63,7 +81,10 @@ __all__ = [
     "ssm_selective_scan_bwd", "ssm_checkpoint_shape", "selective_scan_fn", "causal_conv1d_fn",
     "ssm_selective_scan_bwd_workspace_size", "ssm_causal_conv1d_fwd", "ssm_causal_conv1d_update",
     "ssm_causal_conv1d_bwd", "ssm_ssd_fwd", "ssm_ssd_workspace_size", "ssm_ssd_fwd_noalloc",
-    "ssm_ssd_scratch_bytes", "ssm_status_str",
+    "ssm_ssd_scratch_bytes", "ssm_conv_ssd_fwd", "ssm_conv_ssd_update",
+    "ssm_conv_ssd_workspace_size", "ssm_group_norm_fwd", "ssm_group_norm_bwd",
+    "ssm_group_norm_bwd_workspace_size", "group_norm_fn", "ssm_status_str",
     "ssm_last_error", "ssm_abi_version", "SelscanError", "library_path", "lib",
+    "SSM_ACT_NONE", "SSM_ACT_SILU", "SSM_GATE_NONE", "SSM_GATE_BEFORE", "SSM_GATE_AFTER",
     "SSM_DTYPE_F32", "SSM_DTYPE_BF16", "SSM_BBAR_DELTA_B", "SSM_BBAR_ZOH_EXACT",
 ]

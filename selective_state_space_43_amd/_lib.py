@@ -10,6 +10,8 @@ _SO = os.path.join(_HERE, "libselscan.so")
 ABI_VERSION = 3  # the SSM_ABI_VERSION these signatures follow
 SSM_DTYPE_F32, SSM_DTYPE_BF16 = 0, 1
 SSM_BBAR_DELTA_B, SSM_BBAR_ZOH_EXACT, SSM_DISC_EULER, SSM_DISC_BILINEAR = 0, 1, 2, 3
+SSM_ACT_NONE, SSM_ACT_SILU = 0, 1
+SSM_GATE_NONE, SSM_GATE_BEFORE, SSM_GATE_AFTER = 0, 1, 2
 STATUS_NAMES = {0: "SSM_OK", 1: "SSM_E_NULL", 2: "SSM_E_SHAPE", 3: "SSM_E_DTYPE",
                 4: "SSM_E_ALIGN", 5: "SSM_E_ALIAS", 6: "SSM_E_UNSUPPORTED", 7: "SSM_E_HIP"}
 
@@ -65,6 +67,23 @@ def lib() -> ctypes.CDLL:
         L.ssm_ssd_fwd_noalloc.restype = i32
         L.ssm_ssd_scratch_bytes.argtypes = []
         L.ssm_ssd_scratch_bytes.restype = i64
+        f32 = ctypes.c_float
+        rows = [vp, i64]  # a row tensor and its row stride
+        L.ssm_conv_ssd_fwd.argtypes = [*rows, *rows, *rows, vp, vp, vp, vp, vp, i32, vp, vp, vp,
+                                       vp, vp, *rows, *rows, *[i64] * 8, i32, vp]
+        L.ssm_conv_ssd_update.argtypes = [*rows, *rows, *rows, vp, vp, vp, vp, vp, i32, vp, vp,
+                                          vp, *rows, *[i64] * 7, i32, vp]
+        L.ssm_conv_ssd_workspace_size.argtypes = [*[i64] * 6, i32]
+        L.ssm_conv_ssd_workspace_size.restype = i64
+        L.ssm_group_norm_fwd.argtypes = [*rows, *rows, vp, vp, f32, i32, i32, i32, *rows, i64, i64,
+                                         i64, i32, vp]
+        L.ssm_group_norm_bwd.argtypes = [*rows, *rows, *rows, vp, vp, f32, i32, i32, i32, *rows,
+                                         *rows, vp, vp, *rows, i64, i64, i64, i32, vp]
+        L.ssm_group_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
+        L.ssm_group_norm_bwd_workspace_size.restype = i64
+        for f in (L.ssm_conv_ssd_fwd, L.ssm_conv_ssd_update, L.ssm_group_norm_fwd,
+                  L.ssm_group_norm_bwd):
+            f.restype = i32
         for f in (L.ssm_selective_scan_fwd, L.ssm_state_update, L.ssm_lti_kernel,
                   L.ssm_selective_scan_bwd, L.ssm_causal_conv1d_fwd, L.ssm_causal_conv1d_update,
                   L.ssm_causal_conv1d_bwd, L.ssm_ssd_fwd, L.ssm_lti_conv,

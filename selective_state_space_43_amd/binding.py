@@ -487,3 +487,256 @@ def ssm_ssd_fwd_noalloc(x, dt, A, B, C, nheads, ngroups, y, D=None, z=None, dt_b
                                        N, SSM_DTYPE_BF16, _stream(dev))
     check(st, "ssm_ssd_fwd_noalloc")
     return y, final_state
+
+
+# ---------------------------------------------------------------- the Mamba-2 mixer, rows are tokens
+
+_ACT = {"none": 0, "silu": 1}
+_GATE = {"none": 0, "before": 1, "after": 2}
+
+
+def _rows(t, name, dtype, rows, cols, dev):
+    """A [rows, cols] tensor whose rows may be slices of wider ones."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        _dev(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t
+
+
+def _stride(t):
+    """The row stride that the library checks (one row has none)."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _flat(t, name, dtype, shape, dev):
+    """A dense tensor of this exact shape, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
+        _dev(t, name, dev)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _launch(dev, f, *args):
+    """Calls f(*args, stream) with the tensors' device current."""
+    if torch.cuda.current_device() == dev.index:
+        return f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    with torch.cuda.device(dev):
+        return f(*args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _row_input(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.dim() != 2 or t.dtype not in _IO:
+        raise TypeError(f"{name} must be [rows, channels] bfloat16 or float32")
+    return t.shape[0], t.shape[1], t.dtype, t.device
+
+
+def _workspace(ws, need, dev):
+    """The caller's workspace, or a new one; (tensor, bytes)."""
+    if need < 0:
+        return ws, 0  # the call reports why
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    if ws.device != dev or not ws.is_contiguous():
+        _dev(ws, "workspace", dev)
+    return ws, ws.numel() * ws.element_size()
+
+
+def ssm_conv_ssd_workspace_size(tokens, nseq, nheads, headdim, ngroups, dstate,
+                                dtype=torch.bfloat16):
+    """Bytes of workspace ssm_conv_ssd_fwd needs for tensors of this dtype."""
+    n = lib().ssm_conv_ssd_workspace_size(tokens, nseq, nheads, headdim, ngroups, dstate, _IO[dtype])
+    if n < 0:
+        raise ValueError("extents out of range")
+    return int(n)
+
+
+def ssm_conv_ssd_fwd(xbc, dt, conv_weight, A, cu_seqlens, headdim, ngroups, conv_bias=None, D=None,
+                     z=None, dt_bias=None, dt_softplus=True, slots=None, has_state=None,
+                     conv_state=None, ssm_state=None, y=None, workspace=None):
+    """Causal convolution, silu and Mamba-2 scan over packed prompts; returns y.
+
+    xbc [tokens, nheads * headdim + 2 * ngroups * dstate], dt [tokens, nheads]
+    and z [tokens, nheads * headdim] are rows (slices of wider rows too);
+    sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] (int32, on the GPU).
+    conv_state [nslots, channels, width - 1] and ssm_state [nslots, nheads,
+    headdim, dstate] (float32) are updated in place at slots[s] (int32; None:
+    slot s; outside the states: the sequence is padding and skipped), from
+    their contents where has_state[s] (bool or uint8) is set and from zero
+    elsewhere.  y of rows that belong to no sequence is left as it was (a new
+    y is not cleared)."""
+    rows, ch, io, dev = _row_input(xbc, "xbc")
+    H = A.shape[0]
+    inner = H * headdim
+    W = conv_weight.shape[-1]
+    if ch <= inner or ngroups < 1 or (ch - inner) % (2 * ngroups):
+        raise ValueError(f"xbc has {ch} channels: expected nheads * headdim + 2 * ngroups * dstate")
+    N = (ch - inner) // (2 * ngroups)
+    _rows(xbc, "xbc", io, rows, ch, dev)
+    _rows(dt, "dt", io, rows, H, dev)
+    if z is not None:
+        _rows(z, "z", io, rows, inner, dev)
+    if y is None:
+        y = torch.empty((rows, inner), dtype=io, device=dev)
+    else:
+        _rows(y, "y", io, rows, inner, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [nseq + 1]")
+    nseq = cu_seqlens.shape[0] - 1
+    nslots = 0 if ssm_state is None else ssm_state.shape[0]
+    if has_state is not None and has_state.dtype == torch.bool:
+        has_state = has_state.view(torch.uint8)
+    f32 = torch.float32
+    args = (xbc.data_ptr(), _stride(xbc), dt.data_ptr(), _stride(dt), _ptr(z), _stride(z),
+            _flat(conv_weight, "conv_weight", f32, (ch, W), dev),
+            _flat(conv_bias, "conv_bias", f32, (ch,), dev), _flat(A, "A", f32, (H,), dev),
+            _flat(D, "D", f32, (H,), dev), _flat(dt_bias, "dt_bias", f32, (H,), dev),
+            int(bool(dt_softplus)), _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev),
+            _flat(slots, "slots", torch.int32, (nseq,), dev),
+            _flat(has_state, "has_state", torch.uint8, (nseq,), dev),
+            _flat(conv_state, "conv_state", f32, (nslots, ch, W - 1), dev),
+            _flat(ssm_state, "ssm_state", f32, (nslots, H, headdim, N), dev), y.data_ptr(),
+            _stride(y))
+    L = lib()
+    ws, nbytes = _workspace(workspace, L.ssm_conv_ssd_workspace_size(
+        rows, nseq, H, headdim, ngroups, N, _IO[io]), dev)
+    st = _launch(dev, L.ssm_conv_ssd_fwd, *args, _ptr(ws), nbytes, rows, nseq, nslots, H, headdim,
+                 ngroups, N, W, _IO[io])
+    check(st, "ssm_conv_ssd_fwd")
+    return y
+
+
+def ssm_conv_ssd_update(xbc, dt, conv_state, ssm_state, conv_weight, A, ngroups, conv_bias=None,
+                        D=None, z=None, dt_bias=None, dt_softplus=True, slots=None, y=None):
+    """One token for every row of a batch, its states updated in place at
+    slots[i] (int32; None: slot i; outside the states: the row is padding and
+    skipped, its y left as it was); returns y.  Layouts as ssm_conv_ssd_fwd."""
+    rows, ch, io, dev = _row_input(xbc, "xbc")
+    if ssm_state.dim() != 4:
+        raise ValueError("ssm_state must be [nslots, nheads, headdim, dstate]")
+    nslots, H, P, N = ssm_state.shape
+    inner = H * P
+    W = conv_weight.shape[-1]
+    _rows(xbc, "xbc", io, rows, inner + 2 * ngroups * N, dev)
+    _rows(dt, "dt", io, rows, H, dev)
+    if z is not None:
+        _rows(z, "z", io, rows, inner, dev)
+    if y is None:
+        y = torch.empty((rows, inner), dtype=io, device=dev)
+    else:
+        _rows(y, "y", io, rows, inner, dev)
+    f32 = torch.float32
+    st = _launch(dev, lib().ssm_conv_ssd_update, xbc.data_ptr(), _stride(xbc), dt.data_ptr(),
+                 _stride(dt), _ptr(z), _stride(z),
+                 _flat(conv_weight, "conv_weight", f32, (ch, W), dev),
+                 _flat(conv_bias, "conv_bias", f32, (ch,), dev), _flat(A, "A", f32, (H,), dev),
+                 _flat(D, "D", f32, (H,), dev), _flat(dt_bias, "dt_bias", f32, (H,), dev),
+                 int(bool(dt_softplus)), _flat(slots, "slots", torch.int32, (rows,), dev),
+                 _flat(conv_state, "conv_state", f32, (nslots, ch, W - 1), dev),
+                 _flat(ssm_state, "ssm_state", f32, (nslots, H, P, N), dev), y.data_ptr(),
+                 _stride(y), rows, nslots, H, P, ngroups, N, W, _IO[io])
+    check(st, "ssm_conv_ssd_update")
+    return y
+
+
+def _norm_args(x, weight, ngroups, bias, z, activation, gate):
+    rows, C, io, dev = _row_input(x, "x")
+    _rows(x, "x", io, rows, C, dev)
+    if activation not in _ACT:
+        raise ValueError(f"activation {activation!r}: expected one of {sorted(_ACT)}")
+    if gate not in _GATE:
+        raise ValueError(f"gate {gate!r}: expected one of {sorted(_GATE)}")
+    if z is not None:
+        _rows(z, "z", io, rows, C, dev)
+    w = _flat(weight, "weight", torch.float32, (C,), dev)
+    b = _flat(bias, "bias", torch.float32, (C,), dev)
+    return rows, C, io, dev, w, b
+
+
+def ssm_group_norm_fwd(x, weight, ngroups, bias=None, z=None, eps=1e-5, center=False,
+                       activation="none", gate="none", y=None):
+    """Norm over groups of a row's channels; returns y.  With v = x, or
+    x * silu(z) for gate "before": (v - mean) / sqrt(var + eps) per group (mean
+    0 unless center), times weight, plus bias, through the activation ("none"
+    or "silu"), times silu(z) for gate "after".  x, z, y [rows, channels], rows
+    may be slices of wider ones; weight, bias [channels] float32 or None."""
+    rows, C, io, dev, w, b = _norm_args(x, weight, ngroups, bias, z, activation, gate)
+    if y is None:
+        y = torch.empty((rows, C), dtype=io, device=dev)
+    else:
+        _rows(y, "y", io, rows, C, dev)
+    st = _launch(dev, lib().ssm_group_norm_fwd, x.data_ptr(), _stride(x), _ptr(z), _stride(z), w, b,
+                 eps, int(bool(center)), _ACT[activation], _GATE[gate], y.data_ptr(), _stride(y),
+                 rows, C, ngroups, _IO[io])
+    check(st, "ssm_group_norm_fwd")
+    return y
+
+
+def ssm_group_norm_bwd_workspace_size(rows, channels, ngroups):
+    """Bytes of workspace ssm_group_norm_bwd needs."""
+    n = lib().ssm_group_norm_bwd_workspace_size(rows, channels, ngroups)
+    if n < 0:
+        raise ValueError("extents out of range")
+    return int(n)
+
+
+def ssm_group_norm_bwd(dy, x, weight, ngroups, bias=None, z=None, eps=1e-5, center=False,
+                       activation="none", gate="none", workspace=None):
+    """Gradients of ssm_group_norm_fwd for sum(dy * y): dict dx, dz (if z),
+    dweight (if weight), dbias (if bias)."""
+    rows, C, io, dev, w, b = _norm_args(x, weight, ngroups, bias, z, activation, gate)
+    _rows(dy, "dy", io, rows, C, dev)
+    L = lib()
+    ws, nbytes = _workspace(workspace, L.ssm_group_norm_bwd_workspace_size(rows, C, ngroups), dev)
+    g = dict(dx=torch.empty((rows, C), dtype=io, device=dev),
+             dz=torch.empty((rows, C), dtype=io, device=dev) if z is not None else None,
+             dweight=torch.empty(C, dtype=torch.float32, device=dev) if weight is not None else None,
+             dbias=torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None)
+    st = _launch(dev, L.ssm_group_norm_bwd, dy.data_ptr(), _stride(dy), x.data_ptr(), _stride(x),
+                 _ptr(z), _stride(z), w, b, eps, int(bool(center)), _ACT[activation], _GATE[gate],
+                 _ptr(g["dx"]), C, _ptr(g["dz"]), C, _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(ws),
+                 nbytes, rows, C, ngroups, _IO[io])
+    check(st, "ssm_group_norm_bwd")
+    return g
+
+
+class _GroupNormFn(torch.autograd.Function):
+    """The group norm as an autograd function; the backward starts from the
+    inputs, nothing else is kept."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, z, ngroups, eps, center, activation, gate):
+        y = ssm_group_norm_fwd(x, weight, ngroups, bias=bias, z=z, eps=eps, center=center,
+                               activation=activation, gate=gate)
+        ctx.save_for_backward(x, weight, bias, z)
+        ctx.how = dict(eps=eps, center=center, activation=activation, gate=gate)
+        ctx.ngroups = ngroups
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, z = ctx.saved_tensors
+        g = ssm_group_norm_bwd(dy.contiguous(), x, weight, ctx.ngroups, bias=bias, z=z, **ctx.how)
+        return g["dx"], g["dweight"], g["dbias"], g["dz"], None, None, None, None, None
+
+
+def group_norm_fn(x, weight, ngroups, bias=None, z=None, eps=1e-5, center=False, activation="none",
+                  gate="none"):
+    """ssm_group_norm_fwd's output, differentiable in x, weight, bias and z
+    through ssm_group_norm_bwd."""
+    return _GroupNormFn.apply(x, weight, bias, z, ngroups, eps, center, activation, gate)

@@ -3569,56 +3569,13 @@ lti_conv_fft_long_kernel(const float* K, const void* u, const float* Dskip, void
 
 // ---------------------------------------------------------------- host side
 
-thread_local char g_last_error[512] = "";
+}  // namespace
 
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-int fail(int status, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
-  va_end(ap);
-  return status;
-}
+#include "host.h"
 
-struct Span {
-  const void* p;
-  int64_t bytes;
-  const char* name;
-};
+namespace {
 
-bool overlaps(const Span& x, const Span& y) {
-  if (!x.p || !y.p || x.bytes <= 0 || y.bytes <= 0) return false;
-  const uintptr_t a0 = (uintptr_t)x.p, a1 = a0 + (uintptr_t)x.bytes;
-  const uintptr_t b0 = (uintptr_t)y.p, b1 = b0 + (uintptr_t)y.bytes;
-  return a0 < b1 && b0 < a1;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-constexpr int64_t kMaxExtent = (int64_t)1 << 40;
 constexpr int64_t kMaxDstate = 64;
-
-int check_extent(const char* name, int64_t v) {
-  if (v <= 0 || v > kMaxExtent) return fail(SSM_E_SHAPE, "%s = %lld is out of range", name, (long long)v);
-  return SSM_OK;
-}
-
-// a * b * c * d <= 2^60 (byte sizes of every tensor stay far from overflow)
-bool product_ok(int64_t a, int64_t b, int64_t c = 1, int64_t d = 1) {
-  const int64_t lim = (int64_t)1 << 60;
-  int64_t p = a;
-  for (int64_t f : {b, c, d}) {
-    if (p > lim / f) return false;
-    p *= f;
-  }
-  return true;
-}
-
-int launch_status(const char* what) {
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return fail(SSM_E_HIP, "%s: %s", what, hipGetErrorString(e));
-  return SSM_OK;
-}
 
 // calls f with the rule as a compile-time constant
 template <typename F>
