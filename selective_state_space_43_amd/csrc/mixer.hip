@@ -11,6 +11,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "host.h"
 
 namespace {
@@ -192,6 +194,897 @@ __global__ void __launch_bounds__(256) mix_conv_state_kernel(const MixArgs a) {
 #pragma unroll
   for (int j = 0; j < 3; ++j)
     if (j < W - 1) own[j] = v[j];
+}
+
+// ---------------------------------------------------------------- packed prompts as block products
+//
+// The recurrence over a block of Q = 64 steps, with c_t the running sum of
+// dt A inside the block and h the state entering it, is
+//
+//   y_t  = sum_{s<=t} M[t,s] x_s + exp(c_t) C_t . h
+//   M    = (C_t . B_s) exp(c_t - c_s) dt_s,  D added on the diagonal
+//   h'   = exp(c_Q) h + sum_s (exp(c_Q - c_s) dt_s x_s) B_s^T
+//
+// four products on the matrix cores.  B, C and C.B^T belong to a group of
+// heads: mix_prep_kernel makes them once per block, in the order in which the
+// matrix instructions take their operands.  mix_block_kernel then walks the
+// blocks of a segment of a sequence, one wave per 16 PT channels of a head,
+// the state in the wave's accumulators from block to block.  A sequence
+// longer than a segment is cut: a first pass (SUM) gives each segment's state
+// from zero, mix_join_kernel chains them, and the second pass starts every
+// segment from the state entering it.
+//
+// Precision: the accumulators, the state, the running sums (float64) and all
+// statistics are float32 or more.  The operands are fp16, scaled by a power of
+// two from the largest value of their tile, so that no value of float32's
+// range is lost to fp16's.  What goes into the state has two pieces (hi + lo, 22
+// bits, three products); what goes into y alone has one for bf16 rows (11 bits, 2^-11
+// beside the 2^-8 of the stored y) and two for float32 rows.
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+constexpr int kQ = 64;
+constexpr int kTri = 6;  // 16 x 32 tiles of M on or below the diagonal
+
+// 64 rows at most of one sequence
+struct Chunk {
+  int r0, r1;  // rows [r0, r1)
+  int t0;      // the sequence's first row
+  int seq;     // -1: resumes nothing (see resume)
+};
+// consecutive blocks of one sequence
+struct Seg {
+  int seq, t0, t1;  // the sequence and its rows
+  int c0, nc;       // its blocks [c0, c0 + nc) of the sequence
+  int gc;           // place of the first of them among all blocks
+  int split;        // segments before this one among those of cut sequences; -1: not cut
+  int cut;          // cut sequences before this one
+};
+
+struct PlanHead {
+  int nseg, nchunk, nsplit, pad;
+};
+
+struct BlkArgs : MixArgs {
+  PlanHead* head;
+  Chunk* chunks;
+  Seg* segs;
+  char* ops;       // operands of (block, group)
+  float* local;    // [split][H, P, N] state of a segment from zero, then the state entering it
+  float* decay;    // [split][H] log2 of a segment's whole decay
+  float* cs0;      // [cut][inner, 3] what the first rows of a cut sequence start from
+  int64_t op_bytes;
+  int seg_len;     // blocks of a segment at most
+  int units;       // workgroups a segment needs
+  int per_group;   // of them per group
+  int xvec, zvec, yvec, svec;
+};
+
+// Offsets of the parts of one (block, group)'s operands.
+template <int NT, int NPC>
+struct Ops {
+  static constexpr int piece = kQ * NT * 16 * 2;  // one fp16 piece of B or C
+  static constexpr int c = 0, b = NPC * piece, g = b + 2 * piece;
+  static constexpr int scale = g + kTri * 64 * 8 * 4;
+  static constexpr int bytes = scale + 64;
+};
+
+__device__ __forceinline__ float wave_max(float v) {  // v >= 0; uniform result
+#define MIX_STEP(ctrl, rows)                                                                     \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, \
+                                                          rows == 0xf)));
+  MIX_STEP(0x111, 0xf) MIX_STEP(0x112, 0xf) MIX_STEP(0x114, 0xf) MIX_STEP(0x118, 0xf)
+  MIX_STEP(0x142, 0xa) MIX_STEP(0x143, 0xc)
+#undef MIX_STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// The largest of the four lanes i, i + 16, i + 32, i + 48.
+__device__ __forceinline__ float row_max(float v) {
+  u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  v = fmaxf(__uint_as_float(w.x), __uint_as_float(w.y));
+  w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  return fmaxf(__uint_as_float(w.x), __uint_as_float(w.y));
+}
+
+// Inclusive sum over the wave's lanes in float64: steps of very different
+// sizes follow each other in one block, and differences of the sums count.
+__device__ __forceinline__ double wave_scan(double v) {
+#define MIX_STEP(ctrl, rows)                                                                      \
+  {                                                                                               \
+    const u2 w = __builtin_bit_cast(u2, v);                                                       \
+    u2 o;                                                                                         \
+    o.x = __builtin_amdgcn_update_dpp(0, w.x, ctrl, rows, 0xf, rows == 0xf);                      \
+    o.y = __builtin_amdgcn_update_dpp(0, w.y, ctrl, rows, 0xf, rows == 0xf);                      \
+    v += __builtin_bit_cast(double, o);                                                           \
+  }
+  MIX_STEP(0x111, 0xf) MIX_STEP(0x112, 0xf) MIX_STEP(0x114, 0xf) MIX_STEP(0x118, 0xf)
+  MIX_STEP(0x142, 0xa) MIX_STEP(0x143, 0xc)
+#undef MIX_STEP
+  return v;
+}
+
+__device__ __forceinline__ double lane63(double v) {
+  const u2 w = __builtin_bit_cast(u2, v);
+  u2 o;
+  o.x = __builtin_amdgcn_readlane(w.x, 63);
+  o.y = __builtin_amdgcn_readlane(w.y, 63);
+  return __builtin_bit_cast(double, o);
+}
+
+// The power of two that brings the largest magnitude m of a tile to [2^14,
+// 2^15), held where its own factors stay finite.
+__device__ __forceinline__ int shift_for(float m) {
+  const int e = 15 - __builtin_amdgcn_frexp_expf(m);
+  return e < -112 ? -112 : (e > 60 ? 60 : e);
+}
+__device__ __forceinline__ float two(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
+
+__device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// v = hi + lo in fp16, to 22 bits
+__device__ __forceinline__ void pieces(const float* v, h8& hi, h8& lo) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const h2 a = __builtin_convertvector((f2){v[j], v[j + 1]}, h2);
+    const h2 b = __builtin_convertvector((f2){v[j] - (float)a.x, v[j + 1] - (float)a.y}, h2);
+    hi[j] = a.x; hi[j + 1] = a.y; lo[j] = b.x; lo[j + 1] = b.y;
+  }
+}
+__device__ __forceinline__ h8 piece(const float* v) {
+  h8 o;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const h2 a = __builtin_convertvector((f2){v[j], v[j + 1]}, h2);
+    o[j] = a.x; o[j + 1] = a.y;
+  }
+  return o;
+}
+
+// ---- the plan: sequences -> blocks and segments (one workgroup)
+
+__device__ __forceinline__ int block_scan(int v, int* red, int& total) {  // exclusive, 1024 threads
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int x = v;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(x, d, 64);
+    if (lane >= d) x += o;
+  }
+  __syncthreads();
+  if (lane == 63) red[w] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int i = 0; i < 16; ++i) {
+    if (i < w) before += red[i];
+    all += red[i];
+  }
+  total = all;
+  return before + x - v;
+}
+
+__device__ __forceinline__ int block_scan_max(int v, int* red) {  // inclusive, v >= 0
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v = max(v, o);
+  }
+  __syncthreads();
+  if (lane == 63) red[w] = v;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) v = max(v, red[i]);
+  return v;
+}
+
+__global__ void __launch_bounds__(1024) mix_plan_kernel(const BlkArgs a) {
+  __shared__ int red[16], top;
+  int nchunk = 0, nseg = 0, nsplit = 0, ncut = 0;
+  int reached = max(0, min(a.cu[0], (int)a.tokens));  // the largest offset so far
+  for (int64_t s0 = 0; s0 < a.nseq; s0 += 1024) {
+    // the offsets' running maximum: whatever they hold, the sequences lie one
+    // behind the other inside the rows, and the tables hold their blocks
+    const int64_t s = s0 + threadIdx.x;
+    int end = s < a.nseq ? max(reached, min(a.cu[s + 1], (int)a.tokens)) : reached;
+    end = block_scan_max(end, red);
+    int begin = __shfl_up(end, 1, 64);
+    if ((threadIdx.x & 63) == 0) {
+      begin = reached;
+      for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) begin = max(begin, red[i]);
+    }
+    if (threadIdx.x == 1023) top = end;
+    __syncthreads();
+    reached = top;
+    Seq q;
+    int nc = 0, ns = 0;
+    if (s < a.nseq && load_seq(a, s, q)) {
+      q.t0 = begin;
+      q.t1 = end;
+      nc = (int)((q.t1 - q.t0 + kQ - 1) / kQ);
+      ns = nc ? (nc + a.seg_len - 1) / a.seg_len : 1;
+    }
+    int total;
+    const int cb = nchunk + block_scan(nc, red, total);
+    nchunk += total;
+    const int sb = nseg + block_scan(ns, red, total);
+    nseg += total;
+    const int pb = nsplit + block_scan(ns > 1 ? ns : 0, red, total);
+    nsplit += total;
+    const int ub = ncut + block_scan(ns > 1, red, total);
+    ncut += total;
+    for (int k = 0; k < ns; ++k) {
+      const int lo = (int)((int64_t)nc * k / ns), hi = (int)((int64_t)nc * (k + 1) / ns);
+      a.segs[sb + k] = {(int)s, (int)q.t0, (int)q.t1, lo, hi - lo, cb + lo, ns > 1 ? pb + k : -1, ub};
+    }
+  }
+  if (threadIdx.x == 0) *a.head = {nseg, nchunk, nsplit, 0};
+  __syncthreads();  // the segments are written; now the blocks, a wave per segment
+  const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x >> 6; i < nseg; i += 16) {
+    const Seg g = a.segs[i];
+    for (int c = lane; c < g.nc; c += 64) {
+      const int r0 = g.t0 + (g.c0 + c) * kQ;
+      a.chunks[g.gc + c] = {r0, g.t1 < r0 + kQ ? g.t1 : r0 + kQ, g.t0, g.seq};
+    }
+  }
+}
+
+// ---- the operands of one block and group
+
+template <typename IO, int NT, int NPC>
+__global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
+  constexpr int NP = NT * 16, LD = NP + 8;  // row pitch in LDS: 16 bytes more, banks apart
+  constexpr int UN = (NP + 31) / 32;        // (channel, 16 rows) units of a thread
+  using O = Ops<NT, NPC>;
+  __shared__ __align__(16) _Float16 sm[2][2][kQ * LD];  // [B, C][hi, lo]
+  __shared__ float red[2][4];
+  if ((int)blockIdx.x >= a.head->nchunk) return;
+  const Chunk ck = a.chunks[blockIdx.x];
+  const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int inner = a.H * a.P, W = a.W;
+  const bool resume = a.state && a.has && a.has[ck.seq];
+  const int64_t slot = a.slots ? a.slots[ck.seq] : ck.seq;
+  float v[UN][16], mx[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < UN; ++i) {
+    const int u = tid + 256 * i, chn = u % (2 * NP), run = u / (2 * NP), which = chn / NP, n = chn % NP;
+    const bool on = n < a.N && run < 4;
+    const int c = inner + which * a.G * a.N + g * a.N + (on ? n : 0);
+    float in[19];
+#pragma unroll
+    for (int j = 0; j < 19; ++j) {
+      const int t = ck.r0 + 16 * run + j - 3;
+      float x = 0.0f;
+      if (on && t < ck.r1) {
+        if (t >= ck.t0) x = ld<IO>(a.xbc, (int64_t)t * a.xs + c);
+        else if (resume && t - ck.t0 + W - 1 >= 0)
+          x = a.conv_state[(slot * a.C + c) * (W - 1) + (t - ck.t0 + W - 1)];
+      }
+      in[j] = x;
+    }
+    const float bias = on && a.cb ? a.cb[c] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[i][j] = bias;
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {  // the newest tap last in memory, taken first
+      if (3 - k >= W) break;
+      const float w = on ? a.cw[(int64_t)c * W + (W - 1) - (3 - k)] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[i][j] = fmaf(w, in[j + k], v[i][j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float x = on && ck.r0 + 16 * run + j < ck.r1 ? silu(v[i][j]) : 0.0f;
+      v[i][j] = x;
+      if (finite(x)) mx[which] = fmaxf(mx[which], fabsf(x));
+    }
+  }
+  mx[0] = wave_max(mx[0]);
+  mx[1] = wave_max(mx[1]);
+  if (lane == 0) red[0][wave] = mx[0], red[1][wave] = mx[1];
+  __syncthreads();
+  int sh[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    sh[k] = shift_for(fmaxf(fmaxf(red[k][0], red[k][1]), fmaxf(red[k][2], red[k][3])));
+#pragma unroll
+  for (int i = 0; i < UN; ++i) {
+    const int u = tid + 256 * i, chn = u % (2 * NP), run = u / (2 * NP), which = chn / NP, n = chn % NP;
+    if (run >= 4) continue;
+    const float f = two(sh[which]);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float x = v[i][j] * f;
+      const _Float16 hi = (_Float16)x;
+      sm[which][0][(16 * run + j) * LD + n] = hi;
+      sm[which][1][(16 * run + j) * LD + n] = (_Float16)(x - (float)hi);
+    }
+  }
+  __syncthreads();
+  char* out = a.ops + ((int64_t)blockIdx.x * a.G + g) * O::bytes;
+  // C: lane (t, q) of tile (tt, m) holds n = 32 m + 4 q + {0..3} and 16 more,
+  // the order in which the state's accumulators hold n
+  for (int u = tid; u < 4 * (NT / 2) * 64; u += 256) {
+    const int l = u & 63, m = (u >> 6) % (NT / 2), tt = (u >> 6) / (NT / 2);
+#pragma unroll
+    for (int p = 0; p < NPC; ++p) {
+      const _Float16* s = sm[1][p] + (16 * tt + (l & 15)) * LD + 32 * m + 4 * (l >> 4);
+      h8 o;
+      const h4 x = *reinterpret_cast<const h4*>(s), y = *reinterpret_cast<const h4*>(s + 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = x[j], o[j + 4] = y[j];
+      *reinterpret_cast<h8*>(out + O::c + p * O::piece + u * 16) = o;
+    }
+  }
+  // B transposed: lane (n, q) of tile (nt, kb) holds t = 32 kb + 8 q + {0..7}
+  for (int u = tid; u < NT * 2 * 64; u += 256) {
+    const int l = u & 63, kb = (u >> 6) & 1, nt = u >> 7;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const _Float16* s = sm[0][p] + (32 * kb + 8 * (l >> 4)) * LD + 16 * nt + (l & 15);
+      h8 o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = s[j * LD];
+      *reinterpret_cast<h8*>(out + O::b + p * O::piece + u * 16) = o;
+    }
+  }
+  // C.B^T: wave w has the rows t of tile w; the rows s of B are taken in the order
+  // that leaves lane (t, q) with s = 32 kb + 8 q + {0..7}
+  for (int kb = 0; kb <= (wave >> 1); ++kb) {
+    f4 acc[2] = {};
+#pragma unroll
+    for (int m = 0; m < NT / 2; ++m) {
+      h8 cp[2], bp[2][2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        cp[p] = *reinterpret_cast<const h8*>(sm[1][p] + (16 * wave + (lane & 15)) * LD + 32 * m + 8 * (lane >> 4));
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          bp[e][p] = *reinterpret_cast<const h8*>(
+              sm[0][p] + (32 * kb + 8 * ((lane & 15) >> 2) + 4 * e + (lane & 3)) * LD + 32 * m + 8 * (lane >> 4));
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        acc[e] = mfma(bp[e][1], cp[0], acc[e]);
+        acc[e] = mfma(bp[e][0], cp[1], acc[e]);
+        acc[e] = mfma(bp[e][0], cp[0], acc[e]);
+      }
+    }
+    const int tile = wave < 2 ? wave : 2 * wave - 2 + kb;
+    f4* o = reinterpret_cast<f4*>(out + O::g + (tile * 64 + lane) * 32);
+    o[0] = acc[0];
+    o[1] = acc[1];
+  }
+  if (tid < 2) reinterpret_cast<int*>(out + O::scale)[tid] = sh[tid];
+}
+
+// ---- the walk over a segment
+
+// One wave per 16 PT channels of a head (PT = 2: channels 2 i and 2 i + 1 of
+// its 32 are row i of the two tiles, so that a lane reads x two channels and
+// z, y eight channels at a time).  PC: pieces of the operands of y.
+template <typename IO, int NT, int PT, int PC, bool SUM>
+__global__ void __launch_bounds__(256) mix_block_kernel(const BlkArgs a) {
+  using O = Ops<NT, PC>;
+  constexpr int PB = 16 * PT;  // channels of a wave
+  __shared__ float s_cum[4][64], s_lo[4][64], s_dt[4][64], s_w[4][64];
+  __shared__ int s_bad[4][PB];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i16 = lane & 15, q4 = lane >> 4;
+  const int si = blockIdx.x / a.units, unit = blockIdx.x % a.units;
+  if (si >= a.head->nseg) return;
+  const Seg sg = a.segs[si];
+  if (SUM && (sg.split < 0 || sg.c0 + sg.nc == (sg.t1 - sg.t0 + kQ - 1) / kQ)) return;  // no state asked
+  const int g = unit / a.per_group, hpg = a.H / a.G, bph = (a.P + PB - 1) / PB;
+  const int blk = (unit % a.per_group) * 4 + wave;
+  const bool last = sg.t0 + (int64_t)(sg.c0 + sg.nc) * kQ >= sg.t1;
+  const int inner = a.H * a.P, W = a.W, N = a.N;
+  const bool resume = a.state && a.has && a.has[sg.seq];
+  const int64_t slot = a.slots ? a.slots[sg.seq] : sg.seq;
+  // the last inputs of B and C into the slot: nobody reads the old ones any more
+  if (!SUM && last && a.state && W > 1 && unit % a.per_group == 0) {
+    for (int u = threadIdx.x; u < 2 * N; u += 256) {
+      const int c = inner + (u / N) * a.G * N + g * N + u % N;
+      float* own = a.conv_state + (slot * a.C + c) * (W - 1);
+      float v[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const int64_t r = (int64_t)sg.t1 - (W - 1) + j;
+        v[j] = j >= W - 1 ? 0.0f : r >= sg.t0 ? ld<IO>(a.xbc, r * a.xs + c) : resume ? own[r - sg.t0 + W - 1] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < W - 1) own[j] = v[j];
+    }
+  }
+  if (blk >= hpg * bph) return;
+  const int h = g * hpg + blk / bph, p0 = (blk % bph) * PB;
+  // this lane's channels as rows of the tiles; past the head's last one a copy of a valid one
+  int ch[PT];
+#pragma unroll
+  for (int e = 0; e < PT; ++e) {
+    const int p = p0 + PT * i16 + e;
+    ch[e] = h * a.P + (p < a.P ? p : e && p - 1 < a.P ? p - 1 : p0);
+  }
+  if constexpr (PT == 2)
+    if (a.xvec && p0 + 2 * i16 + 1 >= a.P) ch[1] = ch[0] + 1;  // P even: both or neither are past it
+  float cw[PT][4], cb[PT];
+#pragma unroll
+  for (int e = 0; e < PT; ++e) {
+    cb[e] = a.cb ? a.cb[ch[e]] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cw[e][k] = k < W ? a.cw[(int64_t)ch[e] * W + (W - 1) - k] : 0.0f;  // k rows back
+  }
+  const float A2 = a.A[h] * kLog2e, db = a.dt_bias ? a.dt_bias[h] : 0.0f, D = a.Dskip ? a.Dskip[h] : 0.0f;
+
+  // the state entering the segment: lane (i, q) holds n = 16 nt + 4 q + r of its channels
+  f4 S[PT][NT];
+  {
+    const float* src = nullptr;
+    if (sg.split >= 0 && sg.c0 > 0) src = SUM ? nullptr : a.local + (int64_t)sg.split * inner * N;
+    else if (!SUM && resume) src = a.state + slot * inner * N;
+#pragma unroll
+    for (int e = 0; e < PT; ++e)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int n = 16 * nt + 4 * q4;
+        if (src) {
+          const float* s = src + (int64_t)ch[e] * N + n;
+          if (a.svec) {
+            if (n < N) v = *reinterpret_cast<const f4*>(s);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (n + r < N) v[r] = s[r];
+          }
+        }
+        S[e][nt] = v;
+      }
+  }
+  double dsum = 0.0;  // log2 of the segment's decay
+
+  for (int c = 0; c < sg.nc; ++c) {
+    const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ), cnt = r1 - r0;
+    const char* op = a.ops + ((int64_t)(sg.gc + c) * a.G + g) * O::bytes;
+    // ---- x: rows 32 kb + 8 q - 3 .. + 7 of the lane's channels
+    float v[PT][2][8];
+    {
+      float in[PT][2][11];
+      auto load = [&](auto edge) {
+        constexpr bool EDGE = decltype(edge)::value;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int j = 0; j < 11; ++j) {
+            const int t = 32 * kb + 8 * q4 + j - 3;  // in the block
+            int64_t r = (int64_t)r0 + t;
+            bool ok = true;
+            if constexpr (EDGE) {
+              ok = r >= sg.t0 && r < r1;
+              r = ok ? r : r0;
+            }
+            if constexpr (PT == 2) {
+              if (a.xvec) {
+                if constexpr (sizeof(IO) == 2) {
+                  const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                      static_cast<const uint16_t*>(a.xbc) + r * a.xs + ch[0]);
+                  in[0][kb][j] = __uint_as_float(w << 16);
+                  in[1][kb][j] = __uint_as_float(w & 0xffff0000u);
+                } else {
+                  const f2 w = *reinterpret_cast<const f2*>(static_cast<const float*>(a.xbc) + r * a.xs + ch[0]);
+                  in[0][kb][j] = w.x;
+                  in[1][kb][j] = w.y;
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < PT; ++e) in[e][kb][j] = ld<IO>(a.xbc, r * a.xs + ch[e]);
+              }
+            } else {
+              in[0][kb][j] = ld<IO>(a.xbc, r * a.xs + ch[0]);
+            }
+            if constexpr (EDGE) {
+#pragma unroll
+              for (int e = 0; e < PT; ++e) in[e][kb][j] = ok ? in[e][kb][j] : 0.0f;
+            }
+          }
+      };
+      const bool first = sg.c0 + c == 0;
+      if (first || cnt < kQ) {
+        load(std::integral_constant<bool, true>{});
+        if (first && resume && W > 1 && q4 == 0) {  // the inputs before the sequence
+          const bool saved = !SUM && sg.split >= 0;
+#pragma unroll
+          for (int e = 0; e < PT; ++e)
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+              const int at = j - 3 + W - 1;
+              if (at >= 0)
+                in[e][0][j] = saved ? a.cs0[((int64_t)sg.cut * inner + ch[e]) * 3 + at]
+                                    : a.conv_state[(slot * a.C + ch[e]) * (W - 1) + at];
+            }
+          if constexpr (SUM) {  // the second pass overwrites the slot: it reads these
+#pragma unroll
+            for (int e = 0; e < PT; ++e)
+              if (p0 + PT * i16 + e < a.P)
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                  if (j - 3 + W - 1 >= 0)
+                    a.cs0[((int64_t)sg.cut * inner + ch[e]) * 3 + j - 3 + W - 1] = in[e][0][j];
+          }
+        }
+      } else {
+        load(std::integral_constant<bool, false>{});
+      }
+#pragma unroll
+      for (int e = 0; e < PT; ++e)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[e][kb][j] = fmaf(cw[e][0], in[e][kb][j + 3], cb[e]);
+#pragma unroll
+      for (int k = 1; k < 4; ++k)
+        if (k < W)
+#pragma unroll
+          for (int e = 0; e < PT; ++e)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[e][kb][j] = fmaf(cw[e][k], in[e][kb][j + 3 - k], v[e][kb][j]);
+    }
+    // ---- steps: lane t
+    const bool live = lane < cnt;
+    float dt = 0.0f, dA = 0.0f;
+    if (live) {
+      const float raw = ld<IO>(a.dt, (int64_t)(r0 + lane) * a.ds + h) + db;
+      dt = a.softplus ? softplus(raw) : raw;
+      // below 2^-160 a decay is zero in float32; held there, no sum swallows the steps beside it
+      dA = dt * A2;
+      dA = dA < -160.0f ? -160.0f : dA;
+    }
+    const double cum = wave_scan((double)dA), tot = lane63(cum);
+    const float wt = dt * ex2((float)(tot - cum));
+    const float dec = ex2((float)cum), dec_all = ex2((float)tot);
+    const float wmax = wave_max(finite(wt) ? fabsf(wt) : 0.0f);
+    int shw = -__builtin_amdgcn_frexp_expf(wmax);
+    shw = shw < -112 ? -112 : (shw > 60 ? 60 : shw);
+    dsum += tot;
+    // ---- silu, the tile's scale
+    float mx = 0.0f, chk = 0.0f;
+#pragma unroll
+    for (int e = 0; e < PT; ++e)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float x = silu(v[e][kb][j]);
+          if (cnt < kQ) x = 32 * kb + 8 * q4 + j < cnt ? x : 0.0f;
+          v[e][kb][j] = x;
+          mx = fmaxf(mx, fabsf(x));
+          chk = fmaf(x, 0.0f, chk);
+        }
+    const bool bad = __any(!(chk == 0.0f));
+    if (bad) {
+      mx = 0.0f;
+      int first[PT];
+#pragma unroll
+      for (int e = 0; e < PT; ++e) {
+        first[e] = kQ;
+#pragma unroll
+        for (int kb = 1; kb >= 0; --kb)
+#pragma unroll
+          for (int j = 7; j >= 0; --j) {
+            if (finite(v[e][kb][j])) mx = fmaxf(mx, fabsf(v[e][kb][j]));
+            else first[e] = 32 * kb + 8 * q4 + j;
+          }
+        first[e] = min(first[e], __shfl_xor(first[e], 16, 64));
+        first[e] = min(first[e], __shfl_xor(first[e], 32, 64));
+        if (q4 == 0) s_bad[wave][PT * i16 + e] = first[e];
+      }
+    }
+    const float xmax = wave_max(mx);
+    const int shx = shift_for(xmax);
+    const float fx = two(shx);
+    if (live) s_cum[wave][lane] = (float)cum;
+    else s_cum[wave][lane] = (float)tot;
+    s_lo[wave][lane] = live ? (float)(cum - (double)(float)cum) : 0.0f;
+    s_w[wave][lane] = wt * two(shw);
+    const int* sc = reinterpret_cast<const int*>(op + O::scale);
+    const int shB = sc[0], shC = sc[1];
+    if constexpr (!SUM) s_dt[wave][lane] = dt;
+    __builtin_amdgcn_wave_barrier();
+
+    // ---- operands from x: once as it is (for y), once weighted (for the state)
+    h8 xh[PT][2], xl[PT][2], wh[PT][2], wl[PT][2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float w8[8];
+      *reinterpret_cast<f4*>(w8) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4]);
+      *reinterpret_cast<f4*>(w8 + 4) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4 + 4]);
+#pragma unroll
+      for (int e = 0; e < PT; ++e) {
+        float x[8], w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] = v[e][kb][j] * fx;
+          w[j] = x[j] * w8[j];
+        }
+        pieces(w, wh[e][kb], wl[e][kb]);
+        if constexpr (!SUM) {
+          if (bad)  // 0 x Inf is not 0: y's earlier rows must not meet them
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = finite(x[j]) ? x[j] : 0.0f;
+          if constexpr (PC == 2) pieces(x, xh[e][kb], xl[e][kb]);
+          else xh[e][kb] = piece(x);
+        }
+      }
+    }
+
+    if constexpr (!SUM) {
+      // ---- the state as an operand
+      float sm = 0.0f;
+#pragma unroll
+      for (int e = 0; e < PT; ++e)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sm = fmaxf(sm, fabsf(S[e][nt][r]));
+      sm = wave_max(sm);
+      if (!finite(sm)) {
+        sm = 0.0f;
+#pragma unroll
+        for (int e = 0; e < PT; ++e)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (finite(S[e][nt][r])) sm = fmaxf(sm, fabsf(S[e][nt][r]));
+        sm = wave_max(sm);
+      }
+      const int shS = shift_for(sm);
+      const float fs = two(shS);
+      h8 sh[PT][NT / 2], sl[PT][NT / 2];
+#pragma unroll
+      for (int e = 0; e < PT; ++e)
+#pragma unroll
+        for (int m = 0; m < NT / 2; ++m) {
+          float x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * fs;
+          if constexpr (PC == 2) pieces(x, sh[e][m], sl[e][m]);
+          else sh[e][m] = piece(x);
+        }
+      const int e_mx = -(shB + shC + shx), e_cs = -(shC + shS);
+      const float Dm = __builtin_amdgcn_ldexpf(D, shB + shC);
+      // ---- y, 16 rows at a time
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const int t = 16 * tt + i16;
+        if (16 * tt >= cnt) break;
+        const float cum_t = s_cum[wave][t], lo_t = s_lo[wave][t];
+        f4 ym[PT] = {}, yc[PT] = {};
+        float m[2][8], rm = 0.0f;
+#pragma unroll
+        for (int kb = 0; kb <= tt / 2; ++kb) {
+          const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
+          const f4* gp = reinterpret_cast<const f4*>(op + O::g + (tile * 64 + lane) * 32);
+          const f4 g0 = gp[0], g1 = gp[1];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int s = 32 * kb + 8 * q4 + j;
+            float x = cum_t - s_cum[wave][s];
+            if constexpr (PC == 2) x += lo_t - s_lo[wave][s];
+            x = (j < 4 ? g0[j & 3] : g1[j & 3]) * (ex2(x) * s_dt[wave][s]);
+            if (kb == tt / 2) {
+              x = s <= t ? x : 0.0f;
+              x = s == t ? x + Dm : x;
+            }
+            m[kb][j] = x;
+            rm = fmaxf(rm, fabsf(x));
+          }
+        }
+        // every row by its own largest value: one token's outlier leaves the others their bits
+        const int shM = shift_for(row_max(rm));
+        const float fm = two(shM);
+#pragma unroll
+        for (int kb = 0; kb <= tt / 2; ++kb) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m[kb][j] *= fm;
+          if constexpr (PC == 2) {
+            h8 mh, ml;
+            pieces(m[kb], mh, ml);
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              ym[e] = mfma(xl[e][kb], mh, ym[e]);
+              ym[e] = mfma(xh[e][kb], ml, ym[e]);
+              ym[e] = mfma(xh[e][kb], mh, ym[e]);
+            }
+          } else {
+            const h8 mh = piece(m[kb]);
+#pragma unroll
+            for (int e = 0; e < PT; ++e) ym[e] = mfma(xh[e][kb], mh, ym[e]);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < NT / 2; ++m) {
+          const h8 cp = *reinterpret_cast<const h8*>(op + O::c + ((tt * (NT / 2) + m) * 64 + lane) * 16);
+          if constexpr (PC == 2) {
+            const h8 cl = *reinterpret_cast<const h8*>(op + O::c + O::piece + ((tt * (NT / 2) + m) * 64 + lane) * 16);
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              yc[e] = mfma(sl[e][m], cp, yc[e]);
+              yc[e] = mfma(sh[e][m], cl, yc[e]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < PT; ++e) yc[e] = mfma(sh[e][m], cp, yc[e]);
+        }
+        // lane (t, q): channels p0 + 4 PT q + {0 .. 4 PT - 1}
+        const float dec_t = ex2(cum_t + lo_t);
+        const int pw = p0 + 4 * PT * q4;
+        const int64_t row = (int64_t)r0 + t, col = (int64_t)h * a.P + pw;
+        float o[4 * PT];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < PT; ++e) {
+            float y = __builtin_amdgcn_ldexpf(ym[e][r], e_mx - shM) + __builtin_amdgcn_ldexpf(yc[e][r] * dec_t, e_cs);
+            if (bad) y = t >= s_bad[wave][4 * PT * q4 + PT * r + e] ? __builtin_nanf("") : y;
+            o[PT * r + e] = y;
+          }
+        if (t < cnt) {
+          if (a.z) {
+            if (a.zvec) {
+              if (pw < a.P) {
+                float zz[4 * PT];
+                if constexpr (sizeof(IO) == 4) {
+#pragma unroll
+                  for (int k = 0; k < PT; ++k)
+                    *reinterpret_cast<f4*>(zz + 4 * k) = *reinterpret_cast<const f4*>(
+                        static_cast<const float*>(a.z) + row * a.zs + col + 4 * k);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < PT; ++k) {
+                    const u2 w = *reinterpret_cast<const u2*>(static_cast<const uint16_t*>(a.z) + row * a.zs + col + 4 * k);
+                    zz[4 * k] = __uint_as_float(w.x << 16);
+                    zz[4 * k + 1] = __uint_as_float(w.x & 0xffff0000u);
+                    zz[4 * k + 2] = __uint_as_float(w.y << 16);
+                    zz[4 * k + 3] = __uint_as_float(w.y & 0xffff0000u);
+                  }
+                }
+#pragma unroll
+                for (int k = 0; k < 4 * PT; ++k) o[k] *= silu(zz[k]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4 * PT; ++k)
+                if (pw + k < a.P) o[k] *= silu(ld<IO>(a.z, row * a.zs + col + k));
+            }
+          }
+          if (a.yvec) {
+            if (pw < a.P) {
+              if constexpr (sizeof(IO) == 4) {
+#pragma unroll
+                for (int k = 0; k < PT; ++k)
+                  *reinterpret_cast<f4*>(static_cast<float*>(a.y) + row * a.ys + col + 4 * k) =
+                      *reinterpret_cast<const f4*>(o + 4 * k);
+              } else {
+                typedef __bf16 bf __attribute__((ext_vector_type(4 * PT)));
+                typedef float fv __attribute__((ext_vector_type(4 * PT)));
+                fv f;
+#pragma unroll
+                for (int k = 0; k < 4 * PT; ++k) f[k] = o[k];
+                *reinterpret_cast<bf*>(static_cast<uint16_t*>(a.y) + row * a.ys + col) =
+                    __builtin_convertvector(f, bf);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4 * PT; ++k)
+              if (pw + k < a.P) st<IO>(a.y, row * a.ys + col + k, o[k]);
+          }
+        }
+      }
+    }
+    // ---- the state after the block
+    const int e_su = -(shB + shx + shw);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      h8 bh[2], bl[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        bh[kb] = *reinterpret_cast<const h8*>(op + O::b + ((nt * 2 + kb) * 64 + lane) * 16);
+        bl[kb] = *reinterpret_cast<const h8*>(op + O::b + O::piece + ((nt * 2 + kb) * 64 + lane) * 16);
+      }
+#pragma unroll
+      for (int e = 0; e < PT; ++e) {
+        f4 d = {};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          d = mfma(bh[kb], wl[e][kb], d);
+          d = mfma(bl[kb], wh[e][kb], d);
+          d = mfma(bh[kb], wh[e][kb], d);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          S[e][nt][r] = fmaf(S[e][nt][r], dec_all, __builtin_amdgcn_ldexpf(d[r], e_su));
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+
+  // ---- what the segment leaves
+  float* dst = nullptr;
+  if constexpr (SUM) {
+    dst = a.local + (int64_t)sg.split * inner * N;
+    if (lane == 0 && p0 == 0) a.decay[(int64_t)sg.split * a.H + h] = (float)dsum;
+  } else {
+    if (last && a.state) dst = a.state + slot * inner * N;
+  }
+  if (dst) {
+#pragma unroll
+    for (int e = 0; e < PT; ++e)
+      if (p0 + PT * i16 + e < a.P)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int n = 16 * nt + 4 * q4;
+          float* s = dst + (int64_t)ch[e] * N + n;
+          if (a.svec) {
+            if (n < N) *reinterpret_cast<f4*>(s) = S[e][nt];
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (n + r < N) s[r] = S[e][nt][r];
+          }
+        }
+  }
+  // the last inputs of the wave's own channels (read by nobody else, or saved by the first pass)
+  if (!SUM && last && a.state && W > 1) {
+    for (int u = lane; u < PB; u += 64) {
+      if (p0 + u >= a.P) break;
+      const int c = h * a.P + p0 + u;
+      float* own = a.conv_state + (slot * a.C + c) * (W - 1);
+      float x[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const int64_t r = (int64_t)sg.t1 - (W - 1) + j;
+        x[j] = j >= W - 1 ? 0.0f : r >= sg.t0 ? ld<IO>(a.xbc, r * a.xs + c) : resume ? own[r - sg.t0 + W - 1] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < W - 1) own[j] = x[j];
+    }
+  }
+}
+
+// ---- the states entering the segments of a cut sequence, from their states from zero
+
+__global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
+  const int si = blockIdx.x;
+  if (si >= a.head->nseg) return;
+  const Seg sg = a.segs[si];
+  if (sg.split < 0 || sg.c0 > 0) return;  // the first segment of each cut sequence does all of its
+  const int64_t per = (int64_t)a.H * a.P * a.N;
+  const int ns = ((sg.t1 - sg.t0 + kQ - 1) / kQ + a.seg_len - 1) / a.seg_len;
+  const bool resume = a.state && a.has && a.has[sg.seq];
+  const int64_t slot = a.slots ? a.slots[sg.seq] : sg.seq;
+  const int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x;
+  if (i >= per) return;
+  const int h = (int)(i / ((int64_t)a.P * a.N));
+  float s = resume ? a.state[slot * per + i] : 0.0f;
+  float* l = a.local + (int64_t)sg.split * per + i;
+  const float* d = a.decay + (int64_t)sg.split * a.H + h;
+  for (int k = 0; k < ns; ++k) {
+    const float own = k + 1 < ns ? l[k * per] : 0.0f;
+    l[k * per] = s;
+    s = fmaf(s, ex2(k + 1 < ns ? d[(int64_t)k * a.H] : 0.0f), own);
+  }
 }
 
 // ---------------------------------------------------------------- group norm
@@ -470,6 +1363,79 @@ int check_mix(MixArgs& a, bool step, int64_t rows, int64_t nseq, int64_t nslots,
   return SSM_OK;
 }
 
+// Workspace of ssm_conv_ssd_fwd, and how its sequences are cut.
+struct MixLayout {
+  int nt, pt, pc;
+  int64_t nchunk, nseg, nsplit, ncut;  // at most
+  int seg_len, per_group, units;
+  int64_t op_bytes, chunks, segs, ops, local, decay, cs0, bytes;
+};
+
+// A segment is one workgroup's work, one after another; the card holds 512
+// workgroups of four waves at two waves a SIMD.
+constexpr int64_t kSegWorkgroups = 512;
+constexpr int kSegMin = 4;
+
+MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N, int io_dtype) {
+  MixLayout l;
+  l.nt = N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16;
+  l.pt = l.nt == 16 ? 1 : 2;
+  l.pc = io_dtype == SSM_DTYPE_BF16 ? 1 : 2;
+  const int64_t bph = (P + 16 * l.pt - 1) / (16 * l.pt);
+  l.per_group = (int)((H / G * bph + 3) / 4);
+  l.units = (int)(l.per_group * G);
+  l.nchunk = tokens / kQ + nseq;
+  const int64_t work = (tokens + kQ - 1) / kQ * l.units;
+  int64_t len = (work + kSegWorkgroups - 1) / kSegWorkgroups;
+  if (len < kSegMin) len = kSegMin;
+  l.seg_len = (int)len;
+  const bool cut = (tokens + kQ - 1) / kQ > len;
+  l.nsplit = cut ? 2 * (l.nchunk / len) : 0;
+  l.ncut = cut ? l.nchunk / len : 0;
+  l.nseg = nseq + l.nchunk / len;
+  const int64_t piece = (int64_t)kQ * l.nt * 16 * 2;
+  l.op_bytes = (l.pc + 2) * piece + kTri * 64 * 8 * 4 + 64;
+  int64_t at = 0;
+  auto take = [&](int64_t n) {
+    const int64_t o = at;
+    at += (n + 255) / 256 * 256;
+    return o;
+  };
+  take(sizeof(PlanHead));
+  l.chunks = take(l.nchunk * sizeof(Chunk));
+  l.segs = take(l.nseg * sizeof(Seg));
+  l.ops = take(l.nchunk * G * l.op_bytes);
+  l.local = take(l.nsplit * H * P * N * 4);
+  l.decay = take(l.nsplit * H * 4);
+  l.cs0 = take(l.ncut * H * P * 3 * 4);
+  l.bytes = at;
+  return l;
+}
+
+template <typename IO, int NT, int PT, int PC>
+void launch_mix_blocks(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
+  static_assert(Ops<NT, PC>::bytes == (PC + 2) * kQ * NT * 32 + kTri * 64 * 32 + 64, "as in mix_layout");
+  mix_plan_kernel<<<1, 1024, 0, s>>>(b);
+  mix_prep_kernel<IO, NT, PC><<<dim3((unsigned)l.nchunk, b.G), 256, 0, s>>>(b);
+  const unsigned grid = (unsigned)(l.nseg * l.units);
+  if (l.nsplit) {
+    mix_block_kernel<IO, NT, PT, PC, true><<<grid, 256, 0, s>>>(b);
+    const int64_t per = (int64_t)b.H * b.P * b.N;
+    mix_join_kernel<<<dim3((unsigned)l.nseg, (unsigned)((per + 255) / 256)), 256, 0, s>>>(b);
+  }
+  mix_block_kernel<IO, NT, PT, PC, false><<<grid, 256, 0, s>>>(b);
+}
+
+template <typename IO, int PC>
+void launch_mix(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
+  switch (l.nt) {
+    case 2: launch_mix_blocks<IO, 2, 2, PC>(b, l, s); break;
+    case 4: launch_mix_blocks<IO, 4, 2, PC>(b, l, s); break;
+    case 8: launch_mix_blocks<IO, 8, 2, PC>(b, l, s); break;
+    default: launch_mix_blocks<IO, 16, 1, PC>(b, l, s); break;
+  }
+}
+
 template <typename IO>
 void launch_mix_simple(const MixArgs& a, hipStream_t s) {
   mix_scan_kernel<IO><<<dim3((unsigned)a.nseq, a.H, (a.P + 15) / 16), 256, 0, s>>>(a);
@@ -514,7 +1480,7 @@ int64_t ssm_conv_ssd_workspace_size(int64_t tokens, int64_t nseq, int64_t nheads
                                     int64_t ngroups, int64_t dstate, int io_dtype) {
   g_last_error[0] = 0;
   if (check_mix_extents(tokens, nseq, nheads, headdim, ngroups, dstate) || check_io(io_dtype)) return -1;
-  return 256;
+  return mix_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype).bytes;
 }
 
 int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_t dt_stride,
@@ -527,7 +1493,7 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
                      int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
                      int64_t width, int io_dtype, void* hip_stream) {
   g_last_error[0] = 0;
-  MixArgs a;
+  BlkArgs a;
   memset(&a, 0, sizeof a);
   a.xbc = xbc; a.dt = dt; a.z = z; a.cw = conv_weight; a.cb = conv_bias; a.A = A; a.Dskip = Dskip;
   a.dt_bias = dt_bias; a.cu = cu_seqlens; a.slots = slots; a.has = has_state;
@@ -544,9 +1510,29 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
     return fail(SSM_E_SHAPE, "workspace holds %lld bytes, needs %lld", (long long)workspace_bytes,
                 (long long)need);
   if (!aligned16(workspace)) return fail(SSM_E_ALIGN, "workspace is not 16-byte aligned");
+  const MixLayout l = mix_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype);
+  if (l.nseg * l.units > 0x7fffffff || l.nchunk > 0x7fffffff)
+    return fail(SSM_E_SHAPE, "too many sequences and heads for one call");
+  char* w = static_cast<char*>(workspace);
+  a.head = reinterpret_cast<PlanHead*>(w);
+  a.chunks = reinterpret_cast<Chunk*>(w + l.chunks);
+  a.segs = reinterpret_cast<Seg*>(w + l.segs);
+  a.ops = w + l.ops;
+  a.local = reinterpret_cast<float*>(w + l.local);
+  a.decay = reinterpret_cast<float*>(w + l.decay);
+  a.cs0 = reinterpret_cast<float*>(w + l.cs0);
+  a.op_bytes = l.op_bytes; a.seg_len = l.seg_len; a.units = l.units; a.per_group = l.per_group;
+  const int es = io_dtype == SSM_DTYPE_BF16 ? 2 : 4, wide = 4 * l.pt * es < 16 ? 4 * l.pt * es : 16;
+  auto lanes = [&](const void* p, int64_t stride, int bytes) {  // whole accesses of that many bytes
+    return ((uintptr_t)p | (uintptr_t)(stride * es) | (uintptr_t)(headdim * es)) % bytes == 0;
+  };
+  a.xvec = lanes(xbc, xbc_stride, 2 * es);
+  a.zvec = headdim % (4 * l.pt) == 0 && lanes(z, z_stride, wide);
+  a.yvec = headdim % (4 * l.pt) == 0 && lanes(y, y_stride, wide);
+  a.svec = dstate % 4 == 0 && aligned16(ssm_state);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (io_dtype == SSM_DTYPE_BF16) launch_mix_simple<uint16_t>(a, s);
-  else launch_mix_simple<float>(a, s);
+  if (io_dtype == SSM_DTYPE_BF16) launch_mix<uint16_t, 1>(a, l, s);
+  else launch_mix<float, 2>(a, l, s);
   return launch_status("ssm_conv_ssd_fwd launch");
 }
 
