@@ -263,7 +263,7 @@ struct BlkArgs : MixArgs {
   int seg_len;     // blocks of a segment at most
   int units;       // workgroups a segment needs
   int per_group;   // of them per group
-  int xvec, zvec, yvec, svec;
+  int fast;
 };
 
 // Offsets of the parts of one (block, group)'s operands.
@@ -457,17 +457,19 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
     const int u = tid + 256 * i, chn = u % (2 * NP), run = u / (2 * NP), which = chn / NP, n = chn % NP;
     const bool on = n < a.N && run < 4;
     const int c = inner + which * a.G * a.N + g * a.N + (on ? n : 0);
+    // rows outside the block or the sequence are read from inside and replaced,
+    // so that the loads of all rows are in flight together
     float in[19];
+    const int lo = ck.r0 + 16 * run - 3, top = ck.r1 - 1;
 #pragma unroll
-    for (int j = 0; j < 19; ++j) {
-      const int t = ck.r0 + 16 * run + j - 3;
-      float x = 0.0f;
-      if (on && t < ck.r1) {
-        if (t >= ck.t0) x = ld<IO>(a.xbc, (int64_t)t * a.xs + c);
-        else if (resume && t - ck.t0 + W - 1 >= 0)
-          x = a.conv_state[(slot * a.C + c) * (W - 1) + (t - ck.t0 + W - 1)];
-      }
-      in[j] = x;
+    for (int j = 0; j < 19; ++j)
+      in[j] = ld<IO>(a.xbc, (int64_t)max(min(lo + j, top), ck.t0) * a.xs + c);
+#pragma unroll
+    for (int j = 0; j < 19; ++j) in[j] = on && lo + j >= ck.t0 && lo + j <= top ? in[j] : 0.0f;
+    if (resume && lo < ck.t0 && on) {  // the sequence's first rows: the inputs before it
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j - 3 + W - 1 >= 0) in[j] = a.conv_state[(slot * a.C + c) * (W - 1) + j - 3 + W - 1];
     }
     const float bias = on && a.cb ? a.cb[c] : 0.0f;
 #pragma unroll
@@ -567,53 +569,100 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
 
 // ---- the walk over a segment
 
+// Copies BYTES from global memory to LDS, 16 bytes a lane, on their way when it
+// returns: staged() waits for them and for the other waves.
+template <int WV, int BYTES>
+__device__ __forceinline__ void stage(const char* from, char* to) {
+  static_assert(BYTES % 1024 == 0, "whole waves");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < (BYTES / 1024 + WV - 1) / WV; ++i) {
+    const int at = (i * WV + wave) * 1024;
+    if (BYTES / 1024 % WV == 0 || at < BYTES)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(from + at + lane * 16),
+          (__attribute__((address_space(3))) void*)(to + at), 16, 0, 0);
+  }
+}
+__device__ __forceinline__ void staged() {
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __syncthreads();
+}
+
+// The last W - 1 inputs of channel c of a sequence into its slot.
+template <typename IO>
+__device__ __forceinline__ void keep_inputs(const MixArgs& a, const Seg& sg, int64_t slot, bool resume, int c) {
+  const int W = a.W;
+  float* own = a.conv_state + (slot * a.C + c) * (W - 1);
+  float v[3];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const int64_t r = (int64_t)sg.t1 - (W - 1) + j;
+    v[j] = j >= W - 1 ? 0.0f : r >= sg.t0 ? ld<IO>(a.xbc, r * a.xs + c) : resume ? own[r - sg.t0 + W - 1] : 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    if (j < W - 1) own[j] = v[j];
+}
+
+// What a wave reads of a block's rows ahead of time: x of its channels at rows
+// 32 kb + 8 q - 3 .. + 7, as they lie in memory.
+template <typename IO, int PT, bool FAST>
+struct XRaw {
+  static constexpr bool pair = FAST && PT == 2 && sizeof(IO) == 2;  // two channels in one word
+  static constexpr int K = pair ? 1 : PT;
+  uint32_t w[K][2][11];
+  __device__ __forceinline__ float get(int e, int kb, int j) const {
+    if constexpr (pair) return __uint_as_float(e ? w[0][kb][j] & 0xffff0000u : w[0][kb][j] << 16);
+    else if constexpr (sizeof(IO) == 2) return __uint_as_float(w[e][kb][j] << 16);
+    else return __uint_as_float(w[e][kb][j]);
+  }
+};
+
 // One wave per 16 PT channels of a head (PT = 2: channels 2 i and 2 i + 1 of
 // its 32 are row i of the two tiles, so that a lane reads x two channels and
-// z, y eight channels at a time).  PC: pieces of the operands of y.
-template <typename IO, int NT, int PT, int PC, bool SUM>
-__global__ void __launch_bounds__(256) mix_block_kernel(const BlkArgs a) {
+// z, y eight channels at a time).  The WV waves of a workgroup share a group
+// of heads and stage its operands in LDS, B of this block while the waves
+// work on y, C and C.B^T of the next while they work on the state; x, dt and z
+// of the next block are on their way in registers meanwhile.  PC: pieces of
+// the operands of y.  FAST: rows and channels allow whole vectors (headdim a
+// multiple of 4 PT, dstate of 4, rows aligned to the accesses).
+template <typename IO, int NT, int PT, int PC, int WV, bool SUM, bool FAST>
+__global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(2, 2)))
+mix_block_kernel(const BlkArgs a) {
   using O = Ops<NT, PC>;
   constexpr int PB = 16 * PT;  // channels of a wave
-  __shared__ float s_cum[4][64], s_lo[4][64], s_dt[4][64], s_w[4][64];
-  __shared__ int s_bad[4][PB];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i16 = lane & 15, q4 = lane >> 4;
+  __shared__ __align__(16) char s_b[2 * O::piece];
+  __shared__ __align__(16) char s_cg[SUM ? 16 : O::scale - O::g + PC * O::piece];
+  constexpr int CG = PC * O::piece;  // C.B^T behind C
+  __shared__ __align__(16) float s_cum[WV][64], s_lo[WV][64], s_dt[WV][64], s_w[WV][64];
+  __shared__ int s_bad[WV][PB];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int i16 = lane & 15, q4 = lane >> 4;
   const int si = blockIdx.x / a.units, unit = blockIdx.x % a.units;
   if (si >= a.head->nseg) return;
   const Seg sg = a.segs[si];
   if (SUM && (sg.split < 0 || sg.c0 + sg.nc == (sg.t1 - sg.t0 + kQ - 1) / kQ)) return;  // no state asked
   const int g = unit / a.per_group, hpg = a.H / a.G, bph = (a.P + PB - 1) / PB;
-  const int blk = (unit % a.per_group) * 4 + wave;
+  const int blk = (unit % a.per_group) * WV + wave;
+  const bool on = blk < hpg * bph;  // else the wave only helps to stage
   const bool last = sg.t0 + (int64_t)(sg.c0 + sg.nc) * kQ >= sg.t1;
   const int inner = a.H * a.P, W = a.W, N = a.N;
   const bool resume = a.state && a.has && a.has[sg.seq];
   const int64_t slot = a.slots ? a.slots[sg.seq] : sg.seq;
   // the last inputs of B and C into the slot: nobody reads the old ones any more
   if (!SUM && last && a.state && W > 1 && unit % a.per_group == 0) {
-    for (int u = threadIdx.x; u < 2 * N; u += 256) {
-      const int c = inner + (u / N) * a.G * N + g * N + u % N;
-      float* own = a.conv_state + (slot * a.C + c) * (W - 1);
-      float v[3];
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const int64_t r = (int64_t)sg.t1 - (W - 1) + j;
-        v[j] = j >= W - 1 ? 0.0f : r >= sg.t0 ? ld<IO>(a.xbc, r * a.xs + c) : resume ? own[r - sg.t0 + W - 1] : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 3; ++j)
-        if (j < W - 1) own[j] = v[j];
-    }
+    for (int u = threadIdx.x; u < 2 * N; u += 64 * WV)
+      keep_inputs<IO>(a, sg, slot, resume, inner + (u / N) * a.G * N + g * N + u % N);
   }
-  if (blk >= hpg * bph) return;
-  const int h = g * hpg + blk / bph, p0 = (blk % bph) * PB;
+  const int h = on ? g * hpg + blk / bph : 0, p0 = on ? (blk % bph) * PB : 0;
   // this lane's channels as rows of the tiles; past the head's last one a copy of a valid one
   int ch[PT];
 #pragma unroll
   for (int e = 0; e < PT; ++e) {
     const int p = p0 + PT * i16 + e;
-    ch[e] = h * a.P + (p < a.P ? p : e && p - 1 < a.P ? p - 1 : p0);
+    ch[e] = h * a.P + (p < a.P ? p : FAST ? p0 + e : e && p - 1 < a.P ? p - 1 : p0);
   }
-  if constexpr (PT == 2)
-    if (a.xvec && p0 + 2 * i16 + 1 >= a.P) ch[1] = ch[0] + 1;  // P even: both or neither are past it
   float cw[PT][4], cb[PT];
 #pragma unroll
   for (int e = 0; e < PT; ++e) {
@@ -637,7 +686,7 @@ __global__ void __launch_bounds__(256) mix_block_kernel(const BlkArgs a) {
         const int n = 16 * nt + 4 * q4;
         if (src) {
           const float* s = src + (int64_t)ch[e] * N + n;
-          if (a.svec) {
+          if constexpr (FAST) {
             if (n < N) v = *reinterpret_cast<const f4*>(s);
           } else {
 #pragma unroll
@@ -650,374 +699,421 @@ __global__ void __launch_bounds__(256) mix_block_kernel(const BlkArgs a) {
   }
   double dsum = 0.0;  // log2 of the segment's decay
 
-  for (int c = 0; c < sg.nc; ++c) {
-    const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ), cnt = r1 - r0;
-    const char* op = a.ops + ((int64_t)(sg.gc + c) * a.G + g) * O::bytes;
-    // ---- x: rows 32 kb + 8 q - 3 .. + 7 of the lane's channels
-    float v[PT][2][8];
-    {
-      float in[PT][2][11];
-      auto load = [&](auto edge) {
-        constexpr bool EDGE = decltype(edge)::value;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int j = 0; j < 11; ++j) {
-            const int t = 32 * kb + 8 * q4 + j - 3;  // in the block
-            int64_t r = (int64_t)r0 + t;
-            bool ok = true;
-            if constexpr (EDGE) {
-              ok = r >= sg.t0 && r < r1;
-              r = ok ? r : r0;
-            }
-            if constexpr (PT == 2) {
-              if (a.xvec) {
-                if constexpr (sizeof(IO) == 2) {
-                  const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                      static_cast<const uint16_t*>(a.xbc) + r * a.xs + ch[0]);
-                  in[0][kb][j] = __uint_as_float(w << 16);
-                  in[1][kb][j] = __uint_as_float(w & 0xffff0000u);
-                } else {
-                  const f2 w = *reinterpret_cast<const f2*>(static_cast<const float*>(a.xbc) + r * a.xs + ch[0]);
-                  in[0][kb][j] = w.x;
-                  in[1][kb][j] = w.y;
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < PT; ++e) in[e][kb][j] = ld<IO>(a.xbc, r * a.xs + ch[e]);
-              }
-            } else {
-              in[0][kb][j] = ld<IO>(a.xbc, r * a.xs + ch[0]);
-            }
-            if constexpr (EDGE) {
-#pragma unroll
-              for (int e = 0; e < PT; ++e) in[e][kb][j] = ok ? in[e][kb][j] : 0.0f;
-            }
-          }
-      };
-      const bool first = sg.c0 + c == 0;
-      if (first || cnt < kQ) {
-        load(std::integral_constant<bool, true>{});
-        if (first && resume && W > 1 && q4 == 0) {  // the inputs before the sequence
-          const bool saved = !SUM && sg.split >= 0;
-#pragma unroll
-          for (int e = 0; e < PT; ++e)
-#pragma unroll
-            for (int j = 0; j < 3; ++j) {
-              const int at = j - 3 + W - 1;
-              if (at >= 0)
-                in[e][0][j] = saved ? a.cs0[((int64_t)sg.cut * inner + ch[e]) * 3 + at]
-                                    : a.conv_state[(slot * a.C + ch[e]) * (W - 1) + at];
-            }
-          if constexpr (SUM) {  // the second pass overwrites the slot: it reads these
-#pragma unroll
-            for (int e = 0; e < PT; ++e)
-              if (p0 + PT * i16 + e < a.P)
-#pragma unroll
-                for (int j = 0; j < 3; ++j)
-                  if (j - 3 + W - 1 >= 0)
-                    a.cs0[((int64_t)sg.cut * inner + ch[e]) * 3 + j - 3 + W - 1] = in[e][0][j];
-          }
-        }
-      } else {
-        load(std::integral_constant<bool, false>{});
-      }
-#pragma unroll
-      for (int e = 0; e < PT; ++e)
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[e][kb][j] = fmaf(cw[e][0], in[e][kb][j + 3], cb[e]);
-#pragma unroll
-      for (int k = 1; k < 4; ++k)
-        if (k < W)
-#pragma unroll
-          for (int e = 0; e < PT; ++e)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[e][kb][j] = fmaf(cw[e][k], in[e][kb][j + 3 - k], v[e][kb][j]);
-    }
-    // ---- steps: lane t
-    const bool live = lane < cnt;
-    float dt = 0.0f, dA = 0.0f;
-    if (live) {
-      const float raw = ld<IO>(a.dt, (int64_t)(r0 + lane) * a.ds + h) + db;
-      dt = a.softplus ? softplus(raw) : raw;
-      // below 2^-160 a decay is zero in float32; held there, no sum swallows the steps beside it
-      dA = dt * A2;
-      dA = dA < -160.0f ? -160.0f : dA;
-    }
-    const double cum = wave_scan((double)dA), tot = lane63(cum);
-    const float wt = dt * ex2((float)(tot - cum));
-    const float dec = ex2((float)cum), dec_all = ex2((float)tot);
-    const float wmax = wave_max(finite(wt) ? fabsf(wt) : 0.0f);
-    int shw = -__builtin_amdgcn_frexp_expf(wmax);
-    shw = shw < -112 ? -112 : (shw > 60 ? 60 : shw);
-    dsum += tot;
-    // ---- silu, the tile's scale
-    float mx = 0.0f, chk = 0.0f;
-#pragma unroll
-    for (int e = 0; e < PT; ++e)
+  // a block's x, dt and z on their way
+  XRaw<IO, PT, FAST> xr;
+  float dt_raw = 0.0f;
+  typedef uint32_t zv __attribute__((ext_vector_type(2 * PT)));
+  constexpr bool ZAHEAD = FAST && !SUM && sizeof(IO) == 2;
+  zv zr[4];
+  auto fetch = [&](int c) {
+    const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ);
+    const bool edge = sg.c0 + c == 0 || r1 - r0 < kQ;
+    auto rows = [&](auto e_) {
+      constexpr bool EDGE = decltype(e_)::value;
+      const int first = r0 + 8 * q4 - 3;
+      const IO* base = static_cast<const IO*>(a.xbc) + (int64_t)first * a.xs + ch[0];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float x = silu(v[e][kb][j]);
-          if (cnt < kQ) x = 32 * kb + 8 * q4 + j < cnt ? x : 0.0f;
-          v[e][kb][j] = x;
-          mx = fmaxf(mx, fabsf(x));
-          chk = fmaf(x, 0.0f, chk);
-        }
-    const bool bad = __any(!(chk == 0.0f));
-    if (bad) {
-      mx = 0.0f;
-      int first[PT];
+        for (int j = 0; j < 11; ++j) {
+          // rows outside the sequence are read from inside it and replaced later
+          const IO* x = base;
+          if constexpr (EDGE) x += (int64_t)(max(min(first + 32 * kb + j, r1 - 1), sg.t0) - first) * a.xs;
+          else x += (int64_t)(32 * kb + j) * a.xs;
+          if constexpr (XRaw<IO, PT, FAST>::pair) {
+            xr.w[0][kb][j] = *reinterpret_cast<const uint32_t*>(x);
+          } else if constexpr (FAST && PT == 2) {
+            const u2 w = *reinterpret_cast<const u2*>(x);
+            xr.w[0][kb][j] = w.x;
+            xr.w[1][kb][j] = w.y;
+          } else {
 #pragma unroll
-      for (int e = 0; e < PT; ++e) {
-        first[e] = kQ;
-#pragma unroll
-        for (int kb = 1; kb >= 0; --kb)
-#pragma unroll
-          for (int j = 7; j >= 0; --j) {
-            if (finite(v[e][kb][j])) mx = fmaxf(mx, fabsf(v[e][kb][j]));
-            else first[e] = 32 * kb + 8 * q4 + j;
+            for (int e = 0; e < PT; ++e) {
+              if constexpr (sizeof(IO) == 2) xr.w[e][kb][j] = x[ch[e] - ch[0]];
+              else xr.w[e][kb][j] = __float_as_uint(x[ch[e] - ch[0]]);
+            }
           }
-        first[e] = min(first[e], __shfl_xor(first[e], 16, 64));
-        first[e] = min(first[e], __shfl_xor(first[e], 32, 64));
-        if (q4 == 0) s_bad[wave][PT * i16 + e] = first[e];
+        }
+    };
+    if (edge) rows(std::integral_constant<bool, true>{});
+    else rows(std::integral_constant<bool, false>{});
+    dt_raw = ld<IO>(a.dt, (int64_t)min(r0 + lane, r1 - 1) * a.ds + h);
+    if constexpr (ZAHEAD) {
+      if (a.z) {
+        const int pw = p0 + 4 * PT * q4;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+          zr[tt] = *reinterpret_cast<const zv*>(
+              static_cast<const IO*>(a.z) + (int64_t)min(r0 + 16 * tt + i16, r1 - 1) * a.zs + h * a.P + (pw < a.P ? pw : p0));
       }
     }
-    const float xmax = wave_max(mx);
-    const int shx = shift_for(xmax);
-    const float fx = two(shx);
-    if (live) s_cum[wave][lane] = (float)cum;
-    else s_cum[wave][lane] = (float)tot;
-    s_lo[wave][lane] = live ? (float)(cum - (double)(float)cum) : 0.0f;
-    s_w[wave][lane] = wt * two(shw);
+  };
+  const char* ops = a.ops + ((int64_t)sg.gc * a.G + g) * O::bytes;
+  const int64_t op_step = (int64_t)a.G * O::bytes;
+  if (sg.nc > 0) {
+    fetch(0);
+    if constexpr (!SUM) {
+      stage<WV, CG>(ops + O::c, s_cg);
+      stage<WV, O::scale - O::g>(ops + O::g, s_cg + CG);
+    }
+  }
+
+  for (int c = 0; c < sg.nc; ++c) {
+    const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ), cnt = r1 - r0;
+    const char* op = ops + c * op_step;
+    staged();  // C and C.B^T are there; the waves are done with the last block's B
+    stage<WV, 2 * O::piece>(op + O::b, s_b);
     const int* sc = reinterpret_cast<const int*>(op + O::scale);
     const int shB = sc[0], shC = sc[1];
-    if constexpr (!SUM) s_dt[wave][lane] = dt;
-    __builtin_amdgcn_wave_barrier();
-
-    // ---- operands from x: once as it is (for y), once weighted (for the state)
-    h8 xh[PT][2], xl[PT][2], wh[PT][2], wl[PT][2];
+    h8 wh[PT][2], wl[PT][2];
+    float dec_all = 1.0f, f_su = 0.0f;
+    if (on) {
+      // ---- the convolution
+      float v[PT][2][8];
+      {
+        float in[PT][2][11];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float w8[8];
-      *reinterpret_cast<f4*>(w8) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4]);
-      *reinterpret_cast<f4*>(w8 + 4) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4 + 4]);
+        for (int e = 0; e < PT; ++e)
 #pragma unroll
-      for (int e = 0; e < PT; ++e) {
-        float x[8], w[8];
+          for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] = v[e][kb][j] * fx;
-          w[j] = x[j] * w8[j];
+            for (int j = 0; j < 11; ++j) in[e][kb][j] = xr.get(e, kb, j);
+        const bool first = sg.c0 + c == 0;
+        if (first || cnt < kQ) {
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int j = 0; j < 11; ++j) {
+              const int r = r0 + 32 * kb + 8 * q4 + j - 3;
+#pragma unroll
+              for (int e = 0; e < PT; ++e) in[e][kb][j] = r >= sg.t0 && r < r1 ? in[e][kb][j] : 0.0f;
+            }
+          if (first && resume && W > 1 && q4 == 0) {  // the inputs before the sequence
+            const bool saved = !SUM && sg.split >= 0;
+#pragma unroll
+            for (int e = 0; e < PT; ++e)
+#pragma unroll
+              for (int j = 0; j < 3; ++j) {
+                const int at = j - 3 + W - 1;
+                if (at >= 0)
+                  in[e][0][j] = saved ? a.cs0[((int64_t)sg.cut * inner + ch[e]) * 3 + at]
+                                      : a.conv_state[(slot * a.C + ch[e]) * (W - 1) + at];
+              }
+            if constexpr (SUM) {  // the second pass overwrites the slot: it reads these
+#pragma unroll
+              for (int e = 0; e < PT; ++e)
+                if (p0 + PT * i16 + e < a.P)
+#pragma unroll
+                  for (int j = 0; j < 3; ++j)
+                    if (j - 3 + W - 1 >= 0)
+                      a.cs0[((int64_t)sg.cut * inner + ch[e]) * 3 + j - 3 + W - 1] = in[e][0][j];
+            }
+          }
         }
-        pieces(w, wh[e][kb], wl[e][kb]);
-        if constexpr (!SUM) {
-          if (bad)  // 0 x Inf is not 0: y's earlier rows must not meet them
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = finite(x[j]) ? x[j] : 0.0f;
-          if constexpr (PC == 2) pieces(x, xh[e][kb], xl[e][kb]);
-          else xh[e][kb] = piece(x);
-        }
+        for (int e = 0; e < PT; ++e)
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[e][kb][j] = fmaf(cw[e][0], in[e][kb][j + 3], cb[e]);
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+          if (k < W)
+#pragma unroll
+            for (int e = 0; e < PT; ++e)
+#pragma unroll
+              for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[e][kb][j] = fmaf(cw[e][k], in[e][kb][j + 3 - k], v[e][kb][j]);
       }
-    }
-
-    if constexpr (!SUM) {
-      // ---- the state as an operand
-      float sm = 0.0f;
+      // ---- steps: lane t
+      const bool live = lane < cnt;
+      float dt = 0.0f, dA = 0.0f;
+      if (live) {
+        const float raw = dt_raw + db;
+        dt = a.softplus ? softplus(raw) : raw;
+        // below 2^-160 a decay is zero in float32; held there, no sum swallows the steps beside it
+        dA = dt * A2;
+        dA = dA < -160.0f ? -160.0f : dA;
+      }
+      const double cum = wave_scan((double)dA), tot = lane63(cum);
+      const float wt = dt * ex2((float)(tot - cum));
+      dec_all = ex2((float)tot);
+      const float wmax = wave_max(finite(wt) ? fabsf(wt) : 0.0f);
+      int shw = -__builtin_amdgcn_frexp_expf(wmax);
+      shw = shw < -112 ? -112 : (shw > 60 ? 60 : shw);
+      dsum += tot;
+      s_cum[wave][lane] = (float)cum;
+      s_lo[wave][lane] = (float)(cum - (double)(float)cum);
+      s_w[wave][lane] = wt * two(shw);
+      if constexpr (!SUM) s_dt[wave][lane] = dt;
+      // ---- silu, the tile's scale
+      float mx = 0.0f, chk = 0.0f;
 #pragma unroll
       for (int e = 0; e < PT; ++e)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sm = fmaxf(sm, fabsf(S[e][nt][r]));
-      sm = wave_max(sm);
-      if (!finite(sm)) {
-        sm = 0.0f;
+          for (int j = 0; j < 8; ++j) {
+            const float x = silu(v[e][kb][j]);
+            v[e][kb][j] = x;
+            mx = fmaxf(mx, fabsf(x));
+            chk = fmaf(x, 0.0f, chk);
+          }
+      if (cnt < kQ) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < PT; ++e) v[e][kb][j] = 32 * kb + 8 * q4 + j < cnt ? v[e][kb][j] : 0.0f;
+      }
+      const bool bad = __any(!(chk == 0.0f));
+      if (bad) {
+        mx = 0.0f;
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          int first = kQ;
+#pragma unroll
+          for (int kb = 1; kb >= 0; --kb)
+#pragma unroll
+            for (int j = 7; j >= 0; --j) {
+              if (finite(v[e][kb][j])) mx = fmaxf(mx, fabsf(v[e][kb][j]));
+              else first = 32 * kb + 8 * q4 + j;
+            }
+          first = min(first, __shfl_xor(first, 16, 64));
+          first = min(first, __shfl_xor(first, 32, 64));
+          if (q4 == 0) s_bad[wave][PT * i16 + e] = first;
+        }
+      }
+      const int shx = shift_for(wave_max(mx));
+      const float fx = two(shx);
+      f_su = two(max(-126, -(shB + shx + shw)));
+      __builtin_amdgcn_wave_barrier();
+
+      // ---- operands from x: once as it is (for y), once weighted (for the state)
+      h8 xh[PT][2], xl[PT][2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        float w8[8];
+        *reinterpret_cast<f4*>(w8) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4]);
+        *reinterpret_cast<f4*>(w8 + 4) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4 + 4]);
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          float x[8], w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[j] = v[e][kb][j] * fx;
+            w[j] = x[j] * w8[j];
+          }
+          pieces(w, wh[e][kb], wl[e][kb]);
+          if constexpr (!SUM) {
+            if (bad)  // 0 x Inf is not 0: y's earlier rows must not meet them
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = finite(x[j]) ? x[j] : 0.0f;
+            if constexpr (PC == 2) pieces(x, xh[e][kb], xl[e][kb]);
+            else xh[e][kb] = piece(x);
+          }
+        }
+      }
+
+      if constexpr (!SUM) {
+        // ---- the state as an operand
+        float sm = 0.0f;
 #pragma unroll
         for (int e = 0; e < PT; ++e)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (finite(S[e][nt][r])) sm = fmaxf(sm, fabsf(S[e][nt][r]));
+            for (int r = 0; r < 4; ++r) sm = fmaxf(sm, fabsf(S[e][nt][r]));
         sm = wave_max(sm);
-      }
-      const int shS = shift_for(sm);
-      const float fs = two(shS);
-      h8 sh[PT][NT / 2], sl[PT][NT / 2];
+        if (!finite(sm)) {
+          sm = 0.0f;
 #pragma unroll
-      for (int e = 0; e < PT; ++e)
+          for (int e = 0; e < PT; ++e)
 #pragma unroll
-        for (int m = 0; m < NT / 2; ++m) {
-          float x[8];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * fs;
-          if constexpr (PC == 2) pieces(x, sh[e][m], sl[e][m]);
-          else sh[e][m] = piece(x);
+              for (int r = 0; r < 4; ++r)
+                if (finite(S[e][nt][r])) sm = fmaxf(sm, fabsf(S[e][nt][r]));
+          sm = wave_max(sm);
         }
-      const int e_mx = -(shB + shC + shx), e_cs = -(shC + shS);
-      const float Dm = __builtin_amdgcn_ldexpf(D, shB + shC);
-      // ---- y, 16 rows at a time
+        const int shS = shift_for(sm);
+        const float fs = two(shS);
+        h8 sh[PT][NT / 2], sl[PT][NT / 2];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const int t = 16 * tt + i16;
-        if (16 * tt >= cnt) break;
-        const float cum_t = s_cum[wave][t], lo_t = s_lo[wave][t];
-        f4 ym[PT] = {}, yc[PT] = {};
-        float m[2][8], rm = 0.0f;
+        for (int e = 0; e < PT; ++e)
 #pragma unroll
-        for (int kb = 0; kb <= tt / 2; ++kb) {
-          const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
-          const f4* gp = reinterpret_cast<const f4*>(op + O::g + (tile * 64 + lane) * 32);
-          const f4 g0 = gp[0], g1 = gp[1];
+          for (int m = 0; m < NT / 2; ++m) {
+            float x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int s = 32 * kb + 8 * q4 + j;
-            float x = cum_t - s_cum[wave][s];
-            if constexpr (PC == 2) x += lo_t - s_lo[wave][s];
-            x = (j < 4 ? g0[j & 3] : g1[j & 3]) * (ex2(x) * s_dt[wave][s]);
-            if (kb == tt / 2) {
-              x = s <= t ? x : 0.0f;
-              x = s == t ? x + Dm : x;
-            }
-            m[kb][j] = x;
-            rm = fmaxf(rm, fabsf(x));
+            for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * fs;
+            if constexpr (PC == 2) pieces(x, sh[e][m], sl[e][m]);
+            else sh[e][m] = piece(x);
           }
-        }
-        // every row by its own largest value: one token's outlier leaves the others their bits
-        const int shM = shift_for(row_max(rm));
-        const float fm = two(shM);
+        const int e_mx = -(shB + shC + shx), e_cs = -(shC + shS);
+        const float Dm = __builtin_amdgcn_ldexpf(D, shB + shC);
+        // ---- y, 16 rows at a time
 #pragma unroll
-        for (int kb = 0; kb <= tt / 2; ++kb) {
+        for (int tt = 0; tt < 4; ++tt) {
+          if (16 * tt >= cnt) break;
+          int t = 16 * tt + i16, s0 = 8 * q4;
+          asm volatile("" : "+v"(t), "+v"(s0));  // else the causal masks of all tiles are kept in registers
+          const float cum_t = s_cum[wave][t], lo_t = s_lo[wave][t];
+          f4 ym[PT] = {}, yc[PT] = {};
+          float m[2][8], rm = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m[kb][j] *= fm;
-          if constexpr (PC == 2) {
-            h8 mh, ml;
-            pieces(m[kb], mh, ml);
+          for (int kb = 0; kb <= tt / 2; ++kb) {
+            const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
+            const f4* gp = reinterpret_cast<const f4*>(s_cg + CG + (tile * 64 + lane) * 32);
+            const f4 g0 = gp[0], g1 = gp[1];
 #pragma unroll
-            for (int e = 0; e < PT; ++e) {
-              ym[e] = mfma(xl[e][kb], mh, ym[e]);
-              ym[e] = mfma(xh[e][kb], ml, ym[e]);
-              ym[e] = mfma(xh[e][kb], mh, ym[e]);
-            }
-          } else {
-            const h8 mh = piece(m[kb]);
-#pragma unroll
-            for (int e = 0; e < PT; ++e) ym[e] = mfma(xh[e][kb], mh, ym[e]);
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < NT / 2; ++m) {
-          const h8 cp = *reinterpret_cast<const h8*>(op + O::c + ((tt * (NT / 2) + m) * 64 + lane) * 16);
-          if constexpr (PC == 2) {
-            const h8 cl = *reinterpret_cast<const h8*>(op + O::c + O::piece + ((tt * (NT / 2) + m) * 64 + lane) * 16);
-#pragma unroll
-            for (int e = 0; e < PT; ++e) {
-              yc[e] = mfma(sl[e][m], cp, yc[e]);
-              yc[e] = mfma(sh[e][m], cl, yc[e]);
+            for (int j = 0; j < 8; ++j) {
+              const int s = 32 * kb + s0 + j;
+              float x = cum_t - s_cum[wave][s];
+              if constexpr (PC == 2) x += lo_t - s_lo[wave][s];
+              x = (j < 4 ? g0[j & 3] : g1[j & 3]) * (ex2(x) * s_dt[wave][s]);
+              if (kb == tt / 2) {
+                x = s <= t ? x : 0.0f;
+                x = s == t ? x + Dm : x;
+              }
+              m[kb][j] = x;
+              rm = fmaxf(rm, fabsf(x));
             }
           }
+          // every row by its own largest value: one token's outlier leaves the others their bits
+          const int shM = shift_for(row_max(rm));
+          const float fm = two(shM);
 #pragma unroll
-          for (int e = 0; e < PT; ++e) yc[e] = mfma(sh[e][m], cp, yc[e]);
-        }
-        // lane (t, q): channels p0 + 4 PT q + {0 .. 4 PT - 1}
-        const float dec_t = ex2(cum_t + lo_t);
-        const int pw = p0 + 4 * PT * q4;
-        const int64_t row = (int64_t)r0 + t, col = (int64_t)h * a.P + pw;
-        float o[4 * PT];
+          for (int kb = 0; kb <= tt / 2; ++kb) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+            for (int j = 0; j < 8; ++j) m[kb][j] *= fm;
+            if constexpr (PC == 2) {
+              h8 mh, ml;
+              pieces(m[kb], mh, ml);
 #pragma unroll
-          for (int e = 0; e < PT; ++e) {
-            float y = __builtin_amdgcn_ldexpf(ym[e][r], e_mx - shM) + __builtin_amdgcn_ldexpf(yc[e][r] * dec_t, e_cs);
-            if (bad) y = t >= s_bad[wave][4 * PT * q4 + PT * r + e] ? __builtin_nanf("") : y;
-            o[PT * r + e] = y;
+              for (int e = 0; e < PT; ++e) {
+                ym[e] = mfma(xl[e][kb], mh, ym[e]);
+                ym[e] = mfma(xh[e][kb], ml, ym[e]);
+                ym[e] = mfma(xh[e][kb], mh, ym[e]);
+              }
+            } else {
+              const h8 mh = piece(m[kb]);
+#pragma unroll
+              for (int e = 0; e < PT; ++e) ym[e] = mfma(xh[e][kb], mh, ym[e]);
+            }
           }
-        if (t < cnt) {
+#pragma unroll
+          for (int m = 0; m < NT / 2; ++m) {
+            const h8 cp = *reinterpret_cast<const h8*>(s_cg + ((tt * (NT / 2) + m) * 64 + lane) * 16);
+            if constexpr (PC == 2) {
+              const h8 cl = *reinterpret_cast<const h8*>(s_cg + O::piece + ((tt * (NT / 2) + m) * 64 + lane) * 16);
+#pragma unroll
+              for (int e = 0; e < PT; ++e) {
+                yc[e] = mfma(sl[e][m], cp, yc[e]);
+                yc[e] = mfma(sh[e][m], cl, yc[e]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < PT; ++e) yc[e] = mfma(sh[e][m], cp, yc[e]);
+          }
+          // lane (t, q): channels p0 + 4 PT q + {0 .. 4 PT - 1}
+          const float f_cs = __builtin_amdgcn_ldexpf(ex2(cum_t + lo_t), e_cs);
+          const float f_mx = __builtin_amdgcn_ldexpf(1.0f, e_mx - shM);
+          const int pw = p0 + 4 * PT * q4;
+          const int64_t row = (int64_t)r0 + t, col = (int64_t)h * a.P + pw;
+          float o[4 * PT];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < PT; ++e) o[PT * r + e] = fmaf(ym[e][r], f_mx, yc[e][r] * f_cs);
+          if (bad)
+#pragma unroll
+            for (int k = 0; k < 4 * PT; ++k) o[k] = t >= s_bad[wave][4 * PT * q4 + k] ? __builtin_nanf("") : o[k];
           if (a.z) {
-            if (a.zvec) {
-              if (pw < a.P) {
+            if constexpr (ZAHEAD) {
+#pragma unroll
+              for (int k = 0; k < 2 * PT; ++k) {
+                o[2 * k] *= silu(__uint_as_float(zr[tt][k] << 16));
+                o[2 * k + 1] *= silu(__uint_as_float(zr[tt][k] & 0xffff0000u));
+              }
+            } else if constexpr (FAST) {
+              if (t < cnt && pw < a.P) {
                 float zz[4 * PT];
-                if constexpr (sizeof(IO) == 4) {
 #pragma unroll
-                  for (int k = 0; k < PT; ++k)
-                    *reinterpret_cast<f4*>(zz + 4 * k) = *reinterpret_cast<const f4*>(
-                        static_cast<const float*>(a.z) + row * a.zs + col + 4 * k);
-                } else {
-#pragma unroll
-                  for (int k = 0; k < PT; ++k) {
-                    const u2 w = *reinterpret_cast<const u2*>(static_cast<const uint16_t*>(a.z) + row * a.zs + col + 4 * k);
-                    zz[4 * k] = __uint_as_float(w.x << 16);
-                    zz[4 * k + 1] = __uint_as_float(w.x & 0xffff0000u);
-                    zz[4 * k + 2] = __uint_as_float(w.y << 16);
-                    zz[4 * k + 3] = __uint_as_float(w.y & 0xffff0000u);
-                  }
-                }
+                for (int k = 0; k < PT; ++k)
+                  *reinterpret_cast<f4*>(zz + 4 * k) = *reinterpret_cast<const f4*>(
+                      static_cast<const float*>(a.z) + row * a.zs + col + 4 * k);
 #pragma unroll
                 for (int k = 0; k < 4 * PT; ++k) o[k] *= silu(zz[k]);
               }
-            } else {
+            } else if (t < cnt) {
 #pragma unroll
               for (int k = 0; k < 4 * PT; ++k)
                 if (pw + k < a.P) o[k] *= silu(ld<IO>(a.z, row * a.zs + col + k));
             }
           }
-          if (a.yvec) {
-            if (pw < a.P) {
-              if constexpr (sizeof(IO) == 4) {
+          if (t < cnt) {
+            if constexpr (FAST) {
+              if (pw < a.P) {
+                if constexpr (sizeof(IO) == 4) {
 #pragma unroll
-                for (int k = 0; k < PT; ++k)
-                  *reinterpret_cast<f4*>(static_cast<float*>(a.y) + row * a.ys + col + 4 * k) =
-                      *reinterpret_cast<const f4*>(o + 4 * k);
-              } else {
-                typedef __bf16 bf __attribute__((ext_vector_type(4 * PT)));
-                typedef float fv __attribute__((ext_vector_type(4 * PT)));
-                fv f;
+                  for (int k = 0; k < PT; ++k)
+                    *reinterpret_cast<f4*>(static_cast<float*>(a.y) + row * a.ys + col + 4 * k) =
+                        *reinterpret_cast<const f4*>(o + 4 * k);
+                } else {
+                  typedef __bf16 bf __attribute__((ext_vector_type(4 * PT)));
+                  typedef float fv __attribute__((ext_vector_type(4 * PT)));
+                  fv f;
 #pragma unroll
-                for (int k = 0; k < 4 * PT; ++k) f[k] = o[k];
-                *reinterpret_cast<bf*>(static_cast<uint16_t*>(a.y) + row * a.ys + col) =
-                    __builtin_convertvector(f, bf);
+                  for (int k = 0; k < 4 * PT; ++k) f[k] = o[k];
+                  *reinterpret_cast<bf*>(static_cast<uint16_t*>(a.y) + row * a.ys + col) =
+                      __builtin_convertvector(f, bf);
+                }
               }
-            }
-          } else {
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4 * PT; ++k)
-              if (pw + k < a.P) st<IO>(a.y, row * a.ys + col + k, o[k]);
+              for (int k = 0; k < 4 * PT; ++k)
+                if (pw + k < a.P) st<IO>(a.y, row * a.ys + col + k, o[k]);
+            }
           }
         }
       }
     }
-    // ---- the state after the block
-    const int e_su = -(shB + shx + shw);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      h8 bh[2], bl[2];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        bh[kb] = *reinterpret_cast<const h8*>(op + O::b + ((nt * 2 + kb) * 64 + lane) * 16);
-        bl[kb] = *reinterpret_cast<const h8*>(op + O::b + O::piece + ((nt * 2 + kb) * 64 + lane) * 16);
+    staged();  // B is there; the waves are done with C and C.B^T
+    if (c + 1 < sg.nc) {
+      if constexpr (!SUM) {
+        stage<WV, CG>(op + op_step + O::c, s_cg);
+        stage<WV, O::scale - O::g>(op + op_step + O::g, s_cg + CG);
       }
+      fetch(c + 1);
+    }
+    if (on) {
+      // ---- the state after the block
 #pragma unroll
-      for (int e = 0; e < PT; ++e) {
-        f4 d = {};
+      for (int nt = 0; nt < NT; ++nt) {
+        h8 bh[2], bl[2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-          d = mfma(bh[kb], wl[e][kb], d);
-          d = mfma(bl[kb], wh[e][kb], d);
-          d = mfma(bh[kb], wh[e][kb], d);
+          bh[kb] = *reinterpret_cast<const h8*>(s_b + ((nt * 2 + kb) * 64 + lane) * 16);
+          bl[kb] = *reinterpret_cast<const h8*>(s_b + O::piece + ((nt * 2 + kb) * 64 + lane) * 16);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          S[e][nt][r] = fmaf(S[e][nt][r], dec_all, __builtin_amdgcn_ldexpf(d[r], e_su));
+        for (int e = 0; e < PT; ++e) {
+          f4 d = {};
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            d = mfma(bh[kb], wl[e][kb], d);
+            d = mfma(bl[kb], wh[e][kb], d);
+            d = mfma(bh[kb], wh[e][kb], d);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[e][nt][r] = fmaf(d[r], f_su, S[e][nt][r] * dec_all);
+        }
       }
     }
-    __builtin_amdgcn_wave_barrier();
   }
+  if (!on) return;
 
   // ---- what the segment leaves
   float* dst = nullptr;
@@ -1035,7 +1131,7 @@ __global__ void __launch_bounds__(256) mix_block_kernel(const BlkArgs a) {
         for (int nt = 0; nt < NT; ++nt) {
           const int n = 16 * nt + 4 * q4;
           float* s = dst + (int64_t)ch[e] * N + n;
-          if (a.svec) {
+          if constexpr (FAST) {
             if (n < N) *reinterpret_cast<f4*>(s) = S[e][nt];
           } else {
 #pragma unroll
@@ -1045,22 +1141,8 @@ __global__ void __launch_bounds__(256) mix_block_kernel(const BlkArgs a) {
         }
   }
   // the last inputs of the wave's own channels (read by nobody else, or saved by the first pass)
-  if (!SUM && last && a.state && W > 1) {
-    for (int u = lane; u < PB; u += 64) {
-      if (p0 + u >= a.P) break;
-      const int c = h * a.P + p0 + u;
-      float* own = a.conv_state + (slot * a.C + c) * (W - 1);
-      float x[3];
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const int64_t r = (int64_t)sg.t1 - (W - 1) + j;
-        x[j] = j >= W - 1 ? 0.0f : r >= sg.t0 ? ld<IO>(a.xbc, r * a.xs + c) : resume ? own[r - sg.t0 + W - 1] : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 3; ++j)
-        if (j < W - 1) own[j] = x[j];
-    }
-  }
+  if (!SUM && last && a.state && W > 1 && lane < PB && p0 + lane < a.P)
+    keep_inputs<IO>(a, sg, slot, resume, h * a.P + p0 + lane);
 }
 
 // ---- the states entering the segments of a cut sequence, from their states from zero
@@ -1365,15 +1447,15 @@ int check_mix(MixArgs& a, bool step, int64_t rows, int64_t nseq, int64_t nslots,
 
 // Workspace of ssm_conv_ssd_fwd, and how its sequences are cut.
 struct MixLayout {
-  int nt, pt, pc;
+  int nt, pt, pc, wv;
   int64_t nchunk, nseg, nsplit, ncut;  // at most
   int seg_len, per_group, units;
   int64_t op_bytes, chunks, segs, ops, local, decay, cs0, bytes;
 };
 
-// A segment is one workgroup's work, one after another; the card holds 512
-// workgroups of four waves at two waves a SIMD.
-constexpr int64_t kSegWorkgroups = 512;
+// A segment is one workgroup's work, one after another; the card holds 2048
+// waves at two a SIMD.
+constexpr int64_t kSegWaves = 2048;
 constexpr int kSegMin = 4;
 
 MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N, int io_dtype) {
@@ -1382,14 +1464,16 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   l.pt = l.nt == 16 ? 1 : 2;
   l.pc = io_dtype == SSM_DTYPE_BF16 ? 1 : 2;
   const int64_t bph = (P + 16 * l.pt - 1) / (16 * l.pt);
-  l.per_group = (int)((H / G * bph + 3) / 4);
+  l.wv = l.nt == 16 ? 8 : 4;
+  l.per_group = (int)((H / G * bph + l.wv - 1) / l.wv);
   l.units = (int)(l.per_group * G);
   l.nchunk = tokens / kQ + nseq;
-  const int64_t work = (tokens + kQ - 1) / kQ * l.units;
-  int64_t len = (work + kSegWorkgroups - 1) / kSegWorkgroups;
+  // as many segments as the card holds at once, not a few more
+  const int64_t at_once = kSegWaves / l.wv / l.units, blocks = (tokens + kQ - 1) / kQ;
+  int64_t len = at_once ? (blocks + at_once - 1) / at_once : blocks;
   if (len < kSegMin) len = kSegMin;
   l.seg_len = (int)len;
-  const bool cut = (tokens + kQ - 1) / kQ > len;
+  const bool cut = blocks > len;
   l.nsplit = cut ? 2 * (l.nchunk / len) : 0;
   l.ncut = cut ? l.nchunk / len : 0;
   l.nseg = nseq + l.nchunk / len;
@@ -1412,27 +1496,32 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   return l;
 }
 
-template <typename IO, int NT, int PT, int PC>
+template <typename IO, int NT, int PT, int PC, int WV>
 void launch_mix_blocks(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
   static_assert(Ops<NT, PC>::bytes == (PC + 2) * kQ * NT * 32 + kTri * 64 * 32 + 64, "as in mix_layout");
   mix_plan_kernel<<<1, 1024, 0, s>>>(b);
   mix_prep_kernel<IO, NT, PC><<<dim3((unsigned)l.nchunk, b.G), 256, 0, s>>>(b);
   const unsigned grid = (unsigned)(l.nseg * l.units);
-  if (l.nsplit) {
-    mix_block_kernel<IO, NT, PT, PC, true><<<grid, 256, 0, s>>>(b);
-    const int64_t per = (int64_t)b.H * b.P * b.N;
-    mix_join_kernel<<<dim3((unsigned)l.nseg, (unsigned)((per + 255) / 256)), 256, 0, s>>>(b);
-  }
-  mix_block_kernel<IO, NT, PT, PC, false><<<grid, 256, 0, s>>>(b);
+  auto walk = [&](auto fast) {
+    constexpr bool F = decltype(fast)::value;
+    if (l.nsplit) {
+      mix_block_kernel<IO, NT, PT, PC, WV, true, F><<<grid, 64 * WV, 0, s>>>(b);
+      const int64_t per = (int64_t)b.H * b.P * b.N;
+      mix_join_kernel<<<dim3((unsigned)l.nseg, (unsigned)((per + 255) / 256)), 256, 0, s>>>(b);
+    }
+    mix_block_kernel<IO, NT, PT, PC, WV, false, F><<<grid, 64 * WV, 0, s>>>(b);
+  };
+  if (b.fast) walk(std::integral_constant<bool, true>{});
+  else walk(std::integral_constant<bool, false>{});
 }
 
 template <typename IO, int PC>
 void launch_mix(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
   switch (l.nt) {
-    case 2: launch_mix_blocks<IO, 2, 2, PC>(b, l, s); break;
-    case 4: launch_mix_blocks<IO, 4, 2, PC>(b, l, s); break;
-    case 8: launch_mix_blocks<IO, 8, 2, PC>(b, l, s); break;
-    default: launch_mix_blocks<IO, 16, 1, PC>(b, l, s); break;
+    case 2: launch_mix_blocks<IO, 2, 2, PC, 4>(b, l, s); break;
+    case 4: launch_mix_blocks<IO, 4, 2, PC, 4>(b, l, s); break;
+    case 8: launch_mix_blocks<IO, 8, 2, PC, 4>(b, l, s); break;
+    default: launch_mix_blocks<IO, 16, 1, PC, 8>(b, l, s); break;
   }
 }
 
@@ -1526,10 +1615,8 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
   auto lanes = [&](const void* p, int64_t stride, int bytes) {  // whole accesses of that many bytes
     return ((uintptr_t)p | (uintptr_t)(stride * es) | (uintptr_t)(headdim * es)) % bytes == 0;
   };
-  a.xvec = lanes(xbc, xbc_stride, 2 * es);
-  a.zvec = headdim % (4 * l.pt) == 0 && lanes(z, z_stride, wide);
-  a.yvec = headdim % (4 * l.pt) == 0 && lanes(y, y_stride, wide);
-  a.svec = dstate % 4 == 0 && aligned16(ssm_state);
+  a.fast = headdim % (4 * l.pt) == 0 && dstate % 4 == 0 && lanes(xbc, xbc_stride, l.pt * es) &&
+           lanes(y, y_stride, wide) && (!z || lanes(z, z_stride, wide)) && aligned16(ssm_state);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   if (io_dtype == SSM_DTYPE_BF16) launch_mix<uint16_t, 1>(a, l, s);
   else launch_mix<float, 2>(a, l, s);
