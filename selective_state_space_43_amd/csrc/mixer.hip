@@ -270,9 +270,11 @@ struct BlkArgs : MixArgs {
 template <int NT, int NPC>
 struct Ops {
   static constexpr int piece = kQ * NT * 16 * 2;  // one fp16 piece of B or C
+  static constexpr int ge = NPC == 1 ? 2 : 4;     // bytes of an element of C.B^T: fp16 or float32
   static constexpr int c = 0, b = NPC * piece, g = b + 2 * piece;
-  static constexpr int scale = g + kTri * 64 * 8 * 4;
-  static constexpr int bytes = scale + 64;
+  static constexpr int gsize = kTri * 64 * 8 * ge;
+  static constexpr int scale = g + gsize;  // 64 rows' shifts of C.B^T, B's, C's
+  static constexpr int bytes = scale + 320;
 };
 
 __device__ __forceinline__ float wave_max(float v) {  // v >= 0; uniform result
@@ -325,10 +327,20 @@ __device__ __forceinline__ int shift_for(float m) {
   return e < -112 ? -112 : (e > 60 ? 60 : e);
 }
 __device__ __forceinline__ float two(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
+__device__ __forceinline__ float max3(float m, float x, float y) { return fmaxf(fmaxf(m, fabsf(x)), fabsf(y)); }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
 
 __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// a fp16 (the lower or the upper half of w) times float32, in one instruction
+template <int HALF>
+__device__ __forceinline__ float mul_half(uint32_t w, float x) {
+  float o;
+  if constexpr (HALF) asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(o) : "v"(w), "v"(x));
+  else asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(o) : "v"(w), "v"(x));
+  return o;
 }
 
 // v = hi + lo in fp16, to 22 bits
@@ -336,7 +348,8 @@ __device__ __forceinline__ void pieces(const float* v, h8& hi, h8& lo) {
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const h2 a = __builtin_convertvector((f2){v[j], v[j + 1]}, h2);
-    const h2 b = __builtin_convertvector((f2){v[j] - (float)a.x, v[j + 1] - (float)a.y}, h2);
+    const h2 b = __builtin_convertvector(
+        (f2){__builtin_fmaf((float)a.x, -1.0f, v[j]), __builtin_fmaf((float)a.y, -1.0f, v[j + 1])}, h2);
     hi[j] = a.x; hi[j + 1] = a.y; lo[j] = b.x; lo[j + 1] = b.y;
   }
 }
@@ -539,8 +552,10 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
   }
   // C.B^T: wave w has the rows t of tile w; the rows s of B are taken in the order
   // that leaves lane (t, q) with s = 32 kb + 8 q + {0..7}
-  for (int kb = 0; kb <= (wave >> 1); ++kb) {
-    f4 acc[2] = {};
+  f4 acc[2][2] = {};
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    if (kb > (wave >> 1)) break;
 #pragma unroll
     for (int m = 0; m < NT / 2; ++m) {
       h8 cp[2], bp[2][2];
@@ -554,17 +569,41 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        acc[e] = mfma(bp[e][1], cp[0], acc[e]);
-        acc[e] = mfma(bp[e][0], cp[1], acc[e]);
-        acc[e] = mfma(bp[e][0], cp[0], acc[e]);
+        acc[kb][e] = mfma(bp[e][1], cp[0], acc[kb][e]);
+        acc[kb][e] = mfma(bp[e][0], cp[1], acc[kb][e]);
+        acc[kb][e] = mfma(bp[e][0], cp[0], acc[kb][e]);
       }
     }
-    const int tile = wave < 2 ? wave : 2 * wave - 2 + kb;
-    f4* o = reinterpret_cast<f4*>(out + O::g + (tile * 64 + lane) * 32);
-    o[0] = acc[0];
-    o[1] = acc[1];
   }
-  if (tid < 2) reinterpret_cast<int*>(out + O::scale)[tid] = sh[tid];
+  int shG = 0;
+  if constexpr (NPC == 1) {  // to fp16, every row by its own largest value
+    float gm = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = acc[i >> 3][(i >> 2) & 1][i & 3];
+      if (finite(x)) gm = fmaxf(gm, fabsf(x));
+    }
+    shG = shift_for(row_max(gm));
+  }
+  const float fg = two(shG);
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    if (kb > (wave >> 1)) break;
+    const int tile = wave < 2 ? wave : 2 * wave - 2 + kb;
+    char* o = out + O::g + (tile * 64 + lane) * 8 * O::ge;
+    if constexpr (NPC == 1) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = acc[kb][j >> 2][j & 3] * fg;
+      *reinterpret_cast<h8*>(o) = piece(x);
+    } else {
+      reinterpret_cast<f4*>(o)[0] = acc[kb][0];
+      reinterpret_cast<f4*>(o)[1] = acc[kb][1];
+    }
+  }
+  int* sc = reinterpret_cast<int*>(out + O::scale);
+  if (lane < 16) sc[16 * wave + lane] = shG;
+  if (tid < 2) sc[64 + tid] = sh[tid];
 }
 
 // ---- the walk over a segment
@@ -584,10 +623,21 @@ __device__ __forceinline__ void stage(const char* from, char* to) {
           (__attribute__((address_space(3))) void*)(to + at), 16, 0, 0);
   }
 }
-__device__ __forceinline__ void staged() {
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-  __syncthreads();
+// The first LANES lanes' 16 bytes of a wave, by the first wave.
+template <int LANES>
+__device__ __forceinline__ void stage_few(const char* from, char* to) {
+  if (threadIdx.x < LANES)
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + threadIdx.x * 16),
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
+// All of this wave's memory accesses but the last LEFT have ended.
+template <int LEFT>
+__device__ __forceinline__ void arrived() {
+  static_assert(LEFT < 16, "the low bits of vmcnt");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+}
+// The waves of the workgroup meet; what is on its way from memory stays so.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // The last W - 1 inputs of channel c of a sequence into its slot.
 template <typename IO>
@@ -605,8 +655,22 @@ __device__ __forceinline__ void keep_inputs(const MixArgs& a, const Seg& sg, int
     if (j < W - 1) own[j] = v[j];
 }
 
-// What a wave reads of a block's rows ahead of time: x of its channels at rows
-// 32 kb + 8 q - 3 .. + 7, as they lie in memory.
+// x of a wave's PB channels (bf16) at a block's 64 rows and the three before
+// them, in LDS by direct loads of 16 bytes a lane: 1024 bytes at a time hold GP
+// groups of eight rows, interleaved row by row so that the four rows that the
+// lanes of a wave read together lie in different banks.
+template <int PT>
+struct XTile {
+  static constexpr int RB = 32 * PT, RI = 1024 / RB, GP = RI / 8;  // bytes of a row, rows and groups a load
+  static constexpr int step = PT == 2 ? 1152 : 1024, loads = (kQ + 3 + RI - 1) / RI;
+  static constexpr int bytes = PT == 2 ? 5120 : 3072;
+  static_assert((loads - 1) * step + ((kQ + 2) % 8 * GP + 1) * RB <= bytes, "the last rows fit");
+  // bytes of row 8 a + b
+  __device__ static __forceinline__ int at(int a, int b) { return a / GP * step + (GP * b + a % GP) * RB; }
+};
+
+// What a wave reads of a block's rows ahead of time where they are not staged:
+// x of its channels at rows 32 kb + 8 q - 3 .. + 7, as they lie in memory.
 template <typename IO, int PT, bool FAST>
 struct XRaw {
   static constexpr bool pair = FAST && PT == 2 && sizeof(IO) == 2;  // two channels in one word
@@ -633,9 +697,13 @@ mix_block_kernel(const BlkArgs a) {
   using O = Ops<NT, PC>;
   constexpr int PB = 16 * PT;  // channels of a wave
   __shared__ __align__(16) char s_b[2 * O::piece];
-  __shared__ __align__(16) char s_cg[SUM ? 16 : O::scale - O::g + PC * O::piece];
+  __shared__ __align__(16) char s_cg[SUM ? 16 : O::gsize + PC * O::piece];
   constexpr int CG = PC * O::piece;  // C.B^T behind C
-  __shared__ __align__(16) float s_cum[WV][64], s_lo[WV][64], s_dt[WV][64], s_w[WV][64];
+  constexpr bool XLDS = FAST && sizeof(IO) == 2;
+  using X = XTile<PT>;
+  __shared__ __align__(16) char s_x[XLDS ? WV * X::bytes : 16];
+  __shared__ __align__(16) int s_sc[68];
+  __shared__ __align__(16) float s_cum[WV][64], s_lo[PC == 2 ? WV : 1][64], s_dt[WV][64], s_w[WV][64];
   __shared__ int s_bad[WV][PB];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i16 = lane & 15, q4 = lane >> 4;
@@ -699,7 +767,7 @@ mix_block_kernel(const BlkArgs a) {
   }
   double dsum = 0.0;  // log2 of the segment's decay
 
-  // a block's x, dt and z on their way
+  // a block's x and dt, and its z, on their way
   XRaw<IO, PT, FAST> xr;
   float dt_raw = 0.0f;
   typedef uint32_t zv __attribute__((ext_vector_type(2 * PT)));
@@ -707,22 +775,28 @@ mix_block_kernel(const BlkArgs a) {
   zv zr[4];
   auto fetch = [&](int c) {
     const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ);
-    const bool edge = sg.c0 + c == 0 || r1 - r0 < kQ;
-    auto rows = [&](auto e_) {
-      constexpr bool EDGE = decltype(e_)::value;
+    // rows outside the sequence are read from inside it and replaced later
+    if constexpr (XLDS) {
+#pragma unroll
+      for (int i = 0; i < X::loads; ++i) {
+        const int slot = lane / (X::RB / 16), row = X::RI * i + 8 * (slot % X::GP) + slot / X::GP;
+        if (i + 1 < X::loads || row < kQ + 3) {
+          const int64_t r = max(min(r0 + row - 3, r1 - 1), sg.t0);
+          __builtin_amdgcn_global_load_lds(
+              (const __attribute__((address_space(1))) void*)(static_cast<const IO*>(a.xbc) + r * a.xs + h * a.P +
+                                                              p0 + lane % (X::RB / 16) * 8),
+              (__attribute__((address_space(3))) void*)(s_x + wave * X::bytes + i * X::step), 16, 0, 0);
+        }
+      }
+    } else {
       const int first = r0 + 8 * q4 - 3;
-      const IO* base = static_cast<const IO*>(a.xbc) + (int64_t)first * a.xs + ch[0];
+      const IO* base = static_cast<const IO*>(a.xbc) + ch[0];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int j = 0; j < 11; ++j) {
-          // rows outside the sequence are read from inside it and replaced later
-          const IO* x = base;
-          if constexpr (EDGE) x += (int64_t)(max(min(first + 32 * kb + j, r1 - 1), sg.t0) - first) * a.xs;
-          else x += (int64_t)(32 * kb + j) * a.xs;
-          if constexpr (XRaw<IO, PT, FAST>::pair) {
-            xr.w[0][kb][j] = *reinterpret_cast<const uint32_t*>(x);
-          } else if constexpr (FAST && PT == 2) {
+          const IO* x = base + (int64_t)max(min(first + 32 * kb + j, r1 - 1), sg.t0) * a.xs;
+          if constexpr (FAST && PT == 2) {
             const u2 w = *reinterpret_cast<const u2*>(x);
             xr.w[0][kb][j] = w.x;
             xr.w[1][kb][j] = w.y;
@@ -734,37 +808,42 @@ mix_block_kernel(const BlkArgs a) {
             }
           }
         }
-    };
-    if (edge) rows(std::integral_constant<bool, true>{});
-    else rows(std::integral_constant<bool, false>{});
+    }
     dt_raw = ld<IO>(a.dt, (int64_t)min(r0 + lane, r1 - 1) * a.ds + h);
+  };
+  auto fetch_z = [&](int c) {
     if constexpr (ZAHEAD) {
-      if (a.z) {
-        const int pw = p0 + 4 * PT * q4;
+      asm volatile("" ::: "memory");  // these are the last loads: arrived<4>() counts on it
+      const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ), pw = p0 + 4 * PT * q4;
+      const IO* base = static_cast<const IO*>(a.z) + h * a.P + (pw < a.P ? pw : p0);
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-          zr[tt] = *reinterpret_cast<const zv*>(
-              static_cast<const IO*>(a.z) + (int64_t)min(r0 + 16 * tt + i16, r1 - 1) * a.zs + h * a.P + (pw < a.P ? pw : p0));
-      }
+      for (int tt = 0; tt < 4; ++tt)
+        zr[tt] = *reinterpret_cast<const zv*>(base + (int64_t)min(r0 + 16 * tt + i16, r1 - 1) * a.zs);
     }
   };
-  const char* ops = a.ops + ((int64_t)sg.gc * a.G + g) * O::bytes;
+  const char* op = a.ops + ((int64_t)sg.gc * a.G + g) * O::bytes;
   const int64_t op_step = (int64_t)a.G * O::bytes;
-  if (sg.nc > 0) {
-    fetch(0);
+  auto stage_y = [&](const char* from) {  // what the waves need for y
     if constexpr (!SUM) {
-      stage<WV, CG>(ops + O::c, s_cg);
-      stage<WV, O::scale - O::g>(ops + O::g, s_cg + CG);
+      stage<WV, CG>(from + O::c, s_cg);
+      stage<WV, O::gsize>(from + O::g, s_cg + CG);
     }
+    stage_few<17>(from + O::scale, reinterpret_cast<char*>(s_sc));
+  };
+  if (sg.nc > 0) {
+    if (on) fetch(0);
+    stage_y(op);
+    if (on && a.z) fetch_z(0);
   }
 
   for (int c = 0; c < sg.nc; ++c) {
     const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ), cnt = r1 - r0;
-    const char* op = ops + c * op_step;
-    staged();  // C and C.B^T are there; the waves are done with the last block's B
+    // what y needs and x are there (z, the last four loads, may still come)
+    if (ZAHEAD && on && a.z) arrived<4>();
+    else arrived<0>();
+    meet();  // and the waves are done with the last block's B
     stage<WV, 2 * O::piece>(op + O::b, s_b);
-    const int* sc = reinterpret_cast<const int*>(op + O::scale);
-    const int shB = sc[0], shC = sc[1];
+    const int shB = __builtin_amdgcn_readfirstlane(s_sc[64]), shC = __builtin_amdgcn_readfirstlane(s_sc[65]);
     h8 wh[PT][2], wl[PT][2];
     float dec_all = 1.0f, f_su = 0.0f;
     if (on) {
@@ -773,11 +852,23 @@ mix_block_kernel(const BlkArgs a) {
       {
         float in[PT][2][11];
 #pragma unroll
-        for (int e = 0; e < PT; ++e)
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
+          for (int j = 0; j < 11; ++j) {
+            if constexpr (XLDS) {
+              const char* x = s_x + wave * X::bytes + X::at(4 * kb + q4 + (j >> 3), j & 7) + i16 * 2 * PT;
+              if constexpr (PT == 2) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(x);
+                in[0][kb][j] = __uint_as_float(w << 16);
+                in[1][kb][j] = __uint_as_float(w & 0xffff0000u);
+              } else {
+                in[0][kb][j] = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(x) << 16);
+              }
+            } else {
 #pragma unroll
-            for (int j = 0; j < 11; ++j) in[e][kb][j] = xr.get(e, kb, j);
+              for (int e = 0; e < PT; ++e) in[e][kb][j] = xr.get(e, kb, j);
+            }
+          }
         const bool first = sg.c0 + c == 0;
         if (first || cnt < kQ) {
 #pragma unroll
@@ -844,7 +935,7 @@ mix_block_kernel(const BlkArgs a) {
       shw = shw < -112 ? -112 : (shw > 60 ? 60 : shw);
       dsum += tot;
       s_cum[wave][lane] = (float)cum;
-      s_lo[wave][lane] = (float)(cum - (double)(float)cum);
+      if constexpr (PC == 2) s_lo[wave][lane] = (float)(cum - (double)(float)cum);
       s_w[wave][lane] = wt * two(shw);
       if constexpr (!SUM) s_dt[wave][lane] = dt;
       // ---- silu, the tile's scale
@@ -857,9 +948,17 @@ mix_block_kernel(const BlkArgs a) {
           for (int j = 0; j < 8; ++j) {
             const float x = silu(v[e][kb][j]);
             v[e][kb][j] = x;
-            mx = fmaxf(mx, fabsf(x));
             chk = fmaf(x, 0.0f, chk);
           }
+#pragma unroll
+      for (int e = 0; e < PT; ++e)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) mx = max3(mx, v[e][kb][j], v[e][kb][j + 1]);
+      // this block's x is used up: the next one's may come (B's loads have ended long ago)
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      if (c + 1 < sg.nc) fetch(c + 1);
       if (cnt < kQ) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
@@ -925,7 +1024,7 @@ mix_block_kernel(const BlkArgs a) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sm = fmaxf(sm, fabsf(S[e][nt][r]));
+            for (int r = 0; r < 4; r += 2) sm = max3(sm, S[e][nt][r], S[e][nt][r + 1]);
         sm = wave_max(sm);
         if (!finite(sm)) {
           sm = 0.0f;
@@ -952,27 +1051,30 @@ mix_block_kernel(const BlkArgs a) {
             else sh[e][m] = piece(x);
           }
         const int e_mx = -(shB + shC + shx), e_cs = -(shC + shS);
-        const float Dm = __builtin_amdgcn_ldexpf(D, shB + shC);
         // ---- y, 16 rows at a time
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           if (16 * tt >= cnt) break;
           int t = 16 * tt + i16, s0 = 8 * q4;
           asm volatile("" : "+v"(t), "+v"(s0));  // else the causal masks of all tiles are kept in registers
-          const float cum_t = s_cum[wave][t], lo_t = s_lo[wave][t];
+          const float cum_t = s_cum[wave][t], lo_t = PC == 2 ? s_lo[PC == 2 ? wave : 0][t] : 0.0f;
+          const int shG = PC == 1 ? s_sc[t] : 0;
+          const float Dm = __builtin_amdgcn_ldexpf(D, shB + shC + shG);
           f4 ym[PT] = {}, yc[PT] = {};
           float m[2][8], rm = 0.0f;
 #pragma unroll
           for (int kb = 0; kb <= tt / 2; ++kb) {
             const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
-            const f4* gp = reinterpret_cast<const f4*>(s_cg + CG + (tile * 64 + lane) * 32);
-            const f4 g0 = gp[0], g1 = gp[1];
+            const u4* gp = reinterpret_cast<const u4*>(s_cg + CG + (tile * 64 + lane) * 8 * O::ge);
+            const u4 g0 = gp[0], g1 = PC == 2 ? gp[PC == 2] : g0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int s = 32 * kb + s0 + j;
               float x = cum_t - s_cum[wave][s];
-              if constexpr (PC == 2) x += lo_t - s_lo[wave][s];
-              x = (j < 4 ? g0[j & 3] : g1[j & 3]) * (ex2(x) * s_dt[wave][s]);
+              if constexpr (PC == 2) x += lo_t - s_lo[PC == 2 ? wave : 0][s];
+              x = ex2(x) * s_dt[wave][s];
+              if constexpr (PC == 2) x *= __uint_as_float(j < 4 ? g0[j & 3] : g1[j & 3]);
+              else x = j & 1 ? mul_half<1>(g0[j >> 1], x) : mul_half<0>(g0[j >> 1], x);
               if (kb == tt / 2) {
                 x = s <= t ? x : 0.0f;
                 x = s == t ? x + Dm : x;
@@ -1019,7 +1121,7 @@ mix_block_kernel(const BlkArgs a) {
           }
           // lane (t, q): channels p0 + 4 PT q + {0 .. 4 PT - 1}
           const float f_cs = __builtin_amdgcn_ldexpf(ex2(cum_t + lo_t), e_cs);
-          const float f_mx = __builtin_amdgcn_ldexpf(1.0f, e_mx - shM);
+          const float f_mx = __builtin_amdgcn_ldexpf(1.0f, e_mx - shM - shG);
           const int pw = p0 + 4 * PT * q4;
           const int64_t row = (int64_t)r0 + t, col = (int64_t)h * a.P + pw;
           float o[4 * PT];
@@ -1080,13 +1182,14 @@ mix_block_kernel(const BlkArgs a) {
         }
       }
     }
-    staged();  // B is there; the waves are done with C and C.B^T
+    else {
+      arrived<0>();
+    }
+    meet();  // B is there; the waves are done with C and C.B^T
+    op += op_step;
     if (c + 1 < sg.nc) {
-      if constexpr (!SUM) {
-        stage<WV, CG>(op + op_step + O::c, s_cg);
-        stage<WV, O::scale - O::g>(op + op_step + O::g, s_cg + CG);
-      }
-      fetch(c + 1);
+      stage_y(op);
+      if (on && a.z) fetch_z(c + 1);
     }
     if (on) {
       // ---- the state after the block
@@ -1478,7 +1581,7 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   l.ncut = cut ? l.nchunk / len : 0;
   l.nseg = nseq + l.nchunk / len;
   const int64_t piece = (int64_t)kQ * l.nt * 16 * 2;
-  l.op_bytes = (l.pc + 2) * piece + kTri * 64 * 8 * 4 + 64;
+  l.op_bytes = (l.pc + 2) * piece + kTri * 64 * 8 * (l.pc == 1 ? 2 : 4) + 320;
   int64_t at = 0;
   auto take = [&](int64_t n) {
     const int64_t o = at;
@@ -1498,7 +1601,8 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
 
 template <typename IO, int NT, int PT, int PC, int WV>
 void launch_mix_blocks(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
-  static_assert(Ops<NT, PC>::bytes == (PC + 2) * kQ * NT * 32 + kTri * 64 * 32 + 64, "as in mix_layout");
+  static_assert(Ops<NT, PC>::bytes == (PC + 2) * kQ * NT * 32 + kTri * 64 * 8 * (PC == 1 ? 2 : 4) + 320,
+                "as in mix_layout");
   mix_plan_kernel<<<1, 1024, 0, s>>>(b);
   mix_prep_kernel<IO, NT, PC><<<dim3((unsigned)l.nchunk, b.G), 256, 0, s>>>(b);
   const unsigned grid = (unsigned)(l.nseg * l.units);
@@ -1612,10 +1716,11 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
   a.cs0 = reinterpret_cast<float*>(w + l.cs0);
   a.op_bytes = l.op_bytes; a.seg_len = l.seg_len; a.units = l.units; a.per_group = l.per_group;
   const int es = io_dtype == SSM_DTYPE_BF16 ? 2 : 4, wide = 4 * l.pt * es < 16 ? 4 * l.pt * es : 16;
+  const int64_t inner = nheads * headdim, ch = inner + 2 * ngroups * dstate;
   auto lanes = [&](const void* p, int64_t stride, int bytes) {  // whole accesses of that many bytes
     return ((uintptr_t)p | (uintptr_t)(stride * es) | (uintptr_t)(headdim * es)) % bytes == 0;
   };
-  a.fast = headdim % (4 * l.pt) == 0 && dstate % 4 == 0 && lanes(xbc, xbc_stride, l.pt * es) &&
+  a.fast = headdim % (4 * l.pt) == 0 && dstate % 4 == 0 && lanes(xbc, xbc_stride, es == 2 ? 16 : 4 * l.pt) && (es == 4 || ch >= inner + 32) &&
            lanes(y, y_stride, wide) && (!z || lanes(z, z_stride, wide)) && aligned16(ssm_state);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   if (io_dtype == SSM_DTYPE_BF16) launch_mix<uint16_t, 1>(a, l, s);
