@@ -247,14 +247,20 @@ struct Seg {
   int cut;          // cut sequences before this one
 };
 
+// A cut sequence: its segments' places among those of cut sequences.
+struct Cut {
+  int seq, split, nseg, pad;
+};
+
 struct PlanHead {
-  int nseg, nchunk, nsplit, pad;
+  int nseg, nchunk, ncut, pad;
 };
 
 struct BlkArgs : MixArgs {
   PlanHead* head;
   Chunk* chunks;
   Seg* segs;
+  Cut* cuts;
   char* ops;       // operands of (block, group)
   float* local;    // [split][H, P, N] state of a segment from zero, then the state entering it
   float* decay;    // [split][H] log2 of a segment's whole decay
@@ -327,7 +333,14 @@ __device__ __forceinline__ int shift_for(float m) {
   return e < -112 ? -112 : (e > 60 ? 60 : e);
 }
 __device__ __forceinline__ float two(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
-__device__ __forceinline__ float max3(float m, float x, float y) { return fmaxf(fmaxf(m, fabsf(x)), fabsf(y)); }
+// The larger of m and two magnitudes; a NaN among them is passed over.
+__device__ __forceinline__ float max3(float m, float x, float y) {
+  float o;
+  asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(o) : "v"(m), "v"(x), "v"(y));
+  return o;
+}
+// In a branch that is hardly ever taken: keeps the compiler from computing both sides.
+__device__ __forceinline__ void rarely() { asm volatile(""); }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
 
 __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
@@ -397,56 +410,64 @@ __device__ __forceinline__ int block_scan_max(int v, int* red) {  // inclusive, 
   return v;
 }
 
+// The last index whose prefix (of 1024) is at most i.
+__device__ __forceinline__ int find(const int* prefix, int i) {
+  int at = 0;
+#pragma unroll
+  for (int d = 512; d; d >>= 1)
+    if (prefix[at + d] <= i) at += d;
+  return at;
+}
+
 __global__ void __launch_bounds__(1024) mix_plan_kernel(const BlkArgs a) {
   __shared__ int red[16], top;
+  __shared__ int s_t0[1024], s_t1[1024], s_chunk[1024], s_seg[1024], s_split[1024], s_cut[1024];
   int nchunk = 0, nseg = 0, nsplit = 0, ncut = 0;
+  const int i = threadIdx.x;
   int reached = max(0, min(a.cu[0], (int)a.tokens));  // the largest offset so far
-  for (int64_t s0 = 0; s0 < a.nseq; s0 += 1024) {
+  for (int64_t base = 0; base < a.nseq; base += 1024) {
     // the offsets' running maximum: whatever they hold, the sequences lie one
     // behind the other inside the rows, and the tables hold their blocks
-    const int64_t s = s0 + threadIdx.x;
+    const int64_t s = base + i;
     int end = s < a.nseq ? max(reached, min(a.cu[s + 1], (int)a.tokens)) : reached;
     end = block_scan_max(end, red);
-    int begin = __shfl_up(end, 1, 64);
-    if ((threadIdx.x & 63) == 0) {
-      begin = reached;
-      for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) begin = max(begin, red[i]);
-    }
-    if (threadIdx.x == 1023) top = end;
     __syncthreads();
+    s_t1[i] = end;
+    if (i == 1023) top = end;
+    __syncthreads();
+    const int begin = i ? s_t1[i - 1] : reached;
     reached = top;
+    s_t0[i] = begin;
     Seq q;
     int nc = 0, ns = 0;
     if (s < a.nseq && load_seq(a, s, q)) {
-      q.t0 = begin;
-      q.t1 = end;
-      nc = (int)((q.t1 - q.t0 + kQ - 1) / kQ);
+      nc = (end - begin + kQ - 1) / kQ;
       ns = nc ? (nc + a.seg_len - 1) / a.seg_len : 1;
     }
-    int total;
-    const int cb = nchunk + block_scan(nc, red, total);
-    nchunk += total;
-    const int sb = nseg + block_scan(ns, red, total);
-    nseg += total;
-    const int pb = nsplit + block_scan(ns > 1 ? ns : 0, red, total);
-    nsplit += total;
-    const int ub = ncut + block_scan(ns > 1, red, total);
-    ncut += total;
-    for (int k = 0; k < ns; ++k) {
-      const int lo = (int)((int64_t)nc * k / ns), hi = (int)((int64_t)nc * (k + 1) / ns);
-      a.segs[sb + k] = {(int)s, (int)q.t0, (int)q.t1, lo, hi - lo, cb + lo, ns > 1 ? pb + k : -1, ub};
+    int chunks, segs, splits, cuts;
+    s_chunk[i] = block_scan(nc, red, chunks);
+    s_seg[i] = block_scan(ns, red, segs);
+    s_split[i] = nsplit + block_scan(ns > 1 ? ns : 0, red, splits);
+    s_cut[i] = ncut + block_scan(ns > 1, red, cuts);
+    if (ns > 1) a.cuts[s_cut[i]] = {(int)s, s_split[i], ns, 0};
+    __syncthreads();
+    for (int c = i; c < chunks; c += 1024) {
+      const int k = find(s_chunk, c), r0 = s_t0[k] + (c - s_chunk[k]) * kQ;
+      a.chunks[nchunk + c] = {r0, min(s_t1[k], r0 + kQ), s_t0[k], (int)(base + k)};
     }
-  }
-  if (threadIdx.x == 0) *a.head = {nseg, nchunk, nsplit, 0};
-  __syncthreads();  // the segments are written; now the blocks, a wave per segment
-  const int lane = threadIdx.x & 63;
-  for (int i = threadIdx.x >> 6; i < nseg; i += 16) {
-    const Seg g = a.segs[i];
-    for (int c = lane; c < g.nc; c += 64) {
-      const int r0 = g.t0 + (g.c0 + c) * kQ;
-      a.chunks[g.gc + c] = {r0, g.t1 < r0 + kQ ? g.t1 : r0 + kQ, g.t0, g.seq};
+    for (int g = i; g < segs; g += 1024) {
+      const int k = find(s_seg, g), n = (s_t1[k] - s_t0[k] + kQ - 1) / kQ, of = n ? (n + a.seg_len - 1) / a.seg_len : 1;
+      const int j = g - s_seg[k], lo = (int)((int64_t)n * j / of), hi = (int)((int64_t)n * (j + 1) / of);
+      a.segs[nseg + g] = {(int)(base + k), s_t0[k], s_t1[k], lo, hi - lo, nchunk + s_chunk[k] + lo,
+                          of > 1 ? s_split[k] + j : -1, s_cut[k]};
     }
+    nchunk += chunks;
+    nseg += segs;
+    nsplit += splits;
+    ncut += cuts;
+    __syncthreads();
   }
+  if (i == 0) *a.head = {nseg, nchunk, ncut, 0};
 }
 
 // ---- the operands of one block and group
@@ -576,11 +597,13 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
     }
   }
   int shG = 0;
-  if constexpr (NPC == 1) {  // to fp16, every row by its own largest value
+  if constexpr (NPC == 1) {  // to fp16, every row by its own largest value, zero after the row's token
     float gm = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float x = acc[i >> 3][(i >> 2) & 1][i & 3];
+      const bool after = 32 * (i >> 3) + 8 * (lane >> 4) + (i & 7) > 16 * wave + (lane & 15);
+      const float x = after ? 0.0f : acc[i >> 3][(i >> 2) & 1][i & 3];
+      acc[i >> 3][(i >> 2) & 1][i & 3] = x;
       if (finite(x)) gm = fmaxf(gm, fabsf(x));
     }
     shG = shift_for(row_max(gm));
@@ -633,7 +656,6 @@ __device__ __forceinline__ void stage_few(const char* from, char* to) {
 // All of this wave's memory accesses but the last LEFT have ended.
 template <int LEFT>
 __device__ __forceinline__ void arrived() {
-  static_assert(LEFT < 16, "the low bits of vmcnt");
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
 }
 // The waves of the workgroup meet; what is on its way from memory stays so.
@@ -688,7 +710,7 @@ struct XRaw {
 // z, y eight channels at a time).  The WV waves of a workgroup share a group
 // of heads and stage its operands in LDS, B of this block while the waves
 // work on y, C and C.B^T of the next while they work on the state; x, dt and z
-// of the next block are on their way in registers meanwhile.  PC: pieces of
+// of the next block are on their way meanwhile.  PC: pieces of
 // the operands of y.  FAST: rows and channels allow whole vectors (headdim a
 // multiple of 4 PT, dstate of 4, rows aligned to the accesses).
 template <typename IO, int NT, int PT, int PC, int WV, bool SUM, bool FAST>
@@ -702,7 +724,7 @@ mix_block_kernel(const BlkArgs a) {
   constexpr bool XLDS = FAST && sizeof(IO) == 2;
   using X = XTile<PT>;
   __shared__ __align__(16) char s_x[XLDS ? WV * X::bytes : 16];
-  __shared__ __align__(16) int s_sc[68];
+  __shared__ __align__(16) int s_sc[2][68];
   __shared__ __align__(16) float s_cum[WV][64], s_lo[PC == 2 ? WV : 1][64], s_dt[WV][64], s_w[WV][64];
   __shared__ int s_bad[WV][PB];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -813,7 +835,6 @@ mix_block_kernel(const BlkArgs a) {
   };
   auto fetch_z = [&](int c) {
     if constexpr (ZAHEAD) {
-      asm volatile("" ::: "memory");  // these are the last loads: arrived<4>() counts on it
       const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ), pw = p0 + 4 * PT * q4;
       const IO* base = static_cast<const IO*>(a.z) + h * a.P + (pw < a.P ? pw : p0);
 #pragma unroll
@@ -823,29 +844,35 @@ mix_block_kernel(const BlkArgs a) {
   };
   const char* op = a.ops + ((int64_t)sg.gc * a.G + g) * O::bytes;
   const int64_t op_step = (int64_t)a.G * O::bytes;
-  auto stage_y = [&](const char* from) {  // what the waves need for y
-    if constexpr (!SUM) {
-      stage<WV, CG>(from + O::c, s_cg);
-      stage<WV, O::gsize>(from + O::g, s_cg + CG);
-    }
-    stage_few<17>(from + O::scale, reinterpret_cast<char*>(s_sc));
+  auto stage_b = [&](const char* from, int at) {  // B and the scales
+    stage<WV, 2 * O::piece>(from + O::b, s_b);
+    stage_few<17>(from + O::scale, reinterpret_cast<char*>(s_sc[at]));
   };
   if (sg.nc > 0) {
     if (on) fetch(0);
-    stage_y(op);
-    if (on && a.z) fetch_z(0);
+    if constexpr (!SUM) stage_b(op, 0);
   }
 
   for (int c = 0; c < sg.nc; ++c) {
     const int r0 = sg.t0 + (sg.c0 + c) * kQ, r1 = min(sg.t1, r0 + kQ), cnt = r1 - r0;
-    // what y needs and x are there (z, the last four loads, may still come)
-    if (ZAHEAD && on && a.z) arrived<4>();
+    // places in LDS are computed from the lane in every turn: kept all through, they cost registers
+    int here = threadIdx.x & 63;
+    asm volatile("" : "+v"(here));
+    const int lane = here, i16 = here & 15, q4 = here >> 4;
+    // x, dt (and B) are there; y's four stores, at least, came after their loads
+    if (!SUM && on && c) arrived<4>();
     else arrived<0>();
-    meet();  // and the waves are done with the last block's B
-    stage<WV, 2 * O::piece>(op + O::b, s_b);
-    const int shB = __builtin_amdgcn_readfirstlane(s_sc[64]), shC = __builtin_amdgcn_readfirstlane(s_sc[65]);
-    h8 wh[PT][2], wl[PT][2];
-    float dec_all = 1.0f, f_su = 0.0f;
+    meet();  // and the waves are done with the last block's C (SUM: B)
+    if constexpr (SUM) {
+      stage_b(op, 0);
+    } else {
+      stage<WV, CG>(op + O::c, s_cg);
+      stage<WV, O::gsize>(op + O::g, s_cg + CG);
+    }
+    h8 xh[PT][2], xl[PT][2], wh[PT][2], wl[PT][2], sh[PT][NT / 2], sl[PT][NT / 2];
+    float dec_all = 1.0f, cap = 0.0f;
+    int shx = 0, shw = 0, shd = 0, shS = 0;
+    bool bad = false;
     if (on) {
       // ---- the convolution
       float v[PT][2][8];
@@ -871,11 +898,13 @@ mix_block_kernel(const BlkArgs a) {
           }
         const bool first = sg.c0 + c == 0;
         if (first || cnt < kQ) {
+          int first_row = r0;
+          asm volatile("" : "+s"(first_row));  // keeps these comparisons in this branch
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int j = 0; j < 11; ++j) {
-              const int r = r0 + 32 * kb + 8 * q4 + j - 3;
+              const int r = first_row + 32 * kb + 8 * q4 + j - 3;
 #pragma unroll
               for (int e = 0; e < PT; ++e) in[e][kb][j] = r >= sg.t0 && r < r1 ? in[e][kb][j] : 0.0f;
             }
@@ -926,18 +955,29 @@ mix_block_kernel(const BlkArgs a) {
         // below 2^-160 a decay is zero in float32; held there, no sum swallows the steps beside it
         dA = dt * A2;
         dA = dA < -160.0f ? -160.0f : dA;
+        if (!finite(dt)) dA = __builtin_nanf("");  // and all after it
       }
       const double cum = wave_scan((double)dA), tot = lane63(cum);
       const float wt = dt * ex2((float)(tot - cum));
       dec_all = ex2((float)tot);
       const float wmax = wave_max(finite(wt) ? fabsf(wt) : 0.0f);
-      int shw = -__builtin_amdgcn_frexp_expf(wmax);
+      shw = -__builtin_amdgcn_frexp_expf(wmax);
       shw = shw < -112 ? -112 : (shw > 60 ? 60 : shw);
       dsum += tot;
       s_cum[wave][lane] = (float)cum;
       if constexpr (PC == 2) s_lo[wave][lane] = (float)(cum - (double)(float)cum);
       s_w[wave][lane] = wt * two(shw);
-      if constexpr (!SUM) s_dt[wave][lane] = dt;
+      // the weights exp(c_t - c_s) dt_s of M: at most the largest dt, unless the state grows
+      if constexpr (!SUM && PC == 1) {
+        shd = -__builtin_amdgcn_frexp_expf(wave_max(finite(dt) ? fabsf(dt) : 0.0f));
+        if (__any(dA > 0.0f)) {
+          rarely();
+          cap = fminf(wave_max(fmaxf((float)cum, 0.0f)) + wave_max(fmaxf(-(float)cum, 0.0f)), 100.0f);
+          shd -= (int)cap + 1;
+        }
+        shd = shd < -112 ? -112 : (shd > 60 ? 60 : shd);
+      }
+      if constexpr (!SUM) s_dt[wave][lane] = PC == 2 || finite(dt) ? dt * two(shd) : 0.0f;
       // ---- silu, the tile's scale
       float mx = 0.0f, chk = 0.0f;
 #pragma unroll
@@ -958,8 +998,10 @@ mix_block_kernel(const BlkArgs a) {
           for (int j = 0; j < 8; j += 2) mx = max3(mx, v[e][kb][j], v[e][kb][j + 1]);
       // this block's x is used up: the next one's may come (B's loads have ended long ago)
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      if (a.z) fetch_z(c);
       if (c + 1 < sg.nc) fetch(c + 1);
       if (cnt < kQ) {
+        rarely();
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -967,8 +1009,9 @@ mix_block_kernel(const BlkArgs a) {
 #pragma unroll
             for (int e = 0; e < PT; ++e) v[e][kb][j] = 32 * kb + 8 * q4 + j < cnt ? v[e][kb][j] : 0.0f;
       }
-      const bool bad = __any(!(chk == 0.0f));
+      bad = __any(!(chk == 0.0f));
       if (bad) {
+        rarely();
         mx = 0.0f;
 #pragma unroll
         for (int e = 0; e < PT; ++e) {
@@ -985,13 +1028,11 @@ mix_block_kernel(const BlkArgs a) {
           if (q4 == 0) s_bad[wave][PT * i16 + e] = first;
         }
       }
-      const int shx = shift_for(wave_max(mx));
+      shx = shift_for(wave_max(mx));
       const float fx = two(shx);
-      f_su = two(max(-126, -(shB + shx + shw)));
       __builtin_amdgcn_wave_barrier();
 
       // ---- operands from x: once as it is (for y), once weighted (for the state)
-      h8 xh[PT][2], xl[PT][2];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         float w8[8];
@@ -1007,9 +1048,11 @@ mix_block_kernel(const BlkArgs a) {
           }
           pieces(w, wh[e][kb], wl[e][kb]);
           if constexpr (!SUM) {
-            if (bad)  // 0 x Inf is not 0: y's earlier rows must not meet them
+            if (bad) {  // 0 x Inf is not 0: y's earlier rows must not meet them
+              rarely();
 #pragma unroll
               for (int j = 0; j < 8; ++j) x[j] = finite(x[j]) ? x[j] : 0.0f;
+            }
             if constexpr (PC == 2) pieces(x, xh[e][kb], xl[e][kb]);
             else xh[e][kb] = piece(x);
           }
@@ -1027,6 +1070,7 @@ mix_block_kernel(const BlkArgs a) {
             for (int r = 0; r < 4; r += 2) sm = max3(sm, S[e][nt][r], S[e][nt][r + 1]);
         sm = wave_max(sm);
         if (!finite(sm)) {
+          rarely();
           sm = 0.0f;
 #pragma unroll
           for (int e = 0; e < PT; ++e)
@@ -1037,9 +1081,8 @@ mix_block_kernel(const BlkArgs a) {
                 if (finite(S[e][nt][r])) sm = fmaxf(sm, fabsf(S[e][nt][r]));
           sm = wave_max(sm);
         }
-        const int shS = shift_for(sm);
+        shS = shift_for(sm);
         const float fs = two(shS);
-        h8 sh[PT][NT / 2], sl[PT][NT / 2];
 #pragma unroll
         for (int e = 0; e < PT; ++e)
 #pragma unroll
@@ -1050,47 +1093,119 @@ mix_block_kernel(const BlkArgs a) {
             if constexpr (PC == 2) pieces(x, sh[e][m], sl[e][m]);
             else sh[e][m] = piece(x);
           }
+      }  // the state as an operand
+
+      auto su = [&](int shB) {  // ---- the state after the block
+        const float f_su = two(max(-126, -(shB + shx + shw)));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          h8 bh[2], bl[2];
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            bh[kb] = *reinterpret_cast<const h8*>(s_b + ((nt * 2 + kb) * 64 + lane) * 16);
+            bl[kb] = *reinterpret_cast<const h8*>(s_b + O::piece + ((nt * 2 + kb) * 64 + lane) * 16);
+          }
+#pragma unroll
+          for (int e = 0; e < PT; ++e) {
+            f4 d = {};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+              d = mfma(bh[kb], wl[e][kb], d);
+              d = mfma(bl[kb], wh[e][kb], d);
+              d = mfma(bh[kb], wh[e][kb], d);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[e][nt][r] = fmaf(d[r], f_su, S[e][nt][r] * dec_all);
+          }
+        }
+      };
+      if constexpr (SUM) {
+        arrived<0>();
+        meet();  // B is there
+        su(__builtin_amdgcn_readfirstlane(s_sc[0][64]));
+      } else {
+        su(__builtin_amdgcn_readfirstlane(s_sc[c & 1][64]));
+      }
+    } else {
+      arrived<0>();
+      if constexpr (SUM) meet();
+    }
+    op += op_step;
+    if constexpr (!SUM) {
+      meet();  // C and C.B^T are there; the waves are done with B
+      if (c + 1 < sg.nc) stage_b(op, (c + 1) & 1);
+      asm volatile("" ::: "memory");  // the stores of y stay behind these loads: arrived<4>() counts on it
+      if (on) {
+        const int* sc = s_sc[c & 1];
+        const int shB = __builtin_amdgcn_readfirstlane(sc[64]), shC = __builtin_amdgcn_readfirstlane(sc[65]);
         const int e_mx = -(shB + shC + shx), e_cs = -(shC + shS);
         // ---- y, 16 rows at a time
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           if (16 * tt >= cnt) break;
-          int t = 16 * tt + i16, s0 = 8 * q4;
-          asm volatile("" : "+v"(t), "+v"(s0));  // else the causal masks of all tiles are kept in registers
+          const int t = 16 * tt + i16;
           const float cum_t = s_cum[wave][t], lo_t = PC == 2 ? s_lo[PC == 2 ? wave : 0][t] : 0.0f;
-          const int shG = PC == 1 ? s_sc[t] : 0;
-          const float Dm = __builtin_amdgcn_ldexpf(D, shB + shC + shG);
-          f4 ym[PT] = {}, yc[PT] = {};
-          float m[2][8], rm = 0.0f;
+          f4 ym[PT] = {}, yc[PT] = {}, yd[PT] = {};
+          int shM;  // M's rows are scaled by 2^shM beside the operands' own scales
+          if constexpr (PC == 1) {
+            // x itself, for D, by the unit matrix: of row i the columns 8 q + j (- 16 in odd tiles)
+            const int jd = i16 + 16 * (tt & 1) - 8 * q4;
+            u4 unit_bits;
 #pragma unroll
-          for (int kb = 0; kb <= tt / 2; ++kb) {
-            const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
-            const u4* gp = reinterpret_cast<const u4*>(s_cg + CG + (tile * 64 + lane) * 8 * O::ge);
-            const u4 g0 = gp[0], g1 = PC == 2 ? gp[PC == 2] : g0;
+            for (int k = 0; k < 4; ++k) unit_bits[k] = jd >> 1 == k ? (jd & 1 ? 0x3c000000u : 0x3c00u) : 0u;
+            const h8 unit = __builtin_bit_cast(h8, unit_bits);
+            // C.B^T is zero above the diagonal, the weights are at most 2^cap there
+            shM = sc[t] + shd;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int s = 32 * kb + s0 + j;
-              float x = cum_t - s_cum[wave][s];
-              if constexpr (PC == 2) x += lo_t - s_lo[PC == 2 ? wave : 0][s];
-              x = ex2(x) * s_dt[wave][s];
-              if constexpr (PC == 2) x *= __uint_as_float(j < 4 ? g0[j & 3] : g1[j & 3]);
-              else x = j & 1 ? mul_half<1>(g0[j >> 1], x) : mul_half<0>(g0[j >> 1], x);
-              if (kb == tt / 2) {
-                x = s <= t ? x : 0.0f;
-                x = s == t ? x + Dm : x;
+            for (int kb = 0; kb <= tt / 2; ++kb) {
+              const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
+              const u4 g = *reinterpret_cast<const u4*>(s_cg + CG + (tile * 64 + lane) * 16);
+              float m[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int s = 32 * kb + 8 * q4 + j;
+                float x = cum_t - s_cum[wave][s];
+                if (kb == tt / 2) x = fminf(x, cap);
+                x = ex2(x) * s_dt[wave][s];
+                m[j] = j & 1 ? mul_half<1>(g[j >> 1], x) : mul_half<0>(g[j >> 1], x);
               }
-              m[kb][j] = x;
-              rm = fmaxf(rm, fabsf(x));
+              const h8 mh = piece(m);
+#pragma unroll
+              for (int e = 0; e < PT; ++e) ym[e] = mfma(xh[e][kb], mh, ym[e]);
             }
-          }
-          // every row by its own largest value: one token's outlier leaves the others their bits
-          const int shM = shift_for(row_max(rm));
-          const float fm = two(shM);
 #pragma unroll
-          for (int kb = 0; kb <= tt / 2; ++kb) {
+            for (int e = 0; e < PT; ++e) yd[e] = mfma(xh[e][tt / 2], unit, yd[e]);
+          } else {
+            int tq = t, s0 = 8 * q4;
+            asm volatile("" : "+v"(tq), "+v"(s0));  // else the causal masks of all tiles are kept in registers
+            const float Dm = __builtin_amdgcn_ldexpf(D, shB + shC);
+            float m[2][8], rm = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m[kb][j] *= fm;
-            if constexpr (PC == 2) {
+            for (int kb = 0; kb <= tt / 2; ++kb) {
+              const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
+              const f4* gp = reinterpret_cast<const f4*>(s_cg + CG + (tile * 64 + lane) * 32);
+              const f4 g0 = gp[0], g1 = gp[1];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int s = 32 * kb + s0 + j;
+                float x = cum_t - s_cum[wave][s] + (lo_t - s_lo[PC == 2 ? wave : 0][s]);
+                x = (j < 4 ? g0[j & 3] : g1[j & 3]) * (ex2(x) * s_dt[wave][s]);
+                if (kb == tt / 2) {
+                  x = s <= tq ? x : 0.0f;
+                  x = s == tq ? x + Dm : x;
+                }
+                m[kb][j] = x;
+              }
+#pragma unroll
+              for (int j = 0; j < 8; j += 2) rm = max3(rm, m[kb][j], m[kb][j + 1]);
+            }
+            // every row by its own largest value: one token's outlier leaves the others their bits
+            shM = shift_for(row_max(rm));
+            const float fm = two(shM);
+#pragma unroll
+            for (int kb = 0; kb <= tt / 2; ++kb) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) m[kb][j] *= fm;
               h8 mh, ml;
               pieces(m[kb], mh, ml);
 #pragma unroll
@@ -1099,10 +1214,6 @@ mix_block_kernel(const BlkArgs a) {
                 ym[e] = mfma(xh[e][kb], ml, ym[e]);
                 ym[e] = mfma(xh[e][kb], mh, ym[e]);
               }
-            } else {
-              const h8 mh = piece(m[kb]);
-#pragma unroll
-              for (int e = 0; e < PT; ++e) ym[e] = mfma(xh[e][kb], mh, ym[e]);
             }
           }
 #pragma unroll
@@ -1121,17 +1232,23 @@ mix_block_kernel(const BlkArgs a) {
           }
           // lane (t, q): channels p0 + 4 PT q + {0 .. 4 PT - 1}
           const float f_cs = __builtin_amdgcn_ldexpf(ex2(cum_t + lo_t), e_cs);
-          const float f_mx = __builtin_amdgcn_ldexpf(1.0f, e_mx - shM - shG);
+          const float f_mx = __builtin_amdgcn_ldexpf(1.0f, e_mx - shM);
+          const float f_d = __builtin_amdgcn_ldexpf(D, -shx);
           const int pw = p0 + 4 * PT * q4;
           const int64_t row = (int64_t)r0 + t, col = (int64_t)h * a.P + pw;
           float o[4 * PT];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int e = 0; e < PT; ++e) o[PT * r + e] = fmaf(ym[e][r], f_mx, yc[e][r] * f_cs);
-          if (bad)
+            for (int e = 0; e < PT; ++e) {
+              o[PT * r + e] = fmaf(ym[e][r], f_mx, yc[e][r] * f_cs);
+              if constexpr (PC == 1) o[PT * r + e] = fmaf(yd[e][r], f_d, o[PT * r + e]);
+            }
+          if (bad) {
+            rarely();
 #pragma unroll
             for (int k = 0; k < 4 * PT; ++k) o[k] = t >= s_bad[wave][4 * PT * q4 + k] ? __builtin_nanf("") : o[k];
+          }
           if (a.z) {
             if constexpr (ZAHEAD) {
 #pragma unroll
@@ -1182,39 +1299,6 @@ mix_block_kernel(const BlkArgs a) {
         }
       }
     }
-    else {
-      arrived<0>();
-    }
-    meet();  // B is there; the waves are done with C and C.B^T
-    op += op_step;
-    if (c + 1 < sg.nc) {
-      stage_y(op);
-      if (on && a.z) fetch_z(c + 1);
-    }
-    if (on) {
-      // ---- the state after the block
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        h8 bh[2], bl[2];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          bh[kb] = *reinterpret_cast<const h8*>(s_b + ((nt * 2 + kb) * 64 + lane) * 16);
-          bl[kb] = *reinterpret_cast<const h8*>(s_b + O::piece + ((nt * 2 + kb) * 64 + lane) * 16);
-        }
-#pragma unroll
-        for (int e = 0; e < PT; ++e) {
-          f4 d = {};
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb) {
-            d = mfma(bh[kb], wl[e][kb], d);
-            d = mfma(bl[kb], wh[e][kb], d);
-            d = mfma(bh[kb], wh[e][kb], d);
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) S[e][nt][r] = fmaf(d[r], f_su, S[e][nt][r] * dec_all);
-        }
-      }
-    }
   }
   if (!on) return;
 
@@ -1250,25 +1334,47 @@ mix_block_kernel(const BlkArgs a) {
 
 // ---- the states entering the segments of a cut sequence, from their states from zero
 
+// One pass over them, read and written once; four values a thread, four
+// segments of each on their way together.
 __global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
-  const int si = blockIdx.x;
-  if (si >= a.head->nseg) return;
-  const Seg sg = a.segs[si];
-  if (sg.split < 0 || sg.c0 > 0) return;  // the first segment of each cut sequence does all of its
+  if ((int)blockIdx.x >= a.head->ncut) return;
+  const Cut ct = a.cuts[blockIdx.x];
   const int64_t per = (int64_t)a.H * a.P * a.N;
-  const int ns = ((sg.t1 - sg.t0 + kQ - 1) / kQ + a.seg_len - 1) / a.seg_len;
-  const bool resume = a.state && a.has && a.has[sg.seq];
-  const int64_t slot = a.slots ? a.slots[sg.seq] : sg.seq;
-  const int64_t i = (int64_t)blockIdx.y * 256 + threadIdx.x;
-  if (i >= per) return;
-  const int h = (int)(i / ((int64_t)a.P * a.N));
-  float s = resume ? a.state[slot * per + i] : 0.0f;
-  float* l = a.local + (int64_t)sg.split * per + i;
-  const float* d = a.decay + (int64_t)sg.split * a.H + h;
-  for (int k = 0; k < ns; ++k) {
-    const float own = k + 1 < ns ? l[k * per] : 0.0f;
-    l[k * per] = s;
-    s = fmaf(s, ex2(k + 1 < ns ? d[(int64_t)k * a.H] : 0.0f), own);
+  const int hs = a.P * a.N;  // values of a head
+  const bool resume = a.state && a.has && a.has[ct.seq];
+  const int64_t slot = a.slots ? a.slots[ct.seq] : ct.seq;
+  const float* d = a.decay + (int64_t)ct.split * a.H;
+  constexpr int V = 4, K = 4;
+  int64_t at[V];
+  int h[V];
+  float s[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    at[v] = ((int64_t)blockIdx.y * V + v) * 256 + threadIdx.x;
+    if (at[v] >= per) at[v] = per;
+    h[v] = at[v] < per ? (int)(at[v] / hs) : 0;
+    s[v] = resume && at[v] < per ? a.state[slot * per + at[v]] : 0.0f;
+  }
+  float* l = a.local + (int64_t)ct.split * per;
+  for (int k0 = 0; k0 < ct.nseg; k0 += K) {
+    float own[K][V], dec[K][V];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const int k = min(k0 + j, ct.nseg - 2);  // nothing enters a segment from the last one
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        own[j][v] = l[k * per + (at[v] < per ? at[v] : 0)];
+        dec[j][v] = d[(int64_t)k * a.H + h[v]];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (k0 + j < ct.nseg)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (at[v] < per) l[(k0 + j) * per + at[v]] = s[v];
+          s[v] = fmaf(s[v], ex2(dec[j][v]), own[j][v]);
+        }
   }
 }
 
@@ -1553,7 +1659,7 @@ struct MixLayout {
   int nt, pt, pc, wv;
   int64_t nchunk, nseg, nsplit, ncut;  // at most
   int seg_len, per_group, units;
-  int64_t op_bytes, chunks, segs, ops, local, decay, cs0, bytes;
+  int64_t op_bytes, chunks, segs, cuts, ops, local, decay, cs0, bytes;
 };
 
 // A segment is one workgroup's work, one after another; the card holds 2048
@@ -1591,6 +1697,7 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   take(sizeof(PlanHead));
   l.chunks = take(l.nchunk * sizeof(Chunk));
   l.segs = take(l.nseg * sizeof(Seg));
+  l.cuts = take(l.ncut * sizeof(Cut));
   l.ops = take(l.nchunk * G * l.op_bytes);
   l.local = take(l.nsplit * H * P * N * 4);
   l.decay = take(l.nsplit * H * 4);
@@ -1611,7 +1718,7 @@ void launch_mix_blocks(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
     if (l.nsplit) {
       mix_block_kernel<IO, NT, PT, PC, WV, true, F><<<grid, 64 * WV, 0, s>>>(b);
       const int64_t per = (int64_t)b.H * b.P * b.N;
-      mix_join_kernel<<<dim3((unsigned)l.nseg, (unsigned)((per + 255) / 256)), 256, 0, s>>>(b);
+      mix_join_kernel<<<dim3((unsigned)l.ncut, (unsigned)((per + 1023) / 1024)), 256, 0, s>>>(b);
     }
     mix_block_kernel<IO, NT, PT, PC, WV, false, F><<<grid, 64 * WV, 0, s>>>(b);
   };
@@ -1710,6 +1817,7 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
   a.head = reinterpret_cast<PlanHead*>(w);
   a.chunks = reinterpret_cast<Chunk*>(w + l.chunks);
   a.segs = reinterpret_cast<Seg*>(w + l.segs);
+  a.cuts = reinterpret_cast<Cut*>(w + l.cuts);
   a.ops = w + l.ops;
   a.local = reinterpret_cast<float*>(w + l.local);
   a.decay = reinterpret_cast<float*>(w + l.decay);
