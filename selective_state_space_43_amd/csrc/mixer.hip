@@ -1388,8 +1388,9 @@ struct NormArgs {
   const float* b;
   void* y;   // forward output, or dx
   void* dz;
-  float* pw;  // per-block sums of dweight, dbias [blocks, C]
+  float* pw;  // the strips' sums of dweight, dbias [strips, C], or NULL
   float* pb;
+  int strips;
   int64_t xs, zs, gs, ys, dzs;  // row strides; gs of dy
   int64_t rows;
   int C, G;
@@ -1397,128 +1398,340 @@ struct NormArgs {
   int center, act, gate;
 };
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return red[0] + red[1] + red[2] + red[3];
+// A group is held in the registers of a team of TL threads, thread i with
+// vectors i, i + TL, .. (K at most) of VE channels each: one pass over the
+// rows, the statistics in two steps over registers (mean, then the squares
+// around it), so nothing cancels.  VE is 16 bytes' worth where the rows and the
+// groups allow it and one element elsewhere.
+
+template <typename IO, int VE>
+struct Vec {
+  static constexpr int words = VE * (int)sizeof(IO) < 4 ? 1 : VE * (int)sizeof(IO) / 4;
+  uint32_t w[words];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (VE > 1) {
+      const u4 v = *reinterpret_cast<const u4*>(static_cast<const IO*>(p) + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = v[k];
+    } else if constexpr (sizeof(IO) == 2) {
+      w[0] = static_cast<const uint16_t*>(p)[i];
+    } else {
+      w[0] = static_cast<const uint32_t*>(p)[i];
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[j]);
+    else return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+  }
+};
+template <typename IO, int VE>
+__device__ __forceinline__ void put(void* p, int64_t i, const float* v) {
+  if constexpr (VE == 1) {
+    st<IO>(p, i, v[0]);
+  } else if constexpr (sizeof(IO) == 4) {
+    *reinterpret_cast<f4*>(static_cast<float*>(p) + i) = *reinterpret_cast<const f4*>(v);
+  } else {
+    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+    typedef float f8 __attribute__((ext_vector_type(8)));
+    f8 f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = v[k];
+    *reinterpret_cast<b8*>(static_cast<uint16_t*>(p) + i) = __builtin_convertvector(f, b8);
+  }
 }
 
-template <typename IO>
-__global__ void __launch_bounds__(256) norm_fwd_kernel(const NormArgs a) {
-  __shared__ float red[4];
-  const int gs = a.C / a.G, c0 = blockIdx.y * gs;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    auto val = [&](int c) {
-      float v = ld<IO>(a.x, r * a.xs + c);
-      if (a.gate == SSM_GATE_BEFORE) v *= silu(ld<IO>(a.z, r * a.zs + c));
-      return v;
-    };
+// VE parameters from column c on, or the value that leaves things as they are.
+template <int VE>
+__device__ __forceinline__ void params(const float* p, int c, float none, float (&o)[VE]) {
+  if (p) {
+    if constexpr (VE == 1) {
+      o[0] = p[c];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VE; j += 4) *reinterpret_cast<f4*>(o + j) = *reinterpret_cast<const f4*>(p + c + j);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) o[j] = none;
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// Sums of NV values over the team, the same bits in all of its threads.  Teams
+// wider than a wave meet once a call, in two sets of places by turns.
+template <int TL, int NV>
+__device__ __forceinline__ void team_sum(float (&v)[NV], float (*red)[NV][TL < 64 ? 1 : TL / 64], int& turn) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = dpp_add<0xB1>(v[i]);   // lanes 1, 0, 3, 2
+    v[i] = dpp_add<0x4E>(v[i]);   // lanes 2, 3, 0, 1
+    v[i] = dpp_add<0x141>(v[i]);  // the half row mirrored: its other four
+    if constexpr (TL >= 32) {
+      v[i] = dpp_add<0x140>(v[i]);  // the row mirrored: its other eight
+      const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i]), false, false));
+      v[i] = __uint_as_float(w.x) + __uint_as_float(w.y);
+    }
+    if constexpr (TL >= 64) {
+      const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i]), false, false));
+      v[i] = __uint_as_float(w.x) + __uint_as_float(w.y);
+    }
+  }
+  if constexpr (TL > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) red[turn][i][wave] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < TL / 64; ++k) v[i] += red[turn][i][k];
+    }
+    turn ^= 1;
+  }
+}
+
+constexpr int team_threads(int tl) { return tl < 256 ? 256 : tl; }
+
+template <typename IO, int VE, int TL, int K>
+__global__ void __launch_bounds__(team_threads(TL)) norm_fwd_kernel(const NormArgs a) {
+  __shared__ float red[2][1][TL < 64 ? 1 : TL / 64];
+  int turn = 0;
+  const int gs = a.C / a.G, nv = gs / VE, i = threadIdx.x % TL;
+  const int64_t item = (int64_t)blockIdx.x * (team_threads(TL) / TL) + threadIdx.x / TL;
+  const bool on = item < a.rows * a.G;  // the others only keep the waves whole
+  const int64_t r = on ? item / a.G : 0;
+  const int c0 = on ? (int)(item - r * a.G) * gs : 0;
+  Vec<IO, VE> xr[K], zr[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * TL >= nv) break;
+    const int c = c0 + min(i + k * TL, nv - 1) * VE;
+    xr[k].load(a.x, r * a.xs + c);
+    if (a.gate) zr[k].load(a.z, r * a.zs + c);
+  }
+  const float inv = 1.0f / (float)gs;
+  float v[K][VE];
+  float sum[1] = {0.0f};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * TL >= nv) break;
+    const bool in = i + k * TL < nv;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      float x = xr[k].get(j);
+      if (a.gate == SSM_GATE_BEFORE) x *= silu(zr[k].get(j));
+      v[k][j] = in ? x : 0.0f;
+      sum[0] += v[k][j];
+    }
+  }
+  float mean = 0.0f;
+  if (a.center) {
+    team_sum<TL, 1>(sum, red, turn);
+    mean = sum[0] * inv;
+  }
+  float sq[1] = {0.0f};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * TL >= nv) break;
+    if (i + k * TL < nv)
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        v[k][j] -= mean;
+        sq[0] = fmaf(v[k][j], v[k][j], sq[0]);
+      }
+  }
+  team_sum<TL, 1>(sq, red, turn);
+  const float rs = rsqrtf(fmaf(sq[0], inv, a.eps));
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * TL >= nv) break;
+    if (on && i + k * TL < nv) {
+      const int c = c0 + (i + k * TL) * VE;
+      float o[VE], w[VE], b[VE];
+      params<VE>(a.w, c, 1.0f, w);
+      params<VE>(a.b, c, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        float y = fmaf(v[k][j] * rs, w[j], b[j]);
+        if (a.act == SSM_ACT_SILU) y = silu(y);
+        if (a.gate == SSM_GATE_AFTER) y *= silu(zr[k].get(j));
+        o[j] = y;
+      }
+      put<IO, VE>(a.y, r * a.ys + c, o);
+    }
+  }
+}
+
+// The backward: with u = g w (g the gradient of the affine result) and n the
+// normalised values, d = (u - mean(u) - n mean(u n)) / deviation, mean(u) only
+// where the forward is centred.  A team keeps its group and its columns' sums of
+// g n and g in registers over a strip of rows; norm_bwd_sum_kernel adds the
+// strips in order.
+template <typename IO, int VE, int TL, int K, bool DB>
+__global__ void __launch_bounds__(team_threads(TL)) norm_bwd_kernel(const NormArgs a) {
+  __shared__ float red1[2][1][TL < 64 ? 1 : TL / 64], red2[2][2][TL < 64 ? 1 : TL / 64];
+  int turn1 = 0, turn2 = 0;
+  const int gs = a.C / a.G, nv = gs / VE, i = threadIdx.x % TL;
+  const int64_t team = (int64_t)blockIdx.x * (team_threads(TL) / TL) + threadIdx.x / TL;
+  const int strips = a.strips;
+  const bool on = team < (int64_t)strips * a.G;
+  const int64_t strip = on ? team / a.G : 0;
+  const int c0 = on ? (int)(team - strip * a.G) * gs : 0;
+  const int64_t r0 = a.rows * strip / strips, r1 = a.rows * (strip + 1) / strips;
+  // every team of the workgroup takes as many turns as the longest strip: they meet inside
+  const int64_t turns = (a.rows + strips - 1) / strips;
+  const float inv = 1.0f / (float)gs;
+  float dw[K][VE] = {}, db[DB ? K : 1][VE] = {};
+  for (int64_t q = 0; q < turns; ++q) {
+    const int64_t r = r0 + q;
+    const bool live = on && r < r1;
+    Vec<IO, VE> x[K], z[K], gr[K];
+    {
+      const int64_t rr = live ? r : 0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k * TL >= nv) break;
+        const int c = c0 + min(i + k * TL, nv - 1) * VE;
+        x[k].load(a.x, rr * a.xs + c);
+        gr[k].load(a.dy, rr * a.gs + c);
+        if (a.gate) z[k].load(a.z, rr * a.zs + c);
+      }
+    }
+    float v[K][VE], g[K][VE];
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      const bool in = live && i + k * TL < nv;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        g[k][j] = in ? gr[k].get(j) : 0.0f;
+        float t = x[k].get(j);
+        if (a.gate == SSM_GATE_BEFORE) t *= silu(z[k].get(j));
+        v[k][j] = in ? t : 0.0f;
+        sum[0] += v[k][j];
+      }
+    }
     float mean = 0.0f;
     if (a.center) {
-      float sum = 0.0f;
-      for (int c = threadIdx.x; c < gs; c += 256) sum += val(c0 + c);
-      mean = block_sum(sum, red) / gs;
+      team_sum<TL, 1>(sum, red1, turn1);
+      mean = sum[0] * inv;
     }
-    float sq = 0.0f;
-    for (int c = threadIdx.x; c < gs; c += 256) {
-      const float v = val(c0 + c) - mean;
-      sq = fmaf(v, v, sq);
+    float sq[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      if (live && i + k * TL < nv)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          v[k][j] -= mean;
+          sq[0] = fmaf(v[k][j], v[k][j], sq[0]);
+        }
     }
-    const float rs = rsqrtf(block_sum(sq, red) / gs + a.eps);
-    for (int c = c0 + threadIdx.x; c < c0 + gs; c += 256) {
-      float v = (val(c) - mean) * rs;
-      if (a.w) v *= a.w[c];
-      if (a.b) v += a.b[c];
-      if (a.act == SSM_ACT_SILU) v = silu(v);
-      if (a.gate == SSM_GATE_AFTER) v *= silu(ld<IO>(a.z, r * a.zs + c));
-      st<IO>(a.y, r * a.ys + c, v);
+    team_sum<TL, 1>(sq, red1, turn1);
+    const float rs = rsqrtf(fmaf(sq[0], inv, a.eps));
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      if (live && i + k * TL < nv) {
+        const int c = c0 + (i + k * TL) * VE;
+        float dz[VE], w[VE], b[VE];
+        params<VE>(a.w, c, 1.0f, w);
+        params<VE>(a.b, c, 0.0f, b);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float n = v[k][j] * rs;
+          float t = g[k][j];
+          if (a.act == SSM_ACT_SILU || a.gate == SSM_GATE_AFTER) {
+            const float y = fmaf(n, w[j], b[j]);
+            const float sy = sigmoid(y);
+            if (a.gate == SSM_GATE_AFTER) {
+              const float zz = z[k].get(j), sz = sigmoid(zz);
+              const float o = a.act == SSM_ACT_SILU ? y * sy : y;
+              dz[j] = t * o * sz * fmaf(zz, 1.0f - sz, 1.0f);
+              t *= zz * sz;
+            }
+            if (a.act == SSM_ACT_SILU) t *= sy * fmaf(y, 1.0f - sy, 1.0f);
+          }
+          dw[k][j] = fmaf(t, n, dw[k][j]);
+          if constexpr (DB) db[k][j] += t;
+          const float u = t * w[j];
+          s[0] += u;
+          s[1] = fmaf(u, n, s[1]);
+          v[k][j] = n;
+          g[k][j] = u;
+        }
+        if (a.gate == SSM_GATE_AFTER) put<IO, VE>(a.dz, r * a.dzs + c, dz);
+      }
+    }
+    team_sum<TL, 2>(s, red2, turn2);
+    const float s1 = a.center ? s[0] * inv : 0.0f, s2 = s[1] * inv;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      if (live && i + k * TL < nv) {
+        const int c = c0 + (i + k * TL) * VE;
+        float dx[VE], dz[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          float d = rs * (g[k][j] - fmaf(v[k][j], s2, s1));
+          if (a.gate == SSM_GATE_BEFORE) {
+            const float zz = z[k].get(j), sz = sigmoid(zz);
+            dz[j] = d * x[k].get(j) * sz * fmaf(zz, 1.0f - sz, 1.0f);
+            d *= zz * sz;
+          }
+          dx[j] = d;
+        }
+        put<IO, VE>(a.y, r * a.ys + c, dx);
+        if (a.gate == SSM_GATE_BEFORE) put<IO, VE>(a.dz, r * a.dzs + c, dz);
+      }
+    }
+  }
+  if (!on) return;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * TL >= nv) break;
+    if (i + k * TL < nv) {
+      const int64_t at = strip * a.C + c0 + (i + k * TL) * VE;
+      auto keep = [&](float* p, const float* v) {
+        put<float, VE < 4 ? 1 : 4>(p, at, v);
+        if constexpr (VE == 8) put<float, 4>(p, at + 4, v + 4);
+      };
+      if (a.pw) keep(a.pw, dw[k]);
+      if constexpr (DB) keep(a.pb, db[k]);
     }
   }
 }
 
-template <typename IO>
-__global__ void __launch_bounds__(256) norm_bwd_kernel(const NormArgs a) {
-  __shared__ float red[4];
-  const int gs = a.C / a.G, c0 = blockIdx.y * gs;
-  float* pw = a.pw + (int64_t)blockIdx.x * a.C;
-  float* pb = a.pb + (int64_t)blockIdx.x * a.C;
-  for (int c = c0 + threadIdx.x; c < c0 + gs; c += 256) pw[c] = pb[c] = 0.0f;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    auto val = [&](int c) {
-      float v = ld<IO>(a.x, r * a.xs + c);
-      if (a.gate == SSM_GATE_BEFORE) v *= silu(ld<IO>(a.z, r * a.zs + c));
-      return v;
-    };
-    float mean = 0.0f;
-    if (a.center) {
-      float sum = 0.0f;
-      for (int c = threadIdx.x; c < gs; c += 256) sum += val(c0 + c);
-      mean = block_sum(sum, red) / gs;
-    }
-    float sq = 0.0f;
-    for (int c = threadIdx.x; c < gs; c += 256) {
-      const float v = val(c0 + c) - mean;
-      sq = fmaf(v, v, sq);
-    }
-    const float rs = rsqrtf(block_sum(sq, red) / gs + a.eps);
-    // gradient of the affine result, and what the gate behind it takes
-    auto grad = [&](int c, float n, float* dz) {
-      float g = ld<IO>(a.dy, r * a.gs + c);
-      float v = n * (a.w ? a.w[c] : 1.0f) + (a.b ? a.b[c] : 0.0f);
-      if (a.gate == SSM_GATE_AFTER) {
-        const float z = ld<IO>(a.z, r * a.zs + c), sg = sigmoid(z);
-        const float o = a.act == SSM_ACT_SILU ? silu(v) : v;
-        if (dz) *dz = g * o * sg * fmaf(z, 1.0f - sg, 1.0f);
-        g *= z * sg;
-      }
-      if (a.act == SSM_ACT_SILU) {
-        const float sv = sigmoid(v);
-        g *= sv * fmaf(v, 1.0f - sv, 1.0f);
-      }
-      return g;
-    };
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int c = c0 + threadIdx.x; c < c0 + gs; c += 256) {
-      const float n = (val(c) - mean) * rs, g = grad(c, n, nullptr);
-      const float u = g * (a.w ? a.w[c] : 1.0f);
-      s1 += u;
-      s2 = fmaf(u, n, s2);
-      pw[c] = fmaf(g, n, pw[c]);
-      pb[c] += g;
-    }
-    s1 = block_sum(s1, red) / gs;
-    s2 = block_sum(s2, red) / gs;
-    if (!a.center) s1 = 0.0f;
-    for (int c = c0 + threadIdx.x; c < c0 + gs; c += 256) {
-      const float n = (val(c) - mean) * rs;
-      float dz = 0.0f;
-      const float u = grad(c, n, &dz) * (a.w ? a.w[c] : 1.0f);
-      float d = rs * (u - n * s2 - s1);
-      if (a.gate == SSM_GATE_BEFORE) {
-        const float z = ld<IO>(a.z, r * a.zs + c), sg = sigmoid(z);
-        dz = d * ld<IO>(a.x, r * a.xs + c) * sg * fmaf(z, 1.0f - sg, 1.0f);
-        d *= z * sg;
-      }
-      st<IO>(a.y, r * a.ys + c, d);
-      if (a.dz) st<IO>(a.dz, r * a.dzs + c, dz);
-    }
+// Column sums of the strips' partial sums, in order: sixteen runs of strips a
+// column, then the sixteen.  blockIdx.y: dweight or dbias.
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const NormArgs a, float* dw, float* db) {
+  __shared__ float run[16][64];
+  const float* part = blockIdx.y ? a.pb : a.pw;
+  float* out = blockIdx.y ? db : dw;
+  if (!out) return;
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  const int lo = a.strips * q / 16, hi = a.strips * (q + 1) / 16;
+  float s = 0.0f;
+  if (c < a.C) {
+#pragma unroll 8
+    for (int i = lo; i < hi; ++i) s += part[(int64_t)i * a.C + c];
   }
-}
-
-// column sums of the blocks' partial sums, in block order
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* pw, const float* pb,
-                                                           int blocks, int C, float* dw, float* db) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= C) return;
-  float sw = 0.0f, sb = 0.0f;
-  for (int i = 0; i < blocks; ++i) {
-    sw += pw[(int64_t)i * C + c];
-    sb += pb[(int64_t)i * C + c];
+  run[q][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (q == 0 && c < a.C) {
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += run[k][threadIdx.x];
+    out[c] = s;
   }
-  if (dw) dw[c] = sw;
-  if (db) db[c] = sb;
 }
 
 // ---------------------------------------------------------------- host side
@@ -1743,7 +1956,15 @@ void launch_mix_simple(const MixArgs& a, hipStream_t s) {
     mix_conv_state_kernel<IO><<<dim3((unsigned)a.nseq, (a.C + 255) / 256), 256, 0, s>>>(a);
 }
 
-constexpr int64_t kNormBlocks = 256;
+// Strips of rows whose column sums are kept apart, at most: three waves for every
+// SIMD of the card where the partial sums stay under 16 MB a gradient.
+int64_t norm_strips(int64_t rows, int64_t channels) {
+  int64_t n = ((int64_t)1 << 22) / channels;
+  n = n < 256 ? 256 : (n > 1024 ? 1024 : n);
+  return n < rows ? n : rows;
+}
+constexpr int64_t kNormThreads = 256 * 4 * 3 * 64;
+
 constexpr int64_t kMaxGroup = 32768;
 
 int check_norm(const NormArgs& a, int64_t rows, int64_t channels, int64_t ngroups, int io_dtype) {
@@ -1768,6 +1989,64 @@ int check_norm(const NormArgs& a, int64_t rows, int64_t channels, int64_t ngroup
     return fail(SSM_E_NULL, a.z ? "z without a gate" : "z is NULL beside a gate");
   if (!(a.eps >= 0.0f) || a.eps > 3e38f) return fail(SSM_E_SHAPE, "eps is negative or not finite");
   return check_io(io_dtype);
+}
+
+// Whole 16-byte vectors: the groups start and end on them in every tensor.
+bool norm_vectors(const NormArgs& a, int es) {
+  const uintptr_t at = (uintptr_t)a.x | (uintptr_t)a.z | (uintptr_t)a.dy | (uintptr_t)a.y | (uintptr_t)a.dz |
+                       (uintptr_t)a.w | (uintptr_t)a.b;
+  const int64_t all = (a.xs | a.zs | a.gs | a.ys | a.dzs | (int64_t)(a.C / a.G)) * es;
+  return at % 16 == 0 && all % 16 == 0;
+}
+
+template <bool BWD, typename IO, int VE, int TL, int K>
+int launch_norm_team(NormArgs& a, hipStream_t s) {
+  if constexpr (BWD) {
+    const int64_t fill = (kNormThreads + (int64_t)TL * a.G - 1) / ((int64_t)TL * a.G);
+    if (fill < a.strips) a.strips = (int)fill;
+  }
+  const int64_t items = (BWD ? a.strips : a.rows) * (int64_t)a.G, per = team_threads(TL) / TL;
+  const int64_t blocks = (items + per - 1) / per;
+  if (blocks > 0x7fffffff) return fail(SSM_E_SHAPE, "rows and ngroups: too many for one call");
+  if constexpr (BWD) {
+    if (a.pb) norm_bwd_kernel<IO, VE, TL, K, true><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
+    else norm_bwd_kernel<IO, VE, TL, K, false><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
+  } else norm_fwd_kernel<IO, VE, TL, K><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
+  return launch_status(BWD ? "ssm_group_norm_bwd launch" : "ssm_group_norm_fwd launch");
+}
+
+// The smallest team whose registers hold the group.
+template <bool BWD, typename IO>
+int launch_norm_io(NormArgs& a, bool vec, hipStream_t s) {
+  constexpr int VE = 16 / sizeof(IO);
+  const int gs = a.C / a.G, nv = vec ? gs / VE : gs;
+  if (vec) {
+    if constexpr (BWD) {
+      if (nv <= 8 * 3) return launch_norm_team<true, IO, VE, 8, 3>(a, s);
+      if (nv <= 32 * 3) return launch_norm_team<true, IO, VE, 32, 3>(a, s);
+      if (nv <= 64 * 3) return launch_norm_team<true, IO, VE, 64, 3>(a, s);
+      if (nv <= 256 * 3) return launch_norm_team<true, IO, VE, 256, 3>(a, s);
+    } else {
+      if (nv <= 8 * 4) return launch_norm_team<false, IO, VE, 8, 4>(a, s);
+      // a wave a group has the least to wait for, 256 threads the least to do one after
+      // the other, which counts while there are few groups
+      const bool few = a.rows * a.G <= 512;
+      if (nv <= (few ? 64 : 64 * 10)) return launch_norm_team<false, IO, VE, 64, 10>(a, s);
+      if (nv <= 256 * 4) return launch_norm_team<false, IO, VE, 256, 4>(a, s);
+    }
+    if (nv <= 1024 * 4) return launch_norm_team<BWD, IO, VE, 1024, 4>(a, s);
+    if constexpr (VE == 4) return launch_norm_team<BWD, IO, VE, 1024, 8>(a, s);
+  }
+  if (nv <= 8 * 8) return launch_norm_team<BWD, IO, 1, 8, 8>(a, s);
+  if (nv <= 64 * 16) return launch_norm_team<BWD, IO, 1, 64, 16>(a, s);
+  if (nv <= 256 * 16) return launch_norm_team<BWD, IO, 1, 256, 16>(a, s);
+  if (nv <= 1024 * 16) return launch_norm_team<BWD, IO, 1, 1024, 16>(a, s);
+  return launch_norm_team<BWD, IO, 1, 1024, 32>(a, s);
+}
+
+template <bool BWD>
+int launch_norm(NormArgs& a, bool vec, int io_dtype, hipStream_t s) {
+  return io_dtype == SSM_DTYPE_BF16 ? launch_norm_io<BWD, uint16_t>(a, vec, s) : launch_norm_io<BWD, float>(a, vec, s);
 }
 
 }  // namespace
@@ -1884,11 +2163,8 @@ int ssm_group_norm_fwd(const void* x, int64_t x_stride, const void* z, int64_t z
   const Rows out = {y, rows, y_stride * es, channels * es, "y"};
   if ((st = check_no_alias(&out, 1, ins, 4))) return st;
   a.rows = rows; a.C = (int)channels; a.G = (int)ngroups;
-  hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  const dim3 grid((unsigned)(rows < 65536 ? rows : 65536), a.G);
-  if (io_dtype == SSM_DTYPE_BF16) norm_fwd_kernel<uint16_t><<<grid, 256, 0, s>>>(a);
-  else norm_fwd_kernel<float><<<grid, 256, 0, s>>>(a);
-  return launch_status("ssm_group_norm_fwd launch");
+  const bool vec = norm_vectors(a, es);
+  return launch_norm<false>(a, vec, io_dtype, static_cast<hipStream_t>(hip_stream));
 }
 
 int64_t ssm_group_norm_bwd_workspace_size(int64_t rows, int64_t channels, int64_t ngroups) {
@@ -1896,7 +2172,7 @@ int64_t ssm_group_norm_bwd_workspace_size(int64_t rows, int64_t channels, int64_
   if (check_extent("rows", rows) || check_extent("channels", channels) ||
       check_extent("ngroups", ngroups) || channels > 0x7fffffff)
     return -1;
-  return 2 * kNormBlocks * channels * 4;
+  return (2 * norm_strips(rows, channels) * channels * 4 + 15) / 16 * 16;
 }
 
 int ssm_group_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
@@ -1940,14 +2216,13 @@ int ssm_group_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t
                        flat(workspace, need, "workspace")};
   if ((st = check_no_alias(outs, 5, ins, 5))) return st;
   a.rows = rows; a.C = (int)channels; a.G = (int)ngroups;
-  a.pw = static_cast<float*>(workspace);
-  a.pb = a.pw + kNormBlocks * channels;
+  a.strips = (int)norm_strips(rows, channels);
+  a.pw = dweight ? static_cast<float*>(workspace) : nullptr;
+  a.pb = dbias ? static_cast<float*>(workspace) + a.strips * channels : nullptr;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  const int blocks = (int)(rows < kNormBlocks ? rows : kNormBlocks);
-  if (io_dtype == SSM_DTYPE_BF16) norm_bwd_kernel<uint16_t><<<dim3(blocks, a.G), 256, 0, s>>>(a);
-  else norm_bwd_kernel<float><<<dim3(blocks, a.G), 256, 0, s>>>(a);
+  if ((st = launch_norm<true>(a, norm_vectors(a, es), io_dtype, s))) return st;
   if (dweight || dbias)
-    norm_bwd_sum_kernel<<<(a.C + 255) / 256, 256, 0, s>>>(a.pw, a.pb, blocks, a.C, dweight, dbias);
+    norm_bwd_sum_kernel<<<dim3((unsigned)((channels + 63) / 64), 2), 1024, 0, s>>>(a, dweight, dbias);
   return launch_status("ssm_group_norm_bwd launch");
 }
 
