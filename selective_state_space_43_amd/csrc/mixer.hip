@@ -1573,8 +1573,14 @@ __global__ void __launch_bounds__(team_threads(TL)) norm_fwd_kernel(const NormAr
 // where the forward is centred.  A team keeps its group and its columns' sums of
 // g n and g in registers over a strip of rows; norm_bwd_sum_kernel adds the
 // strips in order.
-template <typename IO, int VE, int TL, int K, bool DB>
-__global__ void __launch_bounds__(team_threads(TL)) norm_bwd_kernel(const NormArgs a) {
+//
+// PLAIN: no centring, no activation, no gate behind and no bias, as the Mamba-2
+// block has it: then u does not wait for the statistics, and one meeting gives both
+// sums.  Three waves a SIMD hide each other's loads better than two that fetch
+// their next rows ahead (16384 x 5120 bf16, 8 groups: 204 against 254 us).
+template <typename IO, int VE, int TL, int K, bool PLAIN>
+__global__ void __launch_bounds__(team_threads(TL))
+__attribute__((amdgpu_waves_per_eu(TL > 256 ? 4 : PLAIN || sizeof(IO) == 4 ? 3 : 2))) norm_bwd_kernel(const NormArgs a) {
   __shared__ float red1[2][1][TL < 64 ? 1 : TL / 64], red2[2][2][TL < 64 ? 1 : TL / 64];
   int turn1 = 0, turn2 = 0;
   const int gs = a.C / a.G, nv = gs / VE, i = threadIdx.x % TL;
@@ -1587,102 +1593,131 @@ __global__ void __launch_bounds__(team_threads(TL)) norm_bwd_kernel(const NormAr
   // every team of the workgroup takes as many turns as the longest strip: they meet inside
   const int64_t turns = (a.rows + strips - 1) / strips;
   const float inv = 1.0f / (float)gs;
-  float dw[K][VE] = {}, db[DB ? K : 1][VE] = {};
+  const bool before = a.gate == SSM_GATE_BEFORE, after = !PLAIN && a.gate == SSM_GATE_AFTER;
+  float dw[K][VE] = {}, db[PLAIN ? 1 : K][VE] = {};
   for (int64_t q = 0; q < turns; ++q) {
     const int64_t r = r0 + q;
     const bool live = on && r < r1;
-    Vec<IO, VE> x[K], z[K], gr[K];
-    {
-      const int64_t rr = live ? r : 0;
+    const int64_t rr = min(r, a.rows - 1);
+    Vec<IO, VE> x[K], z[K], g[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      const int c = c0 + min(i + k * TL, nv - 1) * VE;
+      x[k].load(a.x, rr * a.xs + c);
+      g[k].load(a.dy, rr * a.gs + c);
+      if (a.gate) z[k].load(a.z, rr * a.zs + c);
+    }
+    float v[K][VE];  // what is normalised; zero where there is nothing
+    float both[2] = {0.0f, 0.0f}, rs;
+    if constexpr (PLAIN) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (k * TL >= nv) break;
-        const int c = c0 + min(i + k * TL, nv - 1) * VE;
-        x[k].load(a.x, rr * a.xs + c);
-        gr[k].load(a.dy, rr * a.gs + c);
-        if (a.gate) z[k].load(a.z, rr * a.zs + c);
-      }
-    }
-    float v[K][VE], g[K][VE];
-    float sum[1] = {0.0f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (k * TL >= nv) break;
-      const bool in = live && i + k * TL < nv;
-#pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        g[k][j] = in ? gr[k].get(j) : 0.0f;
-        float t = x[k].get(j);
-        if (a.gate == SSM_GATE_BEFORE) t *= silu(z[k].get(j));
-        v[k][j] = in ? t : 0.0f;
-        sum[0] += v[k][j];
-      }
-    }
-    float mean = 0.0f;
-    if (a.center) {
-      team_sum<TL, 1>(sum, red1, turn1);
-      mean = sum[0] * inv;
-    }
-    float sq[1] = {0.0f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (k * TL >= nv) break;
-      if (live && i + k * TL < nv)
+        const bool in = live && i + k * TL < nv;
+        float w[VE];
+        params<VE>(a.w, c0 + min(i + k * TL, nv - 1) * VE, 1.0f, w);
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          v[k][j] -= mean;
-          sq[0] = fmaf(v[k][j], v[k][j], sq[0]);
+          float t = x[k].get(j);
+          if (before) t *= silu(z[k].get(j));
+          t = in ? t : 0.0f;
+          v[k][j] = t;
+          both[0] = fmaf(t, t, both[0]);
+          both[1] = fmaf(g[k].get(j) * w[j], in ? t : 0.0f, both[1]);
         }
-    }
-    team_sum<TL, 1>(sq, red1, turn1);
-    const float rs = rsqrtf(fmaf(sq[0], inv, a.eps));
-    float s[2] = {0.0f, 0.0f};
+      }
+      team_sum<TL, 2>(both, red2, turn2);
+      rs = rsqrtf(fmaf(both[0], inv, a.eps));
+      both[1] *= rs;
+      both[0] = 0.0f;
+    } else {
+      float sum[1] = {0.0f};
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (k * TL >= nv) break;
-      if (live && i + k * TL < nv) {
-        const int c = c0 + (i + k * TL) * VE;
-        float dz[VE], w[VE], b[VE];
-        params<VE>(a.w, c, 1.0f, w);
-        params<VE>(a.b, c, 0.0f, b);
+      for (int k = 0; k < K; ++k) {
+        if (k * TL >= nv) break;
+        const bool in = live && i + k * TL < nv;
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          const float n = v[k][j] * rs;
-          float t = g[k][j];
-          if (a.act == SSM_ACT_SILU || a.gate == SSM_GATE_AFTER) {
-            const float y = fmaf(n, w[j], b[j]);
-            const float sy = sigmoid(y);
-            if (a.gate == SSM_GATE_AFTER) {
-              const float zz = z[k].get(j), sz = sigmoid(zz);
-              const float o = a.act == SSM_ACT_SILU ? y * sy : y;
-              dz[j] = t * o * sz * fmaf(zz, 1.0f - sz, 1.0f);
-              t *= zz * sz;
-            }
-            if (a.act == SSM_ACT_SILU) t *= sy * fmaf(y, 1.0f - sy, 1.0f);
+          float t = x[k].get(j);
+          if (before) t *= silu(z[k].get(j));
+          v[k][j] = in ? t : 0.0f;
+          sum[0] += v[k][j];
+        }
+      }
+      float mean = 0.0f;
+      if (a.center) {
+        team_sum<TL, 1>(sum, red1, turn1);
+        mean = sum[0] * inv;
+      }
+      float sq[1] = {0.0f};
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k * TL >= nv) break;
+        if (live && i + k * TL < nv)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            v[k][j] -= mean;
+            sq[0] = fmaf(v[k][j], v[k][j], sq[0]);
           }
-          dw[k][j] = fmaf(t, n, dw[k][j]);
-          if constexpr (DB) db[k][j] += t;
-          const float u = t * w[j];
-          s[0] += u;
-          s[1] = fmaf(u, n, s[1]);
-          v[k][j] = n;
-          g[k][j] = u;
-        }
-        if (a.gate == SSM_GATE_AFTER) put<IO, VE>(a.dz, r * a.dzs + c, dz);
       }
+      team_sum<TL, 1>(sq, red1, turn1);
+      rs = rsqrtf(fmaf(sq[0], inv, a.eps));
     }
-    team_sum<TL, 2>(s, red2, turn2);
-    const float s1 = a.center ? s[0] * inv : 0.0f, s2 = s[1] * inv;
+    // the gradient of the affine result n w + b; dz of a gate behind it
+    auto grad = [&](int k, int j, float n, float w, float b, float& dz) {
+      float t = g[k].get(j);
+      if constexpr (!PLAIN) {
+        if (a.act == SSM_ACT_SILU || after) {
+          const float y = fmaf(n, w, b), sy = sigmoid(y);
+          if (after) {
+            const float zz = z[k].get(j), sz = sigmoid(zz);
+            dz = t * (a.act == SSM_ACT_SILU ? y * sy : y) * sz * fmaf(zz, 1.0f - sz, 1.0f);
+            t *= zz * sz;
+          }
+          if (a.act == SSM_ACT_SILU) t *= sy * fmaf(y, 1.0f - sy, 1.0f);
+        }
+      }
+      return t;
+    };
+    if constexpr (!PLAIN) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k * TL >= nv) break;
+        if (live && i + k * TL < nv) {
+          const int c = c0 + (i + k * TL) * VE;
+          float w[VE], b[VE], dz[VE];
+          params<VE>(a.w, c, 1.0f, w);
+          params<VE>(a.b, c, 0.0f, b);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const float n = v[k][j] * rs, t = grad(k, j, n, w[j], b[j], dz[j]), u = t * w[j];
+            dw[k][j] = fmaf(t, n, dw[k][j]);
+            db[k][j] += t;
+            both[0] += u;
+            both[1] = fmaf(u, n, both[1]);
+          }
+          if (after) put<IO, VE>(a.dz, r * a.dzs + c, dz);
+        }
+      }
+      team_sum<TL, 2>(both, red2, turn2);
+      if (!a.center) both[0] = 0.0f;
+    }
+    const float s1 = both[0] * inv, s2 = both[1] * inv;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (k * TL >= nv) break;
       if (live && i + k * TL < nv) {
         const int c = c0 + (i + k * TL) * VE;
-        float dx[VE], dz[VE];
+        float dx[VE], dz[VE], w[VE], b[VE], none;
+        params<VE>(a.w, c, 1.0f, w);
+        if constexpr (!PLAIN) params<VE>(a.b, c, 0.0f, b);
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          float d = rs * (g[k][j] - fmaf(v[k][j], s2, s1));
-          if (a.gate == SSM_GATE_BEFORE) {
+          const float n = v[k][j] * rs, t = grad(k, j, n, w[j], PLAIN ? 0.0f : b[j], none);
+          if constexpr (PLAIN) dw[k][j] = fmaf(t, n, dw[k][j]);
+          float d = rs * (t * w[j] - fmaf(n, s2, s1));
+          if (before) {
             const float zz = z[k].get(j), sz = sigmoid(zz);
             dz[j] = d * x[k].get(j) * sz * fmaf(zz, 1.0f - sz, 1.0f);
             d *= zz * sz;
@@ -1690,7 +1725,7 @@ __global__ void __launch_bounds__(team_threads(TL)) norm_bwd_kernel(const NormAr
           dx[j] = d;
         }
         put<IO, VE>(a.y, r * a.ys + c, dx);
-        if (a.gate == SSM_GATE_BEFORE) put<IO, VE>(a.dz, r * a.dzs + c, dz);
+        if (before) put<IO, VE>(a.dz, r * a.dzs + c, dz);
       }
     }
   }
@@ -1705,7 +1740,8 @@ __global__ void __launch_bounds__(team_threads(TL)) norm_bwd_kernel(const NormAr
         if constexpr (VE == 8) put<float, 4>(p, at + 4, v + 4);
       };
       if (a.pw) keep(a.pw, dw[k]);
-      if constexpr (DB) keep(a.pb, db[k]);
+      if constexpr (!PLAIN)
+        if (a.pb) keep(a.pb, db[k]);
     }
   }
 }
@@ -2009,8 +2045,10 @@ int launch_norm_team(NormArgs& a, hipStream_t s) {
   const int64_t blocks = (items + per - 1) / per;
   if (blocks > 0x7fffffff) return fail(SSM_E_SHAPE, "rows and ngroups: too many for one call");
   if constexpr (BWD) {
-    if (a.pb) norm_bwd_kernel<IO, VE, TL, K, true><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
-    else norm_bwd_kernel<IO, VE, TL, K, false><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
+    if (!a.center && a.act == SSM_ACT_NONE && a.gate != SSM_GATE_AFTER && !a.pb)
+      norm_bwd_kernel<IO, VE, TL, K, true><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
+    else
+      norm_bwd_kernel<IO, VE, TL, K, false><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
   } else norm_fwd_kernel<IO, VE, TL, K><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
   return launch_status(BWD ? "ssm_group_norm_bwd launch" : "ssm_group_norm_fwd launch");
 }
