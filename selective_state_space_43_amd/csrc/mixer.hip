@@ -93,108 +93,7 @@ __device__ __forceinline__ bool load_seq(const MixArgs& a, int64_t s, Seq& q) {
   return true;
 }
 
-// One output of the convolution and its silu: channel c at row t of a
-// sequence that starts at row t0.
-template <typename IO>
-__device__ __forceinline__ float conv_at(const MixArgs& a, const Seq& q, int64_t t, int c) {
-  const int W = a.W;
-  float acc = a.cb ? a.cb[c] : 0.0f;
-  for (int k = 0; k < W; ++k) {
-    const int64_t r = t - (W - 1) + k;
-    float v = 0.0f;
-    if (r >= q.t0)
-      v = ld<IO>(a.xbc, r * a.xs + c);
-    else if (q.resume)
-      v = a.conv_state[(q.slot * a.C + c) * (W - 1) + (r - q.t0 + W - 1)];
-    acc = fmaf(a.cw[(int64_t)c * W + k], v, acc);
-  }
-  return silu(acc);
-}
-
-// The recurrence in time order: a workgroup owns 16 channels of one head of
-// one sequence, 16 lanes a channel, each with every sixteenth state.
 constexpr int kMaxN = 256;
-
-template <typename IO>
-__global__ void __launch_bounds__(256) mix_scan_kernel(const MixArgs a) {
-  __shared__ float sB[kMaxN], sC[kMaxN], sx[16];
-  const int64_t s = blockIdx.x;
-  const int h = blockIdx.y, p0 = blockIdx.z * 16;
-  const int tid = threadIdx.x, pl = tid >> 4, nl = tid & 15, p = p0 + pl;
-  const int N = a.N, g = h / (a.H / a.G), inner = a.H * a.P;
-  Seq q;
-  if (!load_seq(a, s, q)) return;
-  float hst[kMaxN / 16];
-  float* own = a.state ? a.state + ((q.slot * a.H + h) * a.P + p) * N : nullptr;
-#pragma unroll
-  for (int i = 0; i < kMaxN / 16; ++i) {
-    const int n = nl + 16 * i;
-    hst[i] = (q.resume && p < a.P && n < N) ? own[n] : 0.0f;
-  }
-  const float A = a.A[h], D = a.Dskip ? a.Dskip[h] : 0.0f, db = a.dt_bias ? a.dt_bias[h] : 0.0f;
-  for (int64_t t = q.t0; t < q.t1; ++t) {
-    __syncthreads();
-    for (int i = tid; i < 2 * N; i += 256) {
-      const int n = i < N ? i : i - N;
-      const float v = conv_at<IO>(a, q, t, inner + (i < N ? 0 : a.G * N) + g * N + n);
-      (i < N ? sB : sC)[n] = v;
-    }
-    if (tid < 16) sx[tid] = p0 + tid < a.P ? conv_at<IO>(a, q, t, h * a.P + p0 + tid) : 0.0f;
-    __syncthreads();
-    const float raw = ld<IO>(a.dt, t * a.ds + h) + db;
-    const float dt = a.softplus ? softplus(raw) : raw;
-    const float e = ex2(dt * A * kLog2e), x = sx[pl], w = dt * x;
-    float acc = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxN / 16; ++i) {
-      const int n = nl + 16 * i;
-      if (n < N) {
-        hst[i] = fmaf(e, hst[i], w * sB[n]);
-        acc = fmaf(sC[n], hst[i], acc);
-      }
-    }
-    for (int m = 8; m; m >>= 1) acc += __shfl_xor(acc, m, 16);
-    if (nl == 0 && p < a.P) {
-      float v = fmaf(D, x, acc);
-      const int64_t j = (int64_t)h * a.P + p;
-      if (a.z) v *= silu(ld<IO>(a.z, t * a.zs + j));
-      st<IO>(a.y, t * a.ys + j, v);
-    }
-  }
-  if (own && p < a.P) {
-#pragma unroll
-    for (int i = 0; i < kMaxN / 16; ++i) {
-      const int n = nl + 16 * i;
-      if (n < N) own[n] = hst[i];
-    }
-  }
-}
-
-// The last W - 1 inputs of every sequence into its slot, after every reader
-// of the old ones.
-template <typename IO>
-__global__ void __launch_bounds__(256) mix_conv_state_kernel(const MixArgs a) {
-  const int64_t s = blockIdx.x;
-  const int c = blockIdx.y * 256 + threadIdx.x;
-  if (c >= a.C) return;
-  Seq q;
-  if (!load_seq(a, s, q)) return;
-  const int W = a.W;
-  float* own = a.conv_state + (q.slot * a.C + c) * (W - 1);
-  float v[3];
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    if (j >= W - 1) break;
-    const int64_t r = q.t1 - (W - 1) + j;  // row of the input to keep
-    if (r >= q.t0)
-      v[j] = ld<IO>(a.xbc, r * a.xs + c);
-    else
-      v[j] = q.resume ? own[r - q.t0 + W - 1] : 0.0f;
-  }
-#pragma unroll
-  for (int j = 0; j < 3; ++j)
-    if (j < W - 1) own[j] = v[j];
-}
 
 // ---------------------------------------------------------------- packed prompts as block products
 //
@@ -1378,6 +1277,150 @@ __global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- one token a sequence
+//
+// h' = exp(dt A) h + dt x B^T, y = h' C + D x: the state is read and written
+// once, which is all the time there is.  A workgroup owns rows (channels) of one
+// head of one entry, LN lanes a row with four states each, and RPL rows after
+// one another whose loads go out first; meanwhile it makes B, C (again in every
+// workgroup of a group: 4 KB from the cache beside 64 KB of state) and its x
+// from the convolution's inputs.
+
+// Sum over the LN lanes of a row.
+template <int LN>
+__device__ __forceinline__ float lane_sum(float v) {
+  auto add = [&](int o) { v += __int_as_float(o); };
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));
+  if constexpr (LN >= 8) add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
+  if constexpr (LN >= 16) add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
+  if constexpr (LN >= 32) {
+    const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+    v = __uint_as_float(w.x) + __uint_as_float(w.y);
+  }
+  if constexpr (LN >= 64) {
+    const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+    v = __uint_as_float(w.x) + __uint_as_float(w.y);
+  }
+  return v;
+}
+
+// VEC: a lane's states are neighbours (dstate a multiple of 4, the states on 16
+// bytes); else they are 64 apart, any dstate.
+template <typename IO, int LN, int RPL, bool VEC>
+__global__ void __launch_bounds__(256) mix_step_kernel(const MixArgs a, int splits) {
+  constexpr int RW = 256 / LN, ROWS = RW * RPL;
+  static_assert(VEC || LN == 64, "four states a lane, 64 apart");
+  __shared__ __align__(16) float s_bc[2][kMaxN];
+  __shared__ float s_x[ROWS], s_y[ROWS];
+  const int tid = threadIdx.x, ln = tid % LN, rg = tid / LN;
+  const int64_t row = blockIdx.x / ((int64_t)a.H * splits);
+  const int hs = (int)(blockIdx.x - row * a.H * splits), h = hs / splits, p0 = (hs - h * splits) * ROWS;
+  const int64_t slot = a.slots ? (int64_t)a.slots[row] : row;
+  if (slot < 0 || slot >= a.nslots) return;  // padding
+  const int N = a.N, g = h / (a.H / a.G), inner = a.H * a.P, W = a.W;
+  float* own = a.state + ((slot * a.H + h) * a.P + p0) * (int64_t)N;
+  f4 hst[RPL];
+#pragma unroll
+  for (int i = 0; i < RPL; ++i) {
+    const int p = rg + RW * i;
+    hst[i] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (p0 + p < a.P) {
+      if constexpr (VEC) {
+        if (4 * ln < N) hst[i] = *reinterpret_cast<const f4*>(own + (int64_t)p * N + 4 * ln);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (ln + 64 * j < N) hst[i][j] = own[(int64_t)p * N + ln + 64 * j];
+      }
+    }
+  }
+  const float raw = ld<IO>(a.dt, row * a.ds + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
+  const float dt = a.softplus ? softplus(raw) : raw;
+  const float e = ex2(dt * a.A[h] * kLog2e);
+  for (int u = tid; u < 2 * N + ROWS; u += 256) {
+    const int which = u < N ? 0 : u < 2 * N ? 1 : 2, n = u - (which < 2 ? which * N : 2 * N);
+    if (which == 2 && p0 + n >= a.P) break;
+    const int c = which == 2 ? h * a.P + p0 + n : inner + which * a.G * N + g * N + n;
+    float in[4], w[4];
+    float* st = a.conv_state + (slot * a.C + c) * (int64_t)(W - 1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // k: inputs before this one
+      in[k] = k == 0 ? ld<IO>(a.xbc, row * a.xs + c) : k < W ? st[W - 1 - k] : 0.0f;
+      w[k] = k < W ? a.cw[(int64_t)c * W + W - 1 - k] : 0.0f;
+    }
+    float v = a.cb ? a.cb[c] : 0.0f;
+#pragma unroll
+    for (int k = 3; k >= 0; --k)
+      if (k < W) v = fmaf(w[k], in[k], v);
+    v = silu(v);
+    if (which < 2) {
+      s_bc[which][n] = v;
+    } else {
+      s_x[n] = v;  // and this channel's inputs move on by one: nobody else reads them
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < W - 1) st[W - 2 - k] = in[k];
+    }
+  }
+  __syncthreads();
+  float B[4], C[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = VEC ? 4 * ln + j : ln + 64 * j;
+    B[j] = n < N ? s_bc[0][n] : 0.0f;
+    C[j] = n < N ? s_bc[1][n] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < RPL; ++i) {
+    const int p = rg + RW * i;
+    const bool in = p0 + p < a.P;
+    const float wx = in ? dt * s_x[p] : 0.0f;
+    float acc = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hst[i][j] = fmaf(e, hst[i][j], wx * B[j]);
+      acc = fmaf(C[j], hst[i][j], acc);
+    }
+    if (in) {
+      if constexpr (VEC) {
+        if (4 * ln < N) *reinterpret_cast<f4*>(own + (int64_t)p * N + 4 * ln) = hst[i];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (ln + 64 * j < N) own[(int64_t)p * N + ln + 64 * j] = hst[i][j];
+      }
+    }
+    acc = lane_sum<LN>(acc);
+    if (ln == 0) s_y[p] = acc;
+  }
+  __syncthreads();
+  for (int p = tid; p < ROWS; p += 256) {
+    if (p0 + p >= a.P) break;
+    const int64_t j = (int64_t)h * a.P + p0 + p;
+    float v = s_y[p];
+    if (a.Dskip) v = fmaf(a.Dskip[h], s_x[p], v);
+    if (a.z) v *= silu(ld<IO>(a.z, row * a.zs + j));
+    st<IO>(a.y, row * a.ys + j, v);
+  }
+}
+
+// The inputs of B and C move on by one, after every reader of the old ones.
+template <typename IO>
+__global__ void __launch_bounds__(256) mix_step_conv_kernel(const MixArgs a) {
+  const int64_t row = blockIdx.x;
+  const int c = a.H * a.P + blockIdx.y * 256 + threadIdx.x, W = a.W;
+  const int64_t slot = a.slots ? (int64_t)a.slots[row] : row;
+  if (c >= a.C || slot < 0 || slot >= a.nslots) return;
+  float* st = a.conv_state + (slot * a.C + c) * (int64_t)(W - 1);
+  float v[3];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) v[j] = j + 1 < W - 1 ? st[j + 1] : j + 1 == W - 1 ? ld<IO>(a.xbc, row * a.xs + c) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    if (j < W - 1) st[j] = v[j];
+}
+
 // ---------------------------------------------------------------- group norm
 
 struct NormArgs {
@@ -1985,11 +2028,36 @@ void launch_mix(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
   }
 }
 
+// Eight rows a lane where that leaves two workgroups for every CU, two where
+// the card would stand half empty.
+constexpr int64_t kStepWorkgroups = 512;
+
+template <typename IO, int LN, bool VEC>
+int launch_step(const MixArgs& a, hipStream_t s) {
+  auto go = [&](auto rpl) {
+    constexpr int R = decltype(rpl)::value, rows = 256 / LN * R;
+    const int splits = (a.P + rows - 1) / rows;
+    const int64_t grid = a.nseq * a.H * splits;
+    if (grid > 0x7fffffff) return fail(SSM_E_SHAPE, "too many entries and heads for one call");
+    mix_step_kernel<IO, LN, R, VEC><<<(unsigned)grid, 256, 0, s>>>(a, splits);
+    return (int)SSM_OK;
+  };
+  const int64_t wide = a.nseq * a.H * ((a.P + 256 / LN * 8 - 1) / (256 / LN * 8));
+  const int st = wide >= kStepWorkgroups ? go(std::integral_constant<int, 8>{}) : go(std::integral_constant<int, 2>{});
+  if (st) return st;
+  if (a.W > 1)
+    mix_step_conv_kernel<IO><<<dim3((unsigned)a.nseq, (unsigned)((2 * a.G * a.N + 255) / 256)), 256, 0, s>>>(a);
+  return launch_status("ssm_conv_ssd_update launch");
+}
+
 template <typename IO>
-void launch_mix_simple(const MixArgs& a, hipStream_t s) {
-  mix_scan_kernel<IO><<<dim3((unsigned)a.nseq, a.H, (a.P + 15) / 16), 256, 0, s>>>(a);
-  if (a.state && a.W > 1)
-    mix_conv_state_kernel<IO><<<dim3((unsigned)a.nseq, (a.C + 255) / 256), 256, 0, s>>>(a);
+int launch_step_io(const MixArgs& a, hipStream_t s) {
+  if (a.N % 4 || !aligned16(a.state)) return launch_step<IO, 64, false>(a, s);
+  if (a.N <= 16) return launch_step<IO, 4, true>(a, s);
+  if (a.N <= 32) return launch_step<IO, 8, true>(a, s);
+  if (a.N <= 64) return launch_step<IO, 16, true>(a, s);
+  if (a.N <= 128) return launch_step<IO, 32, true>(a, s);
+  return launch_step<IO, 64, true>(a, s);
 }
 
 // Strips of rows whose column sums are kept apart, at most: three waves for every
@@ -2172,9 +2240,7 @@ int ssm_conv_ssd_update(const void* xbc, int64_t xbc_stride, const void* dt, int
                            io_dtype, nullptr, 0);
   if (st) return st;
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (io_dtype == SSM_DTYPE_BF16) launch_mix_simple<uint16_t>(a, s);
-  else launch_mix_simple<float>(a, s);
-  return launch_status("ssm_conv_ssd_update launch");
+  return io_dtype == SSM_DTYPE_BF16 ? launch_step_io<uint16_t>(a, s) : launch_step_io<float>(a, s);
 }
 
 int ssm_group_norm_fwd(const void* x, int64_t x_stride, const void* z, int64_t z_stride,
