@@ -495,33 +495,33 @@ _ACT = {"none": 0, "silu": 1}
 _GATE = {"none": 0, "before": 1, "after": 2}
 
 
+# These run before every call of a decode loop, so they ask in the cheapest way
+# first (get_device() is an int, dtypes are singletons) and name what is wrong after.
+
 def _rows(t, name, dtype, rows, cols, dev):
-    """A [rows, cols] tensor whose rows may be slices of wider ones."""
+    """A [rows, cols] tensor whose rows may be slices of wider ones; its row
+    stride (one row has none of its own)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
+    if t.get_device() != dev.index:
         _dev(t, name, dev)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if cols > 1 and t.stride(1) != 1:
+    stride, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t
-
-
-def _stride(t):
-    """The row stride that the library checks (one row has none)."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return stride if rows > 1 else cols
 
 
 def _flat(t, name, dtype, shape, dev):
-    """A dense tensor of this exact shape, or None."""
+    """Address of a dense tensor of this exact shape, or None."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev.index or not t.is_contiguous():
         _dev(t, name, dev)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -531,9 +531,9 @@ def _flat(t, name, dtype, shape, dev):
 def _launch(dev, f, *args):
     """Calls f(*args, stream) with the tensors' device current."""
     if torch.cuda.current_device() == dev.index:
-        return f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        return f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     with torch.cuda.device(dev):
-        return f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        return f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 def _row_input(t, name):
@@ -587,14 +587,12 @@ def ssm_conv_ssd_fwd(xbc, dt, conv_weight, A, cu_seqlens, headdim, ngroups, conv
     if ch <= inner or ngroups < 1 or (ch - inner) % (2 * ngroups):
         raise ValueError(f"xbc has {ch} channels: expected nheads * headdim + 2 * ngroups * dstate")
     N = (ch - inner) // (2 * ngroups)
-    _rows(xbc, "xbc", io, rows, ch, dev)
-    _rows(dt, "dt", io, rows, H, dev)
-    if z is not None:
-        _rows(z, "z", io, rows, inner, dev)
+    xs = _rows(xbc, "xbc", io, rows, ch, dev)
+    ds = _rows(dt, "dt", io, rows, H, dev)
+    zs = 0 if z is None else _rows(z, "z", io, rows, inner, dev)
     if y is None:
         y = torch.empty((rows, inner), dtype=io, device=dev)
-    else:
-        _rows(y, "y", io, rows, inner, dev)
+    ys = _rows(y, "y", io, rows, inner, dev)
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be [nseq + 1]")
     nseq = cu_seqlens.shape[0] - 1
@@ -602,7 +600,7 @@ def ssm_conv_ssd_fwd(xbc, dt, conv_weight, A, cu_seqlens, headdim, ngroups, conv
     if has_state is not None and has_state.dtype == torch.bool:
         has_state = has_state.view(torch.uint8)
     f32 = torch.float32
-    args = (xbc.data_ptr(), _stride(xbc), dt.data_ptr(), _stride(dt), _ptr(z), _stride(z),
+    args = (xbc.data_ptr(), xs, dt.data_ptr(), ds, _ptr(z), zs,
             _flat(conv_weight, "conv_weight", f32, (ch, W), dev),
             _flat(conv_bias, "conv_bias", f32, (ch,), dev), _flat(A, "A", f32, (H,), dev),
             _flat(D, "D", f32, (H,), dev), _flat(dt_bias, "dt_bias", f32, (H,), dev),
@@ -610,8 +608,7 @@ def ssm_conv_ssd_fwd(xbc, dt, conv_weight, A, cu_seqlens, headdim, ngroups, conv
             _flat(slots, "slots", torch.int32, (nseq,), dev),
             _flat(has_state, "has_state", torch.uint8, (nseq,), dev),
             _flat(conv_state, "conv_state", f32, (nslots, ch, W - 1), dev),
-            _flat(ssm_state, "ssm_state", f32, (nslots, H, headdim, N), dev), y.data_ptr(),
-            _stride(y))
+            _flat(ssm_state, "ssm_state", f32, (nslots, H, headdim, N), dev), y.data_ptr(), ys)
     L = lib()
     ws, nbytes = _workspace(workspace, L.ssm_conv_ssd_workspace_size(
         rows, nseq, H, headdim, ngroups, N, _IO[io]), dev)
@@ -632,40 +629,36 @@ def ssm_conv_ssd_update(xbc, dt, conv_state, ssm_state, conv_weight, A, ngroups,
     nslots, H, P, N = ssm_state.shape
     inner = H * P
     W = conv_weight.shape[-1]
-    _rows(xbc, "xbc", io, rows, inner + 2 * ngroups * N, dev)
-    _rows(dt, "dt", io, rows, H, dev)
-    if z is not None:
-        _rows(z, "z", io, rows, inner, dev)
+    xs = _rows(xbc, "xbc", io, rows, inner + 2 * ngroups * N, dev)
+    ds = _rows(dt, "dt", io, rows, H, dev)
+    zs = 0 if z is None else _rows(z, "z", io, rows, inner, dev)
     if y is None:
         y = torch.empty((rows, inner), dtype=io, device=dev)
-    else:
-        _rows(y, "y", io, rows, inner, dev)
+    ys = _rows(y, "y", io, rows, inner, dev)
     f32 = torch.float32
-    st = _launch(dev, lib().ssm_conv_ssd_update, xbc.data_ptr(), _stride(xbc), dt.data_ptr(),
-                 _stride(dt), _ptr(z), _stride(z),
+    st = _launch(dev, lib().ssm_conv_ssd_update, xbc.data_ptr(), xs, dt.data_ptr(), ds, _ptr(z), zs,
                  _flat(conv_weight, "conv_weight", f32, (ch, W), dev),
                  _flat(conv_bias, "conv_bias", f32, (ch,), dev), _flat(A, "A", f32, (H,), dev),
                  _flat(D, "D", f32, (H,), dev), _flat(dt_bias, "dt_bias", f32, (H,), dev),
                  int(bool(dt_softplus)), _flat(slots, "slots", torch.int32, (rows,), dev),
                  _flat(conv_state, "conv_state", f32, (nslots, ch, W - 1), dev),
                  _flat(ssm_state, "ssm_state", f32, (nslots, H, P, N), dev), y.data_ptr(),
-                 _stride(y), rows, nslots, H, P, ngroups, N, W, _IO[io])
+                 ys, rows, nslots, H, P, ngroups, N, W, _IO[io])
     check(st, "ssm_conv_ssd_update")
     return y
 
 
-def _norm_args(x, weight, ngroups, bias, z, activation, gate):
+def _norm_args(x, weight, bias, z, activation, gate):
     rows, C, io, dev = _row_input(x, "x")
-    _rows(x, "x", io, rows, C, dev)
+    xs = _rows(x, "x", io, rows, C, dev)
     if activation not in _ACT:
         raise ValueError(f"activation {activation!r}: expected one of {sorted(_ACT)}")
     if gate not in _GATE:
         raise ValueError(f"gate {gate!r}: expected one of {sorted(_GATE)}")
-    if z is not None:
-        _rows(z, "z", io, rows, C, dev)
+    zs = 0 if z is None else _rows(z, "z", io, rows, C, dev)
     w = _flat(weight, "weight", torch.float32, (C,), dev)
     b = _flat(bias, "bias", torch.float32, (C,), dev)
-    return rows, C, io, dev, w, b
+    return rows, C, io, dev, (x.data_ptr(), xs, _ptr(z), zs, w, b)
 
 
 def ssm_group_norm_fwd(x, weight, ngroups, bias=None, z=None, eps=1e-5, center=False,
@@ -675,14 +668,12 @@ def ssm_group_norm_fwd(x, weight, ngroups, bias=None, z=None, eps=1e-5, center=F
     0 unless center), times weight, plus bias, through the activation ("none"
     or "silu"), times silu(z) for gate "after".  x, z, y [rows, channels], rows
     may be slices of wider ones; weight, bias [channels] float32 or None."""
-    rows, C, io, dev, w, b = _norm_args(x, weight, ngroups, bias, z, activation, gate)
+    rows, C, io, dev, ins = _norm_args(x, weight, bias, z, activation, gate)
     if y is None:
         y = torch.empty((rows, C), dtype=io, device=dev)
-    else:
-        _rows(y, "y", io, rows, C, dev)
-    st = _launch(dev, lib().ssm_group_norm_fwd, x.data_ptr(), _stride(x), _ptr(z), _stride(z), w, b,
-                 eps, int(bool(center)), _ACT[activation], _GATE[gate], y.data_ptr(), _stride(y),
-                 rows, C, ngroups, _IO[io])
+    ys = _rows(y, "y", io, rows, C, dev)
+    st = _launch(dev, lib().ssm_group_norm_fwd, *ins, eps, int(bool(center)), _ACT[activation],
+                 _GATE[gate], y.data_ptr(), ys, rows, C, ngroups, _IO[io])
     check(st, "ssm_group_norm_fwd")
     return y
 
@@ -699,17 +690,16 @@ def ssm_group_norm_bwd(dy, x, weight, ngroups, bias=None, z=None, eps=1e-5, cent
                        activation="none", gate="none", workspace=None):
     """Gradients of ssm_group_norm_fwd for sum(dy * y): dict dx, dz (if z),
     dweight (if weight), dbias (if bias)."""
-    rows, C, io, dev, w, b = _norm_args(x, weight, ngroups, bias, z, activation, gate)
-    _rows(dy, "dy", io, rows, C, dev)
+    rows, C, io, dev, ins = _norm_args(x, weight, bias, z, activation, gate)
+    gs = _rows(dy, "dy", io, rows, C, dev)
     L = lib()
     ws, nbytes = _workspace(workspace, L.ssm_group_norm_bwd_workspace_size(rows, C, ngroups), dev)
     g = dict(dx=torch.empty((rows, C), dtype=io, device=dev),
              dz=torch.empty((rows, C), dtype=io, device=dev) if z is not None else None,
              dweight=torch.empty(C, dtype=torch.float32, device=dev) if weight is not None else None,
              dbias=torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None)
-    st = _launch(dev, L.ssm_group_norm_bwd, dy.data_ptr(), _stride(dy), x.data_ptr(), _stride(x),
-                 _ptr(z), _stride(z), w, b, eps, int(bool(center)), _ACT[activation], _GATE[gate],
-                 _ptr(g["dx"]), C, _ptr(g["dz"]), C, _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(ws),
+    st = _launch(dev, L.ssm_group_norm_bwd, dy.data_ptr(), gs, *ins, eps, int(bool(center)),
+                 _ACT[activation], _GATE[gate], _ptr(g["dx"]), C, _ptr(g["dz"]), C, _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(ws),
                  nbytes, rows, C, ngroups, _IO[io])
     check(st, "ssm_group_norm_bwd")
     return g

@@ -71,28 +71,6 @@ struct MixArgs {
   int softplus;
 };
 
-// Sequence s: its rows [t0, t1), its slot and whether it starts from that
-// slot's state.  Whatever the index tensors hold, the rows lie inside the
-// tensors; false for a sequence whose slot is outside the cache (padding).
-struct Seq {
-  int64_t t0, t1, slot;
-  bool resume;
-};
-__device__ __forceinline__ bool load_seq(const MixArgs& a, int64_t s, Seq& q) {
-  if (a.cu) {
-    const int64_t b = a.cu[s], e = a.cu[s + 1];
-    q.t0 = b < 0 ? 0 : (b > a.tokens ? a.tokens : b);
-    q.t1 = e < q.t0 ? q.t0 : (e > a.tokens ? a.tokens : e);
-  } else {
-    q.t0 = s;
-    q.t1 = s + 1;
-  }
-  q.slot = a.slots ? (int64_t)a.slots[s] : s;
-  if (a.state && (q.slot < 0 || q.slot >= a.nslots)) return false;
-  q.resume = a.state && (a.cu ? (a.has && a.has[s]) : true);
-  return true;
-}
-
 constexpr int kMaxN = 256;
 
 // ---------------------------------------------------------------- packed prompts as block products
@@ -135,20 +113,20 @@ constexpr int kTri = 6;  // 16 x 32 tiles of M on or below the diagonal
 struct Chunk {
   int r0, r1;  // rows [r0, r1)
   int t0;      // the sequence's first row
-  int seq;     // -1: resumes nothing (see resume)
+  int from;    // the slot whose inputs come before it, or -1
 };
 // consecutive blocks of one sequence
 struct Seg {
-  int seq, t0, t1;  // the sequence and its rows
-  int c0, nc;       // its blocks [c0, c0 + nc) of the sequence
-  int gc;           // place of the first of them among all blocks
-  int split;        // segments before this one among those of cut sequences; -1: not cut
-  int cut;          // cut sequences before this one
+  int slot, t0, t1;  // the sequence's slot and rows
+  int c0, nc;        // its blocks [c0, c0 + nc) of the sequence
+  int gc;            // place of the first of them among all blocks
+  int split;         // segments before this one among those of cut sequences; -1: not cut
+  int cut;           // cut sequences before this one
+  int resume;        // the sequence starts from its slot
 };
-
 // A cut sequence: its segments' places among those of cut sequences.
 struct Cut {
-  int seq, split, nseg, pad;
+  int slot, split, nseg, resume;
 };
 
 struct PlanHead {
@@ -277,35 +255,42 @@ __device__ __forceinline__ h8 piece(const float* v) {
 
 // ---- the plan: sequences -> blocks and segments (one workgroup)
 
-__device__ __forceinline__ int block_scan(int v, int* red, int& total) {  // exclusive, 1024 threads
+// Exclusive sums over the workgroup of four values at once, and their totals.
+typedef int i4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i4 block_scan(i4 v, i4* red, i4& total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int x = v;
+  i4 x = v;
+#pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(x, d, 64);
+    i4 o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = __shfl_up(x[k], d, 64);
     if (lane >= d) x += o;
   }
-  __syncthreads();
   if (lane == 63) red[w] = x;
   __syncthreads();
-  int before = 0, all = 0;
+  i4 before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
+#pragma unroll
   for (int i = 0; i < 16; ++i) {
-    if (i < w) before += red[i];
-    all += red[i];
+    const i4 r = red[i];
+    if (i < w) before += r;
+    all += r;
   }
   total = all;
   return before + x - v;
 }
-
 __device__ __forceinline__ int block_scan_max(int v, int* red) {  // inclusive, v >= 0
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int o = __shfl_up(v, d, 64);
     if (lane >= d) v = max(v, o);
   }
-  __syncthreads();
   if (lane == 63) red[w] = v;
   __syncthreads();
-  for (int i = 0; i < w; ++i) v = max(v, red[i]);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < w) v = max(v, red[i]);
   return v;
 }
 
@@ -319,51 +304,56 @@ __device__ __forceinline__ int find(const int* prefix, int i) {
 }
 
 __global__ void __launch_bounds__(1024) mix_plan_kernel(const BlkArgs a) {
-  __shared__ int red[16], top;
-  __shared__ int s_t0[1024], s_t1[1024], s_chunk[1024], s_seg[1024], s_split[1024], s_cut[1024];
+  __shared__ int red[16];
+  __shared__ i4 red4[16];
+  __shared__ int s_t0[1024], s_t1[1024], s_slot[1024], s_chunk[1024], s_seg[1024], s_split[1024], s_cut[1024];
   int nchunk = 0, nseg = 0, nsplit = 0, ncut = 0;
-  const int i = threadIdx.x;
-  int reached = max(0, min(a.cu[0], (int)a.tokens));  // the largest offset so far
+  const int i = threadIdx.x, tokens = (int)a.tokens;
+  int reached = max(0, min(a.cu[0], tokens));  // the largest offset so far
   for (int64_t base = 0; base < a.nseq; base += 1024) {
     // the offsets' running maximum: whatever they hold, the sequences lie one
     // behind the other inside the rows, and the tables hold their blocks
     const int64_t s = base + i;
-    int end = s < a.nseq ? max(reached, min(a.cu[s + 1], (int)a.tokens)) : reached;
+    const bool in = s < a.nseq;
+    const int64_t slot = in && a.slots ? a.slots[s] : s;
+    const bool resume = in && a.has && a.has[s];
+    int end = in ? max(reached, min(a.cu[s + 1], tokens)) : reached;
     end = block_scan_max(end, red);
-    __syncthreads();
     s_t1[i] = end;
-    if (i == 1023) top = end;
     __syncthreads();
     const int begin = i ? s_t1[i - 1] : reached;
-    reached = top;
+    reached = s_t1[1023];
     s_t0[i] = begin;
-    Seq q;
-    int nc = 0, ns = 0;
-    if (s < a.nseq && load_seq(a, s, q)) {
-      nc = (end - begin + kQ - 1) / kQ;
-      ns = nc ? (nc + a.seg_len - 1) / a.seg_len : 1;
+    i4 n = {0, 0, 0, 0};  // blocks, segments, segments of cut sequences, cut sequences
+    if (in && (!a.state || (slot >= 0 && slot < a.nslots))) {  // else padding
+      n[0] = (end - begin + kQ - 1) / kQ;
+      n[1] = n[0] ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
+      n[2] = n[1] > 1 ? n[1] : 0;
+      n[3] = n[1] > 1;
     }
-    int chunks, segs, splits, cuts;
-    s_chunk[i] = block_scan(nc, red, chunks);
-    s_seg[i] = block_scan(ns, red, segs);
-    s_split[i] = nsplit + block_scan(ns > 1 ? ns : 0, red, splits);
-    s_cut[i] = ncut + block_scan(ns > 1, red, cuts);
-    if (ns > 1) a.cuts[s_cut[i]] = {(int)s, s_split[i], ns, 0};
+    i4 all;
+    const i4 at = block_scan(n, red4, all);
+    s_slot[i] = (int)slot | (resume ? (int)0x80000000 : 0);
+    s_chunk[i] = at[0];
+    s_seg[i] = at[1];
+    s_split[i] = nsplit + at[2];
+    s_cut[i] = ncut + at[3];
+    if (n[3]) a.cuts[ncut + at[3]] = {(int)slot, nsplit + at[2], n[1], resume};
     __syncthreads();
-    for (int c = i; c < chunks; c += 1024) {
-      const int k = find(s_chunk, c), r0 = s_t0[k] + (c - s_chunk[k]) * kQ;
-      a.chunks[nchunk + c] = {r0, min(s_t1[k], r0 + kQ), s_t0[k], (int)(base + k)};
+    for (int c = i; c < all[0]; c += 1024) {
+      const int k = find(s_chunk, c), r0 = s_t0[k] + (c - s_chunk[k]) * kQ, f = s_slot[k];
+      a.chunks[nchunk + c] = {r0, min(s_t1[k], r0 + kQ), s_t0[k], f < 0 ? f & 0x7fffffff : -1};
     }
-    for (int g = i; g < segs; g += 1024) {
-      const int k = find(s_seg, g), n = (s_t1[k] - s_t0[k] + kQ - 1) / kQ, of = n ? (n + a.seg_len - 1) / a.seg_len : 1;
-      const int j = g - s_seg[k], lo = (int)((int64_t)n * j / of), hi = (int)((int64_t)n * (j + 1) / of);
-      a.segs[nseg + g] = {(int)(base + k), s_t0[k], s_t1[k], lo, hi - lo, nchunk + s_chunk[k] + lo,
-                          of > 1 ? s_split[k] + j : -1, s_cut[k]};
+    for (int g = i; g < all[1]; g += 1024) {
+      const int k = find(s_seg, g), nb = (s_t1[k] - s_t0[k] + kQ - 1) / kQ, of = nb ? (nb + a.seg_len - 1) / a.seg_len : 1;
+      const int j = g - s_seg[k], lo = (int)((int64_t)nb * j / of), hi = (int)((int64_t)nb * (j + 1) / of);
+      a.segs[nseg + g] = {s_slot[k] & 0x7fffffff, s_t0[k], s_t1[k], lo, hi - lo, nchunk + s_chunk[k] + lo,
+                          of > 1 ? s_split[k] + j : -1, s_cut[k], s_slot[k] < 0};
     }
-    nchunk += chunks;
-    nseg += segs;
-    nsplit += splits;
-    ncut += cuts;
+    nchunk += all[0];
+    nseg += all[1];
+    nsplit += all[2];
+    ncut += all[3];
     __syncthreads();
   }
   if (i == 0) *a.head = {nseg, nchunk, ncut, 0};
@@ -371,29 +361,34 @@ __global__ void __launch_bounds__(1024) mix_plan_kernel(const BlkArgs a) {
 
 // ---- the operands of one block and group
 
+constexpr int kPrep = 1024;  // threads: one round of loads up to 128 states
+
 template <typename IO, int NT, int NPC>
-__global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
-  constexpr int NP = NT * 16, LD = NP + 8;  // row pitch in LDS: 16 bytes more, banks apart
-  constexpr int UN = (NP + 31) / 32;        // (channel, 16 rows) units of a thread
+__global__ void __launch_bounds__(kPrep) mix_prep_kernel(const BlkArgs a) {
+  constexpr int NP = NT * 16, LD = NP + 8;         // row pitch in LDS: 16 bytes more, banks apart
+  constexpr int UN = (8 * NP + kPrep - 1) / kPrep;  // (channel, 16 rows) units of a thread
   using O = Ops<NT, NPC>;
   __shared__ __align__(16) _Float16 sm[2][2][kQ * LD];  // [B, C][hi, lo]
-  __shared__ float red[2][4];
+  __shared__ float red[2][16];
+  const Chunk ck = a.chunks[blockIdx.x];  // garbage past the last one, which ends here
   if ((int)blockIdx.x >= a.head->nchunk) return;
-  const Chunk ck = a.chunks[blockIdx.x];
   const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int inner = a.H * a.P, W = a.W;
-  const bool resume = a.state && a.has && a.has[ck.seq];
-  const int64_t slot = a.slots ? a.slots[ck.seq] : ck.seq;
+  const bool resume = ck.from >= 0;
+  const int64_t slot = ck.from;
   float v[UN][16], mx[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < UN; ++i) {
-    const int u = tid + 256 * i, chn = u % (2 * NP), run = u / (2 * NP), which = chn / NP, n = chn % NP;
+    const int u = tid + kPrep * i, chn = u % (2 * NP), run = u / (2 * NP), which = chn / NP, n = chn % NP;
     const bool on = n < a.N && run < 4;
     const int c = inner + which * a.G * a.N + g * a.N + (on ? n : 0);
     // rows outside the block or the sequence are read from inside and replaced,
     // so that the loads of all rows are in flight together
-    float in[19];
+    float in[19], w[4];
     const int lo = ck.r0 + 16 * run - 3, top = ck.r1 - 1;
+    const float bias = a.cb ? a.cb[c] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = a.cw[(int64_t)c * W + max(W - 4 + k, 0)];
 #pragma unroll
     for (int j = 0; j < 19; ++j)
       in[j] = ld<IO>(a.xbc, (int64_t)max(min(lo + j, top), ck.t0) * a.xs + c);
@@ -404,16 +399,13 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
       for (int j = 0; j < 3; ++j)
         if (j - 3 + W - 1 >= 0) in[j] = a.conv_state[(slot * a.C + c) * (W - 1) + j - 3 + W - 1];
     }
-    const float bias = on && a.cb ? a.cb[c] : 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[i][j] = bias;
 #pragma unroll
-    for (int k = 3; k >= 0; --k) {  // the newest tap last in memory, taken first
-      if (3 - k >= W) break;
-      const float w = on ? a.cw[(int64_t)c * W + (W - 1) - (3 - k)] : 0.0f;
+    for (int k = 3; k >= 0; --k)  // the newest tap first
+      if (3 - k < W)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[i][j] = fmaf(w, in[j + k], v[i][j]);
-    }
+        for (int j = 0; j < 16; ++j) v[i][j] = fmaf(w[k], in[j + k], v[i][j]);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float x = on && ck.r0 + 16 * run + j < ck.r1 ? silu(v[i][j]) : 0.0f;
@@ -428,10 +420,15 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
   int sh[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    sh[k] = shift_for(fmaxf(fmaxf(red[k][0], red[k][1]), fmaxf(red[k][2], red[k][3])));
+  {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPrep / 64; ++i) m = fmaxf(m, red[k][i]);
+    sh[k] = shift_for(m);
+  }
 #pragma unroll
   for (int i = 0; i < UN; ++i) {
-    const int u = tid + 256 * i, chn = u % (2 * NP), run = u / (2 * NP), which = chn / NP, n = chn % NP;
+    const int u = tid + kPrep * i, chn = u % (2 * NP), run = u / (2 * NP), which = chn / NP, n = chn % NP;
     if (run >= 4) continue;
     const float f = two(sh[which]);
 #pragma unroll
@@ -446,7 +443,7 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
   char* out = a.ops + ((int64_t)blockIdx.x * a.G + g) * O::bytes;
   // C: lane (t, q) of tile (tt, m) holds n = 32 m + 4 q + {0..3} and 16 more,
   // the order in which the state's accumulators hold n
-  for (int u = tid; u < 4 * (NT / 2) * 64; u += 256) {
+  for (int u = tid; u < 4 * (NT / 2) * 64; u += kPrep) {
     const int l = u & 63, m = (u >> 6) % (NT / 2), tt = (u >> 6) / (NT / 2);
 #pragma unroll
     for (int p = 0; p < NPC; ++p) {
@@ -459,7 +456,7 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
     }
   }
   // B transposed: lane (n, q) of tile (nt, kb) holds t = 32 kb + 8 q + {0..7}
-  for (int u = tid; u < NT * 2 * 64; u += 256) {
+  for (int u = tid; u < NT * 2 * 64; u += kPrep) {
     const int l = u & 63, kb = (u >> 6) & 1, nt = u >> 7;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
@@ -470,6 +467,7 @@ __global__ void __launch_bounds__(256) mix_prep_kernel(const BlkArgs a) {
       *reinterpret_cast<h8*>(out + O::b + p * O::piece + u * 16) = o;
     }
   }
+  if (wave >= 4) return;
   // C.B^T: wave w has the rows t of tile w; the rows s of B are taken in the order
   // that leaves lane (t, q) with s = 32 kb + 8 q + {0..7}
   f4 acc[2][2] = {};
@@ -629,16 +627,16 @@ mix_block_kernel(const BlkArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i16 = lane & 15, q4 = lane >> 4;
   const int si = blockIdx.x / a.units, unit = blockIdx.x % a.units;
+  const Seg sg = a.segs[si];  // garbage past the last one, which ends here
   if (si >= a.head->nseg) return;
-  const Seg sg = a.segs[si];
   if (SUM && (sg.split < 0 || sg.c0 + sg.nc == (sg.t1 - sg.t0 + kQ - 1) / kQ)) return;  // no state asked
   const int g = unit / a.per_group, hpg = a.H / a.G, bph = (a.P + PB - 1) / PB;
   const int blk = (unit % a.per_group) * WV + wave;
   const bool on = blk < hpg * bph;  // else the wave only helps to stage
   const bool last = sg.t0 + (int64_t)(sg.c0 + sg.nc) * kQ >= sg.t1;
   const int inner = a.H * a.P, W = a.W, N = a.N;
-  const bool resume = a.state && a.has && a.has[sg.seq];
-  const int64_t slot = a.slots ? a.slots[sg.seq] : sg.seq;
+  const bool resume = sg.resume;
+  const int64_t slot = sg.slot;
   // the last inputs of B and C into the slot: nobody reads the old ones any more
   if (!SUM && last && a.state && W > 1 && unit % a.per_group == 0) {
     for (int u = threadIdx.x; u < 2 * N; u += 64 * WV)
@@ -1240,8 +1238,8 @@ __global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
   const Cut ct = a.cuts[blockIdx.x];
   const int64_t per = (int64_t)a.H * a.P * a.N;
   const int hs = a.P * a.N;  // values of a head
-  const bool resume = a.state && a.has && a.has[ct.seq];
-  const int64_t slot = a.slots ? a.slots[ct.seq] : ct.seq;
+  const bool resume = ct.resume;
+  const int64_t slot = ct.slot;
   const float* d = a.decay + (int64_t)ct.split * a.H;
   constexpr int V = 4, K = 4;
   int64_t at[V];
@@ -2003,7 +2001,7 @@ void launch_mix_blocks(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
   static_assert(Ops<NT, PC>::bytes == (PC + 2) * kQ * NT * 32 + kTri * 64 * 8 * (PC == 1 ? 2 : 4) + 320,
                 "as in mix_layout");
   mix_plan_kernel<<<1, 1024, 0, s>>>(b);
-  mix_prep_kernel<IO, NT, PC><<<dim3((unsigned)l.nchunk, b.G), 256, 0, s>>>(b);
+  mix_prep_kernel<IO, NT, PC><<<dim3((unsigned)l.nchunk, b.G), kPrep, 0, s>>>(b);
   const unsigned grid = (unsigned)(l.nseg * l.units);
   auto walk = [&](auto fast) {
     constexpr bool F = decltype(fast)::value;
