@@ -139,11 +139,12 @@ struct BlkArgs : MixArgs {
   Seg* segs;
   Cut* cuts;
   char* ops;       // operands of (block, group)
-  float* local;    // [split][H, P, N] state of a segment from zero, then the state entering it
-  float* decay;    // [split][H] log2 of a segment's whole decay
+  float* local;    // [split * sub][H, P, N] state of a piece from zero; of the first, then the state entering the segment
+  float* decay;    // [split * sub][H] log2 of a piece's whole decay
   float* cs0;      // [cut][inner, 3] what the first rows of a cut sequence start from
   int64_t op_bytes;
   int seg_len;     // blocks of a segment at most
+  int sub;         // pieces of a segment in the first pass
   int units;       // workgroups a segment needs
   int per_group;   // of them per group
   int fast;
@@ -582,7 +583,7 @@ template <int PT>
 struct XTile {
   static constexpr int RB = 32 * PT, RI = 1024 / RB, GP = RI / 8;  // bytes of a row, rows and groups a load
   static constexpr int step = PT == 2 ? 1152 : 1024, loads = (kQ + 3 + RI - 1) / RI;
-  static constexpr int bytes = PT == 2 ? 5120 : 3072;
+  static constexpr int bytes = PT == 2 ? 4928 : 3072;
   static_assert((loads - 1) * step + ((kQ + 2) % 8 * GP + 1) * RB <= bytes, "the last rows fit");
   // bytes of row 8 a + b
   __device__ static __forceinline__ int at(int a, int b) { return a / GP * step + (GP * b + a % GP) * RB; }
@@ -611,7 +612,7 @@ struct XRaw {
 // the operands of y.  FAST: rows and channels allow whole vectors (headdim a
 // multiple of 4 PT, dstate of 4, rows aligned to the accesses).
 template <typename IO, int NT, int PT, int PC, int WV, bool SUM, bool FAST>
-__global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(2)))
 mix_block_kernel(const BlkArgs a) {
   using O = Ops<NT, PC>;
   constexpr int PB = 16 * PT;  // channels of a wave
@@ -621,15 +622,26 @@ mix_block_kernel(const BlkArgs a) {
   constexpr bool XLDS = FAST && sizeof(IO) == 2;
   using X = XTile<PT>;
   __shared__ __align__(16) char s_x[XLDS ? WV * X::bytes : 16];
-  __shared__ __align__(16) int s_sc[2][68];
-  __shared__ __align__(16) float s_cum[WV][64], s_lo[PC == 2 ? WV : 1][64], s_dt[WV][64], s_w[WV][64];
-  __shared__ int s_bad[WV][PB];
+  __shared__ __align__(16) int s_sc[SUM ? 1 : 2][68];
+  __shared__ __align__(16) float s_w[WV][64];
+  // for y alone
+  __shared__ __align__(16) float s_cum[SUM ? 1 : WV][SUM ? 4 : 64], s_dt[SUM ? 1 : WV][SUM ? 4 : 64];
+  __shared__ __align__(16) float s_lo[!SUM && PC == 2 ? WV : 1][!SUM && PC == 2 ? 64 : 4];
+  __shared__ int s_bad[SUM ? 1 : WV][SUM ? 4 : PB];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i16 = lane & 15, q4 = lane >> 4;
-  const int si = blockIdx.x / a.units, unit = blockIdx.x % a.units;
-  const Seg sg = a.segs[si];  // garbage past the last one, which ends here
+  const int sub = SUM ? a.sub : 1;
+  const int si = blockIdx.x / (a.units * sub), unit = blockIdx.x % a.units;
+  Seg sg = a.segs[si];  // garbage past the last one, which ends here
   if (si >= a.head->nseg) return;
   if (SUM && (sg.split < 0 || sg.c0 + sg.nc == (sg.t1 - sg.t0 + kQ - 1) / kQ)) return;  // no state asked
+  const int piece_of = SUM ? (int)(blockIdx.x / a.units) % sub : 0;
+  if constexpr (SUM) {  // a piece of the segment's blocks
+    const int lo = sg.nc * piece_of / sub, hi = sg.nc * (piece_of + 1) / sub;
+    sg.c0 += lo;
+    sg.gc += lo;
+    sg.nc = hi - lo;
+  }
   const int g = unit / a.per_group, hpg = a.H / a.G, bph = (a.P + PB - 1) / PB;
   const int blk = (unit % a.per_group) * WV + wave;
   const bool on = blk < hpg * bph;  // else the wave only helps to stage
@@ -663,7 +675,7 @@ mix_block_kernel(const BlkArgs a) {
   f4 S[PT][NT];
   {
     const float* src = nullptr;
-    if (sg.split >= 0 && sg.c0 > 0) src = SUM ? nullptr : a.local + (int64_t)sg.split * inner * N;
+    if (sg.split >= 0 && sg.c0 > 0) src = SUM ? nullptr : a.local + (int64_t)sg.split * a.sub * inner * N;
     else if (!SUM && resume) src = a.state + slot * inner * N;
 #pragma unroll
     for (int e = 0; e < PT; ++e)
@@ -861,8 +873,8 @@ mix_block_kernel(const BlkArgs a) {
       shw = -__builtin_amdgcn_frexp_expf(wmax);
       shw = shw < -112 ? -112 : (shw > 60 ? 60 : shw);
       dsum += tot;
-      s_cum[wave][lane] = (float)cum;
-      if constexpr (PC == 2) s_lo[wave][lane] = (float)(cum - (double)(float)cum);
+      if constexpr (!SUM) s_cum[wave][lane] = (float)cum;
+      if constexpr (!SUM && PC == 2) s_lo[wave][lane] = (float)(cum - (double)(float)cum);
       s_w[wave][lane] = wt * two(shw);
       // the weights exp(c_t - c_s) dt_s of M: at most the largest dt, unless the state grows
       if constexpr (!SUM && PC == 1) {
@@ -922,7 +934,8 @@ mix_block_kernel(const BlkArgs a) {
             }
           first = min(first, __shfl_xor(first, 16, 64));
           first = min(first, __shfl_xor(first, 32, 64));
-          if (q4 == 0) s_bad[wave][PT * i16 + e] = first;
+          if constexpr (!SUM)
+            if (q4 == 0) s_bad[wave][PT * i16 + e] = first;
         }
       }
       shx = shift_for(wave_max(mx));
@@ -1017,7 +1030,6 @@ mix_block_kernel(const BlkArgs a) {
         }
       };
       if constexpr (SUM) {
-        arrived<0>();
         meet();  // B is there
         su(__builtin_amdgcn_readfirstlane(s_sc[0][64]));
       } else {
@@ -1202,8 +1214,9 @@ mix_block_kernel(const BlkArgs a) {
   // ---- what the segment leaves
   float* dst = nullptr;
   if constexpr (SUM) {
-    dst = a.local + (int64_t)sg.split * inner * N;
-    if (lane == 0 && p0 == 0) a.decay[(int64_t)sg.split * a.H + h] = (float)dsum;
+    const int64_t at = (int64_t)sg.split * sub + piece_of;
+    dst = a.local + at * inner * N;
+    if (lane == 0 && p0 == 0) a.decay[at * a.H + h] = (float)dsum;
   } else {
     if (last && a.state) dst = a.state + slot * inner * N;
   }
@@ -1240,7 +1253,8 @@ __global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
   const int hs = a.P * a.N;  // values of a head
   const bool resume = ct.resume;
   const int64_t slot = ct.slot;
-  const float* d = a.decay + (int64_t)ct.split * a.H;
+  const int sub = a.sub, last = (ct.nseg - 1) * sub;  // nothing enters a segment from the last one
+  const float* d = a.decay + (int64_t)ct.split * sub * a.H;
   constexpr int V = 4, K = 4;
   int64_t at[V];
   int h[V];
@@ -1252,12 +1266,12 @@ __global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
     h[v] = at[v] < per ? (int)(at[v] / hs) : 0;
     s[v] = resume && at[v] < per ? a.state[slot * per + at[v]] : 0.0f;
   }
-  float* l = a.local + (int64_t)ct.split * per;
-  for (int k0 = 0; k0 < ct.nseg; k0 += K) {
+  float* l = a.local + (int64_t)ct.split * sub * per;
+  for (int k0 = 0; k0 <= last; k0 += K) {
     float own[K][V], dec[K][V];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      const int k = min(k0 + j, ct.nseg - 2);  // nothing enters a segment from the last one
+      const int k = min(k0 + j, last - 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         own[j][v] = l[k * per + (at[v] < per ? at[v] : 0)];
@@ -1266,10 +1280,10 @@ __global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (k0 + j < ct.nseg)
+      if (k0 + j <= last)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          if (at[v] < per) l[(k0 + j) * per + at[v]] = s[v];
+          if ((k0 + j) % sub == 0 && at[v] < per) l[(k0 + j) * per + at[v]] = s[v];
           s[v] = fmaf(s[v], ex2(dec[j][v]), own[j][v]);
         }
   }
@@ -1948,7 +1962,7 @@ int check_mix(MixArgs& a, bool step, int64_t rows, int64_t nseq, int64_t nslots,
 struct MixLayout {
   int nt, pt, pc, wv;
   int64_t nchunk, nseg, nsplit, ncut;  // at most
-  int seg_len, per_group, units;
+  int seg_len, sub, per_group, units;
   int64_t op_bytes, chunks, segs, cuts, ops, local, decay, cs0, bytes;
 };
 
@@ -1976,6 +1990,13 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   l.nsplit = cut ? 2 * (l.nchunk / len) : 0;
   l.ncut = cut ? l.nchunk / len : 0;
   l.nseg = nseq + l.nchunk / len;
+  // the first pass leaves out every sequence's last segment: its segments go in as many
+  // pieces as fill the card's turns best
+  const int64_t slots = kSegWaves / l.wv, first = (at_once - nseq) * l.units;
+  l.sub = cut && at_once <= nseq ? 2 : 1;  // few of them are cut then
+  if (cut && at_once > nseq)
+    for (int n = 2; n <= 4; ++n)
+      if ((first * n + slots - 1) / slots * l.sub < (first * l.sub + slots - 1) / slots * n) l.sub = n;
   const int64_t piece = (int64_t)kQ * l.nt * 16 * 2;
   l.op_bytes = (l.pc + 2) * piece + kTri * 64 * 8 * (l.pc == 1 ? 2 : 4) + 320;
   int64_t at = 0;
@@ -1989,8 +2010,8 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   l.segs = take(l.nseg * sizeof(Seg));
   l.cuts = take(l.ncut * sizeof(Cut));
   l.ops = take(l.nchunk * G * l.op_bytes);
-  l.local = take(l.nsplit * H * P * N * 4);
-  l.decay = take(l.nsplit * H * 4);
+  l.local = take(l.nsplit * l.sub * H * P * N * 4);
+  l.decay = take(l.nsplit * l.sub * H * 4);
   l.cs0 = take(l.ncut * H * P * 3 * 4);
   l.bytes = at;
   return l;
@@ -2006,7 +2027,7 @@ void launch_mix_blocks(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
   auto walk = [&](auto fast) {
     constexpr bool F = decltype(fast)::value;
     if (l.nsplit) {
-      mix_block_kernel<IO, NT, PT, PC, WV, true, F><<<grid, 64 * WV, 0, s>>>(b);
+      mix_block_kernel<IO, NT, PT, PC, WV, true, F><<<grid * l.sub, 64 * WV, 0, s>>>(b);
       const int64_t per = (int64_t)b.H * b.P * b.N;
       mix_join_kernel<<<dim3((unsigned)l.ncut, (unsigned)((per + 1023) / 1024)), 256, 0, s>>>(b);
     }
@@ -2194,7 +2215,7 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
                 (long long)need);
   if (!aligned16(workspace)) return fail(SSM_E_ALIGN, "workspace is not 16-byte aligned");
   const MixLayout l = mix_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype);
-  if (l.nseg * l.units > 0x7fffffff || l.nchunk > 0x7fffffff)
+  if (l.nseg * l.units * l.sub > 0x7fffffff || l.nchunk > 0x7fffffff)
     return fail(SSM_E_SHAPE, "too many sequences and heads for one call");
   char* w = static_cast<char*>(workspace);
   a.head = reinterpret_cast<PlanHead*>(w);
@@ -2205,7 +2226,7 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
   a.local = reinterpret_cast<float*>(w + l.local);
   a.decay = reinterpret_cast<float*>(w + l.decay);
   a.cs0 = reinterpret_cast<float*>(w + l.cs0);
-  a.op_bytes = l.op_bytes; a.seg_len = l.seg_len; a.units = l.units; a.per_group = l.per_group;
+  a.op_bytes = l.op_bytes; a.seg_len = l.seg_len; a.sub = l.sub; a.units = l.units; a.per_group = l.per_group;
   const int es = io_dtype == SSM_DTYPE_BF16 ? 2 : 4, wide = 4 * l.pt * es < 16 ? 4 * l.pt * es : 16;
   const int64_t inner = nheads * headdim, ch = inner + 2 * ngroups * dstate;
   auto lanes = [&](const void* p, int64_t stride, int bytes) {  // whole accesses of that many bytes
