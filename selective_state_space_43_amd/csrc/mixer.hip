@@ -217,6 +217,12 @@ __device__ __forceinline__ float max3(float m, float x, float y) {
   asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(o) : "v"(m), "v"(x), "v"(y));
   return o;
 }
+// The same, and a NaN stays.
+__device__ __forceinline__ float max3_nan(float m, float x, float y) {
+  float o;
+  asm("v_maximum3_f32 %0, %1, |%2|, |%3|" : "=v"(o) : "v"(m), "v"(x), "v"(y));
+  return o;
+}
 // In a branch that is hardly ever taken: keeps the compiler from computing both sides.
 __device__ __forceinline__ void rarely() { asm volatile(""); }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
@@ -225,15 +231,44 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// a fp16 (the lower or the upper half of w) times float32, in one instruction
-template <int HALF>
-__device__ __forceinline__ float mul_half(uint32_t w, float x) {
-  float o;
-  if constexpr (HALF) asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(o) : "v"(w), "v"(x));
-  else asm("v_fma_mix_f32 %0, %1, %2, 0 op_sel:[0,0,0] op_sel_hi:[1,0,0]" : "=v"(o) : "v"(w), "v"(x));
-  return o;
+// Eight products rounded once to fp16, two to a register; the s_nop lets the
+// half-register writes settle before any reader.
+#define MIX_PAIR(d, x0, x1, y0, y1, s0, s1, h)                                  \
+  "v_fma_mixlo_f16 " d ", " x0 ", " y0 ", 0 op_sel:[0,0,0] op_sel_hi:[" h ",0,0]\n\t" \
+  "v_fma_mixhi_f16 " d ", " x1 ", " y1 ", 0 op_sel:[" s1 ",0,0] op_sel_hi:[" h ",0,0]\n\t"
+// v[j] f
+__device__ __forceinline__ h8 scaled(const float* v, float f) {
+  u4 o;
+  asm(MIX_PAIR("%0", "%4", "%5", "%12", "%12", "0", "0", "0") MIX_PAIR("%1", "%6", "%7", "%12", "%12", "0", "0", "0")
+      MIX_PAIR("%2", "%8", "%9", "%12", "%12", "0", "0", "0") MIX_PAIR("%3", "%10", "%11", "%12", "%12", "0", "0", "0")
+      "s_nop 1"
+      : "=&v"(o.x), "=&v"(o.y), "=&v"(o.z), "=&v"(o.w)
+      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "v"(f));
+  return __builtin_bit_cast(h8, o);
 }
+// h[j] v[j], h in fp16
+__device__ __forceinline__ h8 times(u4 h, const float* v) {
+  u4 o;
+  asm(MIX_PAIR("%0", "%4", "%4", "%8", "%9", "0", "1", "1") MIX_PAIR("%1", "%5", "%5", "%10", "%11", "0", "1", "1")
+      MIX_PAIR("%2", "%6", "%6", "%12", "%13", "0", "1", "1") MIX_PAIR("%3", "%7", "%7", "%14", "%15", "0", "1", "1")
+      "s_nop 1"
+      : "=&v"(o.x), "=&v"(o.y), "=&v"(o.z), "=&v"(o.w)
+      : "v"(h.x), "v"(h.y), "v"(h.z), "v"(h.w), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]),
+        "v"(v[6]), "v"(v[7]));
+  return __builtin_bit_cast(h8, o);
+}
+#undef MIX_PAIR
 
+// v w = hi + lo in fp16, to 22 bits; lo takes in what v w itself was rounded by
+__device__ __forceinline__ void pieces(const float* v, const float* w, h8& hi, h8& lo) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const h2 a = __builtin_convertvector((f2){v[j] * w[j], v[j + 1] * w[j + 1]}, h2);
+    hi[j] = a.x; hi[j + 1] = a.y;
+    lo[j] = (_Float16)__builtin_fmaf(v[j], w[j], -(float)a.x);
+    lo[j + 1] = (_Float16)__builtin_fmaf(v[j + 1], w[j + 1], -(float)a.y);
+  }
+}
 // v = hi + lo in fp16, to 22 bits
 __device__ __forceinline__ void pieces(const float* v, h8& hi, h8& lo) {
 #pragma unroll
@@ -780,7 +815,7 @@ mix_block_kernel(const BlkArgs a) {
     }
     h8 xh[PT][2], xl[PT][2], wh[PT][2], wl[PT][2], sh[PT][NT / 2], sl[PT][NT / 2];
     float dec_all = 1.0f, cap = 0.0f;
-    int shx = 0, shw = 0, shd = 0, shS = 0;
+    int shx = 0, shd = 0, shS = 0;
     bool bad = false;
     if (on) {
       // ---- the convolution
@@ -869,26 +904,21 @@ mix_block_kernel(const BlkArgs a) {
       const double cum = wave_scan((double)dA), tot = lane63(cum);
       const float wt = dt * ex2((float)(tot - cum));
       dec_all = ex2((float)tot);
-      const float wmax = wave_max(finite(wt) ? fabsf(wt) : 0.0f);
-      shw = -__builtin_amdgcn_frexp_expf(wmax);
-      shw = shw < -112 ? -112 : (shw > 60 ? 60 : shw);
       dsum += tot;
       if constexpr (!SUM) s_cum[wave][lane] = (float)cum;
       if constexpr (!SUM && PC == 2) s_lo[wave][lane] = (float)(cum - (double)(float)cum);
-      s_w[wave][lane] = wt * two(shw);
-      // the weights exp(c_t - c_s) dt_s of M: at most the largest dt, unless the state grows
-      if constexpr (!SUM && PC == 1) {
-        shd = -__builtin_amdgcn_frexp_expf(wave_max(finite(dt) ? fabsf(dt) : 0.0f));
-        if (__any(dA > 0.0f)) {
-          rarely();
-          cap = fminf(wave_max(fmaxf((float)cum, 0.0f)) + wave_max(fmaxf(-(float)cum, 0.0f)), 100.0f);
-          shd -= (int)cap + 1;
-        }
-        shd = shd < -112 ? -112 : (shd > 60 ? 60 : shd);
+      // the weights exp(c_t - c_s) dt_s of M and of the state: at most the largest dt, unless
+      // the state grows
+      shd = -__builtin_amdgcn_frexp_expf(wave_max(finite(dt) ? fabsf(dt) : 0.0f));
+      if (__any(dA > 0.0f)) {
+        rarely();
+        cap = fminf(wave_max(fmaxf((float)cum, 0.0f)) + wave_max(fmaxf(-(float)cum, 0.0f)), 100.0f);
+        shd -= (int)cap + 1;
       }
-      if constexpr (!SUM) s_dt[wave][lane] = PC == 2 || finite(dt) ? dt * two(shd) : 0.0f;
+      shd = shd < -112 ? -112 : (shd > 60 ? 60 : shd);
+      if constexpr (!SUM) s_dt[wave][lane] = PC == 2 ? dt : finite(dt) ? dt * two(shd) : 0.0f;
       // ---- silu, the tile's scale
-      float mx = 0.0f, chk = 0.0f;
+      float mx = 0.0f;
 #pragma unroll
       for (int e = 0; e < PT; ++e)
 #pragma unroll
@@ -897,14 +927,13 @@ mix_block_kernel(const BlkArgs a) {
           for (int j = 0; j < 8; ++j) {
             const float x = silu(v[e][kb][j]);
             v[e][kb][j] = x;
-            chk = fmaf(x, 0.0f, chk);
           }
 #pragma unroll
       for (int e = 0; e < PT; ++e)
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) mx = max3(mx, v[e][kb][j], v[e][kb][j + 1]);
+          for (int j = 0; j < 8; j += 2) mx = max3_nan(mx, v[e][kb][j], v[e][kb][j + 1]);
       // this block's x is used up: the next one's may come (B's loads have ended long ago)
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       if (a.z) fetch_z(c);
@@ -918,7 +947,7 @@ mix_block_kernel(const BlkArgs a) {
 #pragma unroll
             for (int e = 0; e < PT; ++e) v[e][kb][j] = 32 * kb + 8 * q4 + j < cnt ? v[e][kb][j] : 0.0f;
       }
-      bad = __any(!(chk == 0.0f));
+      bad = __any(!finite(mx));
       if (bad) {
         rarely();
         mx = 0.0f;
@@ -939,6 +968,7 @@ mix_block_kernel(const BlkArgs a) {
         }
       }
       shx = shift_for(wave_max(mx));
+      s_w[wave][lane] = wt * two(shx + shd);
       const float fx = two(shx);
       __builtin_amdgcn_wave_barrier();
 
@@ -950,21 +980,21 @@ mix_block_kernel(const BlkArgs a) {
         *reinterpret_cast<f4*>(w8 + 4) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4 + 4]);
 #pragma unroll
         for (int e = 0; e < PT; ++e) {
-          float x[8], w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[j] = v[e][kb][j] * fx;
-            w[j] = x[j] * w8[j];
-          }
-          pieces(w, wh[e][kb], wl[e][kb]);
+          pieces(v[e][kb], w8, wh[e][kb], wl[e][kb]);
           if constexpr (!SUM) {
             if (bad) {  // 0 x Inf is not 0: y's earlier rows must not meet them
               rarely();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) x[j] = finite(x[j]) ? x[j] : 0.0f;
+              for (int j = 0; j < 8; ++j) v[e][kb][j] = finite(v[e][kb][j]) ? v[e][kb][j] : 0.0f;
             }
-            if constexpr (PC == 2) pieces(x, xh[e][kb], xl[e][kb]);
-            else xh[e][kb] = piece(x);
+            if constexpr (PC == 2) {
+              float x[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = v[e][kb][j] * fx;
+              pieces(x, xh[e][kb], xl[e][kb]);
+            } else {
+              xh[e][kb] = scaled(v[e][kb], fx);
+            }
           }
         }
       }
@@ -999,14 +1029,14 @@ mix_block_kernel(const BlkArgs a) {
           for (int m = 0; m < NT / 2; ++m) {
             float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * fs;
+            for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * (PC == 2 ? fs : 1.0f);
             if constexpr (PC == 2) pieces(x, sh[e][m], sl[e][m]);
-            else sh[e][m] = piece(x);
+            else sh[e][m] = scaled(x, fs);
           }
       }  // the state as an operand
 
       auto su = [&](int shB) {  // ---- the state after the block
-        const float f_su = two(max(-126, -(shB + shx + shw)));
+        const float f_su = two(max(-126, -(shB + shx + shd)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           h8 bh[2], bl[2];
@@ -1075,10 +1105,9 @@ mix_block_kernel(const BlkArgs a) {
                 const int s = 32 * kb + 8 * q4 + j;
                 float x = cum_t - s_cum[wave][s];
                 if (kb == tt / 2) x = fminf(x, cap);
-                x = ex2(x) * s_dt[wave][s];
-                m[j] = j & 1 ? mul_half<1>(g[j >> 1], x) : mul_half<0>(g[j >> 1], x);
+                m[j] = ex2(x) * s_dt[wave][s];
               }
-              const h8 mh = piece(m);
+              const h8 mh = times(g, m);
 #pragma unroll
               for (int e = 0; e < PT; ++e) ym[e] = mfma(xh[e][kb], mh, ym[e]);
             }
