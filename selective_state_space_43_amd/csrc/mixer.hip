@@ -1654,9 +1654,9 @@ __global__ void __launch_bounds__(team_threads(TL)) norm_fwd_kernel(const NormAr
 
 // The backward: with u = g w (g the gradient of the affine result) and n the
 // normalised values, d = (u - mean(u) - n mean(u n)) / deviation, mean(u) only
-// where the forward is centred.  A team keeps its group and its columns' sums of
-// g n and g in registers over a strip of rows; norm_bwd_sum_kernel adds the
-// strips in order.
+// where the forward is centred.  A workgroup's teams keep their group and their columns'
+// sums of g n and g in registers over a strip of rows; norm_bwd_sum_kernel adds
+// the strips in order.
 //
 // PLAIN: no centring, no activation, no gate behind and no bias, as the Mamba-2
 // block has it: then u does not wait for the statistics, and one meeting gives both
@@ -1667,21 +1667,18 @@ __global__ void __launch_bounds__(team_threads(TL))
 __attribute__((amdgpu_waves_per_eu(TL > 256 ? 4 : PLAIN || sizeof(IO) == 4 ? 3 : 2))) norm_bwd_kernel(const NormArgs a) {
   __shared__ float red1[2][1][TL < 64 ? 1 : TL / 64], red2[2][2][TL < 64 ? 1 : TL / 64];
   int turn1 = 0, turn2 = 0;
-  const int gs = a.C / a.G, nv = gs / VE, i = threadIdx.x % TL;
-  const int64_t team = (int64_t)blockIdx.x * (team_threads(TL) / TL) + threadIdx.x / TL;
-  const int strips = a.strips;
-  const bool on = team < (int64_t)strips * a.G;
-  const int64_t strip = on ? team / a.G : 0;
-  const int c0 = on ? (int)(team - strip * a.G) * gs : 0;
-  const int64_t r0 = a.rows * strip / strips, r1 = a.rows * (strip + 1) / strips;
-  // every team of the workgroup takes as many turns as the longest strip: they meet inside
-  const int64_t turns = (a.rows + strips - 1) / strips;
+  constexpr int TW = team_threads(TL) / TL;  // teams of the workgroup: every TW-th row of the strip each
+  const int gs = a.C / a.G, nv = gs / VE, i = threadIdx.x % TL, tw = threadIdx.x / TL;
+  const int64_t strip = blockIdx.x / a.G;
+  const int c0 = (int)(blockIdx.x - strip * a.G) * gs;
+  const int64_t r0 = a.rows * strip / a.strips, r1 = a.rows * (strip + 1) / a.strips;
+  const int64_t turns = (r1 - r0 + TW - 1) / TW;  // of every team: wide ones meet inside
   const float inv = 1.0f / (float)gs;
   const bool before = a.gate == SSM_GATE_BEFORE, after = !PLAIN && a.gate == SSM_GATE_AFTER;
   float dw[K][VE] = {}, db[PLAIN ? 1 : K][VE] = {};
   for (int64_t q = 0; q < turns; ++q) {
-    const int64_t r = r0 + q;
-    const bool live = on && r < r1;
+    const int64_t r = r0 + q * TW + tw;
+    const bool live = r < r1;
     const int64_t rr = min(r, a.rows - 1);
     Vec<IO, VE> x[K], z[K], g[K];
 #pragma unroll
@@ -1813,21 +1810,36 @@ __attribute__((amdgpu_waves_per_eu(TL > 256 ? 4 : PLAIN || sizeof(IO) == 4 ? 3 :
       }
     }
   }
-  if (!on) return;
+  // the teams' column sums, team by team in order
+  auto keep = [&](float* p, const float (&v)[K][VE]) {
+    constexpr int M = VE < 4 ? 1 : 4;
+    float* out = p + strip * a.C + c0;
+    if constexpr (TW > 1) {
+      __shared__ __align__(16) float s_sum[TW][TL * K * VE];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (k * TL >= nv) break;
-    if (i + k * TL < nv) {
-      const int64_t at = strip * a.C + c0 + (i + k * TL) * VE;
-      auto keep = [&](float* p, const float* v) {
-        put<float, VE < 4 ? 1 : 4>(p, at, v);
-        if constexpr (VE == 8) put<float, 4>(p, at + 4, v + 4);
-      };
-      if (a.pw) keep(a.pw, dw[k]);
-      if constexpr (!PLAIN)
-        if (a.pb) keep(a.pb, db[k]);
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < VE; j += M) put<float, M>(s_sum[tw], (i + k * TL) * VE + j, v[k] + j);
+      __syncthreads();
+      for (int c = threadIdx.x; c < gs; c += TW * TL) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < TW; ++k) s += s_sum[k][c];
+        out[c] = s;
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (i + k * TL >= nv) break;
+#pragma unroll
+        for (int j = 0; j < VE; j += M) put<float, M>(out, (i + k * TL) * VE + j, v[k] + j);
+      }
     }
-  }
+  };
+  if (a.pw) keep(a.pw, dw);
+  if constexpr (!PLAIN)
+    if (a.pb) keep(a.pb, db);
 }
 
 // Column sums of the strips' partial sums, in order: sixteen runs of strips a
@@ -2154,10 +2166,10 @@ bool norm_vectors(const NormArgs& a, int es) {
 template <bool BWD, typename IO, int VE, int TL, int K>
 int launch_norm_team(NormArgs& a, hipStream_t s) {
   if constexpr (BWD) {
-    const int64_t fill = (kNormThreads + (int64_t)TL * a.G - 1) / ((int64_t)TL * a.G);
+    const int64_t fill = (kNormThreads + (int64_t)team_threads(TL) * a.G - 1) / ((int64_t)team_threads(TL) * a.G);
     if (fill < a.strips) a.strips = (int)fill;
   }
-  const int64_t items = (BWD ? a.strips : a.rows) * (int64_t)a.G, per = team_threads(TL) / TL;
+  const int64_t items = (BWD ? a.strips : a.rows) * (int64_t)a.G, per = BWD ? 1 : team_threads(TL) / TL;
   const int64_t blocks = (items + per - 1) / per;
   if (blocks > 0x7fffffff) return fail(SSM_E_SHAPE, "rows and ngroups: too many for one call");
   if constexpr (BWD) {
