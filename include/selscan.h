@@ -369,9 +369,10 @@ int64_t ssm_ssd_scratch_bytes(void);
  *               16-byte aligned, owned by the caller; its contents on entry do
  *               not matter; calls sharing it must not run concurrently
  * headdim and dstate are 1..256, width 1..4 (SSM_E_UNSUPPORTED otherwise),
- * tokens below 2^31.  A float32 or bf16 tensor needs the alignment of its
- * elements only.  Offsets outside [0, tokens] or out of order are clamped into
- * it: the sequences they describe are wrong, no other memory is touched.
+ * tokens at most 2^31 - 2^16, nseq below 2^20.  A float32 or bf16 tensor needs
+ * the alignment of its elements only; rows, headdim and dstate that allow 16-byte
+ * accesses are faster.  Offsets are read as their running maximum held inside
+ * [0, tokens], so that whatever they hold no other memory is touched.
  * Outputs must not overlap inputs; slices of one buffer's rows with disjoint
  * columns do not.  Results do not vary from run to run.  A non-finite input
  * makes what depends on it non-finite (an infinity may become a NaN), and

@@ -97,11 +97,25 @@ def mix(x, cu, G, slots=None, has=None, softplus=True):
                                    np.ascontiguousarray(C), H, G, D=D, dt_bias=x["dt_bias"],
                                    dt_softplus=softplus, h0=h0)
                 return yy, h
+
+            # The terms of y_t are decay dt_s x_s B_s C_t, the decays positive: with |B|, |C| and
+            # x = |x| sign(dt) each is its absolute value, also where a step is negative; D x apart.
+            raw = dt[0] + (0 if x["dt_bias"] is None else x["dt_bias"][:, None])
+            sign = np.ones_like(raw) if softplus else np.where(raw < 0, -1.0, 1.0)
+
+            def absolute(c):
+                s = c.copy()
+                s[:inner] *= np.repeat(sign, P, 0)
+                yy, h = scan(s, None, np.abs(h0))
+                if x["D"] is not None:
+                    yy = yy + np.repeat(ab(x["D"]), P)[None, :, None] * c[None, :inner]
+                return yy, h
+
             v, h1 = scan(c[0], x["D"], h0)
             y[a:b] = (v * zt)[0].T
-            v, h1a = scan(np.abs(c[0]), ab(x["D"]), np.abs(h0))
+            v, h1a = absolute(np.abs(c[0]))
             ya[a:b] = (v * np.abs(zt))[0].T
-            v, h1c = scan(cabs[0], ab(x["D"]), np.abs(h0))
+            v, h1c = absolute(cabs[0])
             yc[a:b] = (v * np.abs(zt))[0].T
         else:
             c1, h1, h1a, h1c = c0, h0, np.abs(h0), np.abs(h0)

@@ -234,6 +234,22 @@ def test_packed_reference_is_step_by_step():
         np.testing.assert_allclose(cs[slots[s]], hist, rtol=0, atol=0)
 
 
+def test_bounds_hold_the_terms_absolute_values():
+    """The bounds' sums against the recurrence on absolute values written out, with
+    steps below zero: each term once, with its magnitude."""
+    rng = np.random.default_rng(0)
+    x = ref.mix_inputs(rng, 5, 1, 1, 1, 1, 2, 1, "f32", 1, gate=False)
+    x["inner"], x["dt"], x["dt_bias"] = 1, -np.abs(x["dt"]) * 0.1, np.zeros(1)
+    _, _, _, (ya, _), (ha, _) = ref.mix(x, [0, 5], 1, None, [True], softplus=False)
+    c = x["xbc"] * x["conv_weight"][:, 0] + x["conv_bias"]
+    c = c / (1 + np.exp(-c))
+    h = np.abs(x["ssm_state"][0, 0, 0])
+    for t in range(5):
+        h = np.exp(x["dt"][t, 0] * x["A"][0]) * h + abs(x["dt"][t, 0] * c[t, 0]) * np.abs(c[t, 1:3])
+        np.testing.assert_allclose(ya[t, 0], (h * np.abs(c[t, 3:])).sum() + abs(x["D"][0] * c[t, 0]))
+    np.testing.assert_allclose(ha[0, 0, 0], h)
+
+
 def test_bf16_helper():
     v = np.array([1.0, 1.00390625, 1.01171875, -3.1415927, 1e-20], dtype=np.float32)
     torch = pytest.importorskip("torch")

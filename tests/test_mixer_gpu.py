@@ -294,6 +294,65 @@ def test_extreme_steps(ssm, dev):
         m.check("extreme " + dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("how", ["A", "dt"])
+def test_growing_state(ssm, dev, dtype, how):
+    """A positive A, or raw steps below zero used as they are: the weights of a
+    block pass the largest step."""
+    m = Mix(dev, (150, 40), 2, 64, 1, 64, 4, dtype, 83, has=True, softplus=False)
+    if how == "A":
+        m.x["A"] = np.array([0.5, 0.02])
+    else:
+        m.x["dt"][60:90] *= -1
+        m.x["A"] = np.array([-3.0, -0.1])
+    m.load()
+    m.run(ssm)
+    torch.cuda.synchronize()
+    m.check(f"growing {how} {dtype}")
+
+
+def test_states_without_slots(ssm, dev):
+    """slots None: sequence s has slot s; has_state None: none continues."""
+    m = Mix(dev, (70, 0, 5), 2, 64, 1, 64, 4, "bf16", 84, has=False)
+    m.slots = np.arange(3)
+    m.run(ssm, slots=None, has_state=None)
+    torch.cuda.synchronize()
+    m.check("no slots")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_non_finite_state(ssm, dev, dtype):
+    """A NaN and an infinity in the state that a prompt continues from reach their
+    own channel's y and state only."""
+    m = Mix(dev, (90, 30), 2, 64, 1, 64, 4, dtype, 85, has=True)
+    clean = Mix(dev, (90, 30), 2, 64, 1, 64, 4, dtype, 85, has=True)
+    slot = int(m.slots[0])
+    m.hs[slot, 0, 5, 7], m.hs[slot, 1, 9, 3] = float("nan"), float("inf")
+    m.run(ssm)
+    clean.run(ssm)
+    torch.cuda.synchronize()
+    ya, yb = f64(clean.y), f64(m.y)
+    hit = np.zeros(ya.shape, dtype=bool)
+    hit[:90, 5] = hit[:90, 64 + 9] = True
+    tol = 2.0 ** -7 if dtype == "bf16" else 2.0 ** -14
+    assert (np.abs(ya - yb) <= tol * (1 + np.abs(ya)))[~hit].all()
+    assert np.isnan(yb[:90, 5]).all()
+    ha, hb = f64(clean.hs)[slot], f64(m.hs)[slot]
+    keep = np.ones(ha.shape, dtype=bool)
+    keep[0, 5, 7] = keep[1, 9, 3] = False
+    assert (np.abs(ha - hb) <= 2.0 ** -14 * (1 + np.abs(ha)))[keep].all() and np.isnan(hb[0, 5, 7])
+
+
+def test_many_short_sequences(ssm, dev):
+    """More sequences than the plan takes in one turn, every third one padding."""
+    lens = tuple((i * 7) % 4 for i in range(2300))
+    skip = tuple((i, -1) for i in range(0, 2300, 3))
+    m = Mix(dev, lens, 1, 16, 1, 16, 4, "bf16", 86, skip=skip, behind=2)
+    m.run(ssm)
+    torch.cuda.synchronize()
+    m.check("2300 sequences")
+
+
 def test_far_rows_and_slots(ssm, dev):
     """Rows and slots whose byte offsets pass 32 bits."""
     H, P, G, N, W = 2, 64, 1, 128, 4
@@ -496,6 +555,9 @@ def test_graph_replays_and_streams(ssm, dev):
         ssm.ssm_conv_ssd_update(tok.xbc[:2], tok.dt[:2], m.cs, m.hs, m.par["conv_weight"], m.par["A"], G,
                                 slots=m.slots_t, y=out[:2], **{**m.opts(), "z": None})
         ssm.ssm_group_norm_fwd(m.y, w, G, y=out[2:])
+        # a training program's step beside it: its gradients into the same tensors
+        g = ssm.ssm_group_norm_bwd(out[2:], m.y, w, 2, bias=w, center=True)
+        out[2:].copy_(g["dx"] + g["dweight"].bfloat16() + g["dbias"].bfloat16())
     out, eout = (torch.zeros(rows + 2, H * P, dtype=torch.bfloat16, device=dev) for _ in range(2))
     keep = m.cs.clone(), m.hs.clone()
     side = torch.cuda.Stream(dev)
