@@ -369,7 +369,8 @@ int64_t ssm_ssd_scratch_bytes(void);
  *               16-byte aligned, owned by the caller; its contents on entry do
  *               not matter; calls sharing it must not run concurrently
  * headdim and dstate are 1..256, width 1..4 (SSM_E_UNSUPPORTED otherwise),
- * tokens at most 2^31 - 2^16, nseq below 2^20.  A float32 or bf16 tensor needs
+ * nseq is below 2^20 and tokens / 64 + nseq below 2^22, and a launch has less than
+ * 2^32 threads (SSM_E_SHAPE otherwise).  A float32 or bf16 tensor needs
  * the alignment of its elements only; rows, headdim and dstate that allow 16-byte
  * accesses are faster.  Offsets are read as their running maximum held inside
  * [0, tokens], so that whatever they hold no other memory is touched.

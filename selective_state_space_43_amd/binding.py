@@ -720,6 +720,8 @@ class _GroupNormFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        if torch.is_grad_enabled():  # create_graph: the gradients would pass for constants
+            raise RuntimeError("group_norm_fn: gradients of its gradients are not computed")
         x, weight, bias, z = ctx.saved_tensors
         g = ssm_group_norm_bwd(dy.contiguous(), x, weight, ctx.ngroups, bias=bias, z=z, **ctx.how)
         return g["dx"], g["dweight"], g["dbias"], g["dz"], None, None, None, None, None
@@ -728,5 +730,5 @@ class _GroupNormFn(torch.autograd.Function):
 def group_norm_fn(x, weight, ngroups, bias=None, z=None, eps=1e-5, center=False, activation="none",
                   gate="none"):
     """ssm_group_norm_fwd's output, differentiable in x, weight, bias and z
-    through ssm_group_norm_bwd."""
+    through ssm_group_norm_bwd, once (create_graph is refused)."""
     return _GroupNormFn.apply(x, weight, bias, z, ngroups, eps, center, activation, gate)

@@ -142,7 +142,6 @@ struct BlkArgs : MixArgs {
   float* local;    // [split * sub][H, P, N] state of a piece from zero; of the first, then the state entering the segment
   float* decay;    // [split * sub][H] log2 of a piece's whole decay
   float* cs0;      // [cut][inner, 3] what the first rows of a cut sequence start from
-  int64_t op_bytes;
   int seg_len;     // blocks of a segment at most
   int sub;         // pieces of a segment in the first pass
   int units;       // workgroups a segment needs
@@ -626,14 +625,11 @@ struct XTile {
 
 // What a wave reads of a block's rows ahead of time where they are not staged:
 // x of its channels at rows 32 kb + 8 q - 3 .. + 7, as they lie in memory.
-template <typename IO, int PT, bool FAST>
+template <typename IO, int PT>
 struct XRaw {
-  static constexpr bool pair = FAST && PT == 2 && sizeof(IO) == 2;  // two channels in one word
-  static constexpr int K = pair ? 1 : PT;
-  uint32_t w[K][2][11];
+  uint32_t w[PT][2][11];
   __device__ __forceinline__ float get(int e, int kb, int j) const {
-    if constexpr (pair) return __uint_as_float(e ? w[0][kb][j] & 0xffff0000u : w[0][kb][j] << 16);
-    else if constexpr (sizeof(IO) == 2) return __uint_as_float(w[e][kb][j] << 16);
+    if constexpr (sizeof(IO) == 2) return __uint_as_float(w[e][kb][j] << 16);
     else return __uint_as_float(w[e][kb][j]);
   }
 };
@@ -641,11 +637,21 @@ struct XRaw {
 // One wave per 16 PT channels of a head (PT = 2: channels 2 i and 2 i + 1 of
 // its 32 are row i of the two tiles, so that a lane reads x two channels and
 // z, y eight channels at a time).  The WV waves of a workgroup share a group
-// of heads and stage its operands in LDS, B of this block while the waves
-// work on y, C and C.B^T of the next while they work on the state; x, dt and z
-// of the next block are on their way meanwhile.  PC: pieces of
-// the operands of y.  FAST: rows and channels allow whole vectors (headdim a
-// multiple of 4 PT, dstate of 4, rows aligned to the accesses).
+// of heads and its operands in LDS.  A block goes convolution, state, y: its C
+// and C.B^T arrive while the waves convolve and update the state, the next
+// block's B while they work on y, the next block's x and dt from the
+// convolution's end on.  PC: pieces of the operands of y.  FAST: rows and
+// channels allow whole vectors (headdim a multiple of 4 PT, dstate of 4, rows
+// aligned to the accesses).
+//
+// Bound by latency: four prompts of 8192 with 80 heads of 64 channels and 128
+// states take 579 us in the second pass and 187 in the first.  A wave and block
+// of the second is 2148 vector instructions, 148 of them products: the vector
+// units are busy 60 % of the time, the matrix cores 15 %, and a wave waits 37 %
+// of its own.  The state (64 registers), its fp16 copy and x as two operands hold
+// it to two waves a SIMD (246 registers, 79 KB of LDS a workgroup); the first
+// pass at three spills (802 us a call against 788).  Past 128 states a wave has 16
+// channels instead of 32, so that its state stays at 64 registers.
 template <typename IO, int NT, int PT, int PC, int WV, bool SUM, bool FAST>
 __global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(NT == 8 && PC == 2 && !SUM ? 1 : 2)))
 mix_block_kernel(const BlkArgs a) {
@@ -734,7 +740,7 @@ mix_block_kernel(const BlkArgs a) {
   double dsum = 0.0;  // log2 of the segment's decay
 
   // a block's x and dt, and its z, on their way
-  XRaw<IO, PT, FAST> xr;
+  XRaw<IO, PT> xr;
   float dt_raw = 0.0f;
   typedef uint32_t zv __attribute__((ext_vector_type(2 * PT)));
   constexpr bool ZAHEAD = FAST && !SUM && sizeof(IO) == 2;
@@ -1918,6 +1924,9 @@ int check_io(int io_dtype) {
 
 constexpr int64_t kMaxHeaddim = 256;
 
+// A launch has less than 2^32 threads.
+bool grid_ok(int64_t blocks, int threads) { return blocks <= 0xffffffffll / threads; }
+
 int check_mix_extents(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim,
                       int64_t ngroups, int64_t dstate) {
   int st;
@@ -1933,8 +1942,9 @@ int check_mix_extents(int64_t tokens, int64_t nseq, int64_t nheads, int64_t head
                 (long long)headdim, (long long)dstate);
   if (nheads > 16384)
     return fail(SSM_E_SHAPE, "nheads = %lld exceeds 16384", (long long)nheads);
-  if (tokens > 0x7fff0000 || nseq > 0xfffff)  // a block's rows past the last one still fit an int
-    return fail(SSM_E_SHAPE, "tokens = %lld, nseq = %lld: at most 2^31 - 2^16 and 2^20 - 1",
+  // one launch has a workgroup of 2^10 threads for each of tokens / 64 + nseq blocks
+  if (nseq > 0xfffff || tokens / kQ + nseq >= ((int64_t)1 << 22))
+    return fail(SSM_E_SHAPE, "tokens = %lld, nseq = %lld: nseq is at most 2^20 - 1, tokens / 64 + nseq 2^22 - 1",
                 (long long)tokens, (long long)nseq);
   return SSM_OK;
 }
@@ -2004,7 +2014,7 @@ struct MixLayout {
   int nt, pt, pc, wv;
   int64_t nchunk, nseg, nsplit, ncut;  // at most
   int seg_len, sub, per_group, units;
-  int64_t op_bytes, chunks, segs, cuts, ops, local, decay, cs0, bytes;
+  int64_t chunks, segs, cuts, ops, local, decay, cs0, bytes;
 };
 
 // A segment is one workgroup's work, one after another; the card holds 2048
@@ -2039,7 +2049,7 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
     for (int n = 2; n <= 4; ++n)
       if ((first * n + slots - 1) / slots * l.sub < (first * l.sub + slots - 1) / slots * n) l.sub = n;
   const int64_t piece = (int64_t)kQ * l.nt * 16 * 2;
-  l.op_bytes = (l.pc + 2) * piece + kTri * 64 * 8 * (l.pc == 1 ? 2 : 4) + 320;
+  const int64_t op_bytes = (l.pc + 2) * piece + kTri * 64 * 8 * (l.pc == 1 ? 2 : 4) + 320;
   int64_t at = 0;
   auto take = [&](int64_t n) {
     const int64_t o = at;
@@ -2050,7 +2060,7 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   l.chunks = take(l.nchunk * sizeof(Chunk));
   l.segs = take(l.nseg * sizeof(Seg));
   l.cuts = take(l.ncut * sizeof(Cut));
-  l.ops = take(l.nchunk * G * l.op_bytes);
+  l.ops = take(l.nchunk * G * op_bytes);
   l.local = take(l.nsplit * l.sub * H * P * N * 4);
   l.decay = take(l.nsplit * l.sub * H * 4);
   l.cs0 = take(l.ncut * H * P * 3 * 4);
@@ -2069,7 +2079,7 @@ void launch_mix_blocks(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
     constexpr bool F = decltype(fast)::value;
     if (l.nsplit) {
       mix_block_kernel<IO, NT, PT, PC, WV, true, F><<<grid * l.sub, 64 * WV, 0, s>>>(b);
-      const int64_t per = (int64_t)b.H * b.P * b.N;
+      const int64_t per = (int64_t)b.H * b.P * b.N;  // at most 2^23: larger ones fill the card uncut
       mix_join_kernel<<<dim3((unsigned)l.ncut, (unsigned)((per + 1023) / 1024)), 256, 0, s>>>(b);
     }
     mix_block_kernel<IO, NT, PT, PC, WV, false, F><<<grid, 64 * WV, 0, s>>>(b);
@@ -2098,7 +2108,7 @@ int launch_step(const MixArgs& a, hipStream_t s) {
     constexpr int R = decltype(rpl)::value, rows = 256 / LN * R;
     const int splits = (a.P + rows - 1) / rows;
     const int64_t grid = a.nseq * a.H * splits;
-    if (grid > 0x7fffffff) return fail(SSM_E_SHAPE, "too many entries and heads for one call");
+    if (!grid_ok(grid, 256)) return fail(SSM_E_SHAPE, "too many entries and heads for one call");
     mix_step_kernel<IO, LN, R, VEC><<<(unsigned)grid, 256, 0, s>>>(a, splits);
     return (int)SSM_OK;
   };
@@ -2171,7 +2181,7 @@ int launch_norm_team(NormArgs& a, hipStream_t s) {
   }
   const int64_t items = (BWD ? a.strips : a.rows) * (int64_t)a.G, per = BWD ? 1 : team_threads(TL) / TL;
   const int64_t blocks = (items + per - 1) / per;
-  if (blocks > 0x7fffffff) return fail(SSM_E_SHAPE, "rows and ngroups: too many for one call");
+  if (!grid_ok(blocks, team_threads(TL))) return fail(SSM_E_SHAPE, "rows and ngroups: too many for one call");
   if constexpr (BWD) {
     if (!a.center && a.act == SSM_ACT_NONE && a.gate != SSM_GATE_AFTER && !a.pb)
       norm_bwd_kernel<IO, VE, TL, K, true><<<(unsigned)blocks, team_threads(TL), 0, s>>>(a);
@@ -2264,7 +2274,7 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
                 (long long)need);
   if (!aligned16(workspace)) return fail(SSM_E_ALIGN, "workspace is not 16-byte aligned");
   const MixLayout l = mix_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype);
-  if (l.nseg * l.units * l.sub > 0x7fffffff || l.nchunk > 0x7fffffff)
+  if (!grid_ok(l.nseg * l.units * l.sub, 64 * l.wv))
     return fail(SSM_E_SHAPE, "too many sequences and heads for one call");
   char* w = static_cast<char*>(workspace);
   a.head = reinterpret_cast<PlanHead*>(w);
@@ -2275,7 +2285,7 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
   a.local = reinterpret_cast<float*>(w + l.local);
   a.decay = reinterpret_cast<float*>(w + l.decay);
   a.cs0 = reinterpret_cast<float*>(w + l.cs0);
-  a.op_bytes = l.op_bytes; a.seg_len = l.seg_len; a.sub = l.sub; a.units = l.units; a.per_group = l.per_group;
+  a.seg_len = l.seg_len; a.sub = l.sub; a.units = l.units; a.per_group = l.per_group;
   const int es = io_dtype == SSM_DTYPE_BF16 ? 2 : 4, wide = 4 * l.pt * es < 16 ? 4 * l.pt * es : 16;
   const int64_t inner = nheads * headdim, ch = inner + 2 * ngroups * dstate;
   auto lanes = [&](const void* p, int64_t stride, int bytes) {  // whole accesses of that many bytes

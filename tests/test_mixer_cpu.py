@@ -255,3 +255,30 @@ def test_bf16_helper():
     torch = pytest.importorskip("torch")
     np.testing.assert_array_equal(ref.bf16(v), torch.from_numpy(v).bfloat16().double().numpy())
     assert oracle is not None
+
+
+# A launch has less than 2^32 threads: calls past that are refused before anything is enqueued
+# (pointers far enough apart that nothing overlaps).
+
+FAR = 1 << 44
+
+
+def test_launches_too_large_are_refused(lib):
+    import selective_state_space_43_amd as ssm
+    # a workgroup of 1024 threads for every block of 64 tokens
+    assert lib.ssm_conv_ssd_workspace_size(1 << 28, 1, 4, 64, 1, 64, 1) == -1
+    assert "tokens / 64" in ssm.ssm_last_error()
+    assert lib.ssm_conv_ssd_workspace_size((1 << 28) - 128, 1, 4, 64, 1, 64, 1) > 0
+    assert lib.ssm_conv_ssd_fwd(*fwd_args(tokens=1 << 28)) == 2
+    # 2^20 sequences x 64 workgroups of 256 threads
+    n = (1 << 20) - 1
+    far = dict(xbc=1 * FAR, dt=2 * FAR, y=3 * FAR, cs=4 * FAR, hs=5 * FAR)
+    big = dict(nslots=n, H=256, P=64, G=1, N=8, xs=256 * 64 + 16, ds=256, ys=256 * 64, **far)
+    need = lib.ssm_conv_ssd_workspace_size(1 << 20, n, 256, 64, 1, 8, 1)
+    assert lib.ssm_conv_ssd_fwd(*fwd_args(tokens=1 << 20, nseq=n, cu=6 * FAR, ws=7 * FAR, ws_bytes=need, **big)) == 2
+    assert "one call" in ssm.ssm_last_error()
+    assert lib.ssm_conv_ssd_update(*step_args(batch=n, **big)) == 2
+    assert "one call" in ssm.ssm_last_error()
+    # 2^27 rows of a group of 512, a wave each
+    assert lib.ssm_group_norm_fwd(*norm_args(x=1 * FAR, y=2 * FAR, xs=512, ys=512, rows=1 << 27, C=512, G=1)) == 2
+    assert "one call" in ssm.ssm_last_error()

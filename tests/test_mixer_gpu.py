@@ -446,6 +446,12 @@ def test_norm_autograd(ssm, dev):
         assert np.all(np.abs(f64(leaf.grad) - want[k]) <= 2 * ref.NORM_BWD * bound[k] + 1e-30), k
 
 
+def test_norm_autograd_is_once_differentiable(ssm, dev):
+    x = torch.randn(5, 40, device=dev, requires_grad=True)
+    with pytest.raises(RuntimeError, match="gradients of its gradients"):
+        torch.autograd.grad(ssm.group_norm_fn(x, None, 4).sum(), x, create_graph=True)
+
+
 def test_norm_special_rows(ssm, dev):
     """Constant and zero rows (a variance of zero), a NaN and an infinity in one
     row: the other rows, and the other group of that row, keep their values."""
