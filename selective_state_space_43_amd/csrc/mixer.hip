@@ -1302,7 +1302,7 @@ __global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
     s[v] = resume && at[v] < per ? a.state[slot * per + at[v]] : 0.0f;
   }
   float* l = a.local + (int64_t)ct.split * sub * per;
-  for (int k0 = 0; k0 <= last; k0 += K) {
+  for (int k0 = 0; k0 < last; k0 += K) {
     float own[K][V], dec[K][V];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
@@ -1315,13 +1315,16 @@ __global__ void __launch_bounds__(256) mix_join_kernel(const BlkArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (k0 + j <= last)
+      if (k0 + j < last)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           if ((k0 + j) % sub == 0 && at[v] < per) l[(k0 + j) * per + at[v]] = s[v];
           s[v] = fmaf(s[v], ex2(dec[j][v]), own[j][v]);
         }
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (at[v] < per) l[last * per + at[v]] = s[v];
 }
 
 // ---------------------------------------------------------------- one token a sequence
@@ -2017,10 +2020,15 @@ struct MixLayout {
   int64_t chunks, segs, cuts, ops, local, decay, cs0, bytes;
 };
 
-// A segment is one workgroup's work, one after another; the card holds 2048
-// waves at two a SIMD.
+// A segment is one workgroup's work, one after another, and the card holds 2048
+// waves at two a SIMD.  Segments for 1024 waves leave it half empty where one
+// long prompt has to fill it (four of 8192, 80 heads: 941 against 754 us) and win
+// where the prompts themselves do (16 of 8111 tokens in all: 211 against 228 us; but
+// one of 8000 beside 15 of 10: 268 against 234); for 4096 they come in two turns (872, 263).
+// Up to three blocks one after another take less time than cut (128 tokens, 80
+// heads: 38 against 49 us; four: 56 against 53).
 constexpr int64_t kSegWaves = 2048;
-constexpr int kSegMin = 4;
+constexpr int64_t kUncut = 3;
 
 MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N, int io_dtype) {
   MixLayout l;
@@ -2035,12 +2043,14 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   // as many segments as the card holds at once, not a few more
   const int64_t at_once = kSegWaves / l.wv / l.units, blocks = (tokens + kQ - 1) / kQ;
   int64_t len = at_once ? (blocks + at_once - 1) / at_once : blocks;
-  if (len < kSegMin) len = kSegMin;
+  if (len < kUncut && blocks <= kUncut) len = kUncut;
   l.seg_len = (int)len;
-  const bool cut = blocks > len;
-  l.nsplit = cut ? 2 * (l.nchunk / len) : 0;
-  l.ncut = cut ? l.nchunk / len : 0;
-  l.nseg = nseq + l.nchunk / len;
+  // a sequence of t tokens has 1 + (t - 1) / (64 len) segments and is cut if that is more than one
+  const int64_t more = (tokens - 1) / (kQ * len);
+  l.nsplit = 2 * more;
+  l.ncut = more;
+  l.nseg = nseq + more;
+  const bool cut = more > 0;
   // the first pass leaves out every sequence's last segment: its segments go in as many
   // pieces as fill the card's turns best
   const int64_t slots = kSegWaves / l.wv, first = (at_once - nseq) * l.units;
@@ -2048,6 +2058,7 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   if (cut && at_once > nseq)
     for (int n = 2; n <= 4; ++n)
       if ((first * n + slots - 1) / slots * l.sub < (first * l.sub + slots - 1) / slots * n) l.sub = n;
+  if (l.sub > len) l.sub = (int)len;
   const int64_t piece = (int64_t)kQ * l.nt * 16 * 2;
   const int64_t op_bytes = (l.pc + 2) * piece + kTri * 64 * 8 * (l.pc == 1 ? 2 : 4) + 320;
   int64_t at = 0;
@@ -2098,8 +2109,9 @@ void launch_mix(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
   }
 }
 
-// Eight rows a lane where that leaves two workgroups for every CU, two where
-// the card would stand half empty.
+// Eight rows a lane where that leaves two workgroups for every CU (253 tokens, 80
+// heads: 274 us against 291 with two rows), two where the card would stand half empty
+// (one token: 11.3 against 12.4).
 constexpr int64_t kStepWorkgroups = 512;
 
 template <typename IO, int LN, bool VEC>
@@ -2191,7 +2203,12 @@ int launch_norm_team(NormArgs& a, hipStream_t s) {
   return launch_status(BWD ? "ssm_group_norm_bwd launch" : "ssm_group_norm_fwd launch");
 }
 
-// The smallest team whose registers hold the group.
+// The smallest team whose registers hold the group, with as few of them unused as
+// may be: a wave of up to ten vectors a lane took 203 us where 256 threads of four take
+// 187 (32768 rows of 5120, bf16), and 318 where a wave of up to two takes 207 (eight
+// groups of 640).  The backward holds more a vector: 1024 threads of four took 221 us where
+// 512 of two take 171 (8000 rows of 8192), a wave of two 435 where 32 threads of three
+// take 348 (32768 rows, eight groups of 640).
 template <bool BWD, typename IO>
 int launch_norm_io(NormArgs& a, bool vec, hipStream_t s) {
   constexpr int VE = 16 / sizeof(IO);
@@ -2202,12 +2219,12 @@ int launch_norm_io(NormArgs& a, bool vec, hipStream_t s) {
       if (nv <= 32 * 3) return launch_norm_team<true, IO, VE, 32, 3>(a, s);
       if (nv <= 64 * 3) return launch_norm_team<true, IO, VE, 64, 3>(a, s);
       if (nv <= 256 * 3) return launch_norm_team<true, IO, VE, 256, 3>(a, s);
+      if (nv <= 512 * 2) return launch_norm_team<true, IO, VE, 512, 2>(a, s);
     } else {
+      if (nv <= 8) return launch_norm_team<false, IO, VE, 8, 1>(a, s);
       if (nv <= 8 * 4) return launch_norm_team<false, IO, VE, 8, 4>(a, s);
-      // a wave a group has the least to wait for, 256 threads the least to do one after
-      // the other, which counts while there are few groups
-      const bool few = a.rows * a.G <= 512;
-      if (nv <= (few ? 64 : 64 * 10)) return launch_norm_team<false, IO, VE, 64, 10>(a, s);
+      if (nv <= 64 * 2) return launch_norm_team<false, IO, VE, 64, 2>(a, s);
+      if (nv <= 64 * 4) return launch_norm_team<false, IO, VE, 64, 4>(a, s);
       if (nv <= 256 * 4) return launch_norm_team<false, IO, VE, 256, 4>(a, s);
     }
     if (nv <= 1024 * 4) return launch_norm_team<BWD, IO, VE, 1024, 4>(a, s);
