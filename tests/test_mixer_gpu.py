@@ -142,6 +142,16 @@ PROMPTS = [  # lens, H, P, G, N, W, dtype, options
     ((4100,), 1, 64, 1, 64, 4, "f32", dict(has=True)),
     ((3000, 2000), 10, 64, 5, 128, 4, "bf16", {}),
     ((2100,), 3, 40, 1, 256, 2, "bf16", dict(has=True, lead=1)),
+    # three blocks are not cut, four are; nine leave a whole round of the joining
+    ((192,), 2, 64, 1, 128, 4, "bf16", dict(has=True)),
+    ((193,), 2, 64, 1, 128, 4, "bf16", dict(has=True)),
+    ((576,), 2, 64, 1, 128, 4, "bf16", dict(has=True)),
+    ((513,), 2, 64, 1, 128, 4, "f32", dict(has=True)),
+    # segments of three blocks, their first pass in three pieces, in two, and in one
+    ((1700, 100, 1, 300), 80, 64, 1, 16, 4, "bf16", dict(has=True)),
+    ((1700, 100, 1, 300), 80, 64, 1, 16, 4, "f32", dict(has=True)),
+    ((1500,) + (3,) * 13, 80, 64, 1, 16, 4, "bf16", {}),
+    ((900, 40), 80, 64, 1, 16, 4, "bf16", {}),
 ]
 
 
@@ -393,6 +403,24 @@ NORMS = [  # rows, channels, groups, dtype, center, act, gate, options
     (17, 4096, 1, "f32", True, "silu", "before", {}),
     (600, 260, 13, "bf16", True, "none", "none", dict(lead=3)),
     (130, 12000, 1, "bf16", False, "none", "before", {}),
+    # both sides of every change of team
+    (40, 192, 3, "bf16", False, "none", "before", dict(bias=False)),
+    (21, 72, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (21, 512, 2, "bf16", False, "none", "before", dict(bias=False)),
+    (9, 264, 1, "bf16", True, "silu", "after", {}),
+    (6, 768, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (6, 776, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (6, 1024, 1, "bf16", True, "silu", "after", {}),
+    (6, 1032, 1, "bf16", True, "none", "none", {}),
+    (5, 1536, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (5, 2048, 1, "bf16", False, "silu", "before", {}),
+    (5, 2056, 1, "bf16", True, "none", "after", {}),
+    (9, 6144, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (9, 6152, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (2100, 8192, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (9, 8192, 1, "bf16", True, "silu", "after", {}),
+    (9, 8200, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (7, 4100, 1, "f32", False, "none", "before", dict(bias=False)),
 ]
 
 
@@ -404,7 +432,7 @@ def norm_problem(dev, case, seed):
     x = dict(x=q(rng.standard_normal((rows, C)) + 0.5), dy=q(rng.standard_normal((rows, C))),
              z=q(rng.standard_normal((rows, C))) if gate != "none" else None,
              w=f(1 + 0.3 * rng.standard_normal(C)) if opt.get("weight", True) else None,
-             b=f(0.3 * rng.standard_normal(C)) if opt.get("weight", True) else None)
+             b=f(0.3 * rng.standard_normal(C)) if opt.get("bias", opt.get("weight", True)) else None)
     parts = [v for v in (x["x"], x["dy"], x["z"]) if v is not None]
     t = rows_of(parts, dev, dtype, opt.get("lead", 0))
     t = dict(x=t[0], dy=t[1], z=t[2] if len(t) > 2 else None, w=up(x["w"], dev), b=up(x["b"], dev))
