@@ -624,7 +624,7 @@ template <int PT>
 struct XTile {
   static constexpr int RB = 32 * PT, RI = 1024 / RB, GP = RI / 8;  // bytes of a row, rows and groups a load
   static constexpr int step = PT == 2 ? 1152 : 1024, loads = (kQ + 3 + RI - 1) / RI;
-  static constexpr int bytes = PT == 2 ? 4928 : 3072;
+  static constexpr int bytes = PT == 2 ? 4928 : loads * step;
   static_assert((loads - 1) * step + ((kQ + 2) % 8 * GP + 1) * RB <= bytes, "the last rows fit");
   // bytes of row 8 a + b
   __device__ static __forceinline__ int at(int a, int b) { return a / GP * step + (GP * b + a % GP) * RB; }
