@@ -723,7 +723,8 @@ mix_block_kernel(const BlkArgs a) {
   f4 S[PT][NT];
   {
     const float* src = nullptr;
-    if (sg.split >= 0 && sg.c0 > 0) src = SUM ? nullptr : a.local + (int64_t)sg.split * a.sub * inner * N;
+    // a cut sequence's first segment too has its start in `local`: the last one writes the slot in this same launch
+    if (sg.split >= 0) src = SUM ? nullptr : a.local + (int64_t)sg.split * a.sub * inner * N;
     else if (!SUM && resume) src = a.state + slot * inner * N;
 #pragma unroll
     for (int e = 0; e < PT; ++e)
