@@ -1,13 +1,123 @@
 """The Mamba-2 mixer's operators on the GPU where tests/test_mixer_gpu.py does not
-reach: prompts cut into segments beside other work on the card.  Problems,
-references and bounds as there."""
+reach: rows on 16 bytes, as a model's projection has them, in every size of the
+kernels for whole vectors; the general kernels on cut prompts; prompts cut into
+segments beside other work on the card.  Problems, references and bounds as
+there."""
 import pytest
 
-from test_mixer_gpu import Mix, dev, ssm  # noqa: F401  (fixtures)
+import test_mixer_gpu as base
+from test_mixer_gpu import IO, Mix, dev, rows_of, ssm, up  # noqa: F401  (fixtures)
 
 torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
+
+
+class Aligned(Mix):
+    """Rows in the projection's order, z, xbc, dt, every one of them on 16 bytes."""
+
+    def load(self, lead=0, tail=0):
+        super().load()
+        x = self.x
+        parts = [v for v in (x["z"], x["xbc"], x["dt"]) if v is not None]
+        whole = 16 // IO[self.dtype].itemsize
+        *z, self.xbc, self.dt = rows_of(parts, self.dev, self.dtype, 0, -sum(p.shape[1] for p in parts) % whole)
+        self.z = z[0] if z else None
+        for t in (*z, self.xbc):
+            assert t.data_ptr() % 16 == 0 and t.stride(0) * t.element_size() % 16 == 0
+
+
+CASES = [  # layout, lens, H, P, G, N, W, dtype, options
+    # bf16: 64, 128 and 256 states; heads of whole and of broken tiles; cut from four blocks on
+    (Aligned, (65, 63, 1, 0, 2, 128), 4, 64, 2, 128, 4, "bf16", dict(behind=5)),
+    (Aligned, (192,), 2, 64, 1, 128, 4, "bf16", dict(has=True)),
+    (Aligned, (193,), 2, 64, 1, 128, 4, "bf16", dict(has=True)),
+    (Aligned, (576, 1), 2, 64, 1, 128, 4, "bf16", dict(has=True, gate=False)),
+    (Aligned, (2500, 1, 700), 2, 64, 1, 128, 4, "bf16", dict(has=True)),
+    (Aligned, (3000, 2000), 10, 64, 5, 128, 4, "bf16", {}),
+    (Aligned, (1500, 3, 90), 24, 64, 1, 128, 4, "bf16", dict(has=True, gate=False)),
+    (Aligned, (37,), 24, 64, 1, 128, 4, "bf16", dict(gate=False, state=False)),
+    (Aligned, (90, 33), 8, 48, 2, 128, 4, "bf16", dict(has=True)),
+    (Aligned, (300, 70), 3, 48, 1, 96, 3, "bf16", dict(gate=False, has=True)),
+    (Aligned, (70, 130), 3, 80, 1, 128, 4, "bf16", dict(has=True)),
+    (Aligned, (500,), 2, 80, 2, 64, 4, "bf16", dict(has=True, gate=False)),
+    (Aligned, (100, 64, 30), 5, 64, 1, 64, 4, "bf16", {}),
+    (Aligned, (700, 20), 5, 64, 1, 64, 2, "bf16", dict(has=True, gate=False)),
+    (Aligned, (200, 7), 2, 64, 1, 256, 4, "bf16", {}),
+    (Aligned, (600, 64), 3, 64, 1, 256, 4, "bf16", dict(has=True)),
+    (Aligned, (900,), 4, 48, 2, 256, 4, "bf16", dict(has=True, gate=False)),
+    (Aligned, (77, 300), 3, 24, 1, 200, 3, "bf16", dict(has=True)),
+    (Aligned, (90, 300), 3, 8, 1, 128, 4, "bf16", dict(has=True)),
+    (Aligned, (80,), 2, 256, 1, 128, 1, "bf16", dict(has=True)),
+    (Aligned, (150, 9), 2, 40, 1, 20, 4, "bf16", dict(has=True)),
+    # columns behind x: 32 let whole tiles be read past the last head, 24 do not
+    (Aligned, (150, 9), 3, 48, 1, 16, 4, "bf16", dict(has=True)),
+    (Aligned, (150, 9), 3, 48, 1, 12, 4, "bf16", dict(has=True)),
+    # float32: whole and general, cut and not, up to 256 states
+    (Aligned, (600, 70), 4, 64, 1, 128, 4, "f32", dict(has=True)),
+    (Aligned, (64, 129, 1), 16, 64, 2, 128, 4, "f32", dict(gate=False)),
+    (Aligned, (150, 40), 2, 64, 1, 256, 4, "f32", dict(has=True)),
+    (Aligned, (700,), 3, 48, 1, 256, 4, "f32", dict(has=True, gate=False)),
+    (Aligned, (500, 30), 3, 40, 1, 64, 4, "f32", dict(has=True)),
+    (Aligned, (400,), 2, 24, 2, 32, 2, "f32", dict(has=True)),
+    (Mix, (600, 70), 3, 64, 1, 128, 4, "f32", dict(has=True, lead=1)),
+    (Mix, (500,), 2, 50, 1, 250, 4, "f32", dict(has=True, lead=1)),
+    (Mix, (500,), 3, 33, 1, 30, 3, "f32", dict(has=True)),
+    (Mix, (600, 70), 3, 64, 1, 128, 4, "bf16", dict(has=True, lead=1)),
+    (Mix, (500,), 2, 50, 1, 250, 4, "bf16", dict(has=True, lead=1)),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_prompts(ssm, dev, case):  # noqa: F811
+    layout, lens, H, P, G, N, W, dtype, opt = CASES[case]
+    m = layout(dev, lens, H, P, G, N, W, dtype, 1100 + case, **opt)
+    m.run(ssm)
+    torch.cuda.synchronize()
+    m.check(str(CASES[case][1:]))
+
+
+@pytest.fixture
+def aligned(monkeypatch):
+    monkeypatch.setattr(base, "Mix", Aligned)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["x", "B", "C", "dt", "z"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_input(aligned, ssm, dev, dtype, where, bad):  # noqa: F811
+    base.test_non_finite_input(ssm, dev, dtype, where, bad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_non_finite_state(aligned, ssm, dev, dtype):  # noqa: F811
+    base.test_non_finite_state(ssm, dev, dtype)
+
+
+def test_extreme_steps(aligned, ssm, dev):  # noqa: F811
+    base.test_extreme_steps(ssm, dev)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("how", ["A", "dt"])
+def test_growing_state(aligned, ssm, dev, dtype, how):  # noqa: F811
+    base.test_growing_state(ssm, dev, dtype, how)
+
+
+def test_far_rows_and_slots(aligned, ssm, dev):  # noqa: F811
+    base.test_far_rows_and_slots(ssm, dev)
+
+
+def test_same_as_the_dense_operators(aligned, ssm, dev):  # noqa: F811
+    base.test_same_as_the_dense_operators(ssm, dev)
+
+
+def test_repeatable(aligned, ssm, dev):  # noqa: F811
+    base.test_repeatable(ssm, dev)
+
+
+def test_graph_replays_and_streams(aligned, ssm, dev):  # noqa: F811
+    base.test_graph_replays_and_streams(ssm, dev)
 
 
 def test_cut_prompts_beside_other_work(ssm, dev):  # noqa: F811
