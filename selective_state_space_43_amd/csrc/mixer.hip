@@ -92,11 +92,11 @@ constexpr int kMaxN = 256;
 // segment from the state entering it.
 //
 // Precision: the accumulators, the state, the running sums (float64) and all
-// statistics are float32 or more.  The operands are fp16, scaled by a power of
-// two from the largest value of their tile, so that no value of float32's
-// range is lost to fp16's.  What goes into the state has two pieces (hi + lo, 22
-// bits, three products); what goes into y alone has one for bf16 rows (11 bits, 2^-11
-// beside the 2^-8 of the stored y) and two for float32 rows.
+// statistics are float32 or more.  The operands are fp16 in two pieces (hi + lo, 22
+// bits, three products; lo x lo, 2^-24 of the product, is left out), scaled by a
+// power of two from the largest value of their tile.  One piece for what enters y
+// alone (11 bits beside the 8 of a stored bf16) would cost 1e-3 of y where two cost
+// what the float32 sums do.
 
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -150,14 +150,13 @@ struct BlkArgs : MixArgs {
 };
 
 // Offsets of the parts of one (block, group)'s operands.
-template <int NT, int NPC>
+template <int NT>
 struct Ops {
   static constexpr int piece = kQ * NT * 16 * 2;  // one fp16 piece of B or C
-  static constexpr int ge = NPC == 1 ? 2 : 4;     // bytes of an element of C.B^T: fp16 or float32
-  static constexpr int c = 0, b = NPC * piece, g = b + 2 * piece;
-  static constexpr int gsize = kTri * 64 * 8 * ge;
-  static constexpr int scale = g + gsize;  // 64 rows' shifts of C.B^T, B's, C's
-  static constexpr int bytes = scale + 320;
+  static constexpr int c = 0, b = 2 * piece, g = 4 * piece;
+  static constexpr int gsize = kTri * 64 * 8 * 4;  // C.B^T in float32
+  static constexpr int scale = g + gsize;          // B's and C's shifts
+  static constexpr int bytes = scale + 64;
 };
 
 __device__ __forceinline__ float wave_max(float v) {  // v >= 0; uniform result
@@ -230,34 +229,6 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// Eight products rounded once to fp16, two to a register; the s_nop lets the
-// half-register writes settle before any reader.
-#define MIX_PAIR(d, x0, x1, y0, y1, s0, s1, h)                                  \
-  "v_fma_mixlo_f16 " d ", " x0 ", " y0 ", 0 op_sel:[0,0,0] op_sel_hi:[" h ",0,0]\n\t" \
-  "v_fma_mixhi_f16 " d ", " x1 ", " y1 ", 0 op_sel:[" s1 ",0,0] op_sel_hi:[" h ",0,0]\n\t"
-// v[j] f
-__device__ __forceinline__ h8 scaled(const float* v, float f) {
-  u4 o;
-  asm(MIX_PAIR("%0", "%4", "%5", "%12", "%12", "0", "0", "0") MIX_PAIR("%1", "%6", "%7", "%12", "%12", "0", "0", "0")
-      MIX_PAIR("%2", "%8", "%9", "%12", "%12", "0", "0", "0") MIX_PAIR("%3", "%10", "%11", "%12", "%12", "0", "0", "0")
-      "s_nop 1"
-      : "=&v"(o.x), "=&v"(o.y), "=&v"(o.z), "=&v"(o.w)
-      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "v"(f));
-  return __builtin_bit_cast(h8, o);
-}
-// h[j] v[j], h in fp16
-__device__ __forceinline__ h8 times(u4 h, const float* v) {
-  u4 o;
-  asm(MIX_PAIR("%0", "%4", "%4", "%8", "%9", "0", "1", "1") MIX_PAIR("%1", "%5", "%5", "%10", "%11", "0", "1", "1")
-      MIX_PAIR("%2", "%6", "%6", "%12", "%13", "0", "1", "1") MIX_PAIR("%3", "%7", "%7", "%14", "%15", "0", "1", "1")
-      "s_nop 1"
-      : "=&v"(o.x), "=&v"(o.y), "=&v"(o.z), "=&v"(o.w)
-      : "v"(h.x), "v"(h.y), "v"(h.z), "v"(h.w), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]),
-        "v"(v[6]), "v"(v[7]));
-  return __builtin_bit_cast(h8, o);
-}
-#undef MIX_PAIR
-
 // v w = hi + lo in fp16, to 22 bits; lo takes in what v w itself was rounded by
 __device__ __forceinline__ void pieces(const float* v, const float* w, h8& hi, h8& lo) {
 #pragma unroll
@@ -278,14 +249,10 @@ __device__ __forceinline__ void pieces(const float* v, h8& hi, h8& lo) {
     hi[j] = a.x; hi[j + 1] = a.y; lo[j] = b.x; lo[j + 1] = b.y;
   }
 }
-__device__ __forceinline__ h8 piece(const float* v) {
-  h8 o;
+// hi + lo
+__device__ __forceinline__ void joined(const h8& hi, const h8& lo, float* v) {
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const h2 a = __builtin_convertvector((f2){v[j], v[j + 1]}, h2);
-    o[j] = a.x; o[j + 1] = a.y;
-  }
-  return o;
+  for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf((float)hi[j], 1.0f, (float)lo[j]);
 }
 
 // ---- the plan: sequences -> blocks and segments (one workgroup)
@@ -405,11 +372,11 @@ __global__ void __launch_bounds__(1024) mix_plan_kernel(const BlkArgs a) {
 
 constexpr int kPrep = 1024;  // threads: one round of loads up to 128 states
 
-template <typename IO, int NT, int NPC>
+template <typename IO, int NT>
 __global__ void __launch_bounds__(kPrep) mix_prep_kernel(const BlkArgs a) {
   constexpr int NP = NT * 16, LD = NP + 8;         // row pitch in LDS: 16 bytes more, banks apart
   constexpr int UN = (8 * NP + kPrep - 1) / kPrep;  // (channel, 16 rows) units of a thread
-  using O = Ops<NT, NPC>;
+  using O = Ops<NT>;
   __shared__ __align__(16) _Float16 sm[2][2][kQ * LD];  // [B, C][hi, lo]
   __shared__ float red[2][16];
   const Chunk ck = a.chunks[blockIdx.x];  // garbage past the last one, which ends here
@@ -488,7 +455,7 @@ __global__ void __launch_bounds__(kPrep) mix_prep_kernel(const BlkArgs a) {
   for (int u = tid; u < 4 * (NT / 2) * 64; u += kPrep) {
     const int l = u & 63, m = (u >> 6) % (NT / 2), tt = (u >> 6) / (NT / 2);
 #pragma unroll
-    for (int p = 0; p < NPC; ++p) {
+    for (int p = 0; p < 2; ++p) {
       const _Float16* s = sm[1][p] + (16 * tt + (l & 15)) * LD + 32 * m + 4 * (l >> 4);
       h8 o;
       const h4 x = *reinterpret_cast<const h4*>(s), y = *reinterpret_cast<const h4*>(s + 16);
@@ -535,37 +502,15 @@ __global__ void __launch_bounds__(kPrep) mix_prep_kernel(const BlkArgs a) {
       }
     }
   }
-  int shG = 0;
-  if constexpr (NPC == 1) {  // to fp16, every row by its own largest value, zero after the row's token
-    float gm = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const bool after = 32 * (i >> 3) + 8 * (lane >> 4) + (i & 7) > 16 * wave + (lane & 15);
-      const float x = after ? 0.0f : acc[i >> 3][(i >> 2) & 1][i & 3];
-      acc[i >> 3][(i >> 2) & 1][i & 3] = x;
-      if (finite(x)) gm = fmaxf(gm, fabsf(x));
-    }
-    shG = shift_for(row_max(gm));
-  }
-  const float fg = two(shG);
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
     if (kb > (wave >> 1)) break;
     const int tile = wave < 2 ? wave : 2 * wave - 2 + kb;
-    char* o = out + O::g + (tile * 64 + lane) * 8 * O::ge;
-    if constexpr (NPC == 1) {
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = acc[kb][j >> 2][j & 3] * fg;
-      *reinterpret_cast<h8*>(o) = piece(x);
-    } else {
-      reinterpret_cast<f4*>(o)[0] = acc[kb][0];
-      reinterpret_cast<f4*>(o)[1] = acc[kb][1];
-    }
+    f4* o = reinterpret_cast<f4*>(out + O::g + (tile * 64 + lane) * 32);
+    o[0] = acc[kb][0];
+    o[1] = acc[kb][1];
   }
-  int* sc = reinterpret_cast<int*>(out + O::scale);
-  if (lane < 16) sc[16 * wave + lane] = shG;
-  if (tid < 2) sc[64 + tid] = sh[tid];
+  if (tid < 2) reinterpret_cast<int*>(out + O::scale)[tid] = sh[tid];
 }
 
 // ---- the walk over a segment
@@ -644,37 +589,33 @@ struct XRaw {
 // One wave per 16 PT channels of a head (PT = 2: channels 2 i and 2 i + 1 of
 // its 32 are row i of the two tiles, so that a lane reads x two channels and
 // z, y eight channels at a time).  The WV waves of a workgroup share a group
-// of heads and its operands in LDS.  A block goes convolution, state, y: its C
-// and C.B^T arrive while the waves convolve and update the state, the next
-// block's B while they work on y, the next block's x and dt from the
-// convolution's end on.  PC: pieces of the operands of y.  FAST: rows and
-// channels allow whole vectors (headdim a multiple of 4 PT, dstate of 4, rows
-// aligned to the accesses).
+// of heads and its operands in LDS.  A block goes convolution, C.h, M x with y,
+// state: C arrives while the waves convolve, B, in C's place, while they work on
+// M x, and the next block's C.B^T while they update the state; the next block's x
+// and dt come from the convolution's end on.  FAST: rows and channels allow whole
+// vectors (headdim a multiple of 4 PT, dstate of 4, rows aligned to the accesses).
 //
-// Bound by latency: four prompts of 8192 with 80 heads of 64 channels and 128
-// states take 582 us in the second pass and 188 in the first.  A wave and block
-// of the second is 2148 vector instructions, 148 of them products: the vector
-// units are busy 60 % of the time, the matrix cores 15 %, and a wave waits 37 %
-// of its own.  The state (64 registers), its fp16 copy and x as two operands hold
-// it to two waves a SIMD (246 registers, 79 KB of LDS a workgroup); the first
-// pass at three spills (802 us a call against 788).  Past 128 states a wave has 16
-// channels instead of 32, so that its state stays at 64 registers.
-template <typename IO, int NT, int PT, int PC, int WV, bool SUM, bool FAST>
-__global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(NT == 8 && PC == 2 && !SUM ? 1 : 2)))
+// Bound by latency and vector instructions: two waves a SIMD, which the state (64
+// registers) and the operands of x force.  B and C by turns in one place leave room for two
+// workgroups of four waves a CU at 128 states; both at once, one workgroup of
+// eight, took 892 us for four prompts of 8192 with 80 heads of 64 channels and 128 states
+// against 872, and 286 against 255 for 16 ragged prompts of 8111 tokens.  Past 128 states
+// a wave has 16 channels instead of 32, so that its state stays at 64 registers.
+template <typename IO, int NT, int PT, int WV, bool SUM, bool FAST>
+__global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(2)))
 mix_block_kernel(const BlkArgs a) {
-  using O = Ops<NT, PC>;
+  using O = Ops<NT>;
   constexpr int PB = 16 * PT;  // channels of a wave
-  __shared__ __align__(16) char s_b[2 * O::piece];
-  __shared__ __align__(16) char s_cg[SUM ? 16 : O::gsize + PC * O::piece];
-  constexpr int CG = PC * O::piece;  // C.B^T behind C
+  __shared__ __align__(16) char s_bc[2 * O::piece];  // C, then B
+  __shared__ __align__(16) char s_g[SUM ? 16 : O::gsize];
   constexpr bool XLDS = FAST && sizeof(IO) == 2;
   using X = XTile<PT>;
   __shared__ __align__(16) char s_x[XLDS ? WV * X::bytes : 16];
-  __shared__ __align__(16) int s_sc[SUM ? 1 : 2][68];
+  __shared__ __align__(16) int s_sc[2][4];
   __shared__ __align__(16) float s_w[WV][64];
   // for y alone
-  __shared__ __align__(16) float s_cum[SUM ? 1 : WV][SUM ? 4 : 64], s_dt[SUM ? 1 : WV][SUM ? 4 : 64];
-  __shared__ __align__(16) float s_lo[!SUM && PC == 2 ? WV : 1][!SUM && PC == 2 ? 64 : 4];
+  __shared__ __align__(16) float s_cum[SUM ? 1 : WV][SUM ? 4 : 64], s_low[SUM ? 1 : WV][SUM ? 4 : 64];
+  __shared__ __align__(16) float s_dt[SUM ? 1 : WV][SUM ? 4 : 64];
   __shared__ int s_bad[SUM ? 1 : WV][SUM ? 4 : PB];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i16 = lane & 15, q4 = lane >> 4;
@@ -802,13 +743,18 @@ mix_block_kernel(const BlkArgs a) {
   };
   const char* op = a.ops + ((int64_t)sg.gc * a.G + g) * O::bytes;
   const int64_t op_step = (int64_t)a.G * O::bytes;
-  auto stage_b = [&](const char* from, int at) {  // B and the scales
-    stage<WV, 2 * O::piece>(from + O::b, s_b);
-    stage_few<17>(from + O::scale, reinterpret_cast<char*>(s_sc[at]));
+  auto stage_b = [&] { stage<WV, 2 * O::piece>(op + O::b, s_bc); };
+  auto stage_c = [&] { stage<WV, 2 * O::piece>(op + O::c, s_bc); };
+  auto stage_scales = [&](const char* from, int at) {
+    stage_few<1>(from + O::scale, reinterpret_cast<char*>(s_sc[at]));
+  };
+  auto stage_g = [&](const char* from, int at) {
+    stage<WV, O::gsize>(from + O::g, s_g);
+    stage_scales(from, at);
   };
   if (sg.nc > 0) {
     if (on) fetch(0);
-    if constexpr (!SUM) stage_b(op, 0);
+    if constexpr (!SUM) stage_g(op, 0);
   }
 
   for (int c = 0; c < sg.nc; ++c) {
@@ -817,19 +763,17 @@ mix_block_kernel(const BlkArgs a) {
     int here = threadIdx.x & 63;
     asm volatile("" : "+v"(here));
     const int lane = here, i16 = here & 15, q4 = here >> 4;
-    // x, dt (and B) are there; y's four stores, at least, came after their loads
-    if (!SUM && on && c) arrived<4>();
-    else arrived<0>();
-    meet();  // and the waves are done with the last block's C (SUM: B)
+    arrived<0>();
+    meet();  // x, dt and C.B^T are there; the waves are done with the last block's B
     if constexpr (SUM) {
-      stage_b(op, 0);
+      stage_b();
+      stage_scales(op, 0);
     } else {
-      stage<WV, CG>(op + O::c, s_cg);
-      stage<WV, O::gsize>(op + O::g, s_cg + CG);
+      stage_c();
     }
-    h8 xh[PT][2], xl[PT][2], wh[PT][2], wl[PT][2], sh[PT][NT / 2], sl[PT][NT / 2];
-    float dec_all = 1.0f, cap = 0.0f;
-    int shx = 0, shd = 0, shS = 0;
+    h8 xh[PT][2], xl[PT][2];  // x as an operand; then, and at once in the first pass, weighted for the state
+    float dec_all = 1.0f;
+    int shx = 0, shd = 0;
     bool bad = false;
     if (on) {
       // ---- the convolution
@@ -919,18 +863,19 @@ mix_block_kernel(const BlkArgs a) {
       const float wt = dt * ex2((float)(tot - cum));
       dec_all = ex2((float)tot);
       dsum += tot;
-      if constexpr (!SUM) s_cum[wave][lane] = (float)cum;
-      if constexpr (!SUM && PC == 2) s_lo[wave][lane] = (float)(cum - (double)(float)cum);
-      // the weights exp(c_t - c_s) dt_s of M and of the state: at most the largest dt, unless
+      // what float32 leaves off a running sum goes with the step and with y's row, as a factor
+      const float low = (float)(cum - (double)(float)cum);
+      if constexpr (!SUM) s_cum[wave][lane] = (float)cum, s_low[wave][lane] = ex2(low);
+      // the state's weights exp(c_Q - c_s) dt_s: at most the largest dt, unless
       // the state grows
       shd = -__builtin_amdgcn_frexp_expf(wave_max(finite(dt) ? fabsf(dt) : 0.0f));
       if (__any(dA > 0.0f)) {
         rarely();
-        cap = fminf(wave_max(fmaxf((float)cum, 0.0f)) + wave_max(fmaxf(-(float)cum, 0.0f)), 100.0f);
+        const float cap = fminf(wave_max(fmaxf((float)cum, 0.0f)) + wave_max(fmaxf(-(float)cum, 0.0f)), 100.0f);
         shd -= (int)cap + 1;
       }
       shd = shd < -112 ? -112 : (shd > 60 ? 60 : shd);
-      if constexpr (!SUM) s_dt[wave][lane] = PC == 2 ? dt : finite(dt) ? dt * two(shd) : 0.0f;
+      if constexpr (!SUM) s_dt[wave][lane] = dt * ex2(-low);
       // ---- silu, the tile's scale
       float mx = 0.0f;
 #pragma unroll
@@ -982,39 +927,39 @@ mix_block_kernel(const BlkArgs a) {
         }
       }
       shx = shift_for(wave_max(mx));
-      s_w[wave][lane] = wt * two(shx + shd);
+      s_w[wave][lane] = wt * two(SUM ? shx + shd : shd);
       const float fx = two(shx);
       __builtin_amdgcn_wave_barrier();
-
-      // ---- operands from x: once as it is (for y), once weighted (for the state)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        float w8[8];
-        *reinterpret_cast<f4*>(w8) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4]);
-        *reinterpret_cast<f4*>(w8 + 4) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4 + 4]);
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int e = 0; e < PT; ++e) {
-          pieces(v[e][kb], w8, wh[e][kb], wl[e][kb]);
-          if constexpr (!SUM) {
+          if constexpr (SUM) {
+            float w8[8];
+            *reinterpret_cast<f4*>(w8) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4]);
+            *reinterpret_cast<f4*>(w8 + 4) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4 + 4]);
+            pieces(v[e][kb], w8, xh[e][kb], xl[e][kb]);
+          } else {
             if (bad) {  // 0 x Inf is not 0: y's earlier rows must not meet them
               rarely();
 #pragma unroll
               for (int j = 0; j < 8; ++j) v[e][kb][j] = finite(v[e][kb][j]) ? v[e][kb][j] : 0.0f;
             }
-            if constexpr (PC == 2) {
-              float x[8];
+            float x[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) x[j] = v[e][kb][j] * fx;
-              pieces(x, xh[e][kb], xl[e][kb]);
-            } else {
-              xh[e][kb] = scaled(v[e][kb], fx);
-            }
+            for (int j = 0; j < 8; ++j) x[j] = v[e][kb][j] * fx;
+            pieces(x, xh[e][kb], xl[e][kb]);
           }
         }
-      }
-
-      if constexpr (!SUM) {
-        // ---- the state as an operand
+    } else {
+      arrived<0>();
+    }
+    if constexpr (!SUM) {
+      meet();  // C is there
+      f4 yc[4][PT] = {};
+      int shS = 0;
+      if (on) {
+        // ---- C.h for all rows: the state's pieces are made once and kept no longer than their products
         float sm = 0.0f;
 #pragma unroll
         for (int e = 0; e < PT; ++e)
@@ -1038,164 +983,95 @@ mix_block_kernel(const BlkArgs a) {
         shS = shift_for(sm);
         const float fs = two(shS);
 #pragma unroll
-        for (int e = 0; e < PT; ++e)
-#pragma unroll
-          for (int m = 0; m < NT / 2; ++m) {
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * (PC == 2 ? fs : 1.0f);
-            if constexpr (PC == 2) pieces(x, sh[e][m], sl[e][m]);
-            else sh[e][m] = scaled(x, fs);
-          }
-      }  // the state as an operand
-
-      auto su = [&](int shB) {  // ---- the state after the block
-        const float f_su = two(max(-126, -(shB + shx + shd)));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          h8 bh[2], bl[2];
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb) {
-            bh[kb] = *reinterpret_cast<const h8*>(s_b + ((nt * 2 + kb) * 64 + lane) * 16);
-            bl[kb] = *reinterpret_cast<const h8*>(s_b + O::piece + ((nt * 2 + kb) * 64 + lane) * 16);
-          }
+        for (int m = 0; m < NT / 2; ++m) {
+          h8 sh[PT], sl[PT];
 #pragma unroll
           for (int e = 0; e < PT; ++e) {
-            f4 d = {};
+            float x[8];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-              d = mfma(bh[kb], wl[e][kb], d);
-              d = mfma(bl[kb], wh[e][kb], d);
-              d = mfma(bh[kb], wh[e][kb], d);
+            for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * fs;
+            pieces(x, sh[e], sl[e]);
+          }
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) {
+            const char* cq = s_bc + ((tt * (NT / 2) + m) * 64 + lane) * 16;
+            const h8 ch = *reinterpret_cast<const h8*>(cq), cl = *reinterpret_cast<const h8*>(cq + O::piece);
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              yc[tt][e] = mfma(sl[e], ch, yc[tt][e]);
+              yc[tt][e] = mfma(sh[e], cl, yc[tt][e]);
+              yc[tt][e] = mfma(sh[e], ch, yc[tt][e]);
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[e][nt][r] = fmaf(d[r], f_su, S[e][nt][r] * dec_all);
           }
         }
-      };
-      if constexpr (SUM) {
-        meet();  // B is there
-        su(__builtin_amdgcn_readfirstlane(s_sc[0][64]));
-      } else {
-        su(__builtin_amdgcn_readfirstlane(s_sc[c & 1][64]));
       }
-    } else {
-      arrived<0>();
-      if constexpr (SUM) meet();
-    }
-    op += op_step;
-    if constexpr (!SUM) {
-      meet();  // C and C.B^T are there; the waves are done with B
-      if (c + 1 < sg.nc) stage_b(op, (c + 1) & 1);
+      meet();  // the waves are done with C
+      stage_b();
       asm volatile("" ::: "memory");  // the stores of y stay behind these loads: arrived<4>() counts on it
       if (on) {
-        const int* sc = s_sc[c & 1];
-        const int shB = __builtin_amdgcn_readfirstlane(sc[64]), shC = __builtin_amdgcn_readfirstlane(sc[65]);
-        const int e_mx = -(shB + shC + shx), e_cs = -(shC + shS);
-        // ---- y, 16 rows at a time
+        const int shC = __builtin_amdgcn_readfirstlane(s_sc[c & 1][1]);
+        const int shBC = __builtin_amdgcn_readfirstlane(s_sc[c & 1][0]) + shC;
+        // ---- M x and y, 16 rows at a time
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           if (16 * tt >= cnt) break;
           const int t = 16 * tt + i16;
-          const float cum_t = s_cum[wave][t], lo_t = PC == 2 ? s_lo[PC == 2 ? wave : 0][t] : 0.0f;
-          f4 ym[PT] = {}, yc[PT] = {}, yd[PT] = {};
-          int shM;  // M's rows are scaled by 2^shM beside the operands' own scales
-          if constexpr (PC == 1) {
-            // x itself, for D, by the unit matrix: of row i the columns 8 q + j (- 16 in odd tiles)
-            const int jd = i16 + 16 * (tt & 1) - 8 * q4;
-            u4 unit_bits;
+          const float cum_t = s_cum[wave][t], low_t = s_low[wave][t];
+          const float Dm = __builtin_amdgcn_ldexpf(D * rcp(low_t), shBC);
+          f4 ym[PT] = {};
+          int tq = t, s0 = 8 * q4;
+          asm volatile("" : "+v"(tq), "+v"(s0));  // else the causal masks of all tiles are kept in registers
+          float m[2][8], rm = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) unit_bits[k] = jd >> 1 == k ? (jd & 1 ? 0x3c000000u : 0x3c00u) : 0u;
-            const h8 unit = __builtin_bit_cast(h8, unit_bits);
-            // C.B^T is zero above the diagonal, the weights are at most 2^cap there
-            shM = sc[t] + shd;
+          for (int kb = 0; kb <= tt / 2; ++kb) {
+            const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
+            const f4* gp = reinterpret_cast<const f4*>(s_g + (tile * 64 + lane) * 32);
+            float g[8], cs[8], ds[8];
 #pragma unroll
-            for (int kb = 0; kb <= tt / 2; ++kb) {
-              const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
-              const u4 g = *reinterpret_cast<const u4*>(s_cg + CG + (tile * 64 + lane) * 16);
-              float m[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int s = 32 * kb + 8 * q4 + j;
-                float x = cum_t - s_cum[wave][s];
-                if (kb == tt / 2) x = fminf(x, cap);
-                m[j] = ex2(x) * s_dt[wave][s];
-              }
-              const h8 mh = times(g, m);
-#pragma unroll
-              for (int e = 0; e < PT; ++e) ym[e] = mfma(xh[e][kb], mh, ym[e]);
+            for (int k = 0; k < 2; ++k) {
+              *reinterpret_cast<f4*>(g + 4 * k) = gp[k];
+              *reinterpret_cast<f4*>(cs + 4 * k) = *reinterpret_cast<const f4*>(&s_cum[wave][32 * kb + 8 * q4 + 4 * k]);
+              *reinterpret_cast<f4*>(ds + 4 * k) = *reinterpret_cast<const f4*>(&s_dt[wave][32 * kb + 8 * q4 + 4 * k]);
             }
 #pragma unroll
-            for (int e = 0; e < PT; ++e) yd[e] = mfma(xh[e][tt / 2], unit, yd[e]);
-          } else {
-            int tq = t, s0 = 8 * q4;
-            asm volatile("" : "+v"(tq), "+v"(s0));  // else the causal masks of all tiles are kept in registers
-            const float Dm = __builtin_amdgcn_ldexpf(D, shB + shC);
-            float m[2][8], rm = 0.0f;
-#pragma unroll
-            for (int kb = 0; kb <= tt / 2; ++kb) {
-              const int tile = tt < 2 ? tt : 2 * tt - 2 + kb;
-              const f4* gp = reinterpret_cast<const f4*>(s_cg + CG + (tile * 64 + lane) * 32);
-              const f4 g0 = gp[0], g1 = gp[1];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int s = 32 * kb + s0 + j;
-                float x = cum_t - s_cum[wave][s] + (lo_t - s_lo[PC == 2 ? wave : 0][s]);
-                x = (j < 4 ? g0[j & 3] : g1[j & 3]) * (ex2(x) * s_dt[wave][s]);
-                if (kb == tt / 2) {
-                  x = s <= tq ? x : 0.0f;
-                  x = s == tq ? x + Dm : x;
-                }
-                m[kb][j] = x;
+            for (int j = 0; j < 8; ++j) {
+              const int s = 32 * kb + s0 + j;
+              float x = g[j] * (ex2(cum_t - cs[j]) * ds[j]);
+              if (kb == tt / 2) {
+                x = s <= tq ? x : 0.0f;
+                x = s == tq ? x + Dm : x;
               }
-#pragma unroll
-              for (int j = 0; j < 8; j += 2) rm = max3(rm, m[kb][j], m[kb][j + 1]);
+              m[kb][j] = x;
             }
-            // every row by its own largest value: one token's outlier leaves the others their bits
-            shM = shift_for(row_max(rm));
-            const float fm = two(shM);
 #pragma unroll
-            for (int kb = 0; kb <= tt / 2; ++kb) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) m[kb][j] *= fm;
-              h8 mh, ml;
-              pieces(m[kb], mh, ml);
-#pragma unroll
-              for (int e = 0; e < PT; ++e) {
-                ym[e] = mfma(xl[e][kb], mh, ym[e]);
-                ym[e] = mfma(xh[e][kb], ml, ym[e]);
-                ym[e] = mfma(xh[e][kb], mh, ym[e]);
-              }
-            }
+            for (int j = 0; j < 8; j += 2) rm = max3(rm, m[kb][j], m[kb][j + 1]);
           }
+          // every row by its own largest value: one token's outlier leaves the others their bits
+          const int shM = shift_for(row_max(rm));
+          const float fm = two(shM);
 #pragma unroll
-          for (int m = 0; m < NT / 2; ++m) {
-            const h8 cp = *reinterpret_cast<const h8*>(s_cg + ((tt * (NT / 2) + m) * 64 + lane) * 16);
-            if constexpr (PC == 2) {
-              const h8 cl = *reinterpret_cast<const h8*>(s_cg + O::piece + ((tt * (NT / 2) + m) * 64 + lane) * 16);
+          for (int kb = 0; kb <= tt / 2; ++kb) {
 #pragma unroll
-              for (int e = 0; e < PT; ++e) {
-                yc[e] = mfma(sl[e][m], cp, yc[e]);
-                yc[e] = mfma(sh[e][m], cl, yc[e]);
-              }
+            for (int j = 0; j < 8; ++j) m[kb][j] *= fm;
+            h8 mh, ml;
+            pieces(m[kb], mh, ml);
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              ym[e] = mfma(xl[e][kb], mh, ym[e]);
+              ym[e] = mfma(xh[e][kb], ml, ym[e]);
+              ym[e] = mfma(xh[e][kb], mh, ym[e]);
             }
-#pragma unroll
-            for (int e = 0; e < PT; ++e) yc[e] = mfma(sh[e][m], cp, yc[e]);
           }
           // lane (t, q): channels p0 + 4 PT q + {0 .. 4 PT - 1}
-          const float f_cs = __builtin_amdgcn_ldexpf(ex2(cum_t + lo_t), e_cs);
-          const float f_mx = __builtin_amdgcn_ldexpf(1.0f, e_mx - shM);
-          const float f_d = __builtin_amdgcn_ldexpf(D, -shx);
+          const float f_cs = __builtin_amdgcn_ldexpf(ex2(cum_t) * low_t, -(shC + shS));
+          const float f_mx = __builtin_amdgcn_ldexpf(low_t, -(shBC + shx + shM));
           const int pw = p0 + 4 * PT * q4;
           const int64_t row = (int64_t)r0 + t, col = (int64_t)h * a.P + pw;
           float o[4 * PT];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int e = 0; e < PT; ++e) {
-              o[PT * r + e] = fmaf(ym[e][r], f_mx, yc[e][r] * f_cs);
-              if constexpr (PC == 1) o[PT * r + e] = fmaf(yd[e][r], f_d, o[PT * r + e]);
-            }
+            for (int e = 0; e < PT; ++e) o[PT * r + e] = fmaf(ym[e][r], f_mx, yc[tt][e][r] * f_cs);
           if (bad) {
             rarely();
 #pragma unroll
@@ -1250,7 +1126,63 @@ mix_block_kernel(const BlkArgs a) {
           }
         }
       }
+      // B's loads have ended where at most the stores behind them are left: four at least
+      // of a whole block's wave
+      if (on && cnt == kQ) arrived<4>();
+      else arrived<0>();
+      meet();  // B is there; the waves are done with C.B^T
+      if (c + 1 < sg.nc) stage_g(op + op_step, (c + 1) & 1);
+    } else {
+      meet();  // B is there
     }
+    if (on) {  // ---- the state after the block
+      if constexpr (!SUM) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          float w8[8];
+          *reinterpret_cast<f4*>(w8) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4]);
+          *reinterpret_cast<f4*>(w8 + 4) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4 + 4]);
+#pragma unroll
+          for (int e = 0; e < PT; ++e) {
+            float x[8];
+            joined(xh[e][kb], xl[e][kb], x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= w8[j];
+            if (bad) {  // a channel whose x was not finite has no state any more
+              rarely();
+              if (s_bad[wave][PT * i16 + e] < kQ)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = __builtin_nanf("");
+            }
+            pieces(x, xh[e][kb], xl[e][kb]);
+          }
+        }
+      }
+      const int shB = __builtin_amdgcn_readfirstlane(s_sc[SUM ? 0 : c & 1][0]);
+      const float f_su = two(max(-126, -(shB + shx + shd)));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        h8 bh[2], bl[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          bh[kb] = *reinterpret_cast<const h8*>(s_bc + ((nt * 2 + kb) * 64 + lane) * 16);
+          bl[kb] = *reinterpret_cast<const h8*>(s_bc + O::piece + ((nt * 2 + kb) * 64 + lane) * 16);
+        }
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          f4 d = {};
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            d = mfma(bh[kb], xl[e][kb], d);
+            d = mfma(bl[kb], xh[e][kb], d);
+            d = mfma(bh[kb], xh[e][kb], d);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) S[e][nt][r] = fmaf(d[r], f_su, S[e][nt][r] * dec_all);
+        }
+      }
+    }
+    op += op_step;
   }
   if (!on) return;
 
@@ -2027,7 +1959,7 @@ int check_mix(MixArgs& a, bool step, int64_t rows, int64_t nseq, int64_t nslots,
 
 // Workspace of ssm_conv_ssd_fwd, and how its sequences are cut.
 struct MixLayout {
-  int nt, pt, pc, wv;
+  int nt, pt, wv;
   int64_t nchunk, nseg, nsplit, ncut;  // at most
   int seg_len, sub, per_group, units;
   int64_t chunks, segs, cuts, ops, local, decay, cs0, bytes;
@@ -2043,11 +1975,10 @@ struct MixLayout {
 constexpr int64_t kSegWaves = 2048;
 constexpr int64_t kUncut = 3;
 
-MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N, int io_dtype) {
+MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N) {
   MixLayout l;
   l.nt = N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16;
   l.pt = l.nt == 16 ? 1 : 2;
-  l.pc = io_dtype == SSM_DTYPE_BF16 ? 1 : 2;
   const int64_t bph = (P + 16 * l.pt - 1) / (16 * l.pt);
   l.wv = l.nt == 16 ? 8 : 4;
   l.per_group = (int)((H / G * bph + l.wv - 1) / l.wv);
@@ -2073,7 +2004,7 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
       if ((first * n + slots - 1) / slots * l.sub < (first * l.sub + slots - 1) / slots * n) l.sub = n;
   if (l.sub > len) l.sub = (int)len;
   const int64_t piece = (int64_t)kQ * l.nt * 16 * 2;
-  const int64_t op_bytes = (l.pc + 2) * piece + kTri * 64 * 8 * (l.pc == 1 ? 2 : 4) + 320;
+  const int64_t op_bytes = 4 * piece + kTri * 64 * 32 + 64;
   int64_t at = 0;
   auto take = [&](int64_t n) {
     const int64_t o = at;
@@ -2092,33 +2023,32 @@ MixLayout mix_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t
   return l;
 }
 
-template <typename IO, int NT, int PT, int PC, int WV>
+template <typename IO, int NT, int PT, int WV>
 void launch_mix_blocks(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
-  static_assert(Ops<NT, PC>::bytes == (PC + 2) * kQ * NT * 32 + kTri * 64 * 8 * (PC == 1 ? 2 : 4) + 320,
-                "as in mix_layout");
+  static_assert(Ops<NT>::bytes == 4 * kQ * NT * 32 + kTri * 64 * 32 + 64, "as in mix_layout");
   mix_plan_kernel<<<1, 1024, 0, s>>>(b);
-  mix_prep_kernel<IO, NT, PC><<<dim3((unsigned)l.nchunk, b.G), kPrep, 0, s>>>(b);
+  mix_prep_kernel<IO, NT><<<dim3((unsigned)l.nchunk, b.G), kPrep, 0, s>>>(b);
   const unsigned grid = (unsigned)(l.nseg * l.units);
   auto walk = [&](auto fast) {
     constexpr bool F = decltype(fast)::value;
     if (l.nsplit) {
-      mix_block_kernel<IO, NT, PT, PC, WV, true, F><<<grid * l.sub, 64 * WV, 0, s>>>(b);
+      mix_block_kernel<IO, NT, PT, WV, true, F><<<grid * l.sub, 64 * WV, 0, s>>>(b);
       const int64_t per = (int64_t)b.H * b.P * b.N;
       mix_join_kernel<<<dim3((unsigned)((per + 1023) / 1024), (unsigned)l.ncut), 256, 0, s>>>(b);
     }
-    mix_block_kernel<IO, NT, PT, PC, WV, false, F><<<grid, 64 * WV, 0, s>>>(b);
+    mix_block_kernel<IO, NT, PT, WV, false, F><<<grid, 64 * WV, 0, s>>>(b);
   };
   if (b.fast) walk(std::integral_constant<bool, true>{});
   else walk(std::integral_constant<bool, false>{});
 }
 
-template <typename IO, int PC>
+template <typename IO>
 void launch_mix(const BlkArgs& b, const MixLayout& l, hipStream_t s) {
   switch (l.nt) {
-    case 2: launch_mix_blocks<IO, 2, 2, PC, 4>(b, l, s); break;
-    case 4: launch_mix_blocks<IO, 4, 2, PC, 4>(b, l, s); break;
-    case 8: launch_mix_blocks<IO, 8, 2, PC, 4>(b, l, s); break;
-    default: launch_mix_blocks<IO, 16, 1, PC, 8>(b, l, s); break;
+    case 2: launch_mix_blocks<IO, 2, 2, 4>(b, l, s); break;
+    case 4: launch_mix_blocks<IO, 4, 2, 4>(b, l, s); break;
+    case 8: launch_mix_blocks<IO, 8, 2, 4>(b, l, s); break;
+    default: launch_mix_blocks<IO, 16, 1, 8>(b, l, s); break;
   }
 }
 
@@ -2273,7 +2203,7 @@ int64_t ssm_conv_ssd_workspace_size(int64_t tokens, int64_t nseq, int64_t nheads
                                     int64_t ngroups, int64_t dstate, int io_dtype) {
   g_last_error[0] = 0;
   if (check_mix_extents(tokens, nseq, nheads, headdim, ngroups, dstate) || check_io(io_dtype)) return -1;
-  return mix_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype).bytes;
+  return mix_layout(tokens, nseq, nheads, headdim, ngroups, dstate).bytes;
 }
 
 int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_t dt_stride,
@@ -2303,7 +2233,7 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
     return fail(SSM_E_SHAPE, "workspace holds %lld bytes, needs %lld", (long long)workspace_bytes,
                 (long long)need);
   if (!aligned16(workspace)) return fail(SSM_E_ALIGN, "workspace is not 16-byte aligned");
-  const MixLayout l = mix_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype);
+  const MixLayout l = mix_layout(tokens, nseq, nheads, headdim, ngroups, dstate);
   if (!grid_ok(l.nseg * l.units * l.sub, 64 * l.wv))
     return fail(SSM_E_SHAPE, "too many sequences and heads for one call");
   char* w = static_cast<char*>(workspace);
@@ -2324,8 +2254,8 @@ int ssm_conv_ssd_fwd(const void* xbc, int64_t xbc_stride, const void* dt, int64_
   a.fast = headdim % (4 * l.pt) == 0 && dstate % 4 == 0 && lanes(xbc, xbc_stride, es == 2 ? 16 : 4 * l.pt) && (es == 4 || ch >= inner + 32) &&
            lanes(y, y_stride, wide) && (!z || lanes(z, z_stride, wide)) && aligned16(ssm_state);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (io_dtype == SSM_DTYPE_BF16) launch_mix<uint16_t, 1>(a, l, s);
-  else launch_mix<float, 2>(a, l, s);
+  if (io_dtype == SSM_DTYPE_BF16) launch_mix<uint16_t>(a, l, s);
+  else launch_mix<float>(a, l, s);
   return launch_status("ssm_conv_ssd_fwd launch");
 }
 

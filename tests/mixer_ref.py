@@ -7,9 +7,10 @@ import oracle
 
 # Bounds, per element.  An output stored in bf16 is rounded once (at most half
 # a step, 2^-8 of the value).  Behind it:
-#  - scan, bf16 inputs: six operands of the block products are rounded to 11
+#  - scan, bf16 inputs: six operands of the block products rounded to 11
 #    bits on the way to y (C, the state, C.B^T, the mixing matrix, x and its
-#    skip), 2^-11 each of the sum of the terms' absolute values: 6 2^-11;
+#    skip) would be 2^-11 each of the sum of the terms' absolute values: 6 2^-11.
+#    They hold 22 bits, and tests/test_mixer_rows_gpu.py holds them to it;
 #  - scan, float32 inputs, and the state for both: operands of two 11-bit
 #    pieces, 2^-21 each for four of them, the float32 sums over at most 64
 #    steps and 256 states (bounded by 2^-24 sqrt(n) over random roundings,

@@ -3,8 +3,10 @@ reach: rows on 16 bytes, as a model's projection has them, in every size of the
 kernels for whole vectors; the general kernels on cut prompts; prompts cut into
 segments beside other work on the card.  Problems, references and bounds as
 there."""
+import numpy as np
 import pytest
 
+import mixer_ref as ref
 import test_mixer_gpu as base
 from test_mixer_gpu import IO, Mix, dev, rows_of, ssm, up  # noqa: F401  (fixtures)
 
@@ -145,3 +147,41 @@ def test_cut_prompts_beside_other_work(ssm, dev):  # noqa: F811
         m.run(ssm)
         torch.cuda.synchronize()
         assert torch.equal(m.y, quiet.y) and torch.equal(m.hs, quiet.hs) and torch.equal(m.cs, quiet.cs)
+
+
+# ---------------------------------------------------------------- the bits that bf16 rows keep
+
+def check_to_the_last_bit(m, what):
+    """y of bf16 rows as float32's operators would store it: behind the one rounding
+    (half a step of the stored value, 2^-9 to 2^-8 of it) no more than
+    float32 rows may be off."""
+    y, _, hs, (terms, conv), hsum = ref.mix(m.x, m.cu, m.G, m.slots, m.has, m.softplus)
+    mine = ~np.isnan(y[:, 0])
+    err = ref.INNER["f32"] * terms[mine] + ref.CONV * conv[mine] + 1e-30
+    half = 2.0 ** (np.floor(np.log2(np.abs(y[mine]) + err)) - 8)
+    worst = np.max(np.abs(base.f64(m.y)[mine] - y[mine]) / (half + err))
+    print(f"{what}: {worst:.4f} of the bound", flush=True)
+    assert worst <= 1, worst
+    if hs is not None:
+        assert ref.mix_excess(base.f64(m.hs), hs, hsum, "state") <= 1
+
+
+BITS = [  # layout, lens, H, P, G, N, W, options
+    (Aligned, (130, 64, 3), 8, 64, 1, 128, 4, dict(has=True)),
+    (Aligned, (130, 64, 3), 8, 64, 1, 128, 4, dict(gate=False, state=False, bias=False)),
+    (Aligned, (700,), 8, 64, 2, 64, 4, dict(has=True)),
+    (Aligned, (90,), 6, 48, 1, 16, 3, dict(gate=False)),
+    (Aligned, (200, 30), 4, 64, 1, 256, 4, dict(has=True)),
+    (Mix, (130, 64, 3), 3, 64, 1, 128, 4, dict(has=True, lead=1)),
+    (Mix, (300,), 3, 40, 1, 250, 4, dict(has=True, lead=1)),
+    (Mix, (100,), 5, 33, 1, 40, 2, dict(gate=False)),
+]
+
+
+@pytest.mark.parametrize("case", range(len(BITS)))
+def test_bf16_rows_keep_float32s_bits(ssm, dev, case):  # noqa: F811
+    layout, lens, H, P, G, N, W, opt = BITS[case]
+    m = layout(dev, lens, H, P, G, N, W, "bf16", 1200 + case, **opt)
+    m.run(ssm)
+    torch.cuda.synchronize()
+    check_to_the_last_bit(m, str(BITS[case][1:]))
