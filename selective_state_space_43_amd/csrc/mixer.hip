@@ -507,8 +507,13 @@ __global__ void __launch_bounds__(kPrep) mix_prep_kernel(const BlkArgs a) {
     if (kb > (wave >> 1)) break;
     const int tile = wave < 2 ? wave : 2 * wave - 2 + kb;
     f4* o = reinterpret_cast<f4*>(out + O::g + (tile * 64 + lane) * 32);
-    o[0] = acc[kb][0];
-    o[1] = acc[kb][1];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // its own size again: D joins it
+      f4 v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = __builtin_amdgcn_ldexpf(acc[kb][e][r], -(sh[0] + sh[1]));
+      o[e] = v;
+    }
   }
   if (tid < 2) reinterpret_cast<int*>(out + O::scale)[tid] = sh[tid];
 }
@@ -1010,14 +1015,13 @@ mix_block_kernel(const BlkArgs a) {
       asm volatile("" ::: "memory");  // the stores of y stay behind these loads: arrived<4>() counts on it
       if (on) {
         const int shC = __builtin_amdgcn_readfirstlane(s_sc[c & 1][1]);
-        const int shBC = __builtin_amdgcn_readfirstlane(s_sc[c & 1][0]) + shC;
         // ---- M x and y, 16 rows at a time
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           if (16 * tt >= cnt) break;
           const int t = 16 * tt + i16;
           const float cum_t = s_cum[wave][t], low_t = s_low[wave][t];
-          const float Dm = __builtin_amdgcn_ldexpf(D * rcp(low_t), shBC);
+          const float Dm = D * rcp(low_t);
           f4 ym[PT] = {};
           int tq = t, s0 = 8 * q4;
           asm volatile("" : "+v"(tq), "+v"(s0));  // else the causal masks of all tiles are kept in registers
@@ -1064,7 +1068,7 @@ mix_block_kernel(const BlkArgs a) {
           }
           // lane (t, q): channels p0 + 4 PT q + {0 .. 4 PT - 1}
           const float f_cs = __builtin_amdgcn_ldexpf(ex2(cum_t) * low_t, -(shC + shS));
-          const float f_mx = __builtin_amdgcn_ldexpf(low_t, -(shBC + shx + shM));
+          const float f_mx = __builtin_amdgcn_ldexpf(low_t, -(shx + shM));
           const int pw = p0 + 4 * PT * q4;
           const int64_t row = (int64_t)r0 + t, col = (int64_t)h * a.P + pw;
           float o[4 * PT];

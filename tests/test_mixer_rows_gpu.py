@@ -185,3 +185,18 @@ def test_bf16_rows_keep_float32s_bits(ssm, dev, case):  # noqa: F811
     m.run(ssm)
     torch.cuda.synchronize()
     check_to_the_last_bit(m, str(BITS[case][1:]))
+
+
+# ---------------------------------------------------------------- sizes far apart
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_skip_beside_tiny_B_and_C(ssm, dev, dtype):  # noqa: F811
+    """B and C near 2^-62 beside a skip of 300: y is D x, and finite."""
+    m = Aligned(dev, (100, 30), 2, 64, 1, 64, 4, dtype, 1300, gate=False, has=False)
+    m.x["xbc"][:, 128:] *= 2.0 ** -60
+    m.x["conv_bias"][128:] = 0.0
+    m.x["D"][:] = (300.0, -500.0)
+    m.load()
+    m.run(ssm)
+    torch.cuda.synchronize()
+    m.check("tiny B and C")
