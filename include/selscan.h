@@ -375,7 +375,10 @@ int64_t ssm_ssd_scratch_bytes(void);
  * accesses are faster.  Offsets are read as their running maximum held inside
  * [0, tokens], so that whatever they hold no other memory is touched.
  * Outputs must not overlap inputs; slices of one buffer's rows with disjoint
- * columns do not.  Results do not vary from run to run.  A non-finite input
+ * columns do not.  Results do not vary from run to run.  The products' operands
+ * hold 2^-22 of their value or 2^-40 of the largest value beside them in a block
+ * of 64 tokens, whichever is more: x and the state of their own channel, B and C
+ * of their group.  The rest is float32 or more.  A non-finite input
  * makes what depends on it non-finite (an infinity may become a NaN), and
  * leaves earlier tokens and other sequences as they are.
  */

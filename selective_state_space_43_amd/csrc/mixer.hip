@@ -94,7 +94,12 @@ constexpr int kMaxN = 256;
 // Precision: the accumulators, the state, the running sums (float64) and all
 // statistics are float32 or more.  The operands are fp16 in two pieces (hi + lo, 22
 // bits, three products; lo x lo, 2^-24 of the product, is left out), scaled by a
-// power of two from the largest value of their tile.  One piece for what enters y
+// power of two from the largest value of the block: x and the state by channel, M by
+// row, B, C and the state's weights as a whole.  fp16's exponents reach 2^40 below
+// that: a value is held to 2^-22 of itself or 2^-40 of the largest one.  One scale for
+// a wave's 32 channels would be 3 % faster (868 against 895 us for four prompts of
+// 8192) and let a large channel take its neighbours' bits, another head's among
+// them where a head ends inside a tile.  One piece for what enters y
 // alone (11 bits beside the 8 of a stored bf16) would cost 1e-3 of y where two cost
 // what the float32 sums do.
 
@@ -203,10 +208,10 @@ __device__ __forceinline__ double lane63(double v) {
 }
 
 // The power of two that brings the largest magnitude m of a tile to [2^14,
-// 2^15), held where its own factors stay finite.
+// 2^15), held where it is a float32 itself.
 __device__ __forceinline__ int shift_for(float m) {
   const int e = 15 - __builtin_amdgcn_frexp_expf(m);
-  return e < -112 ? -112 : (e > 60 ? 60 : e);
+  return e < -113 ? -113 : (e > 111 ? 111 : e);
 }
 __device__ __forceinline__ float two(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
 // The larger of m and two magnitudes; a NaN among them is passed over.
@@ -621,6 +626,7 @@ mix_block_kernel(const BlkArgs a) {
   // for y alone
   __shared__ __align__(16) float s_cum[SUM ? 1 : WV][SUM ? 4 : 64], s_low[SUM ? 1 : WV][SUM ? 4 : 64];
   __shared__ __align__(16) float s_dt[SUM ? 1 : WV][SUM ? 4 : 64];
+  __shared__ __align__(16) int s_ex[SUM ? 1 : WV][2][SUM ? 4 : PB];  // shifts of x and of the state, by channel
   __shared__ int s_bad[SUM ? 1 : WV][SUM ? 4 : PB];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i16 = lane & 15, q4 = lane >> 4;
@@ -778,7 +784,7 @@ mix_block_kernel(const BlkArgs a) {
     }
     h8 xh[PT][2], xl[PT][2];  // x as an operand; then, and at once in the first pass, weighted for the state
     float dec_all = 1.0f;
-    int shx = 0, shd = 0;
+    int shx[PT] = {}, shw = 0;
     bool bad = false;
     if (on) {
       // ---- the convolution
@@ -871,18 +877,12 @@ mix_block_kernel(const BlkArgs a) {
       // what float32 leaves off a running sum goes with the step and with y's row, as a factor
       const float low = (float)(cum - (double)(float)cum);
       if constexpr (!SUM) s_cum[wave][lane] = (float)cum, s_low[wave][lane] = ex2(low);
-      // the state's weights exp(c_Q - c_s) dt_s: at most the largest dt, unless
-      // the state grows
-      shd = -__builtin_amdgcn_frexp_expf(wave_max(finite(dt) ? fabsf(dt) : 0.0f));
-      if (__any(dA > 0.0f)) {
-        rarely();
-        const float cap = fminf(wave_max(fmaxf((float)cum, 0.0f)) + wave_max(fmaxf(-(float)cum, 0.0f)), 100.0f);
-        shd -= (int)cap + 1;
-      }
-      shd = shd < -112 ? -112 : (shd > 60 ? 60 : shd);
+      // the state's weights exp(c_Q - c_s) dt_s, by their own largest one
+      shw = shift_for(wave_max(finite(wt) ? fabsf(wt) : 0.0f)) - 15;
+      s_w[wave][lane] = wt * two(shw);
       if constexpr (!SUM) s_dt[wave][lane] = dt * ex2(-low);
-      // ---- silu, the tile's scale
-      float mx = 0.0f;
+      // ---- silu, every channel's scale
+      float mx[PT] = {};
 #pragma unroll
       for (int e = 0; e < PT; ++e)
 #pragma unroll
@@ -897,7 +897,7 @@ mix_block_kernel(const BlkArgs a) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) mx = max3_nan(mx, v[e][kb][j], v[e][kb][j + 1]);
+          for (int j = 0; j < 8; j += 2) mx[e] = max3_nan(mx[e], v[e][kb][j], v[e][kb][j + 1]);
       // this block's x is used up: the next one's may come (B's loads have ended long ago)
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       if (a.z) fetch_z(c);
@@ -911,18 +911,18 @@ mix_block_kernel(const BlkArgs a) {
 #pragma unroll
             for (int e = 0; e < PT; ++e) v[e][kb][j] = 32 * kb + 8 * q4 + j < cnt ? v[e][kb][j] : 0.0f;
       }
-      bad = __any(!finite(mx));
+      bad = __any(!(finite(mx[0]) && finite(mx[PT - 1])));
       if (bad) {
         rarely();
-        mx = 0.0f;
 #pragma unroll
         for (int e = 0; e < PT; ++e) {
           int first = kQ;
+          mx[e] = 0.0f;
 #pragma unroll
           for (int kb = 1; kb >= 0; --kb)
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
-              if (finite(v[e][kb][j])) mx = fmaxf(mx, fabsf(v[e][kb][j]));
+              if (finite(v[e][kb][j])) mx[e] = fmaxf(mx[e], fabsf(v[e][kb][j]));
               else first = 32 * kb + 8 * q4 + j;
             }
           first = min(first, __shfl_xor(first, 16, 64));
@@ -931,28 +931,33 @@ mix_block_kernel(const BlkArgs a) {
             if (q4 == 0) s_bad[wave][PT * i16 + e] = first;
         }
       }
-      shx = shift_for(wave_max(mx));
-      s_w[wave][lane] = wt * two(SUM ? shx + shd : shd);
-      const float fx = two(shx);
+      float fx[PT];
+#pragma unroll
+      for (int e = 0; e < PT; ++e) {
+        shx[e] = shift_for(row_max(mx[e]));
+        fx[e] = two(shx[e]);
+        if constexpr (!SUM)
+          if (q4 == 0) s_ex[wave][0][PT * i16 + e] = shx[e];
+      }
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int e = 0; e < PT; ++e) {
+          if (!SUM && bad) {  // 0 x Inf is not 0: y's earlier rows must not meet them
+            rarely();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[e][kb][j] = finite(v[e][kb][j]) ? v[e][kb][j] : 0.0f;
+          }
+          float x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = v[e][kb][j] * fx[e];
           if constexpr (SUM) {
             float w8[8];
             *reinterpret_cast<f4*>(w8) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4]);
             *reinterpret_cast<f4*>(w8 + 4) = *reinterpret_cast<const f4*>(&s_w[wave][32 * kb + 8 * q4 + 4]);
-            pieces(v[e][kb], w8, xh[e][kb], xl[e][kb]);
+            pieces(x, w8, xh[e][kb], xl[e][kb]);
           } else {
-            if (bad) {  // 0 x Inf is not 0: y's earlier rows must not meet them
-              rarely();
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[e][kb][j] = finite(v[e][kb][j]) ? v[e][kb][j] : 0.0f;
-            }
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = v[e][kb][j] * fx;
             pieces(x, xh[e][kb], xl[e][kb]);
           }
         }
@@ -962,31 +967,29 @@ mix_block_kernel(const BlkArgs a) {
     if constexpr (!SUM) {
       meet();  // C is there
       f4 yc[4][PT] = {};
-      int shS = 0;
       if (on) {
         // ---- C.h for all rows: the state's pieces are made once and kept no longer than their products
-        float sm = 0.0f;
+        float fs[PT];
 #pragma unroll
-        for (int e = 0; e < PT; ++e)
+        for (int e = 0; e < PT; ++e) {
+          float sm = 0.0f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 4; r += 2) sm = max3(sm, S[e][nt][r], S[e][nt][r + 1]);
-        sm = wave_max(sm);
-        if (!finite(sm)) {
-          rarely();
-          sm = 0.0f;
-#pragma unroll
-          for (int e = 0; e < PT; ++e)
+          if (__any(!finite(sm))) {
+            rarely();
+            sm = 0.0f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int r = 0; r < 4; ++r)
                 if (finite(S[e][nt][r])) sm = fmaxf(sm, fabsf(S[e][nt][r]));
-          sm = wave_max(sm);
+          }
+          const int shS = shift_for(row_max(sm));
+          fs[e] = two(shS);
+          if (q4 == 0) s_ex[wave][1][PT * i16 + e] = shS;
         }
-        shS = shift_for(sm);
-        const float fs = two(shS);
 #pragma unroll
         for (int m = 0; m < NT / 2; ++m) {
           h8 sh[PT], sl[PT];
@@ -994,7 +997,7 @@ mix_block_kernel(const BlkArgs a) {
           for (int e = 0; e < PT; ++e) {
             float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * fs;
+            for (int j = 0; j < 8; ++j) x[j] = S[e][2 * m + (j >> 2)][j & 3] * fs[e];
             pieces(x, sh[e], sl[e]);
           }
 #pragma unroll
@@ -1009,13 +1012,24 @@ mix_block_kernel(const BlkArgs a) {
             }
           }
         }
+        // back from the channels' and C's scales; lane (t, q) has the channels 4 PT q + {0 .. 4 PT - 1}
+        const int shC = __builtin_amdgcn_readfirstlane(s_sc[c & 1][1]);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int k = 0; k < 4 * PT; ++k) {
+          const float f = two(min(127, -(shC + s_ex[wave][1][4 * PT * q4 + k])));
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) yc[tt][k % PT][k / PT] *= f;
+        }
       }
       meet();  // the waves are done with C
       stage_b();
       asm volatile("" ::: "memory");  // the stores of y stay behind these loads: arrived<4>() counts on it
       if (on) {
-        const int shC = __builtin_amdgcn_readfirstlane(s_sc[c & 1][1]);
         // ---- M x and y, 16 rows at a time
+        float f_x[4 * PT];
+#pragma unroll
+        for (int k = 0; k < 4 * PT; ++k) f_x[k] = two(-s_ex[wave][0][4 * PT * q4 + k]);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           if (16 * tt >= cnt) break;
@@ -1067,15 +1081,15 @@ mix_block_kernel(const BlkArgs a) {
             }
           }
           // lane (t, q): channels p0 + 4 PT q + {0 .. 4 PT - 1}
-          const float f_cs = __builtin_amdgcn_ldexpf(ex2(cum_t) * low_t, -(shC + shS));
-          const float f_mx = __builtin_amdgcn_ldexpf(low_t, -(shx + shM));
+          const float f_cs = ex2(cum_t) * low_t, f_mx = __builtin_amdgcn_ldexpf(low_t, -shM);
           const int pw = p0 + 4 * PT * q4;
           const int64_t row = (int64_t)r0 + t, col = (int64_t)h * a.P + pw;
           float o[4 * PT];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int e = 0; e < PT; ++e) o[PT * r + e] = fmaf(ym[e][r], f_mx, yc[tt][e][r] * f_cs);
+            for (int e = 0; e < PT; ++e)
+              o[PT * r + e] = fmaf(ym[e][r] * f_x[PT * r + e], f_mx, yc[tt][e][r] * f_cs);
           if (bad) {
             rarely();
 #pragma unroll
@@ -1163,7 +1177,9 @@ mix_block_kernel(const BlkArgs a) {
         }
       }
       const int shB = __builtin_amdgcn_readfirstlane(s_sc[SUM ? 0 : c & 1][0]);
-      const float f_su = two(max(-126, -(shB + shx + shd)));
+      float f_su[PT];
+#pragma unroll
+      for (int e = 0; e < PT; ++e) f_su[e] = two(min(127, -(shB + shw + shx[e])));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         h8 bh[2], bl[2];
@@ -1182,7 +1198,8 @@ mix_block_kernel(const BlkArgs a) {
             d = mfma(bh[kb], xh[e][kb], d);
           }
 #pragma unroll
-          for (int r = 0; r < 4; ++r) S[e][nt][r] = fmaf(d[r], f_su, S[e][nt][r] * dec_all);
+          for (int r = 0; r < 4; ++r)
+            S[e][nt][r] = fmaf(d[r], f_su[e], S[e][nt][r] * dec_all);
         }
       }
     }

@@ -200,3 +200,55 @@ def test_skip_beside_tiny_B_and_C(ssm, dev, dtype):  # noqa: F811
     m.run(ssm)
     torch.cuda.synchronize()
     m.check("tiny B and C")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("how", ["channel", "token", "step", "state"])
+def test_sizes_far_apart(ssm, dev, dtype, how):  # noqa: F811
+    """Large values beside small ones: channels of x and of the state 2^60 and 2^80
+    apart, tokens 2^28, steps of 2e-9 beside one of 64 with neither skip nor state.
+    Every value is held to the bound of its own terms."""
+    m = Aligned(dev, (150, 40), 2, 64, 1, 64, 4, dtype, 1310, gate=False, has=how != "step")
+    x = m.x
+    if how == "channel":
+        for c, f in ((5, 2.0 ** 30), (6, 2.0 ** -30), (70, 2.0 ** 30), (101, 2.0 ** -30)):
+            x["conv_weight"][c] *= f
+            x["conv_bias"][c] *= f
+            x["ssm_state"][:, c // 64, c % 64] *= f
+    elif how == "token":
+        x["xbc"][60, :128] *= 2.0 ** 14
+        x["xbc"][62, :128] *= 2.0 ** -14
+    elif how == "step":
+        x["dt"][:], x["dt_bias"][:], x["D"][:] = -20.0, 0.0, 0.0
+        x["dt"][[10, 100]] = 64.0
+    else:
+        x["ssm_state"][:, 0, 5] *= 2.0 ** 40
+        x["ssm_state"][:, 0, 6] *= 2.0 ** -40
+    m.load()
+    m.run(ssm)
+    torch.cuda.synchronize()
+    if dtype == "bf16":
+        check_to_the_last_bit(m, how)
+    else:
+        m.check(how)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P", [24, 48, 80])
+def test_a_head_does_not_depend_on_its_neighbour(ssm, dev, dtype, P):  # noqa: F811
+    """The tiles of a head that end inside one hold the next head's channels (or B's)
+    beside its own: larger and infinite ones leave its bits as they are."""
+    def run(change):
+        m = Aligned(dev, (150, 40), 2, P, 1, 64, 4, dtype, 1320, gate=False, has=True)
+        if change:
+            m.x["conv_weight"][P:2 * P] *= 2.0 ** 40
+            m.load()
+            if change > 1:
+                m.xbc[20, P:2 * P] = float("inf")
+        m.run(ssm)
+        torch.cuda.synchronize()
+        return m.y[:, :P], m.hs[:, 0]
+    clean = run(0)
+    assert torch.isfinite(clean[0].float()).all()
+    for change in (1, 2):
+        assert all(torch.equal(a, b) for a, b in zip(clean, run(change)))
