@@ -687,17 +687,20 @@ def ssm_group_norm_bwd_workspace_size(rows, channels, ngroups):
 
 
 def ssm_group_norm_bwd(dy, x, weight, ngroups, bias=None, z=None, eps=1e-5, center=False,
-                       activation="none", gate="none", workspace=None):
+                       activation="none", gate="none", workspace=None, want_dweight=True,
+                       want_dbias=True):
     """Gradients of ssm_group_norm_fwd for sum(dy * y): dict dx, dz (if z),
-    dweight (if weight), dbias (if bias)."""
+    dweight (if weight and want_dweight), dbias (if bias and want_dbias)."""
     rows, C, io, dev, ins = _norm_args(x, weight, bias, z, activation, gate)
     gs = _rows(dy, "dy", io, rows, C, dev)
     L = lib()
     ws, nbytes = _workspace(workspace, L.ssm_group_norm_bwd_workspace_size(rows, C, ngroups), dev)
     g = dict(dx=torch.empty((rows, C), dtype=io, device=dev),
              dz=torch.empty((rows, C), dtype=io, device=dev) if z is not None else None,
-             dweight=torch.empty(C, dtype=torch.float32, device=dev) if weight is not None else None,
-             dbias=torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None)
+             dweight=(torch.empty(C, dtype=torch.float32, device=dev)
+                      if weight is not None and want_dweight else None),
+             dbias=(torch.empty(C, dtype=torch.float32, device=dev)
+                    if bias is not None and want_dbias else None))
     st = _launch(dev, L.ssm_group_norm_bwd, dy.data_ptr(), gs, *ins, eps, int(bool(center)),
                  _ACT[activation], _GATE[gate], _ptr(g["dx"]), C, _ptr(g["dz"]), C, _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(ws),
                  nbytes, rows, C, ngroups, _IO[io])
@@ -723,7 +726,9 @@ class _GroupNormFn(torch.autograd.Function):
         if torch.is_grad_enabled():  # create_graph: the gradients would pass for constants
             raise RuntimeError("group_norm_fn: gradients of its gradients are not computed")
         x, weight, bias, z = ctx.saved_tensors
-        g = ssm_group_norm_bwd(dy.contiguous(), x, weight, ctx.ngroups, bias=bias, z=z, **ctx.how)
+        g = ssm_group_norm_bwd(dy.contiguous(), x, weight, ctx.ngroups, bias=bias, z=z,
+                               want_dweight=ctx.needs_input_grad[1],
+                               want_dbias=ctx.needs_input_grad[2], **ctx.how)
         return g["dx"], g["dweight"], g["dbias"], g["dz"], None, None, None, None, None
 
 
