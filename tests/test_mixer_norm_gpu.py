@@ -1,9 +1,11 @@
-"""The group norm on the GPU where tests/test_mixer_gpu.py does not reach: frozen
+"""The group norm on the GPU where tests/test_mixer_gpu.py does not reach: groups
+without whole vectors, frozen
 parameters.  Problems, references and bounds as there."""
 import numpy as np
 import pytest
 
 import mixer_ref as ref
+import test_mixer_gpu as base
 from test_mixer_gpu import dev, f64, norm_problem, ssm  # noqa: F401  (fixtures)
 
 torch = pytest.importorskip("torch")
@@ -30,3 +32,37 @@ def test_frozen_parameters(ssm, dev, monkeypatch, trained):  # noqa: F811
             continue
         rel = ref.NORM_BWD + (4 * 2.0 ** -24 * np.sqrt(300) if k in ("dweight", "dbias") else 0)
         assert np.all(np.abs(f64(leaf.grad) - want[k]) <= (2.0 ** -24 + rel) * bound[k] + 1e-30), k
+
+
+ELEMENTWISE = [  # rows, channels, groups, dtype, center, act, gate, options; no group on 16 bytes
+    (1500, 65, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (1500, 65, 1, "f32", True, "silu", "after", {}),
+    (1300, 256, 1, "bf16", True, "silu", "before", dict(lead=1)),
+    (1300, 256, 1, "f32", False, "none", "before", dict(lead=1, bias=False)),
+    (1300, 257, 1, "bf16", False, "none", "after", {}),
+    (900, 514, 2, "f32", True, "none", "none", {}),
+    (900, 1001, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (900, 1001, 1, "f32", True, "silu", "none", {}),
+    (900, 1024, 1, "bf16", True, "none", "before", dict(lead=1)),
+    (900, 1025, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (500, 1025, 1, "f32", True, "silu", "after", {}),
+    (300, 4096, 1, "f32", False, "silu", "before", dict(lead=1)),
+    (400, 4097, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (300, 4097, 1, "f32", True, "none", "after", {}),
+    (230, 16384, 1, "bf16", False, "none", "none", dict(lead=1)),
+    (230, 16385, 1, "bf16", False, "none", "before", dict(bias=False)),
+    (40, 16385, 1, "f32", True, "silu", "before", {}),
+    (210, 32767, 1, "bf16", True, "silu", "after", {}),
+    (30, 32767, 1, "f32", False, "none", "before", dict(bias=False)),
+]
+
+
+@pytest.mark.parametrize("case", range(len(ELEMENTWISE)))
+def test_element_by_element(ssm, dev, case):  # noqa: F811
+    """Groups that no 16-byte vector fits, both sides of every change of team,
+    one row a strip and several."""
+    base.NORMS, keep = ELEMENTWISE, base.NORMS
+    try:
+        base.test_norm(ssm, dev, case)
+    finally:
+        base.NORMS = keep

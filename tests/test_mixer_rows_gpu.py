@@ -252,3 +252,21 @@ def test_a_head_does_not_depend_on_its_neighbour(ssm, dev, dtype, P):  # noqa: F
     assert torch.isfinite(clean[0].float()).all()
     for change in (1, 2):
         assert all(torch.equal(a, b) for a, b in zip(clean, run(change)))
+
+
+def test_offsets_out_of_order_and_guards(ssm, dev):  # noqa: F811
+    """Offsets that run back or past the rows are read as their running maximum
+    inside them; y, the states and the guards around them are what those
+    offsets give."""
+    for wrong, right in (((0, 20, 10, 60), (0, 20, 20, 60)), ((-5, 30, 20, 1 << 30), (0, 30, 30, 60)),
+                         ((70, 10, 20, 30), (60, 60, 60, 60)), ((10, 5, 50, 40), (10, 10, 50, 50))):
+        m = Mix(dev, (20, 30, 10), 2, 64, 1, 64, 4, "bf16", 1330, has=True)
+        wide = torch.full((64, 160), 7.0, device=dev).bfloat16()
+        m.y = wide[2:62, 16:144]
+        m.cu_t = torch.tensor(wrong, dtype=torch.int32, device=dev)
+        m.run(ssm)
+        torch.cuda.synchronize()
+        m.cu = np.array(right)
+        m.check(f"{wrong}")
+        wide[2:62, 16:144] = 7.0
+        assert (wide == 7.0).all()
