@@ -427,8 +427,9 @@ int ssm_conv_ssd_update(const void* xbc, int64_t xbc_stride, const void* dt, int
  *  x, z, y       [rows, channels] io_dtype with row strides in elements; z is
  *                NULL exactly when the gate is SSM_GATE_NONE
  *  weight, bias  [channels] float32 or NULL (1, 0)
- * A group has at most 32768 channels (SSM_E_UNSUPPORTED otherwise).  y must
- * not overlap an input.  Arithmetic in float32.
+ * A group has at most 32768 channels (SSM_E_UNSUPPORTED otherwise), a launch less
+ * than 2^32 threads (SSM_E_SHAPE otherwise; 8 to 1024 threads a row and group).  y
+ * must not overlap an input.  Arithmetic in float32.
  */
 int ssm_group_norm_fwd(const void* x, int64_t x_stride, const void* z, int64_t z_stride,
                        const float* weight, const float* bias, float eps, int center,

@@ -579,7 +579,8 @@ def ssm_conv_ssd_fwd(xbc, dt, conv_weight, A, cu_seqlens, headdim, ngroups, conv
     slot s; outside the states: the sequence is padding and skipped), from
     their contents where has_state[s] (bool or uint8) is set and from zero
     elsewhere.  y of rows that belong to no sequence is left as it was (a new
-    y is not cleared)."""
+    y is not cleared).  As every ssm_* call it is not differentiable: y carries
+    no gradient, whatever its inputs ask for."""
     rows, ch, io, dev = _row_input(xbc, "xbc")
     H = A.shape[0]
     inner = H * headdim

@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(1024) mix_plan_kernel(const BlkArgs a) {
 
 // ---- the operands of one block and group
 //
-// One workgroup each: 9 us for one block of 128 states, which is latency, 22 for 512.
+// One workgroup each: 9 us for one block of 128 states, which is latency, 21 for 512.
 // Every wave of the group reads them: 160 of them at 80 heads of 64 channels.
 
 constexpr int kPrep = 1024;  // threads: one round of loads up to 128 states
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kPrep) mix_prep_kernel(const BlkArgs a) {
 // ---- the walk over a segment
 
 // Copies BYTES from global memory to LDS, 16 bytes a lane, on their way when it
-// returns: staged() waits for them and for the other waves.
+// returns: arrived() waits for them, meet() for the other waves.
 template <int WV, int BYTES>
 __device__ __forceinline__ void stage(const char* from, char* to) {
   static_assert(BYTES % 1024 == 0, "whole waves");
@@ -605,12 +605,18 @@ struct XRaw {
 // and dt come from the convolution's end on.  FAST: rows and channels allow whole
 // vectors (headdim a multiple of 4 PT, dstate of 4, rows aligned to the accesses).
 //
-// Bound by latency and vector instructions: two waves a SIMD, which the state (64
-// registers) and the operands of x force.  B and C by turns in one place leave room for two
-// workgroups of four waves a CU at 128 states; both at once, one workgroup of
-// eight, took 892 us for four prompts of 8192 with 80 heads of 64 channels and 128 states
-// against 872, and 286 against 255 for 16 ragged prompts of 8111 tokens.  Past 128 states
-// a wave has 16 channels instead of 32, so that its state stays at 64 registers.
+// Bound by vector instructions and their waits at two waves a SIMD, which the state (64
+// registers) and the operands of x force: four prompts of 8192 with 80 heads of 64
+// channels and 128 states take 686 us in the second pass and 176 in the first, of a call of
+// 910 (on one card, traced; 895 to 910 on others).  A wave and block of the second is 2905
+// vector instructions, 228 of them products: the vector units are busy 64 % of the
+// time, the matrix cores 19 %, and a wave waits 29 % of its own (247 registers, 70 KB of
+// LDS a workgroup).  B and C by turns in one place leave room for two workgroups of four
+// waves a CU at 128 states; both at once, one workgroup of eight, took 2 % more there and
+// 12 % more for 16 ragged prompts of 8111 tokens.  Past 128 states a wave has 16 channels
+// instead of 32, so that its state stays at 64 registers.  Rows that are not on 16
+// bytes go through the general kernel, which reads x element by element and spills at
+// 128 states: 1621 us against 919.
 template <typename IO, int NT, int PT, int WV, bool SUM, bool FAST>
 __global__ void __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(2)))
 mix_block_kernel(const BlkArgs a) {
@@ -898,7 +904,7 @@ mix_block_kernel(const BlkArgs a) {
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
           for (int j = 0; j < 8; j += 2) mx[e] = max3_nan(mx[e], v[e][kb][j], v[e][kb][j + 1]);
-      // this block's x is used up: the next one's may come (B's loads have ended long ago)
+      // this block's x is used up: the next one's may come (the staged operand's loads have ended by now)
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       if (a.z) fetch_z(c);
       if (c + 1 < sg.nc) fetch(c + 1);
@@ -1988,11 +1994,11 @@ struct MixLayout {
 
 // A segment is one workgroup's work, one after another, and the card holds 2048
 // waves at two a SIMD.  Segments for 1024 waves leave it half empty where one
-// long prompt has to fill it (four of 8192, 80 heads: 941 against 754 us) and win
-// where the prompts themselves do (16 of 8111 tokens in all: 211 against 228 us; but
-// one of 8000 beside 15 of 10: 268 against 234); for 4096 they come in two turns (872, 263).
+// long prompt has to fill it (four of 8192, 80 heads: 1151 against 919 us; one of 8000
+// beside 15 of 10: 319 against 284) and win nothing where the prompts themselves do (16 of
+// 8111 tokens in all: 265 against 262); for 4096 they come in two turns (1007, 316, 299).
 // Up to three blocks one after another take less time than cut (128 tokens, 80
-// heads: 38 against 49 us; four: 56 against 53).
+// heads: 43 against 52 us; four: 62 against 57).
 constexpr int64_t kSegWaves = 2048;
 constexpr int64_t kUncut = 3;
 
