@@ -241,7 +241,7 @@ def test_a_head_does_not_depend_on_its_neighbour(ssm, dev, dtype, P):  # noqa: F
     def run(change):
         m = Aligned(dev, (150, 40), 2, P, 1, 64, 4, dtype, 1320, gate=False, has=True)
         if change:
-            m.x["conv_weight"][P:2 * P] *= 2.0 ** 40
+            m.x["xbc"][:, P:2 * P] *= 2.0 ** 40
             m.load()
             if change > 1:
                 m.xbc[20, P:2 * P] = float("inf")
@@ -270,3 +270,24 @@ def test_offsets_out_of_order_and_guards(ssm, dev):  # noqa: F811
         m.check(f"{wrong}")
         wide[2:62, 16:144] = 7.0
         assert (wide == 7.0).all()
+
+
+def test_two_calls_at_once(ssm, dev):  # noqa: F811
+    """Two programs on streams of their own, with states and workspaces of their own:
+    both get the bits that they get alone."""
+    def fresh(i):
+        return Aligned(dev, (700, 64, 300), 24, 64, 1, 128, 4, "bf16", 1340 + i, gate=False, has=True)
+    alone = [fresh(0), fresh(1)]
+    for m in alone:
+        m.run(ssm)
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in range(2)]
+    for _ in range(5):
+        both = [fresh(0), fresh(1)]
+        torch.cuda.synchronize()
+        for m, s in zip(both, streams):
+            with torch.cuda.stream(s):
+                m.run(ssm)
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert torch.equal(a.y, b.y) and torch.equal(a.hs, b.hs) and torch.equal(a.cs, b.cs)
