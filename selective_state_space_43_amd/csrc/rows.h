@@ -1,0 +1,400 @@
+// What the operators over rows of tokens share: element access and math, vectors
+// and lane sums, products of fp16 pieces, copies into LDS, a row in the registers of
+// a team of threads, and the checks of row tensors on the host.
+#ifndef SELSCAN_ROWS_H
+#define SELSCAN_ROWS_H
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "host.h"
+
+namespace {
+
+// ---------------------------------------------------------------- math and element access
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// log(1 + e^x): above 15 it is x to within 2e-8 of it; below, the rounding of
+// u = 1 + e is taken back to first order, which keeps tiny steps exact.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = ex2(x * kLog2e), u = 1.0f + e;
+  const float l = __builtin_amdgcn_logf(u) * kLn2 - ((u - 1.0f) - e) * rcp(u);
+  return x > 15.0f ? x : l;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-x * kLog2e)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+
+// float32 or bf16 (as its bits) elements, read and written as float32
+template <typename IO>
+__device__ __forceinline__ float ld(const void* p, int64_t i) {
+  if constexpr (sizeof(IO) == 4) return static_cast<const float*>(p)[i];
+  else return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+}
+template <typename IO>
+__device__ __forceinline__ void st(void* p, int64_t i, float v) {
+  if constexpr (sizeof(IO) == 4) static_cast<float*>(p)[i] = v;
+  else static_cast<uint16_t*>(p)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// ---------------------------------------------------------------- vectors, lanes and matrix products
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float wave_max(float v) {  // v >= 0; uniform result
+#define MIX_STEP(ctrl, rows)                                                                     \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, \
+                                                          rows == 0xf)));
+  MIX_STEP(0x111, 0xf) MIX_STEP(0x112, 0xf) MIX_STEP(0x114, 0xf) MIX_STEP(0x118, 0xf)
+  MIX_STEP(0x142, 0xa) MIX_STEP(0x143, 0xc)
+#undef MIX_STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// The largest of the four lanes i, i + 16, i + 32, i + 48.
+__device__ __forceinline__ float row_max(float v) {
+  u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  v = fmaxf(__uint_as_float(w.x), __uint_as_float(w.y));
+  w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  return fmaxf(__uint_as_float(w.x), __uint_as_float(w.y));
+}
+
+// Inclusive sum over the wave's lanes in float64: steps of very different
+// sizes follow each other in one block, and differences of the sums count.
+__device__ __forceinline__ double wave_scan(double v) {
+#define MIX_STEP(ctrl, rows)                                                                      \
+  {                                                                                               \
+    const u2 w = __builtin_bit_cast(u2, v);                                                       \
+    u2 o;                                                                                         \
+    o.x = __builtin_amdgcn_update_dpp(0, w.x, ctrl, rows, 0xf, rows == 0xf);                      \
+    o.y = __builtin_amdgcn_update_dpp(0, w.y, ctrl, rows, 0xf, rows == 0xf);                      \
+    v += __builtin_bit_cast(double, o);                                                           \
+  }
+  MIX_STEP(0x111, 0xf) MIX_STEP(0x112, 0xf) MIX_STEP(0x114, 0xf) MIX_STEP(0x118, 0xf)
+  MIX_STEP(0x142, 0xa) MIX_STEP(0x143, 0xc)
+#undef MIX_STEP
+  return v;
+}
+
+__device__ __forceinline__ double lane63(double v) {
+  const u2 w = __builtin_bit_cast(u2, v);
+  u2 o;
+  o.x = __builtin_amdgcn_readlane(w.x, 63);
+  o.y = __builtin_amdgcn_readlane(w.y, 63);
+  return __builtin_bit_cast(double, o);
+}
+
+// The power of two that brings the largest magnitude m of a tile to [2^14,
+// 2^15), held where it is a float32 itself.
+__device__ __forceinline__ int shift_for(float m) {
+  const int e = 15 - __builtin_amdgcn_frexp_expf(m);
+  return e < -113 ? -113 : (e > 111 ? 111 : e);
+}
+__device__ __forceinline__ float two(int e) { return __builtin_amdgcn_ldexpf(1.0f, e); }
+// The larger of m and two magnitudes; a NaN among them is passed over.
+__device__ __forceinline__ float max3(float m, float x, float y) {
+  float o;
+  asm("v_max3_f32 %0, %1, |%2|, |%3|" : "=v"(o) : "v"(m), "v"(x), "v"(y));
+  return o;
+}
+// The same, and a NaN stays.
+__device__ __forceinline__ float max3_nan(float m, float x, float y) {
+  float o;
+  asm("v_maximum3_f32 %0, %1, |%2|, |%3|" : "=v"(o) : "v"(m), "v"(x), "v"(y));
+  return o;
+}
+// In a branch that is hardly ever taken: keeps the compiler from computing both sides.
+__device__ __forceinline__ void rarely() { asm volatile(""); }
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
+
+__device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// v w = hi + lo in fp16, to 22 bits; lo takes in what v w itself was rounded by
+__device__ __forceinline__ void pieces(const float* v, const float* w, h8& hi, h8& lo) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const h2 a = __builtin_convertvector((f2){v[j] * w[j], v[j + 1] * w[j + 1]}, h2);
+    hi[j] = a.x; hi[j + 1] = a.y;
+    lo[j] = (_Float16)__builtin_fmaf(v[j], w[j], -(float)a.x);
+    lo[j + 1] = (_Float16)__builtin_fmaf(v[j + 1], w[j + 1], -(float)a.y);
+  }
+}
+// v = hi + lo in fp16, to 22 bits
+__device__ __forceinline__ void pieces(const float* v, h8& hi, h8& lo) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const h2 a = __builtin_convertvector((f2){v[j], v[j + 1]}, h2);
+    const h2 b = __builtin_convertvector(
+        (f2){__builtin_fmaf((float)a.x, -1.0f, v[j]), __builtin_fmaf((float)a.y, -1.0f, v[j + 1])}, h2);
+    hi[j] = a.x; hi[j + 1] = a.y; lo[j] = b.x; lo[j + 1] = b.y;
+  }
+}
+// hi + lo
+__device__ __forceinline__ void joined(const h8& hi, const h8& lo, float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf((float)hi[j], 1.0f, (float)lo[j]);
+}
+
+// Exclusive sums over the workgroup of four values at once, and their totals.
+typedef int i4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ i4 block_scan(i4 v, i4* red, i4& total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  i4 x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    i4 o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = __shfl_up(x[k], d, 64);
+    if (lane >= d) x += o;
+  }
+  if (lane == 63) red[w] = x;
+  __syncthreads();
+  i4 before = {0, 0, 0, 0}, all = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const i4 r = red[i];
+    if (i < w) before += r;
+    all += r;
+  }
+  total = all;
+  return before + x - v;
+}
+__device__ __forceinline__ int block_scan_max(int v, int* red) {  // inclusive, v >= 0
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v = max(v, o);
+  }
+  if (lane == 63) red[w] = v;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < w) v = max(v, red[i]);
+  return v;
+}
+
+// The last index whose prefix (of 1024) is at most i.
+__device__ __forceinline__ int find(const int* prefix, int i) {
+  int at = 0;
+#pragma unroll
+  for (int d = 512; d; d >>= 1)
+    if (prefix[at + d] <= i) at += d;
+  return at;
+}
+
+// Copies BYTES from global memory to LDS, 16 bytes a lane, on their way when it
+// returns: arrived() waits for them, meet() for the other waves.
+template <int WV, int BYTES>
+__device__ __forceinline__ void stage(const char* from, char* to) {
+  static_assert(BYTES % 1024 == 0, "whole waves");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < (BYTES / 1024 + WV - 1) / WV; ++i) {
+    const int at = (i * WV + wave) * 1024;
+    if (BYTES / 1024 % WV == 0 || at < BYTES)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(from + at + lane * 16),
+          (__attribute__((address_space(3))) void*)(to + at), 16, 0, 0);
+  }
+}
+// The first LANES lanes' 16 bytes of a wave, by the first wave.
+template <int LANES>
+__device__ __forceinline__ void stage_few(const char* from, char* to) {
+  if (threadIdx.x < LANES)
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + threadIdx.x * 16),
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+// All of this wave's memory accesses but the last LEFT have ended.
+template <int LEFT>
+__device__ __forceinline__ void arrived() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+}
+// The waves of the workgroup meet; what is on its way from memory stays so.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Sum over the LN lanes of a row.
+template <int LN>
+__device__ __forceinline__ float lane_sum(float v) {
+  auto add = [&](int o) { v += __int_as_float(o); };
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));
+  if constexpr (LN >= 8) add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
+  if constexpr (LN >= 16) add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
+  if constexpr (LN >= 32) {
+    const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+    v = __uint_as_float(w.x) + __uint_as_float(w.y);
+  }
+  if constexpr (LN >= 64) {
+    const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+    v = __uint_as_float(w.x) + __uint_as_float(w.y);
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------- rows in the registers of a team of threads
+
+template <typename IO, int VE>
+struct Vec {
+  static constexpr int words = VE * (int)sizeof(IO) < 4 ? 1 : VE * (int)sizeof(IO) / 4;
+  uint32_t w[words];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (VE > 1) {
+      const u4 v = *reinterpret_cast<const u4*>(static_cast<const IO*>(p) + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = v[k];
+    } else if constexpr (sizeof(IO) == 2) {
+      w[0] = static_cast<const uint16_t*>(p)[i];
+    } else {
+      w[0] = static_cast<const uint32_t*>(p)[i];
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(IO) == 4) return __uint_as_float(w[j]);
+    else return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+  }
+};
+template <typename IO, int VE>
+__device__ __forceinline__ void put(void* p, int64_t i, const float* v) {
+  if constexpr (VE == 1) {
+    st<IO>(p, i, v[0]);
+  } else if constexpr (sizeof(IO) == 4) {
+    *reinterpret_cast<f4*>(static_cast<float*>(p) + i) = *reinterpret_cast<const f4*>(v);
+  } else {
+    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+    typedef float f8 __attribute__((ext_vector_type(8)));
+    f8 f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = v[k];
+    *reinterpret_cast<b8*>(static_cast<uint16_t*>(p) + i) = __builtin_convertvector(f, b8);
+  }
+}
+
+// VE parameters from column c on, or the value that leaves things as they are.
+template <int VE>
+__device__ __forceinline__ void params(const float* p, int c, float none, float (&o)[VE]) {
+  if (p) {
+    if constexpr (VE == 1) {
+      o[0] = p[c];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VE; j += 4) *reinterpret_cast<f4*>(o + j) = *reinterpret_cast<const f4*>(p + c + j);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; ++j) o[j] = none;
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// Sums of NV values over the team, the same bits in all of its threads.  Teams
+// wider than a wave meet once a call, in two sets of places by turns.
+template <int TL, int NV>
+__device__ __forceinline__ void team_sum(float (&v)[NV], float (*red)[NV][TL < 64 ? 1 : TL / 64], int& turn) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = dpp_add<0xB1>(v[i]);   // lanes 1, 0, 3, 2
+    v[i] = dpp_add<0x4E>(v[i]);   // lanes 2, 3, 0, 1
+    v[i] = dpp_add<0x141>(v[i]);  // the half row mirrored: its other four
+    if constexpr (TL >= 32) {
+      v[i] = dpp_add<0x140>(v[i]);  // the row mirrored: its other eight
+      const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i]), false, false));
+      v[i] = __uint_as_float(w.x) + __uint_as_float(w.y);
+    }
+    if constexpr (TL >= 64) {
+      const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i]), false, false));
+      v[i] = __uint_as_float(w.x) + __uint_as_float(w.y);
+    }
+  }
+  if constexpr (TL > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) red[turn][i][wave] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < TL / 64; ++k) v[i] += red[turn][i][k];
+    }
+    turn ^= 1;
+  }
+}
+
+constexpr int team_threads(int tl) { return tl < 256 ? 256 : tl; }
+
+// ---------------------------------------------------------------- host side
+
+// Rows of a tensor that may be a slice of wider rows.
+struct Rows {
+  const void* p;
+  int64_t rows, stride, width;  // bytes
+  const char* name;
+};
+
+Rows flat(const void* p, int64_t bytes, const char* name) { return {p, 1, bytes, bytes, name}; }
+
+// Whether two of them share a byte.  Slices of the same rows (equal strides,
+// interleaved) share none where their columns are disjoint.
+bool share(const Rows& x, const Rows& y) {
+  const Span a = {x.p, (x.rows - 1) * x.stride + x.width, x.name};
+  const Span b = {y.p, (y.rows - 1) * y.stride + y.width, y.name};
+  if (!overlaps(a, b)) return false;
+  const int64_t st = x.rows > 1 ? x.stride : y.stride;
+  if ((x.rows > 1 && x.stride != st) || (y.rows > 1 && y.stride != st)) return true;
+  if (x.width > st || y.width > st) return true;
+  int64_t d = (int64_t)((intptr_t)x.p - (intptr_t)y.p) % st;
+  if (d < 0) d += st;
+  return d < y.width || d + x.width > st;
+}
+
+int check_rows(const char* name, const void* p, int64_t stride, int64_t width, int64_t rows, int esize) {
+  if (stride < width || stride > kMaxExtent)
+    return fail(SSM_E_SHAPE, "%s: row stride %lld is less than its %lld columns or too large", name,
+                (long long)stride, (long long)width);
+  if (!product_ok(rows, stride, esize)) return fail(SSM_E_SHAPE, "tensor sizes overflow");
+  if ((uintptr_t)p % esize) return fail(SSM_E_ALIGN, "%s is not aligned to its elements", name);
+  return SSM_OK;
+}
+
+int check_no_alias(const Rows* outs, int no, const Rows* ins, int ni) {
+  for (int o = 0; o < no; ++o) {
+    for (int i = 0; i < ni; ++i)
+      if (share(outs[o], ins[i])) return fail(SSM_E_ALIAS, "%s overlaps %s", outs[o].name, ins[i].name);
+    for (int i = 0; i < o; ++i)
+      if (share(outs[o], outs[i])) return fail(SSM_E_ALIAS, "%s overlaps %s", outs[o].name, outs[i].name);
+  }
+  return SSM_OK;
+}
+
+int check_io(int io_dtype) {
+  if (io_dtype != SSM_DTYPE_F32 && io_dtype != SSM_DTYPE_BF16)
+    return fail(SSM_E_DTYPE, "io_dtype = %d is not SSM_DTYPE_F32 or SSM_DTYPE_BF16", io_dtype);
+  return SSM_OK;
+}
+
+// A launch has less than 2^32 threads.
+bool grid_ok(int64_t blocks, int threads) { return blocks <= 0xffffffffll / threads; }
+
+}  // namespace
+
+#endif  // SELSCAN_ROWS_H
