@@ -82,6 +82,9 @@ typedef enum { SSM_ACT_NONE = 0, SSM_ACT_SILU = 1 } ssm_activation;
  * statistics, or the output. */
 typedef enum { SSM_GATE_NONE = 0, SSM_GATE_BEFORE = 1, SSM_GATE_AFTER = 2 } ssm_gate;
 
+/* ssm_add_norm_fwd: how the output is stored. */
+typedef enum { SSM_QUANT_NONE = 0, SSM_QUANT_E4M3 = 1 } ssm_quant;
+
 typedef enum {
   SSM_OK = 0,
   SSM_E_NULL = 1,        /* a required pointer is NULL                         */
@@ -459,6 +462,157 @@ int ssm_group_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t
 /* Bytes of workspace ssm_group_norm_bwd needs (-1 if an extent is out of
  * range). */
 int64_t ssm_group_norm_bwd_workspace_size(int64_t rows, int64_t channels, int64_t ngroups);
+
+/*
+ * The gated delta rule over packed prompts: a state per head that forgets by a
+ * decay of its own and writes, at a key, the part of the value that it does not
+ * already hold there.  Rows are tokens as for ssm_conv_ssd_fwd; q and k belong to a
+ * group of heads, v and the two scalars to a head.  Per head and token:
+ *
+ *   a_t  = exp(A softplus(dt_t + dt_bias))     (or without the softplus)
+ *   b_t  = sigmoid(beta_t)                     (or beta_t itself)
+ *   k^_t = k_t / sqrt(|k_t|^2 + eps),  q^_t = scale q_t / sqrt(|q_t|^2 + eps)
+ *                                              (qk_norm; else k_t, scale q_t)
+ *   S~   = a_t S_{t-1}
+ *   S_t  = S~ + b_t (v_t - S~ k^_t) k^_t^T
+ *   y_t  = S_t q^_t
+ *
+ *  q, k         [tokens, ngroups * dstate] io_dtype
+ *  v            [tokens, nheads * headdim] io_dtype
+ *  dt, beta     [tokens, nheads] io_dtype
+ *  A            [nheads] float32 (negative);  dt_bias [nheads] or NULL
+ *  cu_seqlens, slots, has_state, ssm_state [nslots, nheads, headdim, dstate]
+ *               as for ssm_conv_ssd_fwd: read and written in place at the
+ *               sequence's slot; ssm_state NULL: nothing is carried
+ *  y            [tokens, nheads * headdim] io_dtype
+ *  workspace    ssm_gated_delta_workspace_size(...) bytes of device memory,
+ *               16-byte aligned, owned by the caller; its contents on entry do
+ *               not matter; calls sharing it must not run concurrently
+ * headdim and dstate are 1..256 (SSM_E_UNSUPPORTED otherwise), nheads is a multiple of
+ * ngroups and at most 16384; nseq, tokens, alignment, offsets, aliasing and results as
+ * for ssm_conv_ssd_fwd.  Keys longer than one with b_t above 1 / |k^_t|^2 let the
+ * state grow, as the formula says.  A non-finite input makes what depends on it
+ * non-finite (an infinity may become a NaN), and leaves earlier tokens and other
+ * sequences as they are.
+ */
+int ssm_gated_delta_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, const void* dt, int64_t dt_stride,
+                        const void* beta, int64_t beta_stride, const float* A,
+                        const float* dt_bias, int dt_softplus, int beta_sigmoid, int qk_norm,
+                        float eps, float scale, const int32_t* cu_seqlens, const int32_t* slots,
+                        const uint8_t* has_state, float* ssm_state, void* y, int64_t y_stride,
+                        void* workspace, int64_t workspace_bytes, int64_t tokens, int64_t nseq,
+                        int64_t nslots, int64_t nheads, int64_t headdim, int64_t ngroups,
+                        int64_t dstate, int io_dtype, void* hip_stream);
+
+/* Bytes of workspace ssm_gated_delta_fwd needs (-1 if an extent is out of
+ * range).  Host-only, enqueues nothing. */
+int64_t ssm_gated_delta_workspace_size(int64_t tokens, int64_t nseq, int64_t nheads,
+                                       int64_t headdim, int64_t ngroups, int64_t dstate,
+                                       int io_dtype);
+
+/*
+ * One token for every entry of a batch: ssm_gated_delta_fwd with sequences of one
+ * row each, all of them continuing from their slots.  Row i belongs to slot
+ * slots[i] (NULL: i); a slot outside [0, nslots) marks an entry that a padded batch
+ * leaves empty, which is skipped.  No slot may appear twice.  No workspace.
+ */
+int ssm_gated_delta_update(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const void* dt, int64_t dt_stride,
+                           const void* beta, int64_t beta_stride, const float* A,
+                           const float* dt_bias, int dt_softplus, int beta_sigmoid, int qk_norm,
+                           float eps, float scale, const int32_t* slots, float* ssm_state,
+                           void* y, int64_t y_stride, int64_t batch, int64_t nslots,
+                           int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
+                           int io_dtype, void* hip_stream);
+
+/*
+ * Gradients of the gated delta rule over packed sequences for the loss
+ * sum(dy * y) + sum(dfinal_state * final_state), from its inputs (nothing of the
+ * forward is kept).  Sequence s starts from h0[s] and ends in final_state[s].
+ *  h0           [nseq, nheads, headdim, dstate] float32 or NULL (zeros)
+ *  dfinal_state [nseq, nheads, headdim, dstate] float32 or NULL (zeros)
+ *  dq, dk, dv, ddt, dbeta  rows like their inputs, each with a row stride; rows of
+ *               no sequence get zeros.  dq, dk are sums over the heads of a group
+ *  dA, ddt_bias [nheads] float32 or NULL (not computed)
+ *  dh0          [nseq, nheads, headdim, dstate] float32 or NULL (not computed)
+ *  workspace    ssm_gated_delta_bwd_workspace_size(...) bytes, as above
+ * Every sum has a fixed order: results do not vary from run to run.  Extents and
+ * errors as for ssm_gated_delta_fwd.
+ */
+int ssm_gated_delta_bwd(const void* dy, int64_t dy_stride, const void* q, int64_t q_stride,
+                        const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                        const void* dt, int64_t dt_stride, const void* beta,
+                        int64_t beta_stride, const float* A, const float* dt_bias,
+                        int dt_softplus, int beta_sigmoid, int qk_norm, float eps, float scale,
+                        const int32_t* cu_seqlens, const float* h0, const float* dfinal_state,
+                        void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, void* dv,
+                        int64_t dv_stride, void* ddt, int64_t ddt_stride, void* dbeta,
+                        int64_t dbeta_stride, float* dA, float* ddt_bias, float* dh0,
+                        void* workspace, int64_t workspace_bytes, int64_t tokens, int64_t nseq,
+                        int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
+                        int io_dtype, void* hip_stream);
+
+/* Bytes of workspace ssm_gated_delta_bwd needs (-1 if an extent is out of
+ * range). */
+int64_t ssm_gated_delta_bwd_workspace_size(int64_t tokens, int64_t nseq, int64_t nheads,
+                                           int64_t headdim, int64_t ngroups, int64_t dstate,
+                                           int io_dtype);
+
+/*
+ * The norm in front of a block: the residual stream takes in the last block's
+ * output, and the next block gets the stream's rows by their root mean square.
+ *
+ *   r = x + residual          (residual NULL: x)
+ *   y = weight * r / sqrt(mean(r^2) + eps)
+ *
+ *  x             [rows, channels] io_dtype
+ *  residual, residual_out  [rows, channels] res_dtype: io_dtype, or float32
+ *                beside bf16 rows.  residual_out holds r, rounded to its type, and
+ *                it is this value that is normed.  It may be the residual itself
+ *                (same address and stride); NULL: r is not stored, and is x itself
+ *                (a residual without residual_out is refused)
+ *  weight        [channels] float32 or NULL (1)
+ *  quant         SSM_QUANT_NONE: y has io_dtype.  SSM_QUANT_E4M3: y has one byte an
+ *                element (OCP e4m3: largest value 448), y = e4m3(y / scale), nearest,
+ *                with scale = max(max|y|, 2^-100) / 448 over a block of channels
+ *  block         channels of a block: 32, 64, 128 or 256, or 0 for the whole row; the
+ *                last block may be shorter.  0 with SSM_QUANT_NONE
+ *  scales        [rows, number of blocks] float32, exactly with SSM_QUANT_E4M3
+ * A row has at most 32768 channels (SSM_E_UNSUPPORTED otherwise), a launch less than
+ * 2^32 threads (SSM_E_SHAPE otherwise).  Apart from residual_out no output may overlap
+ * an input.  Arithmetic in float32; a NaN stays one in y and is passed over by the scale.
+ */
+int ssm_add_norm_fwd(const void* x, int64_t x_stride, const void* residual,
+                     int64_t residual_stride, const float* weight, float eps, void* residual_out,
+                     int64_t residual_out_stride, void* y, int64_t y_stride, float* scales,
+                     int quant, int64_t block, int64_t rows, int64_t channels, int io_dtype,
+                     int res_dtype, void* hip_stream);
+
+/*
+ * Gradients of ssm_add_norm_fwd (without quantisation) for the loss
+ * sum(dy * y) + sum(dresidual_out * residual_out), from the stored stream r:
+ *  r             [rows, channels] res_dtype: residual_out, or x where none was stored
+ *  dresidual_out [rows, channels] res_dtype or NULL (zeros)
+ *  dx            [rows, channels] io_dtype
+ *  dresidual     [rows, channels] res_dtype or NULL: the same gradient in the
+ *                residual's type
+ *  dweight       [channels] float32 or NULL (not computed); rows added in a fixed
+ *                order, so results do not vary from run to run
+ *  workspace     ssm_add_norm_bwd_workspace_size(...) bytes, 16-byte aligned, owned
+ *                by the caller; contents on entry do not matter; calls sharing it
+ *                must not run concurrently
+ * Outputs must not overlap inputs or each other.
+ */
+int ssm_add_norm_bwd(const void* dy, int64_t dy_stride, const void* r, int64_t r_stride,
+                     const float* weight, float eps, const void* dresidual_out,
+                     int64_t dresidual_out_stride, void* dx, int64_t dx_stride, void* dresidual,
+                     int64_t dresidual_stride, float* dweight, void* workspace,
+                     int64_t workspace_bytes, int64_t rows, int64_t channels, int io_dtype,
+                     int res_dtype, void* hip_stream);
+
+/* Bytes of workspace ssm_add_norm_bwd needs (-1 if an extent is out of range). */
+int64_t ssm_add_norm_bwd_workspace_size(int64_t rows, int64_t channels);
 
 /*
  * Time-invariant path: y = K * u + D u, the causal convolution of every

@@ -51,6 +51,26 @@ Entry points carry the C names:
   ssm_group_norm_bwd(dy, x, weight, ngroups, ...) -> dict of gradients
       the norm over groups of a row's channels, with its gate or activation
   group_norm_fn(x, weight, ngroups, ...) -> y, differentiable
+  ssm_gated_delta_fwd(q, k, v, dt, beta, A, cu_seqlens, ngroups, dt_bias=None,
+                      dt_softplus=True, beta_sigmoid=True, qk_norm=True, eps=1e-6,
+                      scale=None, slots=None, has_state=None, ssm_state=None,
+                      y=None, workspace=None) -> y
+      the gated delta rule over packed prompts, states as for the mixer
+  ssm_gated_delta_update(q, k, v, dt, beta, ssm_state, A, ngroups, ...,
+                         slots=None, y=None) -> y         (one token a sequence)
+  ssm_gated_delta_bwd(dy, q, k, v, dt, beta, A, cu_seqlens, ngroups, ..., h0=None,
+                      dfinal_state=None, workspace=None) -> dict of gradients
+  gated_delta_fn(q, k, v, dt, beta, A, cu_seqlens, ngroups, ..., h0=None)
+      -> (y, final_state), differentiable
+  ssm_add_norm_fwd(x, weight, residual=None, eps=1e-5, quant="none", block=0,
+                   residual_out=None, y=None, scales=None)
+      -> (y, residual_out, scales)
+      the residual's addition and the root-mean-square norm of the sum, the
+      output in 8 bits with scales for quant="e4m3"
+  ssm_add_norm_bwd(dy, r, weight, dresidual_out=None, eps=1e-5, workspace=None)
+      -> dict of gradients
+  add_norm_fn(x, weight, residual=None, eps=1e-5) -> (y, residual_out),
+      differentiable
 
 Layouts: u, delta, z, y [batch, dim, L]; B, C [batch, dstate, L]; A
 [dim, dstate]; D, delta_bias [dim]; h0 / final_state / state
@@ -61,7 +81,7 @@ stride.  Sequence tensors are torch.bfloat16 or torch.float32
 from __future__ import annotations
 
 from ._lib import (SSM_ACT_NONE, SSM_ACT_SILU, SSM_GATE_AFTER, SSM_GATE_BEFORE, SSM_GATE_NONE,
-                   SSM_BBAR_DELTA_B, SSM_BBAR_ZOH_EXACT, SSM_DTYPE_BF16, SSM_DTYPE_F32,
+                   SSM_QUANT_E4M3, SSM_QUANT_NONE, SSM_BBAR_DELTA_B, SSM_BBAR_ZOH_EXACT, SSM_DTYPE_BF16, SSM_DTYPE_F32,
                    SelscanError, library_path, lib, ssm_abi_version, ssm_last_error,
                    ssm_status_str)
 from .binding import (ssm_causal_conv1d_bwd, ssm_causal_conv1d_fwd, ssm_causal_conv1d_update,
@@ -73,7 +93,11 @@ from .binding import (ssm_causal_conv1d_bwd, ssm_causal_conv1d_fwd, ssm_causal_c
                       ssm_state_update, selective_scan_fn, causal_conv1d_fn,
                       ssm_conv_ssd_fwd, ssm_conv_ssd_update, ssm_conv_ssd_workspace_size,
                       ssm_group_norm_fwd, ssm_group_norm_bwd, ssm_group_norm_bwd_workspace_size,
-                      group_norm_fn)
+                      group_norm_fn,
+                      ssm_gated_delta_fwd, ssm_gated_delta_update, ssm_gated_delta_bwd,
+                      ssm_gated_delta_workspace_size, ssm_gated_delta_bwd_workspace_size,
+                      gated_delta_fn, ssm_add_norm_fwd, ssm_add_norm_bwd,
+                      ssm_add_norm_bwd_workspace_size, add_norm_fn)
 
 __all__ = [
     "ssm_selective_scan_fwd", "ssm_state_update", "ssm_lti_kernel", "ssm_lti_conv",
@@ -83,7 +107,11 @@ __all__ = [
     "ssm_causal_conv1d_bwd", "ssm_ssd_fwd", "ssm_ssd_workspace_size", "ssm_ssd_fwd_noalloc",
     "ssm_ssd_scratch_bytes", "ssm_conv_ssd_fwd", "ssm_conv_ssd_update",
     "ssm_conv_ssd_workspace_size", "ssm_group_norm_fwd", "ssm_group_norm_bwd",
-    "ssm_group_norm_bwd_workspace_size", "group_norm_fn", "ssm_status_str",
+    "ssm_group_norm_bwd_workspace_size", "group_norm_fn",
+    "ssm_gated_delta_fwd", "ssm_gated_delta_update", "ssm_gated_delta_bwd",
+    "ssm_gated_delta_workspace_size", "ssm_gated_delta_bwd_workspace_size", "gated_delta_fn",
+    "ssm_add_norm_fwd", "ssm_add_norm_bwd", "ssm_add_norm_bwd_workspace_size", "add_norm_fn",
+    "SSM_QUANT_NONE", "SSM_QUANT_E4M3", "ssm_status_str",
     "ssm_last_error", "ssm_abi_version", "SelscanError", "library_path", "lib",
     "SSM_ACT_NONE", "SSM_ACT_SILU", "SSM_GATE_NONE", "SSM_GATE_BEFORE", "SSM_GATE_AFTER",
     "SSM_DTYPE_F32", "SSM_DTYPE_BF16", "SSM_BBAR_DELTA_B", "SSM_BBAR_ZOH_EXACT",

@@ -12,6 +12,7 @@ SSM_DTYPE_F32, SSM_DTYPE_BF16 = 0, 1
 SSM_BBAR_DELTA_B, SSM_BBAR_ZOH_EXACT, SSM_DISC_EULER, SSM_DISC_BILINEAR = 0, 1, 2, 3
 SSM_ACT_NONE, SSM_ACT_SILU = 0, 1
 SSM_GATE_NONE, SSM_GATE_BEFORE, SSM_GATE_AFTER = 0, 1, 2
+SSM_QUANT_NONE, SSM_QUANT_E4M3 = 0, 1
 STATUS_NAMES = {0: "SSM_OK", 1: "SSM_E_NULL", 2: "SSM_E_SHAPE", 3: "SSM_E_DTYPE",
                 4: "SSM_E_ALIGN", 5: "SSM_E_ALIAS", 6: "SSM_E_UNSUPPORTED", 7: "SSM_E_HIP"}
 
@@ -81,8 +82,23 @@ def lib() -> ctypes.CDLL:
                                          *rows, vp, vp, *rows, i64, i64, i64, i32, vp]
         L.ssm_group_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
         L.ssm_group_norm_bwd_workspace_size.restype = i64
+        delta = [*rows * 5, vp, vp, i32, i32, i32, f32, f32]  # q, k, v, dt, beta, A, dt_bias, how
+        L.ssm_gated_delta_fwd.argtypes = [*delta, vp, vp, vp, vp, *rows, *rows, *[i64] * 7, i32, vp]
+        L.ssm_gated_delta_update.argtypes = [*delta, vp, vp, *rows, *[i64] * 6, i32, vp]
+        L.ssm_gated_delta_bwd.argtypes = [*rows, *delta, vp, vp, vp, *rows * 5, vp, vp, vp, *rows,
+                                          *[i64] * 6, i32, vp]
+        for f in (L.ssm_gated_delta_workspace_size, L.ssm_gated_delta_bwd_workspace_size):
+            f.argtypes = [*[i64] * 6, i32]
+            f.restype = i64
+        L.ssm_add_norm_fwd.argtypes = [*rows, *rows, vp, f32, *rows, *rows, vp, i32, i64, i64, i64,
+                                       i32, i32, vp]
+        L.ssm_add_norm_bwd.argtypes = [*rows, *rows, vp, f32, *rows, *rows, *rows, vp, *rows, i64, i64,
+                                       i32, i32, vp]
+        L.ssm_add_norm_bwd_workspace_size.argtypes = [i64, i64]
+        L.ssm_add_norm_bwd_workspace_size.restype = i64
         for f in (L.ssm_conv_ssd_fwd, L.ssm_conv_ssd_update, L.ssm_group_norm_fwd,
-                  L.ssm_group_norm_bwd):
+                  L.ssm_group_norm_bwd, L.ssm_gated_delta_fwd, L.ssm_gated_delta_update,
+                  L.ssm_gated_delta_bwd, L.ssm_add_norm_fwd, L.ssm_add_norm_bwd):
             f.restype = i32
         for f in (L.ssm_selective_scan_fwd, L.ssm_state_update, L.ssm_lti_kernel,
                   L.ssm_selective_scan_bwd, L.ssm_causal_conv1d_fwd, L.ssm_causal_conv1d_update,

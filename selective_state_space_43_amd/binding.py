@@ -738,3 +738,306 @@ def group_norm_fn(x, weight, ngroups, bias=None, z=None, eps=1e-5, center=False,
     """ssm_group_norm_fwd's output, differentiable in x, weight, bias and z
     through ssm_group_norm_bwd, once (create_graph is refused)."""
     return _GroupNormFn.apply(x, weight, bias, z, ngroups, eps, center, activation, gate)
+
+
+# ---------------------------------------------------------------- the gated delta rule, rows are tokens
+
+def ssm_gated_delta_workspace_size(tokens, nseq, nheads, headdim, ngroups, dstate, dtype=torch.bfloat16):
+    """Bytes of workspace ssm_gated_delta_fwd needs for tensors of this dtype."""
+    n = lib().ssm_gated_delta_workspace_size(tokens, nseq, nheads, headdim, ngroups, dstate, _IO[dtype])
+    if n < 0:
+        raise ValueError("extents out of range")
+    return int(n)
+
+
+def ssm_gated_delta_bwd_workspace_size(tokens, nseq, nheads, headdim, ngroups, dstate,
+                                       dtype=torch.bfloat16):
+    """Bytes of workspace ssm_gated_delta_bwd needs for tensors of this dtype."""
+    n = lib().ssm_gated_delta_bwd_workspace_size(tokens, nseq, nheads, headdim, ngroups, dstate, _IO[dtype])
+    if n < 0:
+        raise ValueError("extents out of range")
+    return int(n)
+
+
+def _delta_args(q, k, v, dt, beta, A, ngroups, dt_bias, dt_softplus, beta_sigmoid, qk_norm, eps, scale):
+    """(rows, nheads, headdim, dstate, dtype, device, the C arguments they share)."""
+    rows, gn, io, dev = _row_input(q, "q")
+    if not isinstance(A, torch.Tensor) or A.dim() != 1:
+        raise ValueError("A must be [nheads]")
+    H = A.shape[0]
+    if ngroups < 1 or gn % ngroups or H < 1 or H % ngroups:
+        raise ValueError(f"q has {gn} channels and A {H} heads: expected ngroups * dstate and a multiple "
+                         f"of ngroups = {ngroups}")
+    if not isinstance(v, torch.Tensor) or v.dim() != 2 or v.shape[1] % H:
+        raise ValueError("v must be [tokens, nheads * headdim]")
+    hp, N = v.shape[1], gn // ngroups
+    args = (q.data_ptr(), _rows(q, "q", io, rows, gn, dev), k.data_ptr(), _rows(k, "k", io, rows, gn, dev),
+            v.data_ptr(), _rows(v, "v", io, rows, hp, dev), dt.data_ptr(), _rows(dt, "dt", io, rows, H, dev),
+            beta.data_ptr(), _rows(beta, "beta", io, rows, H, dev), _flat(A, "A", torch.float32, (H,), dev),
+            _flat(dt_bias, "dt_bias", torch.float32, (H,), dev), int(bool(dt_softplus)),
+            int(bool(beta_sigmoid)), int(bool(qk_norm)), eps, N ** -0.5 if scale is None else scale)
+    return rows, H, hp // H, N, io, dev, args
+
+
+def _cu(cu_seqlens, dev):
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [nseq + 1]")
+    nseq = cu_seqlens.shape[0] - 1
+    return nseq, _flat(cu_seqlens, "cu_seqlens", torch.int32, (nseq + 1,), dev)
+
+
+def ssm_gated_delta_fwd(q, k, v, dt, beta, A, cu_seqlens, ngroups, dt_bias=None, dt_softplus=True,
+                        beta_sigmoid=True, qk_norm=True, eps=1e-6, scale=None, slots=None,
+                        has_state=None, ssm_state=None, y=None, workspace=None):
+    """The gated delta rule over packed prompts; returns y.
+
+    q, k [tokens, ngroups * dstate], v [tokens, nheads * headdim] and dt, beta
+    [tokens, nheads] are rows (slices of wider rows too); with a = exp(A
+    softplus(dt + dt_bias)), b = sigmoid(beta) and q, k divided by their lengths
+    (sqrt(|x|^2 + eps); qk_norm) and q times scale (None: dstate ** -0.5), each
+    head's state follows S = a S + b (v - a S k) k^T, y = S q.  cu_seqlens, slots,
+    has_state and ssm_state [nslots, nheads, headdim, dstate] as for
+    ssm_conv_ssd_fwd.  Not differentiable: gated_delta_fn is."""
+    rows, H, P, N, io, dev, args = _delta_args(q, k, v, dt, beta, A, ngroups, dt_bias, dt_softplus,
+                                               beta_sigmoid, qk_norm, eps, scale)
+    nseq, cu = _cu(cu_seqlens, dev)
+    if y is None:
+        y = torch.empty((rows, H * P), dtype=io, device=dev)
+    ys = _rows(y, "y", io, rows, H * P, dev)
+    nslots = 0 if ssm_state is None else ssm_state.shape[0]
+    if has_state is not None and has_state.dtype == torch.bool:
+        has_state = has_state.view(torch.uint8)
+    args = (*args, cu, _flat(slots, "slots", torch.int32, (nseq,), dev),
+            _flat(has_state, "has_state", torch.uint8, (nseq,), dev),
+            _flat(ssm_state, "ssm_state", torch.float32, (nslots, H, P, N), dev), y.data_ptr(), ys)
+    L = lib()
+    ws, nbytes = _workspace(workspace, L.ssm_gated_delta_workspace_size(
+        rows, nseq, H, P, ngroups, N, _IO[io]), dev)
+    st = _launch(dev, L.ssm_gated_delta_fwd, *args, _ptr(ws), nbytes, rows, nseq, nslots, H, P, ngroups,
+                 N, _IO[io])
+    check(st, "ssm_gated_delta_fwd")
+    return y
+
+
+def ssm_gated_delta_update(q, k, v, dt, beta, ssm_state, A, ngroups, dt_bias=None, dt_softplus=True,
+                           beta_sigmoid=True, qk_norm=True, eps=1e-6, scale=None, slots=None, y=None):
+    """One token for every row of a batch, its state updated in place at slots[i]
+    (int32; None: slot i; outside the states: the row is padding and skipped, its
+    y left as it was); returns y.  Layouts as ssm_gated_delta_fwd."""
+    rows, H, P, N, io, dev, args = _delta_args(q, k, v, dt, beta, A, ngroups, dt_bias, dt_softplus,
+                                               beta_sigmoid, qk_norm, eps, scale)
+    if not isinstance(ssm_state, torch.Tensor) or ssm_state.dim() != 4:
+        raise ValueError("ssm_state must be [nslots, nheads, headdim, dstate]")
+    nslots = ssm_state.shape[0]
+    if y is None:
+        y = torch.empty((rows, H * P), dtype=io, device=dev)
+    ys = _rows(y, "y", io, rows, H * P, dev)
+    st = _launch(dev, lib().ssm_gated_delta_update, *args, _flat(slots, "slots", torch.int32, (rows,), dev),
+                 _flat(ssm_state, "ssm_state", torch.float32, (nslots, H, P, N), dev), y.data_ptr(), ys,
+                 rows, nslots, H, P, ngroups, N, _IO[io])
+    check(st, "ssm_gated_delta_update")
+    return y
+
+
+def ssm_gated_delta_bwd(dy, q, k, v, dt, beta, A, cu_seqlens, ngroups, dt_bias=None, dt_softplus=True,
+                        beta_sigmoid=True, qk_norm=True, eps=1e-6, scale=None, h0=None, dfinal_state=None,
+                        workspace=None, want_dA=True, want_ddt_bias=True, want_dh0=None):
+    """Gradients of ssm_gated_delta_fwd for sum(dy * y) + sum(dfinal_state *
+    final_state), where sequence s starts from h0[s] ([nseq, nheads, headdim,
+    dstate] float32; None: zeros): dict dq, dk, dv, ddt, dbeta, dA (if want_dA),
+    ddt_bias (if dt_bias and want_ddt_bias), dh0 (want_dh0; None: if h0).  Rows of
+    no sequence have zero gradients."""
+    rows, H, P, N, io, dev, args = _delta_args(q, k, v, dt, beta, A, ngroups, dt_bias, dt_softplus,
+                                               beta_sigmoid, qk_norm, eps, scale)
+    nseq, cu = _cu(cu_seqlens, dev)
+    gs = _rows(dy, "dy", io, rows, H * P, dev)
+    f32 = torch.float32
+    state = (nseq, H, P, N)
+    gn, hp = ngroups * N, H * P
+
+    def new(*shape, dtype=io, on=True):
+        return torch.empty(shape, dtype=dtype, device=dev) if on else None
+
+    g = dict(dq=new(rows, gn), dk=new(rows, gn), dv=new(rows, hp), ddt=new(rows, H), dbeta=new(rows, H),
+             dA=new(H, dtype=f32, on=want_dA),
+             ddt_bias=new(H, dtype=f32, on=dt_bias is not None and want_ddt_bias),
+             dh0=new(*state, dtype=f32, on=h0 is not None if want_dh0 is None else want_dh0))
+    args = (dy.data_ptr(), gs, *args, cu, _flat(h0, "h0", f32, state, dev),
+            _flat(dfinal_state, "dfinal_state", f32, state, dev), _ptr(g["dq"]), gn, _ptr(g["dk"]), gn,
+            _ptr(g["dv"]), hp, _ptr(g["ddt"]), H, _ptr(g["dbeta"]), H, _ptr(g["dA"]), _ptr(g["ddt_bias"]),
+            _ptr(g["dh0"]))
+    L = lib()
+    ws, nbytes = _workspace(workspace, L.ssm_gated_delta_bwd_workspace_size(
+        rows, nseq, H, P, ngroups, N, _IO[io]), dev)
+    st = _launch(dev, L.ssm_gated_delta_bwd, *args, _ptr(ws), nbytes, rows, nseq, H, P, ngroups, N, _IO[io])
+    check(st, "ssm_gated_delta_bwd")
+    return g
+
+
+class _GatedDeltaFn(torch.autograd.Function):
+    """The gated delta rule as an autograd function; the backward starts from the
+    inputs, nothing else is kept."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, dt, beta, A, dt_bias, h0, cu_seqlens, ngroups, how):
+        nseq = cu_seqlens.shape[0] - 1
+        if h0 is None:
+            state = torch.empty((nseq, A.shape[0], v.shape[1] // A.shape[0], q.shape[1] // ngroups),
+                                dtype=torch.float32, device=q.device)
+            has = None
+        else:
+            state = h0.clone(memory_format=torch.contiguous_format)
+            has = torch.ones(nseq, dtype=torch.uint8, device=q.device)
+        y = ssm_gated_delta_fwd(q, k, v, dt, beta, A, cu_seqlens, ngroups, dt_bias=dt_bias, has_state=has,
+                                ssm_state=state, **how)
+        ctx.save_for_backward(q, k, v, dt, beta, A, dt_bias, h0, cu_seqlens)
+        ctx.ngroups, ctx.how = ngroups, how
+        ctx.set_materialize_grads(False)
+        return y, state
+
+    @staticmethod
+    def backward(ctx, dy, dfinal):
+        if torch.is_grad_enabled():  # create_graph: the gradients would pass for constants
+            raise RuntimeError("gated_delta_fn: gradients of its gradients are not computed")
+        if dy is None and dfinal is None:
+            return (None,) * 11
+        q, k, v, dt, beta, A, dt_bias, h0, cu = ctx.saved_tensors
+        dy = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if dy is None else dy.contiguous()
+        g = ssm_gated_delta_bwd(dy, q, k, v, dt, beta, A, cu, ctx.ngroups, dt_bias=dt_bias,
+                                h0=None if h0 is None else h0.contiguous(),
+                                dfinal_state=None if dfinal is None else dfinal.contiguous(),
+                                want_dA=ctx.needs_input_grad[5], want_ddt_bias=ctx.needs_input_grad[6],
+                                want_dh0=ctx.needs_input_grad[7], **ctx.how)
+        return (g["dq"], g["dk"], g["dv"], g["ddt"], g["dbeta"], g["dA"], g["ddt_bias"], g["dh0"],
+                None, None, None)
+
+
+def gated_delta_fn(q, k, v, dt, beta, A, cu_seqlens, ngroups, dt_bias=None, dt_softplus=True,
+                   beta_sigmoid=True, qk_norm=True, eps=1e-6, scale=None, h0=None):
+    """(y, final_state) of the gated delta rule over packed sequences, sequence s
+    from h0[s] (None: zeros), differentiable in q, k, v, dt, beta, A, dt_bias and h0
+    through ssm_gated_delta_bwd, once (create_graph is refused).  y of rows that
+    belong to no sequence is not defined."""
+    how = dict(dt_softplus=dt_softplus, beta_sigmoid=beta_sigmoid, qk_norm=qk_norm, eps=eps, scale=scale)
+    return _GatedDeltaFn.apply(q, k, v, dt, beta, A, dt_bias, h0, cu_seqlens, ngroups, how)
+
+
+# ---------------------------------------------------------------- the norm in front of a block
+
+_QUANT = {"none": 0, "e4m3": 1}
+
+
+def _res_dtype(t, name, io):
+    if not isinstance(t, torch.Tensor) or (t.dtype is not io and t.dtype is not torch.float32):
+        raise TypeError(f"{name} must have the rows' dtype or float32")
+    return t.dtype
+
+
+def ssm_add_norm_fwd(x, weight, residual=None, eps=1e-5, quant="none", block=0, residual_out=None, y=None,
+                     scales=None):
+    """The residual's addition and the norm of the sum by its root mean square:
+    r = x + residual, y = weight * r / sqrt(mean(r^2) + eps); returns (y,
+    residual_out, scales).  x [rows, channels]; residual, residual_out the same
+    dtype or float32 (residual_out may be the residual itself; it holds r, and the
+    value that it holds is normed; without a residual it is optional and None is
+    returned for it); weight [channels] float32 or None.  quant "e4m3": y is
+    torch.float8_e4m3fn and y * scales the result, one scale for each block of
+    `block` channels (32, 64, 128 or 256; 0: the whole row) of a row."""
+    rows, C, io, dev = _row_input(x, "x")
+    xs = _rows(x, "x", io, rows, C, dev)
+    if quant not in _QUANT:
+        raise ValueError(f"quant {quant!r}: expected one of {sorted(_QUANT)}")
+    q = quant == "e4m3"
+    rio, rs, os = io, 0, 0
+    if residual is not None:
+        rio = _res_dtype(residual, "residual", io)
+        rs = _rows(residual, "residual", rio, rows, C, dev)
+        if residual_out is None:
+            residual_out = torch.empty((rows, C), dtype=rio, device=dev)
+    if residual_out is not None:
+        if residual is None:
+            rio = _res_dtype(residual_out, "residual_out", io)
+        os = _rows(residual_out, "residual_out", rio, rows, C, dev)
+    yt = torch.float8_e4m3fn if q else io
+    if y is None:
+        y = torch.empty((rows, C), dtype=yt, device=dev)
+    ys = _rows(y, "y", yt, rows, C, dev)
+    if q and scales is None:
+        scales = torch.empty((rows, -(-C // block) if block > 0 else 1), dtype=torch.float32, device=dev)
+    st = _launch(dev, lib().ssm_add_norm_fwd, x.data_ptr(), xs, _ptr(residual), rs,
+                 _flat(weight, "weight", torch.float32, (C,), dev), eps, _ptr(residual_out), os, y.data_ptr(), ys,
+                 _flat(scales, "scales", torch.float32, (rows, -(-C // block) if block > 0 else 1), dev),
+                 _QUANT[quant], block, rows, C, _IO[io], _IO[rio])
+    check(st, "ssm_add_norm_fwd")
+    return y, residual_out, scales
+
+
+def ssm_add_norm_bwd_workspace_size(rows, channels):
+    """Bytes of workspace ssm_add_norm_bwd needs."""
+    n = lib().ssm_add_norm_bwd_workspace_size(rows, channels)
+    if n < 0:
+        raise ValueError("extents out of range")
+    return int(n)
+
+
+def ssm_add_norm_bwd(dy, r, weight, dresidual_out=None, eps=1e-5, workspace=None, want_dweight=True):
+    """Gradients of ssm_add_norm_fwd for sum(dy * y) + sum(dresidual_out *
+    residual_out), from the stored stream r (residual_out, or x where none was
+    stored): dict dx (dy's dtype), dresidual (r's dtype; where that is dy's, dx is
+    the residual's gradient too and dresidual None), dweight (if weight and
+    want_dweight)."""
+    rows, C, io, dev = _row_input(dy, "dy")
+    gs = _rows(dy, "dy", io, rows, C, dev)
+    rio = _res_dtype(r, "r", io)
+    rs = _rows(r, "r", rio, rows, C, dev)
+    ds = 0 if dresidual_out is None else _rows(dresidual_out, "dresidual_out", rio, rows, C, dev)
+    w = _flat(weight, "weight", torch.float32, (C,), dev)
+    L = lib()
+    ws, nbytes = _workspace(workspace, L.ssm_add_norm_bwd_workspace_size(rows, C), dev)
+    g = dict(dx=torch.empty((rows, C), dtype=io, device=dev),
+             dresidual=torch.empty((rows, C), dtype=rio, device=dev) if rio is not io else None,
+             dweight=(torch.empty(C, dtype=torch.float32, device=dev)
+                      if weight is not None and want_dweight else None))
+    st = _launch(dev, L.ssm_add_norm_bwd, dy.data_ptr(), gs, r.data_ptr(), rs, w, eps, _ptr(dresidual_out), ds,
+                 _ptr(g["dx"]), C, _ptr(g["dresidual"]), C, _ptr(g["dweight"]), _ptr(ws), nbytes, rows, C,
+                 _IO[io], _IO[rio])
+    check(st, "ssm_add_norm_bwd")
+    return g
+
+
+class _AddNormFn(torch.autograd.Function):
+    """The residual's addition and its norm as an autograd function; the stored
+    stream is what is kept."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, r, _ = ssm_add_norm_fwd(x, weight, residual=residual, eps=eps)
+        ctx.save_for_backward(x if r is None else r, weight)
+        ctx.eps, ctx.added, ctx.x_dtype = eps, r is not None, x.dtype
+        ctx.set_materialize_grads(False)
+        # without a residual the stream is x itself: x's own gradient path, not an output here
+        return (y, r) if r is not None else (y,)
+
+    @staticmethod
+    def backward(ctx, dy, dr=None):
+        if torch.is_grad_enabled():  # create_graph: the gradients would pass for constants
+            raise RuntimeError("add_norm_fn: gradients of its gradients are not computed")
+        r, weight = ctx.saved_tensors
+        if dy is None:
+            if dr is None:
+                return None, None, None, None
+            # the norm took no part: both terms of the sum have its gradient
+            return dr.to(ctx.x_dtype), None, dr, None
+        g = ssm_add_norm_bwd(dy.contiguous(), r, weight, dresidual_out=None if dr is None else dr.contiguous(),
+                             eps=ctx.eps, want_dweight=ctx.needs_input_grad[1])
+        dres = g["dresidual"] if g["dresidual"] is not None else g["dx"]
+        return g["dx"], g["dweight"], dres if ctx.added else None, None
+
+
+def add_norm_fn(x, weight, residual=None, eps=1e-5):
+    """(y, r): r = x + residual, y its norm, as ssm_add_norm_fwd without quantisation,
+    differentiable in x, weight and residual through ssm_add_norm_bwd, once
+    (create_graph is refused).  Without a residual r is x."""
+    if residual is None:
+        return _AddNormFn.apply(x, weight, None, eps)[0], x
+    return _AddNormFn.apply(x, weight, residual, eps)

@@ -11,7 +11,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SRCS = [os.path.join(CSRC, n) for n in ("selscan.hip", "mixer.hip")]
+SRCS = [os.path.join(CSRC, n) for n in ("selscan.hip", "mixer.hip", "delta.hip", "addnorm.hip")]
 OUT = os.path.join(HERE, "libselscan.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,414 @@
+// libselscan -- the norm in front of a block for AMD Instinct MI355X (gfx950): the
+// residual's addition and the root-mean-square norm in one pass over the rows, the
+// output in 8 bits with scales where it is asked for (ssm_add_norm_fwd), and the
+// gradients (ssm_add_norm_bwd).
+//
+//   r = x + residual,   y = w n,   n = r / sqrt(mean(r^2) + eps)
+//   d = (w dy - n mean(w dy n)) / sqrt(mean(r^2) + eps) + dresidual_out
+//   dweight = sum over rows of dy n
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "rows.h"
+
+namespace {
+
+struct AddNormArgs {
+  const void *x, *res, *dy, *dro;  // x: the stored stream in the backward
+  const float* w;
+  void *ro, *y, *dres;             // y: dx in the backward
+  float* scales;
+  float* pw;                       // the strips' sums of dweight [strips, C], or NULL
+  int strips;
+  int64_t xs, rs, gs, drs, ros, ys, dss;  // row strides
+  int64_t rows;
+  int C, nb, lb;                   // blocks of a row, log2 of a block's channels (31: the whole row)
+  float eps;
+};
+
+// VE neighbours of type T as float32, in 16-byte accesses where there are that many
+template <typename T, int VE>
+struct Some {
+  static constexpr int parts = VE * sizeof(T) > 16 ? VE * sizeof(T) / 16 : 1;
+  Vec<T, VE / parts> v[parts];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+#pragma unroll
+    for (int k = 0; k < parts; ++k) v[k].load(p, i + k * (VE / parts));
+  }
+  __device__ __forceinline__ float get(int j) const { return v[j / (VE / parts)].get(j % (VE / parts)); }
+};
+template <typename T, int VE>
+__device__ __forceinline__ void put_some(void* p, int64_t i, const float* v) {
+  constexpr int parts = Some<T, VE>::parts;
+#pragma unroll
+  for (int k = 0; k < parts; ++k) put<T, VE / parts>(p, i + k * (VE / parts), v + k * (VE / parts));
+}
+// what a value is after it has been stored
+template <typename T>
+__device__ __forceinline__ float stored(float v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else return (float)(__bf16)v;
+}
+template <int VE>
+__device__ __forceinline__ void put_e4m3(void* p, int64_t i, const float* v) {
+  uint8_t* o = static_cast<uint8_t*>(p) + i;
+  if constexpr (VE == 1) {
+    *o = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[0], 0, false);
+  } else {
+    uint32_t w[VE / 4];
+#pragma unroll
+    for (int k = 0; k < VE / 4; ++k) {
+      int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k], v[4 * k + 1], 0, false);
+      w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k + 2], v[4 * k + 3], b, true);
+    }
+    if constexpr (VE == 8) *reinterpret_cast<u2*>(o) = (u2){w[0], w[1]};
+    else *reinterpret_cast<uint32_t*>(o) = w[0];
+  }
+}
+
+// A row is held in the registers of a team of TL threads, thread i with vectors i,
+// i + TL, .. (K at most) of VE channels each: one pass over memory.
+template <typename IO, typename RES, int VE, int TL, int K, bool QUANT>
+__global__ void __launch_bounds__(team_threads(TL)) add_norm_kernel(const AddNormArgs a) {
+  constexpr int TW = team_threads(TL) / TL, NB = QUANT ? (TL * K * VE + 31) / 32 : 1;
+  __shared__ float red[2][1][TL < 64 ? 1 : TL / 64];
+  __shared__ uint32_t s_max[QUANT ? TW : 1][NB];
+  int turn = 0;
+  const int nv = a.C / VE, i = threadIdx.x % TL, tw = threadIdx.x / TL;
+  const int64_t row = (int64_t)blockIdx.x * TW + tw;
+  const bool on = row < a.rows;  // the others only keep the waves whole
+  const int64_t r = on ? row : 0;
+  Some<IO, VE> x[K];
+  Some<RES, VE> res[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * TL >= nv) break;
+    const int c = min(i + k * TL, nv - 1) * VE;
+    x[k].load(a.x, r * a.xs + c);
+    if (a.res) res[k].load(a.res, r * a.rs + c);
+  }
+  if constexpr (QUANT) {
+    for (int u = i; u < a.nb; u += TL) s_max[tw][u] = 0;
+    __syncthreads();
+  }
+  float v[K][VE], sq[1] = {0.0f};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * TL >= nv) break;
+    const bool in = i + k * TL < nv;
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      v[k][j] = x[k].get(j);
+      if (a.res) v[k][j] += res[k].get(j);
+    }
+    if (a.ro) {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) v[k][j] = stored<RES>(v[k][j]);
+      if (on && in) put_some<RES, VE>(a.ro, r * a.ros + (i + k * TL) * VE, v[k]);
+    }
+    if (in)
+#pragma unroll
+      for (int j = 0; j < VE; ++j) sq[0] = fmaf(v[k][j], v[k][j], sq[0]);
+  }
+  team_sum<TL, 1>(sq, red, turn);
+  const float rs = rsqrtf(fmaf(sq[0], 1.0f / (float)a.C, a.eps));
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k * TL >= nv) break;
+    const bool in = i + k * TL < nv;
+    const int c = min(i + k * TL, nv - 1) * VE;
+    float w[VE], m = 0.0f;
+    params<VE>(a.w, c, 1.0f, w);
+#pragma unroll
+    for (int j = 0; j < VE; ++j) {
+      v[k][j] = v[k][j] * rs * w[j];
+      m = fmaxf(m, fabsf(v[k][j]));
+    }
+    if constexpr (QUANT) {
+      if (in) atomicMax(&s_max[tw][c >> a.lb], __float_as_uint(m));
+    } else {
+      if (on && in) put_some<IO, VE>(a.y, r * a.ys + c, v[k]);
+    }
+  }
+  if constexpr (QUANT) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      const int c = (i + k * TL) * VE;
+      if (on && i + k * TL < nv) {
+        const float scale = fmaxf(__uint_as_float(s_max[tw][c >> a.lb]), 0x1p-100f) * (1.0f / 448.0f), f = 1.0f / scale;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) v[k][j] *= f;
+        put_e4m3<VE>(a.y, r * a.ys + c, v[k]);
+      }
+    }
+    if (on)
+      for (int u = i; u < a.nb; u += TL)
+        a.scales[r * a.nb + u] = fmaxf(__uint_as_float(s_max[tw][u]), 0x1p-100f) * (1.0f / 448.0f);
+  }
+}
+
+// The backward: a workgroup's teams keep their columns' sums of dy n in registers over a
+// strip of rows; column_sum_kernel adds the strips in order.
+template <typename IO, typename RES, int VE, int TL, int K>
+__global__ void __launch_bounds__(team_threads(TL)) add_norm_bwd_kernel(const AddNormArgs a) {
+  __shared__ float red[2][2][TL < 64 ? 1 : TL / 64];
+  int turn = 0;
+  constexpr int TW = team_threads(TL) / TL;
+  const int nv = a.C / VE, i = threadIdx.x % TL, tw = threadIdx.x / TL;
+  const int64_t strip = blockIdx.x;
+  const int64_t r0 = a.rows * strip / a.strips, r1 = a.rows * (strip + 1) / a.strips;
+  const int64_t turns = (r1 - r0 + TW - 1) / TW;  // of every team: wide ones meet inside
+  const float inv = 1.0f / (float)a.C;
+  float dw[K][VE] = {};
+  for (int64_t q = 0; q < turns; ++q) {
+    const int64_t r = r0 + q * TW + tw, rr = min(r, a.rows - 1);
+    const bool live = r < r1;
+    Some<RES, VE> x[K], dr[K];
+    Some<IO, VE> g[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      const int c = min(i + k * TL, nv - 1) * VE;
+      x[k].load(a.x, rr * a.xs + c);
+      g[k].load(a.dy, rr * a.gs + c);
+      if (a.dro) dr[k].load(a.dro, rr * a.drs + c);
+    }
+    float both[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      float w[VE];
+      params<VE>(a.w, min(i + k * TL, nv - 1) * VE, 1.0f, w);
+      if (live && i + k * TL < nv)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float t = x[k].get(j);
+          both[0] = fmaf(t, t, both[0]);
+          both[1] = fmaf(g[k].get(j) * w[j], t, both[1]);
+        }
+    }
+    team_sum<TL, 2>(both, red, turn);
+    const float rs = rsqrtf(fmaf(both[0], inv, a.eps)), s2 = both[1] * rs * inv;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k * TL >= nv) break;
+      if (live && i + k * TL < nv) {
+        const int c = (i + k * TL) * VE;
+        float d[VE], w[VE];
+        params<VE>(a.w, c, 1.0f, w);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float n = x[k].get(j) * rs, t = g[k].get(j);
+          dw[k][j] = fmaf(t, n, dw[k][j]);
+          d[j] = rs * (t * w[j] - n * s2);
+          if (a.dro) d[j] += dr[k].get(j);
+        }
+        put_some<IO, VE>(a.y, r * a.ys + c, d);
+        if (a.dres) put_some<RES, VE>(a.dres, r * a.dss + c, d);
+      }
+    }
+  }
+  if (!a.pw) return;
+  // the teams' column sums, team by team in order
+  constexpr int M = VE < 4 ? 1 : 4;
+  float* out = a.pw + strip * a.C;
+  if constexpr (TW > 1) {
+    __shared__ __align__(16) float s_sum[TW][TL * K * VE];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < VE; j += M) put<float, M>(s_sum[tw], (i + k * TL) * VE + j, dw[k] + j);
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.C; c += TW * TL) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < TW; ++k) s += s_sum[k][c];
+      out[c] = s;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (i + k * TL >= nv) break;
+#pragma unroll
+      for (int j = 0; j < VE; j += M) put<float, M>(out, (i + k * TL) * VE + j, dw[k] + j);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+constexpr int64_t kMaxChannels = 32768;
+
+int check_add_norm(int64_t rows, int64_t channels, float eps, int io_dtype, int res_dtype) {
+  int st;
+  if ((st = check_extent("rows", rows)) || (st = check_extent("channels", channels))) return st;
+  if (channels > kMaxChannels)
+    return fail(SSM_E_UNSUPPORTED, "a row of %lld channels: at most %lld", (long long)channels, (long long)kMaxChannels);
+  if (!(eps >= 0.0f) || eps > 3e38f) return fail(SSM_E_SHAPE, "eps is negative or not finite");
+  if ((st = check_io(io_dtype))) return st;
+  if (res_dtype != io_dtype && res_dtype != SSM_DTYPE_F32)
+    return fail(SSM_E_DTYPE, "res_dtype = %d is neither io_dtype nor SSM_DTYPE_F32", res_dtype);
+  return SSM_OK;
+}
+
+// Whether rows start on 16 bytes in every tensor, so that whole vectors can be read.
+bool on16(const void* p, int64_t stride, int es) { return !p || (((uintptr_t)p | (uintptr_t)(stride * es)) & 15) == 0; }
+
+template <bool BWD, bool QUANT, typename IO, typename RES, int VE, int TL, int K>
+int launch_add_norm_team(AddNormArgs& a, hipStream_t s) {
+  constexpr int TH = team_threads(TL), TW = TH / TL;
+  if constexpr (BWD) {
+    const int64_t fill = (kNormThreads + TH - 1) / TH;
+    if (fill < a.strips) a.strips = (int)fill;
+    add_norm_bwd_kernel<IO, RES, VE, TL, K><<<(unsigned)a.strips, TH, 0, s>>>(a);
+  } else {
+    const int64_t blocks = (a.rows + TW - 1) / TW;
+    if (!grid_ok(blocks, TH)) return fail(SSM_E_SHAPE, "rows = %lld: too many for one call", (long long)a.rows);
+    add_norm_kernel<IO, RES, VE, TL, K, QUANT><<<(unsigned)blocks, TH, 0, s>>>(a);
+  }
+  return launch_status(BWD ? "ssm_add_norm_bwd launch" : "ssm_add_norm_fwd launch");
+}
+
+// The smallest team whose registers hold the row.
+template <bool BWD, bool QUANT, typename IO, typename RES>
+int launch_add_norm(AddNormArgs& a, bool vec, hipStream_t s) {
+  constexpr int VE = 16 / sizeof(IO);
+  const int nv = vec ? a.C / VE : a.C;
+#define ADD_NORM(ve, tl, k) return launch_add_norm_team<BWD, QUANT, IO, RES, ve, tl, k>(a, s)
+  if (vec) {
+    if (nv <= 8 * 3) ADD_NORM(VE, 8, 3);
+    if (nv <= 64 * 2) ADD_NORM(VE, 64, 2);
+    if (nv <= 256 * 3) ADD_NORM(VE, 256, 3);
+    if (nv <= 512 * 2) ADD_NORM(VE, 512, 2);
+    if (nv <= 1024 * 4) ADD_NORM(VE, 1024, 4);
+    if constexpr (VE == 4) ADD_NORM(VE, 1024, 8);
+  }
+  if (nv <= 8 * 8) ADD_NORM(1, 8, 8);
+  if (nv <= 64 * 4) ADD_NORM(1, 64, 4);
+  if (nv <= 256 * 4) ADD_NORM(1, 256, 4);
+  if (nv <= 256 * 16) ADD_NORM(1, 256, 16);
+  if (nv <= 1024 * 16) ADD_NORM(1, 1024, 16);
+  ADD_NORM(1, 1024, 32);
+#undef ADD_NORM
+}
+
+template <bool BWD, bool QUANT>
+int launch_add_norm_types(AddNormArgs& a, bool vec, int io_dtype, int res_dtype, hipStream_t s) {
+  if (io_dtype == SSM_DTYPE_F32) return launch_add_norm<BWD, QUANT, float, float>(a, vec, s);
+  if (res_dtype == SSM_DTYPE_F32) return launch_add_norm<BWD, QUANT, uint16_t, float>(a, vec, s);
+  return launch_add_norm<BWD, QUANT, uint16_t, uint16_t>(a, vec, s);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- C ABI
+
+extern "C" {
+
+int ssm_add_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                     const float* weight, float eps, void* residual_out, int64_t residual_out_stride, void* y,
+                     int64_t y_stride, float* scales, int quant, int64_t block, int64_t rows, int64_t channels,
+                     int io_dtype, int res_dtype, void* hip_stream) {
+  g_last_error[0] = 0;
+  if (!x) return fail(SSM_E_NULL, "x is NULL");
+  if (!y) return fail(SSM_E_NULL, "y is NULL");
+  if (residual && !residual_out) return fail(SSM_E_NULL, "residual_out is NULL beside a residual");
+  int st = check_add_norm(rows, channels, eps, io_dtype, res_dtype);
+  if (st) return st;
+  if (quant != SSM_QUANT_NONE && quant != SSM_QUANT_E4M3)
+    return fail(SSM_E_DTYPE, "quant = %d is not a known value", quant);
+  const bool q = quant == SSM_QUANT_E4M3;
+  if (q != (scales != nullptr)) return fail(SSM_E_NULL, q ? "scales is NULL" : "scales without quantisation");
+  if (block != 0 && (!q || (block != 32 && block != 64 && block != 128 && block != 256)))
+    return fail(SSM_E_SHAPE, "block = %lld: 32, 64, 128, 256 or 0 with quantisation, 0 without", (long long)block);
+  const int es = io_dtype == SSM_DTYPE_BF16 ? 2 : 4, er = res_dtype == SSM_DTYPE_BF16 ? 2 : 4, ey = q ? 1 : es;
+  if ((st = check_rows("x", x, x_stride, channels, rows, es)) ||
+      (residual && (st = check_rows("residual", residual, residual_stride, channels, rows, er))) ||
+      (residual_out && (st = check_rows("residual_out", residual_out, residual_out_stride, channels, rows, er))) ||
+      (st = check_rows("y", y, y_stride, channels, rows, ey)))
+    return st;
+  if (((uintptr_t)weight | (uintptr_t)scales) & 3) return fail(SSM_E_ALIGN, "weight or scales is not aligned to its elements");
+  AddNormArgs a;
+  memset(&a, 0, sizeof a);
+  a.nb = block ? (int)((channels + block - 1) / block) : 1;
+  a.lb = block ? __builtin_ctzll((unsigned long long)block) : 31;
+  // the residual may be replaced in place: a thread reads its values before it writes them
+  const bool in_place = residual_out == residual && residual_out_stride == residual_stride;
+  const Rows ins[] = {{x, rows, x_stride * es, channels * es, "x"},
+                      {in_place ? nullptr : residual, rows, residual_stride * er, channels * er, "residual"},
+                      flat(weight, channels * 4, "weight")};
+  const Rows outs[] = {{y, rows, y_stride * ey, channels * ey, "y"},
+                       {residual_out, rows, residual_out_stride * er, channels * er, "residual_out"},
+                       flat(scales, rows * a.nb * 4, "scales")};
+  if ((st = check_no_alias(outs, 3, ins, 3))) return st;
+  a.x = x; a.res = residual; a.w = weight; a.ro = residual_out; a.y = y; a.scales = scales;
+  a.xs = x_stride; a.rs = residual_stride; a.ros = residual_out_stride; a.ys = y_stride;
+  a.rows = rows; a.C = (int)channels; a.eps = eps;
+  const bool vec = channels * es % 16 == 0 && on16(x, x_stride, es) && on16(residual, residual_stride, er) &&
+                   on16(residual_out, residual_out_stride, er) && on16(weight, 0, 4) &&
+                   (q ? (((uintptr_t)y | (uintptr_t)y_stride) % (16 / es)) == 0 : on16(y, y_stride, es));
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  return q ? launch_add_norm_types<false, true>(a, vec, io_dtype, res_dtype, s)
+           : launch_add_norm_types<false, false>(a, vec, io_dtype, res_dtype, s);
+}
+
+int64_t ssm_add_norm_bwd_workspace_size(int64_t rows, int64_t channels) {
+  g_last_error[0] = 0;
+  if (check_extent("rows", rows) || check_extent("channels", channels) || channels > 0x7fffffff) return -1;
+  return (norm_strips(rows, channels) * channels * 4 + 15) / 16 * 16;
+}
+
+int ssm_add_norm_bwd(const void* dy, int64_t dy_stride, const void* r, int64_t r_stride, const float* weight,
+                     float eps, const void* dresidual_out, int64_t dresidual_out_stride, void* dx,
+                     int64_t dx_stride, void* dresidual, int64_t dresidual_stride, float* dweight,
+                     void* workspace, int64_t workspace_bytes, int64_t rows, int64_t channels, int io_dtype,
+                     int res_dtype, void* hip_stream) {
+  g_last_error[0] = 0;
+  const struct { const void* p; const char* name; } req[] = {{dy, "dy"}, {r, "r"}, {dx, "dx"}, {workspace, "workspace"}};
+  for (const auto& p : req)
+    if (!p.p) return fail(SSM_E_NULL, "%s is NULL", p.name);
+  int st = check_add_norm(rows, channels, eps, io_dtype, res_dtype);
+  if (st) return st;
+  const int es = io_dtype == SSM_DTYPE_BF16 ? 2 : 4, er = res_dtype == SSM_DTYPE_BF16 ? 2 : 4;
+  if ((st = check_rows("dy", dy, dy_stride, channels, rows, es)) ||
+      (st = check_rows("r", r, r_stride, channels, rows, er)) ||
+      (dresidual_out && (st = check_rows("dresidual_out", dresidual_out, dresidual_out_stride, channels, rows, er))) ||
+      (st = check_rows("dx", dx, dx_stride, channels, rows, es)) ||
+      (dresidual && (st = check_rows("dresidual", dresidual, dresidual_stride, channels, rows, er))))
+    return st;
+  if (((uintptr_t)weight | (uintptr_t)dweight) & 3) return fail(SSM_E_ALIGN, "weight or dweight is not aligned to its elements");
+  const int64_t need = ssm_add_norm_bwd_workspace_size(rows, channels);
+  if (workspace_bytes < need)
+    return fail(SSM_E_SHAPE, "workspace holds %lld bytes, needs %lld", (long long)workspace_bytes, (long long)need);
+  if (!aligned16(workspace)) return fail(SSM_E_ALIGN, "workspace is not 16-byte aligned");
+  const Rows ins[] = {{dy, rows, dy_stride * es, channels * es, "dy"}, {r, rows, r_stride * er, channels * er, "r"},
+                      {dresidual_out, rows, dresidual_out_stride * er, channels * er, "dresidual_out"},
+                      flat(weight, channels * 4, "weight")};
+  const Rows outs[] = {{dx, rows, dx_stride * es, channels * es, "dx"},
+                       {dresidual, rows, dresidual_stride * er, channels * er, "dresidual"},
+                       flat(dweight, channels * 4, "dweight"), flat(workspace, need, "workspace")};
+  if ((st = check_no_alias(outs, 4, ins, 4))) return st;
+  AddNormArgs a;
+  memset(&a, 0, sizeof a);
+  a.x = r; a.dy = dy; a.dro = dresidual_out; a.w = weight; a.y = dx; a.dres = dresidual;
+  a.xs = r_stride; a.gs = dy_stride; a.drs = dresidual_out_stride; a.ys = dx_stride; a.dss = dresidual_stride;
+  a.rows = rows; a.C = (int)channels; a.eps = eps;
+  a.strips = (int)norm_strips(rows, channels);
+  a.pw = dweight ? static_cast<float*>(workspace) : nullptr;
+  const bool vec = channels * es % 16 == 0 && on16(dy, dy_stride, es) && on16(r, r_stride, er) &&
+                   on16(dresidual_out, dresidual_out_stride, er) && on16(dx, dx_stride, es) &&
+                   on16(dresidual, dresidual_stride, er) && on16(weight, 0, 4);
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  if ((st = launch_add_norm_types<true, false>(a, vec, io_dtype, res_dtype, s))) return st;
+  if (dweight)
+    column_sum_kernel<<<dim3((unsigned)((channels + 63) / 64), 1), 1024, 0, s>>>(a.pw, nullptr, a.strips, a.C, dweight, nullptr);
+  return launch_status("ssm_add_norm_bwd launch");
+}
+
+}  // extern "C"

@@ -1310,7 +1310,7 @@ __global__ void __launch_bounds__(team_threads(TL)) norm_fwd_kernel(const NormAr
 // The backward: with u = g w (g the gradient of the affine result) and n the
 // normalised values, d = (u - mean(u) - n mean(u n)) / deviation, mean(u) only
 // where the forward is centred.  A workgroup's teams keep their group and their columns'
-// sums of g n and g in registers over a strip of rows; norm_bwd_sum_kernel adds
+// sums of g n and g in registers over a strip of rows; column_sum_kernel adds
 // the strips in order.
 //
 // PLAIN: no centring, no activation, no gate behind and no bias, as the Mamba-2
@@ -1495,30 +1495,6 @@ __attribute__((amdgpu_waves_per_eu(TL > 256 ? 4 : PLAIN || sizeof(IO) == 4 ? 3 :
   if (a.pw) keep(a.pw, dw);
   if constexpr (!PLAIN)
     if (a.pb) keep(a.pb, db);
-}
-
-// Column sums of the strips' partial sums, in order: sixteen runs of strips a
-// column, then the sixteen.  blockIdx.y: dweight or dbias.
-__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const NormArgs a, float* dw, float* db) {
-  __shared__ float run[16][64];
-  const float* part = blockIdx.y ? a.pb : a.pw;
-  float* out = blockIdx.y ? db : dw;
-  if (!out) return;
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-  const int lo = a.strips * q / 16, hi = a.strips * (q + 1) / 16;
-  float s = 0.0f;
-  if (c < a.C) {
-#pragma unroll 8
-    for (int i = lo; i < hi; ++i) s += part[(int64_t)i * a.C + c];
-  }
-  run[q][threadIdx.x & 63] = s;
-  __syncthreads();
-  if (q == 0 && c < a.C) {
-    s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) s += run[k][threadIdx.x];
-    out[c] = s;
-  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -1734,15 +1710,6 @@ int launch_step_io(const MixArgs& a, hipStream_t s) {
   if (a.N <= 128) return launch_step<IO, 32, true>(a, s);
   return launch_step<IO, 64, true>(a, s);
 }
-
-// Strips of rows whose column sums are kept apart, at most: three waves for every
-// SIMD of the card where the partial sums stay under 16 MB a gradient.
-int64_t norm_strips(int64_t rows, int64_t channels) {
-  int64_t n = ((int64_t)1 << 22) / channels;
-  n = n < 256 ? 256 : (n > 1024 ? 1024 : n);
-  return n < rows ? n : rows;
-}
-constexpr int64_t kNormThreads = 256 * 4 * 3 * 64;
 
 constexpr int64_t kMaxGroup = 32768;
 
@@ -2014,7 +1981,7 @@ int ssm_group_norm_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
   if ((st = launch_norm<true>(a, norm_vectors(a, es), io_dtype, s))) return st;
   if (dweight || dbias)
-    norm_bwd_sum_kernel<<<dim3((unsigned)((channels + 63) / 64), 2), 1024, 0, s>>>(a, dweight, dbias);
+    column_sum_kernel<<<dim3((unsigned)((channels + 63) / 64), 2), 1024, 0, s>>>(a.pw, a.pb, a.strips, a.C, dweight, dbias);
   return launch_status("ssm_group_norm_bwd launch");
 }
 

@@ -1,0 +1,308 @@
+"""The norm with the residual's addition on the GPU against float64, its output in
+8 bits, its gradients, and a layer's run of it with the gated delta rule.  Bounds:
+tests/delta_ref.py."""
+import numpy as np
+import pytest
+
+import delta_ref as ref
+from test_mixer_gpu import dev, f64, rows_of, ssm, up  # noqa: F401  (fixtures)
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+IO = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+CASES = [  # rows, channels, dtype, residual, lead
+    (1, 5120, "bf16", "bf16", 0), (3, 64, "bf16", "f32", 0), (1, 1, "f32", "f32", 0), (5, 100, "bf16", None, 0),
+    (37, 200, "bf16", "bf16", 0), (33, 192, "bf16", "bf16", 8), (9, 200, "f32", "f32", 4), (70, 1000, "f32", "f32", 1),
+    (50, 1024, "bf16", "f32", 0), (300, 1032, "bf16", "bf16", 0), (129, 1001, "bf16", "bf16", 0), (40, 256, "bf16", "bf16", 1),
+    (40, 257, "bf16", "f32", 0), (11, 1025, "f32", "f32", 0), (7, 4097, "bf16", "bf16", 0), (6, 6144, "bf16", "f32", 8),
+    (6, 6152, "bf16", "bf16", 0), (5, 8200, "bf16", "bf16", 0), (3, 16385, "bf16", "f32", 0), (4, 32768, "bf16", "bf16", 0),
+    (3, 32768, "f32", "f32", 0), (2, 32767, "f32", None, 0), (1100, 520, "f32", "f32", 0), (2500, 96, "bf16", "bf16", 0),
+]
+
+
+class Norm:
+    def __init__(self, dev, rows, C, dtype, residual, lead, seed, weight=True):
+        rng = np.random.default_rng(seed)
+        q, rq = ref._q(dtype), ref._q(residual or dtype)
+        self.x, self.dy = q(rng.standard_normal((rows, C))), q(rng.standard_normal((rows, C)))
+        self.res = rq(rng.standard_normal((rows, C)) * 2) if residual else None
+        self.dr = rq(rng.standard_normal((rows, C)))
+        self.w = np.asarray(1 + 0.2 * rng.standard_normal(C), dtype=np.float32).astype(np.float64) if weight else None
+        self.tx, self.tdy = rows_of([self.x, self.dy], dev, dtype, lead, lead)
+        self.tw = up(self.w, dev)
+        self.tres = rows_of([self.res], dev, residual, lead, lead)[0] if residual else None
+        self.tdr = rows_of([self.dr], dev, residual or dtype, lead, lead)[0]
+        self.dtype, self.rdtype = dtype, residual or dtype
+        # what is stored: the float32 sum, rounded to the stream's type
+        s = self.x if self.res is None else np.asarray(self.x + self.res, dtype=np.float32)
+        self.r = np.asarray(rq(s) if residual else s, dtype=np.float64)
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_forward(ssm, dev, case):  # noqa: F811
+    p = Norm(dev, *CASES[case], seed=case, weight=case % 5 != 4)
+    y, r, scales = ssm.ssm_add_norm_fwd(p.tx, p.tw, residual=p.tres)
+    assert scales is None and (r is None) == (p.res is None)
+    if r is not None:
+        assert np.array_equal(f64(r), p.r), "the stored stream"
+    want = ref.add_norm(p.r, p.w)
+    e = np.max(np.abs(f64(y) - want) / ((ref.HALF[p.dtype] + ref.NORM) * np.abs(want) + 1e-30))
+    print(CASES[case], f"{e:.3f} of the bound")
+    assert e <= 1
+
+
+@pytest.mark.parametrize("block", [0, 32, 64, 128, 256])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_eight_bits(ssm, dev, case, block):  # noqa: F811
+    """The scales to the norm's bound; each value within half a step of y / scale (2^-4 of the
+    value; 2^-10 for the smallest ones), and the norm's own error before it is rounded."""
+    p = Norm(dev, *CASES[case], seed=50 + case)
+    if case % 3 == 0:
+        p.x[0], p.tx[0] = 0.0, 0.0  # a row of nothing
+        if p.res is not None:
+            p.res[0], p.tres[0] = 0.0, 0.0
+        p.r[0] = 0.0
+    y, r, scales = ssm.ssm_add_norm_fwd(p.tx, p.tw, residual=p.tres, quant="e4m3", block=block)
+    want = ref.add_norm(p.r, p.w)
+    C = want.shape[1]
+    size = block or C
+    at = np.arange(0, C, size)
+    amax = np.maximum(np.maximum.reduceat(np.abs(want), at, axis=1), 2.0 ** -100) / 448
+    got = f64(scales)
+    assert got.shape == amax.shape
+    assert np.all(np.abs(got - amax) <= (ref.NORM + 2.0 ** -23) * amax)
+    v = want / np.repeat(amax, size, 1)[:, :C]
+    q = y.float().double().cpu().numpy()
+    assert np.all(np.abs(q) <= 448)
+    off = 2.0 * ref.NORM + 2.0 ** -22
+    assert np.all(np.abs(q - v) <= 2.0 ** -4 * np.abs(v) + 2.0 ** -10 + off * np.abs(v))
+    # nearest: no neighbour in e4m3 is nearer by more than the error of v
+    near = torch.from_numpy(v).float().to(torch.float8_e4m3fn).double().numpy()
+    differ = q != near
+    assert np.all(np.abs(np.abs(q - v) - np.abs(near - v))[differ] <= 2 * off * np.abs(v)[differ] + 1e-30)
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_backward(ssm, dev, case):  # noqa: F811
+    p = Norm(dev, *CASES[case], seed=100 + case, weight=case % 5 != 4)
+    r = p.tres if p.res is not None else p.tx
+    r = rows_of([p.r], dev, p.rdtype, CASES[case][4], CASES[case][4])[0]
+    dr = p.tdr if case % 2 else None
+    g = ssm.ssm_add_norm_bwd(p.tdy, r, p.tw, dresidual_out=dr)
+    d, dw, dabs, dwabs = ref.add_norm_bwd(p.dy, p.r, p.w, p.dr if case % 2 else None)
+    assert (g["dresidual"] is None) == (p.dtype == p.rdtype) and (g["dweight"] is None) == (p.w is None)
+    e = np.max(np.abs(f64(g["dx"]) - d) / (ref.HALF[p.dtype] * np.abs(d) + ref.NORM_BWD * dabs + 1e-30))
+    assert e <= 1, e
+    if g["dresidual"] is not None:
+        assert np.all(np.abs(f64(g["dresidual"]) - d) <= 2.0 ** -24 * np.abs(d) + ref.NORM_BWD * dabs + 1e-30)
+    if g["dweight"] is not None:
+        tol = (2.0 ** -24 + ref.NORM + 4 * 2.0 ** -24 * np.sqrt(len(d))) * dwabs + 1e-30
+        assert np.all(np.abs(f64(g["dweight"]) - dw) <= tol)
+    h = ssm.ssm_add_norm_bwd(p.tdy, r, p.tw, dresidual_out=dr)
+    assert all(torch.equal(g[k], h[k]) for k in g if g[k] is not None)
+
+
+def test_in_place_and_stored_stream(ssm, dev):  # noqa: F811
+    """The residual replaced in place, in rows that are slices; a stream in float32 from
+    rows alone; y in 8 bits into a slice."""
+    p = Norm(dev, 37, 200, "bf16", "bf16", 8, seed=200)
+    want = ssm.ssm_add_norm_fwd(p.tx, p.tw, residual=p.tres)
+    y, r, _ = ssm.ssm_add_norm_fwd(p.tx, p.tw, residual=p.tres, residual_out=p.tres)
+    assert r is p.tres and torch.equal(y, want[0]) and torch.equal(r, want[1])
+    wide = torch.zeros(37, 200, device=dev)
+    y, r, _ = ssm.ssm_add_norm_fwd(p.tx, p.tw, residual_out=wide)
+    assert r is wide and torch.equal(wide, p.tx.float())
+    for lead in (8, 3):
+        out = torch.zeros(37, 224, device=dev, dtype=torch.float8_e4m3fn)
+        y8, _, s8 = ssm.ssm_add_norm_fwd(p.tx, p.tw, quant="e4m3", block=64, y=out[:, lead:lead + 200])
+        ref8, _, refs = ssm.ssm_add_norm_fwd(p.tx, p.tw, quant="e4m3", block=64)
+        if lead == 8:
+            assert torch.equal(y8.float(), ref8.float()) and torch.equal(s8, refs)
+        # rows off 16 bytes are summed in another order: each within the norm's bound, and a value
+        # next to a border within one step of e4m3 (2^-3)
+        assert np.all(np.abs(f64(s8) - f64(refs)) <= 2 * ref.NORM * f64(refs))
+        a, b = y8.float().double().cpu().numpy(), ref8.float().double().cpu().numpy()
+        assert np.all(np.abs(a - b) <= 2.0 ** -3 * np.abs(b)) and (a != b).mean() < 0.01
+        assert (out[:, :lead].float() == 0).all() and (out[:, lead + 200:].float() == 0).all()
+
+
+def test_non_finite_rows(ssm, dev):  # noqa: F811
+    """A NaN or an infinity spoils its own row alone."""
+    p = Norm(dev, 40, 192, "bf16", "bf16", 0, seed=201)
+    clean = ssm.ssm_add_norm_fwd(p.tx, p.tw, residual=p.tres, quant="e4m3", block=32)
+    gclean = ssm.ssm_add_norm_bwd(p.tdy, clean[1], p.tw, want_dweight=False)
+    p.tx[5, 7], p.tx[9, 100] = float("nan"), float("inf")
+    got = ssm.ssm_add_norm_fwd(p.tx, p.tw, residual=p.tres, quant="e4m3", block=32)
+    ok = torch.ones(40, dtype=torch.bool, device=dev)
+    ok[5] = ok[9] = False
+    for a, b in zip(got, clean):
+        assert torch.equal(a.float()[ok], b.float()[ok])
+    assert got[0].float()[5].isnan().all() and got[0].float()[9, 100].isnan()
+    g = ssm.ssm_add_norm_bwd(p.tdy, got[1], p.tw, want_dweight=False)
+    assert torch.equal(g["dx"][ok], gclean["dx"][ok]) and g["dx"][5].isnan().all()
+
+
+def test_autograd(ssm, dev):  # noqa: F811
+    p = Norm(dev, 60, 96, "f32", "f32", 0, seed=202)
+    x, w, res = (t.clone().requires_grad_() for t in (p.tx.contiguous(), p.tw, p.tres.contiguous()))
+    y, r = ssm.add_norm_fn(x, w, res)
+    torch.autograd.backward((y, r), (p.tdy.contiguous(), p.tdr.contiguous()))
+    d, dw, dabs, dwabs = ref.add_norm_bwd(p.dy, p.r, p.w, p.dr)
+    for t in (x, res):
+        assert np.all(np.abs(f64(t.grad) - d) <= 2.0 ** -24 * np.abs(d) + ref.NORM_BWD * dabs)
+    assert np.all(np.abs(f64(w.grad) - dw) <= (2.0 ** -24 + ref.NORM + 4 * 2.0 ** -24 * 8) * dwabs)
+    # the stream alone, the norm alone, and no residual
+    x.grad = res.grad = w.grad = None
+    y, r = ssm.add_norm_fn(x, w, res)
+    r.backward(p.tdr.contiguous())
+    assert torch.equal(x.grad, p.tdr) and torch.equal(res.grad, p.tdr) and w.grad is None
+    x.grad = None
+    y, r = ssm.add_norm_fn(x, w)
+    assert r is x
+    (y * p.tdy + r * p.tdr).sum().backward()
+    d, _, dabs, _ = ref.add_norm_bwd(p.dy, p.x, p.w, p.dr)
+    assert np.all(np.abs(f64(x.grad) - d) <= 2.0 ** -23 * np.abs(d) + ref.NORM_BWD * dabs)
+    with pytest.raises(RuntimeError, match="gradients of its gradients"):
+        torch.autograd.grad(ssm.add_norm_fn(x, w, res)[0].sum(), x, create_graph=True)
+
+
+def test_refusals_with_real_tensors(ssm, dev):  # noqa: F811
+    x = torch.zeros(4, 64, device=dev, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="expected one of"):
+        ssm.ssm_add_norm_fwd(x, None, quant="int8")
+    with pytest.raises(ssm.SelscanError, match="block"):
+        ssm.ssm_add_norm_fwd(x, None, quant="e4m3", block=48)
+    with pytest.raises(TypeError, match="rows' dtype or float32"):
+        ssm.ssm_add_norm_fwd(x, None, residual=x.half())
+    with pytest.raises(ssm.SelscanError, match="overlaps"):
+        ssm.ssm_add_norm_fwd(x, None, y=x)
+
+
+# ---------------------------------------------------------------- a layer's run
+
+def layer64(x, res, W, lens, H, G, P, N):
+    """The same layer in float64 with torch's autograd, one token at a time."""
+    r = x + res
+    n = r / torch.sqrt((r * r).mean(1, keepdim=True) + 1e-5) * W["norm"]
+    proj = n @ W["in"].t()
+    gn, hp = G * N, H * P
+    q, k, v, z = proj[:, :gn], proj[:, gn:2 * gn], proj[:, 2 * gn:2 * gn + hp], proj[:, 2 * gn + hp:2 * gn + 2 * hp]
+    dt, beta = proj[:, -2 * H:-H], proj[:, -H:]
+    T = x.shape[0]
+    unit = lambda t: t / torch.sqrt((t * t).sum(-1, keepdim=True) + 1e-6)  # noqa: E731
+    q = unit(q.reshape(T, G, N)).repeat_interleave(H // G, 1) * N ** -0.5
+    k = unit(k.reshape(T, G, N)).repeat_interleave(H // G, 1)
+    v = v.reshape(T, H, P)
+    a = torch.exp(W["A"] * torch.nn.functional.softplus(dt + W["dt_bias"]))
+    b = torch.sigmoid(beta)
+    ys, at = [], 0
+    for n_ in lens:
+        S = torch.zeros(H, P, N, dtype=torch.float64)
+        for t in range(at, at + n_):
+            S = S * a[t][:, None, None]
+            u = b[t][:, None] * (v[t] - (S * k[t][:, None]).sum(-1))
+            S = S + u[..., None] * k[t][:, None]
+            ys.append((S * q[t][:, None]).sum(-1).reshape(-1))
+        at += n_
+    y = torch.stack(ys)
+    yg = y.reshape(T, H, P)
+    yn = (yg / torch.sqrt((yg * yg).mean(2, keepdim=True) + 1e-5)).reshape(T, hp) * W["gnorm"]
+    yn = yn * torch.nn.functional.silu(z)
+    return yn @ W["out"].t(), r
+
+
+def test_layers_train_together(ssm, dev):  # noqa: F811
+    """Two layers of norm, projection, gated delta rule, gated group norm and projection in
+    float32, forward and every gradient against float64.  The 2-norms of the differences
+    over the values': 2^-16 a block and operator (tests/delta_ref.py) through two layers of five
+    operators and two blocks, sqrt(20) of them at random, each gradient once more: 2^-16 9,
+    and 4 for the chain's condition."""
+    H, G, P, N, C, lens = 4, 2, 32, 32, 64, (70, 1, 33)
+    T = sum(lens)
+    rng = np.random.default_rng(21)
+    wide = 2 * G * N + 2 * H * P + 2 * H
+    f = lambda *s, std=1.0: torch.from_numpy(np.asarray(rng.standard_normal(s) * std, dtype=np.float32))  # noqa: E731
+    layers = [dict(norm=1 + f(C, std=0.1), gnorm=1 + f(H * P, std=0.1), out=f(C, H * P, std=(H * P) ** -0.5),
+                   A=-torch.from_numpy(rng.uniform(1, 8, H).astype(np.float32)), dt_bias=f(H, std=0.5) - 2,
+                   **{"in": f(wide, C, std=C ** -0.5)}) for _ in range(2)]
+    x0, dy, dr = f(T, C), f(T, C), f(T, C)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
+
+    def own(x, res, W):
+        n, r = ssm.add_norm_fn(x, W["norm"], res)
+        proj = n @ W["in"].t()
+        gn, hp = G * N, H * P
+        q, k, v, z = proj[:, :gn], proj[:, gn:2 * gn], proj[:, 2 * gn:2 * gn + hp], proj[:, 2 * gn + hp:2 * gn + 2 * hp]
+        y, _ = ssm.gated_delta_fn(q, k, v, proj[:, -2 * H:-H], proj[:, -H:], W["A"], cu, G, dt_bias=W["dt_bias"])
+        y = ssm.group_norm_fn(y, W["gnorm"], H, z=z, gate="after")
+        return y @ W["out"].t(), r
+
+    out = []
+    for where, dtype, layer in ((dev, torch.float32, own), ("cpu", torch.float64, lambda x, r, W: layer64(x, r, W, lens, H, G, P, N))):
+        Ws = [{k: v.to(where, dtype).requires_grad_() for k, v in W.items()} for W in layers]
+        x = x0.to(where, dtype).requires_grad_()
+        h, r = x, torch.zeros_like(x)
+        for W in Ws:
+            h, r = layer(h, r, W)
+        torch.autograd.backward((h, r), (dy.to(where, dtype), dr.to(where, dtype)))
+        out.append([h, r, x.grad] + [W[k].grad for W in Ws for k in sorted(W)])
+    for a, b in zip(*out):
+        a, b = f64(a), f64(b)
+        off = np.linalg.norm(a - b) / np.linalg.norm(b)
+        assert off <= 2.0 ** -16 * 36, off
+
+
+def test_a_server_run(ssm, dev):  # noqa: F811
+    """Norm in 8 bits, projection, prompts into the cache, tokens from it, gated norm, in bf16:
+    prompts followed by single tokens give what longer prompts give, to half a step of
+    bf16 a rounding (y, the norm's output) and the state's bound."""
+    H, G, P, N, C = 4, 2, 64, 64, 128
+    g = torch.Generator(device=dev)
+    g.manual_seed(22)
+    f = lambda *s, std=1.0: torch.randn(*s, generator=g, device=dev) * std  # noqa: E731
+    wide = 2 * G * N + 2 * H * P + 2 * H
+    win, norm, gnorm = f(C, wide, std=C ** -0.5).bfloat16(), 1 + f(C, std=0.1), 1 + f(H * P, std=0.1)
+    A, db = -torch.rand(H, generator=g, device=dev) * 8, f(H, std=0.5) - 2
+    x, res = f(140, C).bfloat16(), f(140, C).bfloat16()
+    gn, hp = G * N, H * P
+
+    def project(rows):
+        y8, r, s = ssm.ssm_add_norm_fwd(x[rows], norm, residual=res[rows], quant="e4m3", block=64)
+        y = (y8.float().view(len(rows), -1, 64) * s[..., None]).view(len(rows), C)
+        proj = (y @ win.float()).bfloat16()
+        return (proj[:, :gn], proj[:, gn:2 * gn], proj[:, 2 * gn:2 * gn + hp], proj[:, -2 * H:-H], proj[:, -H:]), proj[:, 2 * gn + hp:2 * gn + 2 * hp]
+
+    def gated(y, z):
+        return ssm.ssm_group_norm_fwd(y, gnorm, H, z=z, gate="after")
+
+    cu = torch.tensor([0, 90, 140], dtype=torch.int32, device=dev)
+    ins, z = project(torch.arange(140, device=dev))
+    whole_state = torch.zeros(3, H, P, N, device=dev)
+    slots = torch.tensor([2, 0], dtype=torch.int32, device=dev)
+    raw = ssm.ssm_gated_delta_fwd(*ins, A, cu, G, dt_bias=db, slots=slots, ssm_state=whole_state)
+    whole = gated(raw, z)
+    # the last four tokens of both one at a time, the second entry of the batch padding at the end
+    first = torch.cat([torch.arange(86), torch.arange(90, 136)]).to(dev)
+    ins, z = project(first)
+    state = torch.zeros_like(whole_state)
+    cu = torch.tensor([0, 86, 132], dtype=torch.int32, device=dev)
+    part = torch.zeros(140, hp, device=dev, dtype=torch.bfloat16)
+    part[first] = ssm.ssm_gated_delta_fwd(*ins, A, cu, G, dt_bias=db, slots=slots, ssm_state=state)
+    pad = torch.tensor([2, 0, -1], dtype=torch.int32, device=dev)
+    for i in range(4):
+        rows = torch.tensor([86 + i, 136 + i, 0], device=dev)
+        ins, z = project(rows)
+        y = ssm.ssm_gated_delta_update(*ins, state, A, G, dt_bias=db, slots=pad)
+        part[rows[:2]] = y[:2]
+        out = gated(y[:2], z[:2])
+        both = f64(out), f64(whole[rows[:2]])
+        # two roundings of y, of itself and in the root mean square, and one of the output
+        assert np.all(np.abs(both[0] - both[1]) <= 5 * 2.0 ** -8 * np.abs(both[1]) + 2.0 ** -10)
+    got, want = f64(part), f64(raw)
+    assert np.all(np.abs(got - want) <= 2 * 2.0 ** -8 * np.abs(want) * 1.01 + 2.0 ** -14)
+    # both sides 2^-16 sqrt(2 blocks) of the largest |v|, about four: under 2^-12; y by |q^| = 1/8 of that
+    assert np.all(np.abs(f64(state) - f64(whole_state)) <= 2.0 ** -12)
+    assert (state[1] == 0).all()

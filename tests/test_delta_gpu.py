@@ -1,0 +1,401 @@
+"""The gated delta rule on the GPU against float64: packed prompts, gradients, one
+token a sequence.  Bounds: tests/delta_ref.py."""
+import numpy as np
+import pytest
+
+import delta_ref as ref
+from test_mixer_gpu import dev, f64, rows_of, ssm, up  # noqa: F401  (fixtures)
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+IO = {"bf16": torch.bfloat16, "f32": torch.float32}
+ROWS = ("q", "k", "v", "dt", "beta")
+
+
+class Delta:
+    """One packed problem: float64 arrays, device tensors, the reference."""
+
+    def __init__(self, dev, lens, H, G, P, N, dtype, seed, state=True, behind=0, spare=2, skip=(),
+                 lead=0, tail=0, has=None, how=None, bias=True, kstd=1.0):
+        rng = np.random.default_rng(seed)
+        self.cu = np.concatenate([[0], np.cumsum(lens)])
+        tokens, nseq = int(self.cu[-1]) + behind, len(lens)
+        nslots = nseq + spare
+        self.how = how or ref.How()
+        self.x = x = ref.delta_inputs(rng, tokens, nseq, H, G, P, N, dtype, nslots, bias, state, kstd)
+        if not self.how.softplus:  # raw steps used as they are: small and positive
+            x["dt"] = ref._q(dtype)(np.abs(x["dt"]) * 0.05)
+            x["dt_bias"] = None
+        if not self.how.sigmoid:  # raw strengths between 0 and 1
+            x["beta"] = ref._q(dtype)(np.abs(np.tanh(x["beta"])))
+        slots = rng.permutation(nslots)[:nseq]
+        for i, v in skip:
+            slots[i] = v
+        self.slots = slots if state else None
+        self.has = (rng.random(nseq) < 0.5 if has is None else np.full(nseq, has)) if state else None
+        self.h0, self.dfinal = (np.asarray(rng.standard_normal((nseq, H, P, N)) * 0.3, dtype=np.float32).astype(np.float64)
+                                for _ in range(2))
+        self.G, self.dtype, self.dev, self.hp = G, dtype, dev, H * P
+        self.load(lead, tail)
+
+    def load(self, lead=0, tail=0):
+        x, dev = self.x, self.dev
+        parts = rows_of([x[n] for n in ROWS] + [x["dy"]], dev, self.dtype, lead, tail)
+        self.t = dict(zip(ROWS + ("dy",), parts))
+        self.A, self.dt_bias = up(x["A"], dev), up(x["dt_bias"], dev)
+        self.state = up(x.get("state"), dev)
+        self.y = torch.full((x["v"].shape[0], self.hp), 7.0, device=dev, dtype=IO[self.dtype])
+        self.cu_t = torch.tensor(self.cu, dtype=torch.int32, device=dev)
+        self.slots_t = None if self.slots is None else torch.tensor(self.slots, dtype=torch.int32, device=dev)
+        self.has_t = None if self.has is None else torch.tensor(self.has, device=dev)
+
+    def ins(self):
+        return [self.t[n] for n in ROWS]
+
+    def run(self, ssm, **kw):
+        a = dict(dt_bias=self.dt_bias, slots=self.slots_t, has_state=self.has_t, ssm_state=self.state, y=self.y,
+                 **self.how.kw())
+        a.update(kw)
+        return ssm.ssm_gated_delta_fwd(*self.ins(), self.A, self.cu_t, self.G, **a)
+
+    def step(self, ssm, **kw):
+        a = dict(dt_bias=self.dt_bias, slots=self.slots_t, y=self.y, **self.how.kw())
+        a.update(kw)
+        return ssm.ssm_gated_delta_update(*self.ins(), self.state, self.A, self.G, **a)
+
+    def bwd(self, ssm, carry=True, **kw):
+        a = dict(dt_bias=self.dt_bias, **self.how.kw())
+        if carry:
+            a.update(h0=up(self.h0, self.dev), dfinal_state=up(self.dfinal, self.dev))
+        a.update(kw)
+        return ssm.ssm_gated_delta_bwd(self.t["dy"], *self.ins(), self.A, self.cu_t, self.G, **a)
+
+    def check(self, what="", has=None):
+        y, state, yb, sb = ref.delta(self.x, self.cu, self.G, self.how, self.slots, self.has if has is None else has)
+        got = f64(self.y)
+        mine = ~np.isnan(y[:, 0])
+        assert (got[~mine] == 7.0).all(), "rows of no sequence were written"
+        tol = ref.HALF[self.dtype] * np.abs(y[mine]) + yb[mine] + 1e-30
+        ey = float(np.max(np.abs(got[mine] - y[mine]) / tol)) if mine.any() else 0.0
+        es = 0.0
+        if state is not None:
+            diff = np.abs(f64(self.state) - state)
+            es = float(np.max(diff / (2.0 ** -24 * np.abs(state) + sb + 1e-30)))
+        print(f"{what}: y {ey:.3f}, state {es:.3f} of the bound", flush=True)
+        assert ey <= 1 and es <= 1, (ey, es)
+
+    def check_bwd(self, got, what="", carry=True):
+        want, bound = ref.delta_bwd(self.x, self.cu, self.G, self.how, self.h0 if carry else None,
+                                    self.dfinal if carry else None)
+        worst = {}
+        for k, v in got.items():
+            if v is None:
+                continue
+            half = ref.HALF["f32"] if v.dtype == torch.float32 else ref.HALF["bf16"]
+            tol = half * np.abs(want[k]) + bound[k] + 1e-30
+            worst[k] = float(np.max(np.abs(f64(v) - want[k]) / tol)) if v.numel() else 0.0
+        print(what, {k: round(v, 3) for k, v in worst.items()}, flush=True)
+        assert all(v <= 1 for v in worst.values()), worst
+
+
+CASES = [  # lens, H, G, P, N, dtype, options
+    ((1,), 1, 1, 64, 128, "bf16", {}),
+    ((64,), 2, 1, 128, 128, "bf16", {}),
+    ((65, 63, 1, 0, 2, 128), 4, 2, 64, 128, "bf16", dict(behind=5)),
+    ((0, 0, 37), 3, 3, 64, 64, "bf16", dict(lead=3, tail=2)),
+    ((200, 7), 2, 2, 256, 256, "bf16", {}),
+    ((130, 70), 6, 3, 32, 32, "bf16", dict(lead=8)),
+    ((77,), 5, 1, 48, 96, "bf16", dict(bias=False)),
+    ((90, 33), 2, 2, 80, 16, "bf16", {}),
+    ((100,), 2, 1, 129, 20, "bf16", dict(lead=1)),
+    ((70, 3), 1, 1, 256, 100, "bf16", {}),
+    ((50, 20), 3, 3, 1, 1, "bf16", {}),
+    ((66,), 4, 2, 17, 9, "bf16", dict(lead=1, tail=1)),
+    ((64, 129, 1), 2, 2, 64, 128, "f32", {}),
+    ((33, 0, 95), 4, 2, 32, 64, "f32", dict(behind=3, lead=1)),
+    ((150,), 2, 1, 128, 256, "f32", {}),
+    ((40, 41), 3, 1, 5, 33, "f32", dict(bias=False)),
+    ((70, 90), 2, 1, 128, 128, "bf16", dict(state=False)),
+    ((70, 90), 2, 1, 64, 128, "f32", dict(state=False)),
+    ((70, 30, 20), 2, 2, 64, 128, "bf16", dict(skip=((1, -1), (2, 99)))),
+    ((70, 30), 2, 2, 64, 64, "bf16", dict(has=True)),
+    ((3, 2, 1), 2, 1, 64, 64, "f32", dict(has=True)),
+    ((300,), 2, 2, 64, 128, "bf16", dict(how=ref.How(softplus=False))),
+    ((90, 40), 2, 2, 64, 64, "bf16", dict(how=ref.How(sigmoid=False, scale=1.0))),
+    ((190,), 4, 2, 64, 64, "bf16", dict(how=ref.How(norm=False), kstd=0.1)),
+    ((140, 5), 2, 1, 96, 192, "f32", dict(how=ref.How(norm=False, scale=0.3), kstd=0.06)),
+    ((70, 60), 2, 2, 32, 32, "f32", dict(how=ref.How(eps=0.5))),
+    ((1,) * 40, 2, 1, 64, 128, "bf16", {}),
+    ((1100, 1, 300), 2, 2, 64, 128, "bf16", dict(has=True)),
+    ((900,), 1, 1, 64, 64, "f32", dict(has=True)),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_prompts(ssm, dev, case):  # noqa: F811
+    *dims, opt = CASES[case]
+    p = Delta(dev, *dims, seed=100 + case, **opt)
+    p.run(ssm)
+    p.check(str(CASES[case]))
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_gradients(ssm, dev, case):  # noqa: F811
+    *dims, opt = CASES[case]
+    opt = {k: v for k, v in opt.items() if k not in ("skip", "has", "state")}
+    p = Delta(dev, *dims, seed=300 + case, state=False, **opt)
+    carry = case % 2 == 0
+    g = p.bwd(ssm, carry=carry)
+    p.check_bwd(g, str(CASES[case]), carry)
+    end = int(p.cu[-1])
+    for k in ("dq", "dk", "dv", "ddt", "dbeta"):
+        assert (g[k][end:] == 0).all(), k
+
+
+STEPS = [  # batch, H, G, P, N, dtype, options
+    (1, 4, 2, 128, 128, "bf16", {}),
+    (7, 2, 1, 64, 64, "bf16", dict(skip=((2, -1), (6, 1000)))),
+    (3, 3, 3, 17, 9, "bf16", dict(lead=1)),
+    (5, 2, 2, 256, 256, "f32", {}),
+    (4, 2, 1, 80, 20, "f32", dict(lead=2, how=ref.How(norm=False), kstd=0.2)),
+    (2, 2, 2, 1, 1, "f32", {}),
+    (9, 2, 1, 33, 32, "bf16", dict(how=ref.How(softplus=False, sigmoid=False))),
+    (6, 4, 4, 96, 100, "bf16", {}),
+    (300, 2, 2, 64, 128, "bf16", {}),
+]
+
+
+@pytest.mark.parametrize("case", range(len(STEPS)))
+def test_step(ssm, dev, case):  # noqa: F811
+    n, *dims, opt = STEPS[case]
+    p = Delta(dev, (1,) * n, *dims, seed=500 + case, has=True, **opt)
+    p.step(ssm)
+    p.check(str(STEPS[case]), has=np.ones(n, bool))
+
+
+def test_step_after_prompt_is_a_longer_prompt(ssm, dev):  # noqa: F811
+    """A prompt cut anywhere and continued, by prompts and by single tokens, gives what
+    the whole prompt gives."""
+    p = Delta(dev, (150,), 4, 2, 64, 128, "bf16", seed=7, has=False, spare=0)
+    p.slots_t = None
+    p.run(ssm, slots=None, has_state=None)
+    whole, end = f64(p.y), f64(p.state)
+    y, state = torch.zeros_like(p.y), torch.zeros_like(p.state)
+    at = 0
+    one = torch.ones(1, dtype=torch.bool, device=dev)
+    for n in (70, 1, 64, 3):
+        part = [t[at:at + n] for t in p.ins()]
+        cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+        ssm.ssm_gated_delta_fwd(*part, p.A, cu, 2, dt_bias=p.dt_bias, has_state=one, ssm_state=state, y=y[at:at + n])
+        at += n
+    while at < 150:
+        part = [t[at:at + 1] for t in p.ins()]
+        ssm.ssm_gated_delta_update(*part, state, p.A, 2, dt_bias=p.dt_bias, y=y[at:at + 1])
+        at += 1
+    _, _, yb, sb = ref.delta(p.x, p.cu, 2, p.how, np.array([0]), None)
+    # each side is off by its bound, and each y by half a step of bf16
+    assert np.all(np.abs(f64(y) - whole) <= 2 * (2.0 ** -8 * np.abs(whole) * 1.01 + yb))
+    assert np.all(np.abs(f64(state) - end) <= 2 * (2.0 ** -24 * np.abs(end) + sb))
+
+
+def test_same_bits_every_time_and_shared_workspace(ssm, dev):  # noqa: F811
+    """Two calls in a row on one workspace, of other contents, and again: the same bits."""
+    p = Delta(dev, (300, 41, 0, 129), 4, 2, 64, 128, "bf16", seed=8)
+    o = Delta(dev, (64, 500), 2, 2, 128, 64, "bf16", seed=9)
+    need = max(ssm.ssm_gated_delta_workspace_size(v.x["v"].shape[0], len(v.cu) - 1, *s)
+               for v, s in ((p, (4, 64, 2, 128)), (o, (2, 128, 2, 64))))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=dev)
+    start = p.state.clone()
+    p.run(ssm, workspace=ws)
+    first = p.y.clone(), p.state.clone()
+    o.run(ssm, workspace=ws)
+    p.state.copy_(start)
+    p.run(ssm, workspace=ws)
+    assert torch.equal(first[0], p.y) and torch.equal(first[1], p.state)
+    o.check("the other")
+    g, h = p.bwd(ssm), p.bwd(ssm)
+    assert all(torch.equal(g[k], h[k]) for k in g if g[k] is not None)
+
+
+def test_offsets_out_of_order(ssm, dev):  # noqa: F811
+    """Offsets that fall or leave the rows touch nothing but the rows and their own slots."""
+    p = Delta(dev, (40, 40, 40), 2, 1, 32, 32, "bf16", seed=10, spare=0)
+    guard = torch.full((3, 120, 64), 3.0, device=dev, dtype=torch.bfloat16)
+    states = torch.full((3, 3, 2, 32, 32), 5.0, device=dev)
+    for cu in ([0, 90, 20, 120], [-7, 30, 1 << 30, 50], [50, 10, 200, 300], [200, 300, -5, 7]):
+        p.cu_t = torch.tensor(cu, dtype=torch.int32, device=dev)
+        p.run(ssm, y=guard[1], ssm_state=states[1])
+        p.bwd(ssm, carry=False)
+        torch.cuda.synchronize()
+        assert (guard[0] == 3).all() and (guard[2] == 3).all()
+        assert (states[0] == 5).all() and (states[2] == 5).all()
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "dt", "beta"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_non_finite_rows_stay_behind(ssm, dev, where, value):  # noqa: F811
+    """A token that is not finite: earlier tokens, other sequences and (v, q) other
+    channels are as without it, and what depends on it is not finite."""
+    p = Delta(dev, (150, 100), 2, 2, 64, 64, "bf16", seed=11, has=True, spare=0)
+    p.run(ssm)
+    clean, end = p.y.clone(), p.state.clone()
+    p.load()
+    hit = 85
+    p.t[where][hit, 0] = value
+    p.run(ssm)
+    assert torch.equal(p.y[:hit], clean[:hit]) and torch.equal(p.y[150:], clean[150:])
+    mine, other = int(p.slots[0]), int(p.slots[1])
+    assert torch.equal(p.state[other], end[other])
+    head0 = p.y[hit:150, :64]
+    if where == "q":
+        assert not torch.isfinite(head0[0]).any() and torch.equal(p.y[hit + 1:150], clean[hit + 1:150])
+        assert torch.equal(p.state[mine], end[mine])
+    elif where == "v":
+        assert not torch.isfinite(p.y[hit:150, 0]).any() and not torch.isfinite(p.state[mine, 0, 0]).any()
+        assert torch.equal(p.y[:150, 1:], clean[:150, 1:])
+    elif where == "beta" and value > 0:  # sigmoid(inf) = 1
+        assert torch.isfinite(p.y).all()
+    else:
+        assert not torch.isfinite(head0).any() and not torch.isfinite(p.state[mine, 0]).any()
+        assert torch.equal(p.y[:150, 64:], clean[:150, 64:])  # the other head has a group of its own
+
+
+def test_outliers_keep_their_neighbours(ssm, dev):  # noqa: F811
+    """A channel 2^30 times as large, keys and queries 2^20 times as long, and decays that
+    forget everything: every other channel is held to its own bound."""
+    p = Delta(dev, (200,), 2, 1, 64, 64, "f32", seed=12, has=True, spare=0)
+    p.x["v"][:, 3] *= 2.0 ** 30
+    p.x["k"][17] *= 2.0 ** 20
+    p.x["q"][40] *= 2.0 ** 20
+    p.x["k"][90] *= 2.0 ** -20
+    p.x["dt"][100] = 60.0
+    p.load()
+    p.run(ssm)
+    p.check("outliers")
+
+
+def test_equal_keys(ssm, dev):  # noqa: F811
+    """The same key at every token, written in full each time: T has entries of one all over."""
+    p = Delta(dev, (200,), 2, 1, 64, 64, "bf16", seed=13, has=True, spare=0)
+    p.x["k"][:] = p.x["k"][0]
+    p.x["beta"][:] = 40.0
+    p.x["dt"][:] = -20.0
+    p.load()
+    p.run(ssm)
+    p.check("equal keys")
+    p = Delta(dev, (200,), 2, 1, 64, 64, "bf16", seed=13, state=False)
+    p.x["k"][:] = p.x["k"][0] * np.where(np.arange(200) % 2, 1, -1)[:, None]
+    p.x["beta"][:] = 3.0
+    p.load()
+    p.check_bwd(p.bwd(ssm), "equal keys, signs by turns")
+
+
+def test_gradients_against_differences(ssm, dev):  # noqa: F811
+    """Central differences of the GPU forward in float32: the step h moves the loss by
+    h g; its own error is the forward's rounding over h, and h^2 of the third derivative."""
+    p = Delta(dev, (70, 9), 2, 1, 16, 16, "f32", seed=14, state=False)
+    g = p.bwd(ssm, carry=False)
+    rng = np.random.default_rng(15)
+
+    def loss():
+        y = ssm.ssm_gated_delta_fwd(*p.ins(), p.A, p.cu_t, p.G, dt_bias=p.dt_bias, **p.how.kw())
+        return float((y.double() * p.t["dy"].double()).sum())
+
+    for k in ROWS:
+        d = torch.from_numpy(rng.standard_normal(p.x[k].shape)).to(dev).float()
+        keep, h = p.t[k].clone(), 2.0 ** -7
+        both = []
+        for s in (h, -h):
+            p.t[k].copy_(keep + s * d)
+            both.append(loss())
+        p.t[k].copy_(keep)
+        want = (both[0] - both[1]) / (2 * h)
+        got = float((g["d" + k].double() * d.double()).sum())
+        size = float((g["d" + k].double() * d.double()).abs().sum())
+        # forward: 2^-16 of |y| |dy| summed at random over 79 x 32 values, over h; third order: h^2 of the terms
+        assert abs(got - want) <= 2.0 ** -16 * 50 / h + 4 * h * h * size, (k, got, want)
+
+
+def test_autograd(ssm, dev):  # noqa: F811
+    p = Delta(dev, (70, 30), 4, 2, 32, 32, "f32", seed=16, state=False)
+    leaves = [t.clone().requires_grad_() for t in p.ins()] + [p.A.clone().requires_grad_(), p.dt_bias.clone().requires_grad_()]
+    h0 = up(p.h0, dev).requires_grad_()
+    y, final = ssm.gated_delta_fn(*leaves[:6], p.cu_t, 2, dt_bias=leaves[6], h0=h0)
+    torch.autograd.backward((y, final), (p.t["dy"].contiguous(), up(p.dfinal, dev)))
+    got = {("d" + n) if n != "h0" else "dh0": t.grad for n, t in
+           zip(ROWS + ("A", "dt_bias", "h0"), leaves + [h0])}
+    got = {k if k != "ddt_bias" else "ddt_bias": v for k, v in got.items()}
+    p.check_bwd(got, "autograd")
+    # one output alone
+    for t in leaves:
+        t.grad = None
+    y, final = ssm.gated_delta_fn(*leaves[:6], p.cu_t, 2, dt_bias=leaves[6])
+    y.backward(p.t["dy"].contiguous())
+    p.check_bwd({"d" + n: t.grad for n, t in zip(ROWS, leaves)}, "y alone", carry=False)
+    y, final = ssm.gated_delta_fn(*leaves[:6], p.cu_t, 2, dt_bias=leaves[6])
+    with pytest.raises(RuntimeError, match="gradients of its gradients"):
+        torch.autograd.grad(y.sum(), leaves[0], create_graph=True)
+
+
+def test_graphs_and_streams(ssm, dev):  # noqa: F811
+    """Captured calls replayed between eager work on inputs that changed, and a call on
+    another stream: the same bits as eagerly."""
+    p = Delta(dev, (150, 33), 2, 2, 64, 64, "bf16", seed=17)
+    start = p.state.clone()
+    ws = torch.empty(ssm.ssm_gated_delta_workspace_size(183, 2, 2, 64, 2, 64), dtype=torch.uint8, device=dev)
+    bws = torch.empty(ssm.ssm_gated_delta_bwd_workspace_size(183, 2, 2, 64, 2, 64), dtype=torch.uint8, device=dev)
+    step = [t[:2] for t in p.ins()]
+    ys = torch.empty(2, p.hp, dtype=torch.bfloat16, device=dev)
+
+    def work():
+        p.run(ssm, workspace=ws)
+        ssm.ssm_gated_delta_update(*step, p.state, p.A, 2, dt_bias=p.dt_bias, slots=p.slots_t, y=ys)
+        return p.bwd(ssm, carry=False, workspace=bws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = work()
+    for turn in range(3):
+        p.t["v"].mul_(-1.0)
+        p.state.copy_(start)
+        g = work()
+        torch.cuda.synchronize()
+        want = [p.y.clone(), ys.clone(), p.state.clone()] + [v.clone() for v in g.values() if v is not None]
+        p.y.fill_(0)
+        p.state.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [p.y, ys, p.state] + [v for v in captured.values() if v is not None]
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), turn
+
+
+def test_states_past_32_bits(ssm, dev):  # noqa: F811
+    """A slot whose state lies behind 2^31 values and 2^33 bytes."""
+    H, P, N = 4, 256, 256
+    nslots = (1 << 31) // (H * P * N) + 40
+    big = torch.empty((nslots, H, P, N), dtype=torch.float32, device=dev)
+    p = Delta(dev, (70, 1), H, 4, P, N, "bf16", seed=18, has=True, spare=0)
+    at = [nslots - 3, nslots - 1]
+    small = p.state.clone()
+    for s, a in zip(p.slots, at):
+        big[a] = small[int(s)]
+    p.run(ssm)
+    y = p.y.clone()
+    slots = torch.tensor(at, dtype=torch.int32, device=dev)
+    p.run(ssm, ssm_state=big, slots=slots)
+    assert torch.equal(p.y, y)
+    for s, a in zip(p.slots, at):
+        assert torch.equal(big[a], p.state[int(s)])
+    rows = [t[:2] for t in p.ins()]
+    y = ssm.ssm_gated_delta_update(*rows, p.state, p.A, 4, dt_bias=p.dt_bias, slots=p.slots_t)
+    z = ssm.ssm_gated_delta_update(*rows, big, p.A, 4, dt_bias=p.dt_bias, slots=slots)
+    assert torch.equal(y, z)
+    for s, a in zip(p.slots, at):
+        assert torch.equal(big[a], p.state[int(s)])
