@@ -78,6 +78,7 @@ struct DeltaArgs {
   float *T, *M;          // [block, head][64][64]
   double* cum;           // [block, head][64] G
   float* b;              // [block, head][64]
+  char *gops, *hops;     // operands of a (block, group), of a (block, head)
   // backward
   float *S, *dS;         // [block, head][N][P] the state entering, its gradient behind
   float *U, *dR;         // [block, head][64][P]
@@ -537,6 +538,680 @@ __global__ void __launch_bounds__(256) delta_zero_kernel(const DeltaArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- a block's operands
+//
+// The products run on the matrix cores in fp16 pieces.  A row of k or q is scaled by a
+// power of two from its own largest value: bf16 values are then fp16 values (down to 2^-38
+// of the row's largest), float32 ones two pieces (22 bits); its length goes with the row's
+// scalars.  T, M, the state and what is made of them are float32, taken in two pieces each
+// (22 bits; lo x lo, 2^-24 of a product, is left out), T and M scaled by row, the rest by
+// column, which is a channel of v: a value is held to 2^-22 of itself or 2^-39 of the largest
+// beside it.  Accumulators, the state, statistics and running sums (float64) are float32 or
+// more.
+//
+// Order of rows and states: tile tt's row r of 16 is token 32 (tt / 2) + 8 (r / 4) +
+// 4 (tt % 2) + r % 4, and the states' tiles alike, so that a lane of the matrix
+// instructions, which has rows 4 q .. 4 q + 3 of a result's tile, has eight neighbours in a
+// pair of tiles: what it needs of the next product's other operand, without any exchange.
+
+__device__ __forceinline__ int place_of(int tile, int r) { return 32 * (tile >> 1) + 8 * (r >> 2) + 4 * (tile & 1) + (r & 3); }
+
+constexpr int kTri = 6;  // 16 x 32 tiles of T and M on or below the diagonal
+__device__ __forceinline__ int tri(int tt, int kb) { return tt < 2 ? tt : 2 * tt - 2 + kb; }
+
+// Bytes of the operands of a (block, group): k and q, rows of 2 NP bytes a piece, a row's
+// 16-byte parts in an order of its own (part()); and of a (block, head): T, M, scalars.
+template <typename IO, int NT>
+struct Ops {
+  static constexpr int KP = sizeof(IO) == 4 ? 2 : 1, NP = 16 * NT, RB = 2 * NP;
+  static constexpr int piece = kQ * RB, kq = KP * piece;  // one piece; all of k or q
+  static constexpr int group = 2 * kq;
+  static constexpr int tri_piece = kTri * 1024;
+  static constexpr int t = 0, m = 2 * tri_piece, sc = 4 * tri_piece, head = sc + 2048;
+  // where 16-byte part c of row r lies: rows that are read together are in different banks
+  __device__ static __forceinline__ int part(int r, int c) {
+    constexpr int rows = RB >= 256 ? 1 : 256 / RB;  // rows in one round of the banks
+    const int f = rows == 1 ? (r & 3) | (r >> 3 & 3) << 2 : rows == 2 ? (r >> 1 & 1) | (r >> 3 & 3) << 1 : r >> 3 & 3;
+    return r * RB + ((c ^ f) << 4);
+  }
+};
+// a head's scalars: places of 64 floats each
+enum { kS1, kBeta, kS2, kS3, kFT, kFM, kEC };
+
+__device__ __forceinline__ float max_nan(float a, float b) { return max3_nan(0.0f, a, b); }
+// 2^x of a running sum: what float32 leaves off it goes in to first order
+__device__ __forceinline__ float ex2(double x) {
+  const float hi = (float)x;
+  return ex2(hi) * fmaf((float)(x - (double)hi), kLn2, 1.0f);
+}
+template <int LN>
+__device__ __forceinline__ float lane_max(float v) {
+#pragma unroll
+  for (int d = 1; d < LN; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
+}
+__device__ __forceinline__ f4 mfma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+
+// eight neighbours of a row as float32; zeros from n on
+template <typename IO, bool VEC>
+__device__ __forceinline__ void load8(const void* p, int64_t at, int n, float (&x)[8]) {
+  if constexpr (VEC) {
+    constexpr int E = 16 / sizeof(IO);
+    if (n > 0) {
+#pragma unroll
+      for (int k = 0; k < 8 / E; ++k) {
+        Vec<IO, E> v;
+        if (E * k < n) v.load(p, at + E * k);
+#pragma unroll
+        for (int j = 0; j < E; ++j) x[E * k + j] = E * k < n ? v.get(j) : 0.0f;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j < n ? ld<IO>(p, at + j) : 0.0f;
+  }
+}
+
+// One workgroup per block and group (and, with few of them, head of the group).
+template <typename IO, int NT, bool VEC>
+__global__ void __launch_bounds__(256) delta_ops_kernel(const DeltaArgs a) {
+  using O = Ops<IO, NT>;
+  constexpr int KP = O::KP, LN = 2 * NT, RW = 256 / LN, LD = kQ + 4;
+  constexpr int lds = O::group > 2 * kQ * LD * 4 ? O::group : 2 * kQ * LD * 4;
+  __shared__ __align__(16) char s_buf[lds];
+  __shared__ float s_len[2][kQ];
+  __shared__ __align__(16) double s_cum[kQ];
+  __shared__ float s_b[kQ];
+  __shared__ int s_bad;
+  const int c = blockIdx.x, g = blockIdx.y, N = a.N;
+  if (c >= a.head->nchunk) return;
+  const DeltaChunk ck = a.chunks[c];
+  const int tid = threadIdx.x, lane = tid & 63, tt = tid >> 6, i16 = lane & 15, q4 = lane >> 4, cnt = ck.r1 - ck.r0;
+  // ---- rows of k and q: scaled, their lengths
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+#pragma unroll 4
+    for (int i0 = 0; i0 < kQ; i0 += RW) {
+      const int i = i0 + tid / LN, p = tid % LN;
+      float x[8], m = 0.0f, ss = 0.0f;
+      load8<IO, VEC>(which ? a.q : a.k, (int64_t)(ck.r0 + min(i, cnt - 1)) * (which ? a.qs : a.ks) + (int64_t)g * N + 8 * p,
+                     i < cnt ? N - 8 * p : 0, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, finite(x[j]) ? fabsf(x[j]) : 0.0f);
+      const int e = shift_for(lane_max<LN>(m));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = __builtin_amdgcn_ldexpf(x[j], e);
+        ss = fmaf(x[j], x[j], ss);
+      }
+      ss = lane_sum<LN>(ss);
+      // x / sqrt(|x|^2 + eps) from the scaled row
+      if (p == 0)
+        s_len[which][i] = (a.norm ? rsqrtf(ss + __builtin_amdgcn_ldexpf(a.eps, 2 * e)) : two(-e)) * (which ? a.scale : 1.0f);
+      h8 hi, lo;
+      pieces(x, hi, lo);
+      char* to = s_buf + which * O::kq + O::part(i, p);
+      *reinterpret_cast<h8*>(to) = hi;
+      if constexpr (KP == 2) *reinterpret_cast<h8*>(to + O::piece) = lo;
+    }
+  }
+  __syncthreads();
+  if (blockIdx.z == 0) {
+    char* out = a.gops + ((int64_t)c * a.G + g) * O::group;
+#pragma unroll 4
+    for (int u = tid * 16; u < O::group; u += 4096) *reinterpret_cast<u4*>(out + u) = *reinterpret_cast<const u4*>(s_buf + u);
+  }
+  // ---- their products: lane (i, q) has row i of tile tt at columns 32 kb + 8 q + {0 .. 7}
+  f4 kk[2][2] = {}, qk[2][2] = {};
+  const int row = place_of(tt, i16);
+#pragma unroll
+  for (int m = 0; m < NT / 2; ++m) {
+    h8 kb_[KP], qb[KP];
+#pragma unroll
+    for (int p = 0; p < KP; ++p) {
+      kb_[p] = *reinterpret_cast<const h8*>(s_buf + p * O::piece + O::part(row, 4 * m + q4));
+      qb[p] = *reinterpret_cast<const h8*>(s_buf + O::kq + p * O::piece + O::part(row, 4 * m + q4));
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if (kb > (tt >> 1)) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        h8 ka[KP];
+#pragma unroll
+        for (int p = 0; p < KP; ++p)
+          ka[p] = *reinterpret_cast<const h8*>(s_buf + p * O::piece + O::part(place_of(2 * kb + e, i16), 4 * m + q4));
+        if constexpr (KP == 2) {
+          kk[kb][e] = mfma(ka[1], kb_[0], kk[kb][e]);
+          kk[kb][e] = mfma(ka[0], kb_[1], kk[kb][e]);
+          qk[kb][e] = mfma(ka[1], qb[0], qk[kb][e]);
+          qk[kb][e] = mfma(ka[0], qb[1], qk[kb][e]);
+        }
+        kk[kb][e] = mfma(ka[0], kb_[0], kk[kb][e]);
+        qk[kb][e] = mfma(ka[0], qb[0], qk[kb][e]);
+      }
+    }
+  }
+  float* s_l = reinterpret_cast<float*>(s_buf);  // L, then T beside it: k and q are used up
+  float* s_t = s_l + kQ * LD;
+  for (int j = blockIdx.z; j < a.per; j += gridDim.z) {
+    const int h = g * a.per + j;
+    char* out = a.hops + ((int64_t)c * a.H + h) * O::head;
+    float* sc = reinterpret_cast<float*>(out + O::sc);
+    __syncthreads();  // the last head's T, and k and q, have been read
+    if (tt == 0) {
+      float gr = 0.0f, b = 0.0f;
+      if (lane < cnt) row_scalars<IO>(a, ck.r0 + lane, h, gr, b);
+      const double cum = wave_scan((double)gr), tot = lane63(cum);
+      s_cum[lane] = cum;
+      s_b[lane] = b;
+      const float e = ex2(cum), lk = s_len[0][lane], lq = s_len[1][lane];
+      sc[64 * kS1 + lane] = e * lk;
+      sc[64 * kBeta + lane] = b;
+      sc[64 * kS2 + lane] = e * lq;
+      sc[64 * kS3 + lane] = ex2(tot - cum) * lk;
+      sc[64 * kEC + lane] = ex2(tot);
+      if (lane == 0) s_bad = kQ;
+    }
+    __syncthreads();
+    // ---- L into LDS, M out
+    const double ci = s_cum[row];
+    const float bi = s_b[row], lki = s_len[0][row], lqi = s_len[1][row];
+    float mv[2][8], mx = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if (kb > (tt >> 1)) break;
+      float lv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int col = 32 * kb + 8 * q4 + e;
+        const float w = ex2((float)(ci - s_cum[col])) * s_len[0][col];
+        const float l = bi * lki * (w * kk[kb][e >> 2][e & 3]);
+        const float m = lqi * (w * qk[kb][e >> 2][e & 3]);
+        lv[e] = col < row ? l : 0.0f;
+        mv[kb][e] = col <= row ? m : 0.0f;
+        if (!finite(lv[e])) bad = true, lv[e] = 0.0f;
+        mx = finite(mv[kb][e]) ? fmaxf(mx, fabsf(mv[kb][e])) : mx;
+      }
+      f4* to = reinterpret_cast<f4*>(s_l + row * LD + 32 * kb + 8 * q4);
+      to[0] = *reinterpret_cast<const f4*>(lv);
+      to[1] = *reinterpret_cast<const f4*>(lv + 4);
+    }
+    if (bad) atomicMin(&s_bad, row);
+    {
+      const int sh = shift_for(row_max(mx));
+      const float f = two(sh);
+      if (q4 == 0) sc[64 * kFM + row] = two(-sh);
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb > (tt >> 1)) break;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mv[kb][e] *= f;
+        h8 hi, lo;
+        pieces(mv[kb], hi, lo);
+        char* to = out + O::m + (tri(tt, kb) * 64 + lane) * 16;
+        *reinterpret_cast<h8*>(to) = hi;
+        *reinterpret_cast<h8*>(to + O::tri_piece) = lo;
+      }
+    }
+    __syncthreads();
+    // ---- T: the inverses of the four diagonal tiles by substitution, a lane a column ...
+    {
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float l[16];
+#pragma unroll
+        for (int m = 0; m < i; m += 4) *reinterpret_cast<f4*>(l + m) = *reinterpret_cast<const f4*>(s_l + (16 * tt + i) * LD + 16 * tt + m);
+        x[i] = i == i16 ? 1.0f : 0.0f;
+#pragma unroll
+        for (int m = 0; m < i; ++m) x[i] = fmaf(-l[m], x[m], x[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if ((i >> 2) == q4) s_t[(16 * tt + i) * LD + 16 * tt + i16] = x[i];
+    }
+    __syncthreads();
+    // ---- ... and the tiles below them, T_ij = -T_ii sum_{j <= m < i} L_im T_mj, in float32 products
+    if (tt < 3) {
+      f4 tc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < tt) continue;
+        if (i == tt) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) tc[i][r] = s_t[(16 * i + 4 * q4 + r) * LD + 16 * i + i16];
+          continue;
+        }
+        f4 y = {};
+#pragma unroll
+        for (int m = 0; m < i; ++m) {
+          if (m < tt) continue;
+          const f4 l = *reinterpret_cast<const f4*>(s_l + (16 * i + i16) * LD + 16 * m + 4 * q4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y = mfma32(l[r], tc[m][r], y);
+        }
+        const f4 t = *reinterpret_cast<const f4*>(s_t + (16 * i + i16) * LD + 16 * i + 4 * q4);
+        f4 z = {};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z = mfma32(-t[r], y[r], z);
+        tc[i] = z;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s_t[(16 * i + 4 * q4 + r) * LD + 16 * tt + i16] = z[r];
+      }
+    }
+    __syncthreads();
+    {
+      const bool lost = row >= s_bad;
+      float t[2][8], m = 0.0f;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb > (tt >> 1)) break;
+        const f4* s = reinterpret_cast<const f4*>(s_t + row * LD + 32 * kb + 8 * q4);
+        *reinterpret_cast<f4*>(t[kb]) = s[0];
+        *reinterpret_cast<f4*>(t[kb] + 4) = s[1];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          t[kb][e] = 32 * kb + 8 * q4 + e <= row ? t[kb][e] : 0.0f;
+          m = finite(t[kb][e]) ? fmaxf(m, fabsf(t[kb][e])) : m;
+        }
+      }
+      const int sh = shift_for(row_max(m));
+      const float f = lost ? __builtin_nanf("") : two(sh);
+      if (q4 == 0) sc[64 * kFT + row] = two(-sh);
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb > (tt >> 1)) break;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[kb][e] *= f;
+        h8 hi, lo;
+        pieces(t[kb], hi, lo);
+        char* to = out + O::t + (tri(tt, kb) * 64 + lane) * 16;
+        *reinterpret_cast<h8*>(to) = hi;
+        *reinterpret_cast<h8*>(to + O::tri_piece) = lo;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- from block to block
+
+// four rows of a column of 16-bit values, transposed on the way from LDS: lane i of
+// sixteen points at four neighbours of row i / 4 and gets column i of all four rows
+__device__ __forceinline__ u2 read_tr(const char* p) {
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)p));
+}
+__device__ __forceinline__ h8 joined_tr(u2 a, u2 b) { return __builtin_bit_cast(h8, (u4){a.x, a.y, b.x, b.y}); }
+
+// The power of two for a column: its largest finite value over the four lanes that share it;
+// bad: whether one of the wave's columns has a value that is not finite.
+template <int PT, int NV>
+__device__ __forceinline__ bool column_shifts(const f4 (&v)[NV][PT], int (&sh)[PT]) {
+  float mx[PT];
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < PT; ++e) {
+    mx[e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; r += 2) mx[e] = max3_nan(mx[e], v[k][e][r], v[k][e][r + 1]);
+    bad = bad || !finite(mx[e]);
+  }
+  bad = __any(bad);
+  if (bad) {
+    rarely();
+#pragma unroll
+    for (int e = 0; e < PT; ++e) {
+      mx[e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (finite(v[k][e][r])) mx[e] = fmaxf(mx[e], fabsf(v[k][e][r]));
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < PT; ++e) sh[e] = shift_for(row_max(mx[e]));
+  return bad;
+}
+// the pieces of a pair of tiles of a column, scaled
+__device__ __forceinline__ void pair_pieces(const f4& x, const f4& y, float f, h8& hi, h8& lo) {
+  float v[8];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = x[r] * f, v[r + 4] = y[r] * f;
+  pieces(v, hi, lo);
+}
+
+// A workgroup walks a sequence's blocks with WV waves of 16 PT channels of one head each, the
+// states of a wave's channels in its accumulators.  DB: the next block's operands
+// come while this block's are used.
+template <typename IO, int NT, int PT, int WV, bool FAST>
+__global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, int units) {
+  using O = Ops<IO, NT>;
+  constexpr int KP = O::KP, B = O::group + O::head, PB = 16 * PT;
+  constexpr bool DB = 2 * B <= 160 * 1024;
+  __shared__ __align__(16) char s_op[(DB ? 2 : 1) * B];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int i16 = lane & 15, q4 = lane >> 4;
+  // eight dies take the workgroups by turns: the units of a head, and the heads of a
+  // group where there are eight groups, share a die's cache
+  const int item = blockIdx.x / (8 * units) * 8 + blockIdx.x % 8, unit = blockIdx.x / 8 % units;
+  if (item >= a.nseq * a.H) return;
+  const int s = item / a.H, g = item % a.G, h = g * a.per + item % a.H / a.G;
+  const DeltaSeq sq = a.seqs[s];
+  if (sq.slot < 0) return;
+  const int N = a.N, P = a.P, p0 = (unit * WV + wave) * PB;
+  const bool on = p0 < P;  // else the wave only helps to stage
+  int col[PT];
+#pragma unroll
+  for (int e = 0; e < PT; ++e) {
+    const int p = p0 + PT * i16 + e;
+    col[e] = h * P + (p < P ? p : FAST ? (on ? p0 : 0) + e : 0);
+  }
+  const int nc = (sq.t1 - sq.t0 + kQ - 1) / kQ;
+  auto stage_block = [&](int b) {
+    const int64_t c = sq.c0 + b;
+    char* to = s_op + (DB ? (b & 1) * B : 0);
+    stage<WV, O::group>(a.gops + (c * a.G + g) * O::group, to);
+    stage<WV, O::head>(a.hops + (c * a.H + h) * O::head, to + O::group);
+  };
+  if (nc > 0) stage_block(0);
+
+  // lane (i, q) holds the states 32 m + 8 q + {0 .. 3} of its channels in tile 2 m, {4 .. 7} in 2 m + 1
+  f4 S[NT][PT];
+  const float* src = sq.resume ? a.state : nullptr;
+#pragma unroll
+  for (int e = 0; e < PT; ++e)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
+      f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (src) {
+        const float* at = src + ((int64_t)sq.slot * a.H * P + col[e]) * N + n;
+        if constexpr (FAST) {
+          if (n < N) v = *reinterpret_cast<const f4*>(at);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (n + r < N) v[r] = at[r];
+        }
+      }
+      S[nt][e] = v;
+    }
+  // v of a block's rows 32 kb + 8 q + j
+  float vr[2][8][PT];
+  auto fetch = [&](int b) {
+    const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t r = r0 + min(32 * kb + 8 * q4 + j, cnt - 1);
+        if constexpr (FAST && PT == 2 && sizeof(IO) == 2) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const IO*>(a.v) + r * a.vs + col[0]);
+          vr[kb][j][0] = __uint_as_float(w << 16);
+          vr[kb][j][PT - 1] = __uint_as_float(w & 0xffff0000u);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PT; ++e) vr[kb][j][e] = ld<IO>(a.v, r * a.vs + col[e]);
+        }
+      }
+  };
+  if (nc > 0 && on) fetch(0);
+
+  for (int b = 0; b < nc; ++b) {
+    const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
+    arrived<0>();
+    meet();  // this block's operands are there; the waves are done with the last block's
+    if (DB && b + 1 < nc) stage_block(b + 1);
+    const char* op = s_op + (DB ? (b & 1) * B : 0);
+    const char* hop = op + O::group;
+    const float* sc = reinterpret_cast<const float*>(hop + O::sc);
+    if (on) {
+      // ---- k S and q S
+      f4 ks[4][PT] = {}, qs[4][PT] = {};
+      int sh[PT];
+      column_shifts<PT, NT>(S, sh);
+      float f[PT], fi[PT];
+#pragma unroll
+      for (int e = 0; e < PT; ++e) f[e] = two(sh[e]), fi[e] = two(-sh[e]);
+#pragma unroll
+      for (int m = 0; m < NT / 2; ++m) {
+        h8 hi[PT], lo[PT];
+#pragma unroll
+        for (int e = 0; e < PT; ++e) pair_pieces(S[2 * m][e], S[2 * m + 1][e], f[e], hi[e], lo[e]);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const int at = O::part(place_of(tt, i16), 4 * m + q4);
+          h8 ka[KP], qa[KP];
+#pragma unroll
+          for (int p = 0; p < KP; ++p) {
+            ka[p] = *reinterpret_cast<const h8*>(op + p * O::piece + at);
+            qa[p] = *reinterpret_cast<const h8*>(op + O::kq + p * O::piece + at);
+          }
+#pragma unroll
+          for (int e = 0; e < PT; ++e) {
+            ks[tt][e] = mfma(ka[0], lo[e], ks[tt][e]);
+            qs[tt][e] = mfma(qa[0], lo[e], qs[tt][e]);
+            if constexpr (KP == 2) {
+              ks[tt][e] = mfma(ka[1], hi[e], ks[tt][e]);
+              qs[tt][e] = mfma(qa[1], hi[e], qs[tt][e]);
+            }
+            ks[tt][e] = mfma(ka[0], hi[e], ks[tt][e]);
+            qs[tt][e] = mfma(qa[0], hi[e], qs[tt][e]);
+          }
+        }
+      }
+      // ---- R = b (v - e^G k S); q S to its size
+      if (cnt < kQ) {
+        rarely();
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < PT; ++e) vr[kb][j][e] = 32 * kb + 8 * q4 + j < cnt ? vr[kb][j][e] : 0.0f;
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const int t = place_of(tt, 4 * q4);
+        const f4 s1 = *reinterpret_cast<const f4*>(sc + 64 * kS1 + t), be = *reinterpret_cast<const f4*>(sc + 64 * kBeta + t);
+        const f4 s2 = *reinterpret_cast<const f4*>(sc + 64 * kS2 + t);
+#pragma unroll
+        for (int e = 0; e < PT; ++e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            ks[tt][e][r] = be[r] * fmaf(-(s1[r] * fi[e]), ks[tt][e][r], vr[tt >> 1][4 * (tt & 1) + r][e]);
+            qs[tt][e][r] *= s2[r] * fi[e];
+          }
+      }
+      if (b + 1 < nc) fetch(b + 1);
+      // ---- U = T R.  What is not finite stays behind the first such row of its column:
+      // 0 x Inf is not 0, so the products leave those rows out
+      int first[PT];
+#pragma unroll
+      for (int e = 0; e < PT; ++e) first[e] = kQ;
+      auto clean = [&](f4 (&v)[4][PT]) {
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (!finite(v[tt][e][r])) first[e] = min(first[e], place_of(tt, 4 * q4 + r));
+          first[e] = min(first[e], __shfl_xor(first[e], 16, 64));
+          first[e] = min(first[e], __shfl_xor(first[e], 32, 64));
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (place_of(tt, 4 * q4 + r) >= first[e]) v[tt][e][r] = 0.0f;
+        }
+      };
+      bool bad = column_shifts<PT, 4>(ks, sh);
+      if (bad) {
+        rarely();
+        clean(ks);
+      }
+      f4 u[4][PT] = {};
+      {
+        h8 hi[2][PT], lo[2][PT];
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          f[e] = two(sh[e]), fi[e] = two(-sh[e]);
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) pair_pieces(ks[2 * kb][e], ks[2 * kb + 1][e], f[e], hi[kb][e], lo[kb][e]);
+        }
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+          for (int kb = 0; kb <= tt / 2; ++kb) {
+            const char* at = hop + O::t + (tri(tt, kb) * 64 + lane) * 16;
+            const h8 th = *reinterpret_cast<const h8*>(at), tl = *reinterpret_cast<const h8*>(at + O::tri_piece);
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              u[tt][e] = mfma(tl, hi[kb][e], u[tt][e]);
+              u[tt][e] = mfma(th, lo[kb][e], u[tt][e]);
+              u[tt][e] = mfma(th, hi[kb][e], u[tt][e]);
+            }
+          }
+          const f4 ft = *reinterpret_cast<const f4*>(sc + 64 * kFT + place_of(tt, 4 * q4));
+#pragma unroll
+          for (int e = 0; e < PT; ++e)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[tt][e][r] *= ft[r] * fi[e];
+        }
+      }
+      bad |= column_shifts<PT, 4>(u, sh);
+      if (bad) {
+        rarely();
+        clean(u);
+      }
+      // ---- y = e^G q S + M U
+      {
+        h8 hi[2][PT], lo[2][PT];
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          f[e] = two(sh[e]), fi[e] = two(-sh[e]);
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) pair_pieces(u[2 * kb][e], u[2 * kb + 1][e], f[e], hi[kb][e], lo[kb][e]);
+        }
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          f4 y[PT] = {};
+#pragma unroll
+          for (int kb = 0; kb <= tt / 2; ++kb) {
+            const char* at = hop + O::m + (tri(tt, kb) * 64 + lane) * 16;
+            const h8 mh = *reinterpret_cast<const h8*>(at), ml = *reinterpret_cast<const h8*>(at + O::tri_piece);
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              y[e] = mfma(ml, hi[kb][e], y[e]);
+              y[e] = mfma(mh, lo[kb][e], y[e]);
+              y[e] = mfma(mh, hi[kb][e], y[e]);
+            }
+          }
+          const int t = place_of(tt, 4 * q4);
+          const f4 fm = *reinterpret_cast<const f4*>(sc + 64 * kFM + t);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float o[PT];
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              o[e] = fmaf(y[e][r], fm[r] * fi[e], qs[tt][e][r]);
+              if (bad) o[e] = t + r >= first[e] ? __builtin_nanf("") : o[e];
+            }
+            if (t + r < cnt) {
+              const int64_t at = (int64_t)(r0 + t + r) * a.ys;
+              if constexpr (FAST && PT == 2 && sizeof(IO) == 2) {
+                if (p0 + PT * i16 < P) {
+                  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+                  *reinterpret_cast<b2*>(static_cast<uint16_t*>(a.y) + at + col[0]) =
+                      __builtin_convertvector((f2){o[0], o[PT - 1]}, b2);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < PT; ++e)
+                  if (p0 + PT * i16 + e < P) st<IO>(a.y, at + col[e], o[e]);
+              }
+            }
+          }
+        }
+      }
+      // ---- S = e^G64 S + sum_j k_j (e^(G64 - G_j) U_j)
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const f4 s3 = *reinterpret_cast<const f4*>(sc + 64 * kS3 + place_of(tt, 4 * q4));
+#pragma unroll
+        for (int e = 0; e < PT; ++e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) u[tt][e][r] *= s3[r];
+      }
+      column_shifts<PT, 4>(u, sh);
+      {
+        h8 hi[2][PT], lo[2][PT];
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          f[e] = two(sh[e]), fi[e] = two(-sh[e]);
+          if (bad) fi[e] = first[e] < kQ ? __builtin_nanf("") : fi[e];  // such a column has no state any more
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) pair_pieces(u[2 * kb][e], u[2 * kb + 1][e], f[e], hi[kb][e], lo[kb][e]);
+        }
+        const float ec = sc[64 * kEC];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          f4 d[PT] = {};
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            // rows 32 kb + 8 q + i / 4 (and four on), states 32 (nt / 2) + 8 (i % 4) + 4 (nt % 2) + {0 .. 3}
+            const int r = 32 * kb + 8 * q4 + (i16 >> 2), pt = 4 * (nt >> 1) + (i16 & 3), lowhalf = 8 * (nt & 1);
+            h8 kt[KP];
+#pragma unroll
+            for (int p = 0; p < KP; ++p)
+              kt[p] = joined_tr(read_tr(op + p * O::piece + O::part(r, pt) + lowhalf),
+                                read_tr(op + p * O::piece + O::part(r + 4, pt) + lowhalf));
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              d[e] = mfma(kt[0], lo[kb][e], d[e]);
+              if constexpr (KP == 2) d[e] = mfma(kt[1], hi[kb][e], d[e]);
+              d[e] = mfma(kt[0], hi[kb][e], d[e]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < PT; ++e)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[nt][e][r] = fmaf(d[e][r], fi[e], S[nt][e][r] * ec);
+        }
+      }
+    }
+    if (!DB && b + 1 < nc) {
+      meet();  // the waves are done with this block's operands
+      stage_block(b + 1);
+    }
+  }
+  if (!a.state || !on) return;
+#pragma unroll
+  for (int e = 0; e < PT; ++e)
+    if (p0 + PT * i16 + e < P)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
+        float* at = a.state + ((int64_t)sq.slot * a.H * P + col[e]) * N + n;
+        if constexpr (FAST) {
+          if (n < N) *reinterpret_cast<f4*>(at) = S[nt][e];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (n + r < N) at[r] = S[nt][e][r];
+        }
+      }
+}
+
 // ---------------------------------------------------------------- one token a sequence
 
 // One workgroup per entry, head and 256 / LN rows (channels), LN lanes a row with four
@@ -682,13 +1357,15 @@ int check_state(const DeltaArgs& a, const DeltaCall& c) {
 }
 
 struct DeltaLayout {
+  int nt;  // tiles of 16 states
   int64_t nchunk;
-  int64_t chunks, seqs, qh, kh, T, M, cum, b, S, dS, U, dR, dqh, dkh, part, bytes;
+  int64_t chunks, seqs, gops, hops, qh, kh, T, M, cum, b, S, dS, U, dR, dqh, dkh, part, bytes;
 };
 
-DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N, bool bwd) {
+DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N, int io_dtype, bool bwd) {
   DeltaLayout l;
   memset(&l, 0, sizeof l);
+  l.nt = N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16;
   l.nchunk = tokens / kQ + nseq;
   int64_t at = 0;
   auto take = [&](int64_t n) {
@@ -700,13 +1377,17 @@ DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int
   take(sizeof(DeltaHead));
   l.chunks = take(l.nchunk * sizeof(DeltaChunk));
   l.seqs = take(nseq * sizeof(DeltaSeq));
-  l.qh = take(l.nchunk * G * kQ * N * 4);
-  l.kh = take(l.nchunk * G * kQ * N * 4);
-  l.T = take(ch * kQ * kQ * 4);
-  l.M = take(ch * kQ * kQ * 4);
-  l.cum = take(ch * kQ * 8);
-  l.b = take(ch * kQ * 4);
+  if (!bwd) {
+    l.gops = take(l.nchunk * G * 2 * kQ * l.nt * 32 * (io_dtype == SSM_DTYPE_BF16 ? 1 : 2));
+    l.hops = take(ch * (4 * kTri * 1024 + 2048));
+  }
   if (bwd) {
+    l.qh = take(l.nchunk * G * kQ * N * 4);
+    l.kh = take(l.nchunk * G * kQ * N * 4);
+    l.T = take(ch * kQ * kQ * 4);
+    l.M = take(ch * kQ * kQ * 4);
+    l.cum = take(ch * kQ * 8);
+    l.b = take(ch * kQ * 4);
     l.S = take(ch * N * P * 4);
     l.dS = take(ch * N * P * 4);
     l.U = take(ch * kQ * P * 4);
@@ -736,6 +1417,7 @@ void place(DeltaArgs& a, const DeltaLayout& l, void* workspace) {
   a.cum = reinterpret_cast<double*>(w + l.cum);
   a.S = f(l.S); a.dS = f(l.dS); a.U = f(l.U); a.dR = f(l.dR); a.dqh = f(l.dqh); a.dkh = f(l.dkh);
   a.part = f(l.part);
+  a.gops = w + l.gops; a.hops = w + l.hops;
 }
 
 template <typename IO>
@@ -745,10 +1427,52 @@ void launch_delta_prep(const DeltaArgs& a, const DeltaLayout& l, hipStream_t s) 
   delta_prep_kernel<IO><<<dim3((unsigned)l.nchunk, a.H), 256, 0, s>>>(a);
 }
 
+// 128 channels a workgroup where that gives every CU one, else 64.
+constexpr int64_t kCUs = 256;
+
+template <typename IO, int NT>
+void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, hipStream_t s) {
+  static_assert(Ops<IO, NT>::group == 2 * kQ * NT * 32 * Ops<IO, NT>::KP && Ops<IO, NT>::head == 4 * kTri * 1024 + 2048, "as in delta_layout");
+  delta_plan_kernel<<<1, 1024, 0, s>>>(a);
+  const unsigned split = l.nchunk * a.G < 2 * kCUs ? a.per : 1;
+  const dim3 grid((unsigned)l.nchunk, a.G, split);
+  if (vec) delta_ops_kernel<IO, NT, true><<<grid, 256, 0, s>>>(a);
+  else delta_ops_kernel<IO, NT, false><<<grid, 256, 0, s>>>(a);
+  auto walk = [&](auto pt, auto fa) {
+    constexpr int PT = decltype(pt)::value;
+    const int units = (a.P + 64 * PT - 1) / (64 * PT);
+    const int64_t items = (a.nseq * a.H + 7) / 8 * 8;
+    delta_walk_kernel<IO, NT, PT, 4, decltype(fa)::value><<<(unsigned)(items * units), 256, 0, s>>>(a, units);
+  };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  bool wide = false;
+  if constexpr (NT < 16) wide = a.nseq * a.H * ((a.P + 127) / 128) >= kCUs;
+  if constexpr (NT < 16) {
+    if (wide) {
+      if (fast) walk(Two{}, std::true_type{});
+      else walk(Two{}, std::false_type{});
+      return;
+    }
+  }
+  if (fast) walk(One{}, std::true_type{});
+  else walk(One{}, std::false_type{});
+}
+
 template <typename IO>
-void launch_delta(const DeltaArgs& a, const DeltaLayout& l, hipStream_t s) {
-  launch_delta_prep<IO>(a, l, s);
-  delta_scan_kernel<IO, false><<<dim3((unsigned)a.nseq, a.H, (a.P + 31) / 32), 256, 0, s>>>(a);
+void launch_delta_io(const DeltaArgs& a, const DeltaLayout& l, hipStream_t s) {
+  constexpr int es = sizeof(IO);
+  auto on = [&](const void* p, int64_t stride, int64_t width, int bytes) {
+    return ((uintptr_t)p | (uintptr_t)(stride * es) | (uintptr_t)(width * es)) % bytes == 0;
+  };
+  const bool vec = on(a.q, a.qs, a.N, 16) && on(a.k, a.ks, a.N, 16);
+  const bool fast = a.N % 4 == 0 && aligned16(a.state) && on(a.v, a.vs, a.P, 2 * es) && on(a.y, a.ys, a.P, 2 * es);
+  switch (l.nt) {
+    case 2: launch_delta<IO, 2>(a, l, vec, fast, s); break;
+    case 4: launch_delta<IO, 4>(a, l, vec, fast, s); break;
+    case 8: launch_delta<IO, 8>(a, l, vec, fast, s); break;
+    default: launch_delta<IO, 16>(a, l, vec, fast, s); break;
+  }
 }
 
 template <typename IO>
@@ -784,7 +1508,7 @@ int launch_step_io(const DeltaArgs& a, hipStream_t s) {
 int64_t delta_size(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
                    int io_dtype, bool bwd) {
   if (check_delta_extents(tokens, nseq, nheads, headdim, ngroups, dstate) || check_io(io_dtype)) return -1;
-  return delta_layout(tokens, nseq, nheads, headdim, ngroups, dstate, bwd).bytes;
+  return delta_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype, bwd).bytes;
 }
 
 }  // namespace
@@ -833,12 +1557,12 @@ int ssm_gated_delta_fwd(const void* q, int64_t q_stride, const void* k, int64_t 
                        flat(ssm_state, c.nslots * nheads * headdim * dstate * 4, "ssm_state"),
                        flat(workspace, workspace_bytes, "workspace")};
   if ((st = check_delta(a, c, outs, 3, nullptr, 0))) return st;
-  const DeltaLayout l = delta_layout(tokens, nseq, nheads, headdim, ngroups, dstate, false);
+  const DeltaLayout l = delta_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype, false);
   if ((st = check_workspace(workspace, workspace_bytes, l.bytes))) return st;
   place(a, l, workspace);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (io_dtype == SSM_DTYPE_BF16) launch_delta<uint16_t>(a, l, s);
-  else launch_delta<float>(a, l, s);
+  if (io_dtype == SSM_DTYPE_BF16) launch_delta_io<uint16_t>(a, l, s);
+  else launch_delta_io<float>(a, l, s);
   return launch_status("ssm_gated_delta_fwd launch");
 }
 
@@ -916,7 +1640,7 @@ int ssm_gated_delta_bwd(const void* dy, int64_t dy_stride, const void* q, int64_
   const Rows more[] = {{dy, tokens, dy_stride * es, hp * es, "dy"}, flat(h0, sb, "h0"),
                        flat(dfinal_state, sb, "dfinal_state")};
   if ((st = check_delta(a, c, outs, 9, more, 3))) return st;
-  const DeltaLayout l = delta_layout(tokens, nseq, nheads, headdim, ngroups, dstate, true);
+  const DeltaLayout l = delta_layout(tokens, nseq, nheads, headdim, ngroups, dstate, io_dtype, true);
   if ((st = check_workspace(workspace, workspace_bytes, l.bytes))) return st;
   place(a, l, workspace);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
