@@ -615,9 +615,9 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int n, float (&
   }
 }
 
-// One workgroup per block and group (and, with few of them, head of the group).
+// One workgroup per block and head; the first head of a group writes its k and q.
 template <typename IO, int NT, bool VEC>
-__global__ void __launch_bounds__(256) delta_ops_kernel(const DeltaArgs a) {
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) delta_ops_kernel(const DeltaArgs a) {
   using O = Ops<IO, NT>;
   constexpr int KP = O::KP, LN = 2 * NT, RW = 256 / LN, LD = kQ + 4;
   constexpr int lds = O::group > 2 * kQ * LD * 4 ? O::group : 2 * kQ * LD * 4;
@@ -626,10 +626,13 @@ __global__ void __launch_bounds__(256) delta_ops_kernel(const DeltaArgs a) {
   __shared__ __align__(16) double s_cum[kQ];
   __shared__ float s_b[kQ];
   __shared__ int s_bad;
-  const int c = blockIdx.x, g = blockIdx.y, N = a.N;
+  const int c = blockIdx.x, h = blockIdx.y, g = h / a.per, N = a.N;
   if (c >= a.head->nchunk) return;
   const DeltaChunk ck = a.chunks[c];
-  const int tid = threadIdx.x, lane = tid & 63, tt = tid >> 6, i16 = lane & 15, q4 = lane >> 4, cnt = ck.r1 - ck.r0;
+  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, q4 = lane >> 4, cnt = ck.r1 - ck.r0;
+  const int tt = __builtin_amdgcn_readfirstlane(tid >> 6);
+  float gr = 0.0f, b = 0.0f;
+  if (tt == 0 && lane < cnt) row_scalars<IO>(a, ck.r0 + lane, h, gr, b);
   // ---- rows of k and q: scaled, their lengths
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(256) delta_ops_kernel(const DeltaArgs a) {
     }
   }
   __syncthreads();
-  if (blockIdx.z == 0) {
+  if (h == g * a.per) {
     char* out = a.gops + ((int64_t)c * a.G + g) * O::group;
 #pragma unroll 4
     for (int u = tid * 16; u < O::group; u += 4096) *reinterpret_cast<u4*>(out + u) = *reinterpret_cast<const u4*>(s_buf + u);
@@ -669,6 +672,7 @@ __global__ void __launch_bounds__(256) delta_ops_kernel(const DeltaArgs a) {
   const int row = place_of(tt, i16);
 #pragma unroll
   for (int m = 0; m < NT / 2; ++m) {
+    asm volatile("" ::: "memory");  // else all the operands are read ahead
     h8 kb_[KP], qb[KP];
 #pragma unroll
     for (int p = 0; p < KP; ++p) {
@@ -697,14 +701,10 @@ __global__ void __launch_bounds__(256) delta_ops_kernel(const DeltaArgs a) {
   }
   float* s_l = reinterpret_cast<float*>(s_buf);  // L, then T beside it: k and q are used up
   float* s_t = s_l + kQ * LD;
-  for (int j = blockIdx.z; j < a.per; j += gridDim.z) {
-    const int h = g * a.per + j;
+  {
     char* out = a.hops + ((int64_t)c * a.H + h) * O::head;
     float* sc = reinterpret_cast<float*>(out + O::sc);
-    __syncthreads();  // the last head's T, and k and q, have been read
     if (tt == 0) {
-      float gr = 0.0f, b = 0.0f;
-      if (lane < cnt) row_scalars<IO>(a, ck.r0 + lane, h, gr, b);
       const double cum = wave_scan((double)gr), tot = lane63(cum);
       s_cum[lane] = cum;
       s_b[lane] = b;
@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(256) delta_ops_kernel(const DeltaArgs a) {
       sc[64 * kEC + lane] = ex2(tot);
       if (lane == 0) s_bad = kQ;
     }
-    __syncthreads();
+    __syncthreads();  // k and q have been read, too
     // ---- L into LDS, M out
     const double ci = s_cum[row];
     const float bi = s_b[row], lki = s_len[0][row], lqi = s_len[1][row];
@@ -770,6 +770,7 @@ __global__ void __launch_bounds__(256) delta_ops_kernel(const DeltaArgs a) {
         x[i] = i == i16 ? 1.0f : 0.0f;
 #pragma unroll
         for (int m = 0; m < i; ++m) x[i] = fmaf(-l[m], x[m], x[i]);
+        if (i & 1) asm volatile("" ::: "memory");  // else all of L is held in registers
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -848,6 +849,29 @@ __device__ __forceinline__ u2 read_tr(const char* p) {
 }
 __device__ __forceinline__ h8 joined_tr(u2 a, u2 b) { return __builtin_bit_cast(h8, (u4){a.x, a.y, b.x, b.y}); }
 
+// Copies BYTES from global memory to LDS, 16 bytes a lane, as stage() does, but out of the
+// compiler's sight: it would wait for them before the next read of LDS, whatever that reads.
+// landed() waits for them, meet() for the other waves.
+template <int WV, int BYTES>
+__device__ __forceinline__ void send(const char* from, char* to) {
+  static_assert(BYTES % 1024 == 0, "whole waves");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)to + wave * 1024;
+  const uint32_t off = wave * 1024 + lane * 16;
+#pragma unroll
+  for (int i = 0; i < (BYTES / 1024 + WV - 1) / WV; ++i)
+    if (BYTES / 1024 % WV == 0 || (i * WV + wave) * 1024 < BYTES)
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at + i * WV * 1024), "v"(off),
+                   "s"(from + i * WV * 1024)
+                   : "memory", "m0");
+}
+// All of this wave's memory accesses have ended (a wait that the compiler sees).
+__device__ __forceinline__ void landed() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);
+  asm volatile("" ::: "memory");
+}
+
 // The power of two for a column: its largest finite value over the four lanes that share it;
 // bad: whether one of the wave's columns has a value that is not finite.
 template <int PT, int NV>
@@ -918,8 +942,8 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
   auto stage_block = [&](int b) {
     const int64_t c = sq.c0 + b;
     char* to = s_op + (DB ? (b & 1) * B : 0);
-    stage<WV, O::group>(a.gops + (c * a.G + g) * O::group, to);
-    stage<WV, O::head>(a.hops + (c * a.H + h) * O::head, to + O::group);
+    send<WV, O::group>(a.gops + (c * a.G + g) * O::group, to);
+    send<WV, O::head>(a.hops + (c * a.H + h) * O::head, to + O::group);
   };
   if (nc > 0) stage_block(0);
 
@@ -944,31 +968,73 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
       }
       S[nt][e] = v;
     }
-  // v of a block's rows 32 kb + 8 q + j
-  float vr[2][8][PT];
+  // v of a block's rows 32 kb + 8 q + j.  Whole blocks go by an address of the row, the
+  // same in all lanes, and the lane's own offset
+  constexpr bool PAIR = FAST && PT == 2 && sizeof(IO) == 2;
+  using Raw = typename std::conditional<PAIR, uint32_t, IO>::type;
+  constexpr int RV = PAIR ? 1 : PT;
+  Raw vr[2][8][RV];
+  const uint32_t v_own = (uint32_t)((8 * q4 * a.vs + col[0]) * sizeof(IO)), y_own = (uint32_t)((8 * q4 * a.ys + col[0]) * sizeof(IO));
   auto fetch = [&](int b) {
     const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
+    if (FAST && cnt == kQ) {
+      const char* row = static_cast<const char*>(a.v) + (int64_t)r0 * a.vs * sizeof(IO);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t r = r0 + min(32 * kb + 8 * q4 + j, cnt - 1);
-        if constexpr (FAST && PT == 2 && sizeof(IO) == 2) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const IO*>(a.v) + r * a.vs + col[0]);
-          vr[kb][j][0] = __uint_as_float(w << 16);
-          vr[kb][j][PT - 1] = __uint_as_float(w & 0xffff0000u);
-        } else {
+        for (int j = 0; j < 8; ++j) {
+          const char* at = row + (32 * kb + j) * a.vs * (int64_t)sizeof(IO);
 #pragma unroll
-          for (int e = 0; e < PT; ++e) vr[kb][j][e] = ld<IO>(a.v, r * a.vs + col[e]);
+          for (int e = 0; e < RV; ++e) vr[kb][j][e] = *reinterpret_cast<const Raw*>(at + (v_own + e * (uint32_t)sizeof(IO)));
         }
-      }
+    } else {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const IO* at = static_cast<const IO*>(a.v) + (r0 + min(32 * kb + 8 * q4 + j, cnt - 1)) * a.vs;
+#pragma unroll
+          for (int e = 0; e < RV; ++e) vr[kb][j][e] = *reinterpret_cast<const Raw*>(at + col[e]);
+        }
+    }
+  };
+  auto value = [&](int kb, int j, int e) {
+    if constexpr (PAIR) return __uint_as_float(e ? vr[kb][j][0] & 0xffff0000u : vr[kb][j][0] << 16);
+    else if constexpr (sizeof(IO) == 2) return __uint_as_float((uint32_t)vr[kb][j][e] << 16);
+    else return (float)vr[kb][j][e];
   };
   if (nc > 0 && on) fetch(0);
 
+  // T or M times the pieces of a column's rows
+  auto triangle = [&](const char* op, const h8 (&hi)[2][PT], const h8 (&lo)[2][PT], f4 (&out)[4][PT]) {
+    h8 xh[kTri], xl[kTri];
+#pragma unroll
+    for (int i = 0; i < kTri; ++i) {
+      xh[i] = *reinterpret_cast<const h8*>(op + (i * 64 + lane) * 16);
+      xl[i] = *reinterpret_cast<const h8*>(op + O::tri_piece + (i * 64 + lane) * 16);
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int tt = 2 * kb; tt < 4; ++tt)
+#pragma unroll
+          for (int e = 0; e < PT; ++e)
+            out[tt][e] = mfma(p == 0 ? xl[tri(tt, kb)] : xh[tri(tt, kb)], p == 1 ? lo[kb][e] : hi[kb][e], out[tt][e]);
+  };
+
   for (int b = 0; b < nc; ++b) {
     const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
-    arrived<0>();
+    landed();
     meet();  // this block's operands are there; the waves are done with the last block's
+    // v has come too: else the compiler would wait for it behind what is sent next
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < RV; ++e) asm volatile("" : "+v"(vr[kb][j][e]));
     if (DB && b + 1 < nc) stage_block(b + 1);
     const char* op = s_op + (DB ? (b & 1) * B : 0);
     const char* hop = op + O::group;
@@ -986,27 +1052,29 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
         h8 hi[PT], lo[PT];
 #pragma unroll
         for (int e = 0; e < PT; ++e) pair_pieces(S[2 * m][e], S[2 * m + 1][e], f[e], hi[e], lo[e]);
+        h8 ka[4][KP], qa[4][KP];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           const int at = O::part(place_of(tt, i16), 4 * m + q4);
-          h8 ka[KP], qa[KP];
 #pragma unroll
           for (int p = 0; p < KP; ++p) {
-            ka[p] = *reinterpret_cast<const h8*>(op + p * O::piece + at);
-            qa[p] = *reinterpret_cast<const h8*>(op + O::kq + p * O::piece + at);
-          }
-#pragma unroll
-          for (int e = 0; e < PT; ++e) {
-            ks[tt][e] = mfma(ka[0], lo[e], ks[tt][e]);
-            qs[tt][e] = mfma(qa[0], lo[e], qs[tt][e]);
-            if constexpr (KP == 2) {
-              ks[tt][e] = mfma(ka[1], hi[e], ks[tt][e]);
-              qs[tt][e] = mfma(qa[1], hi[e], qs[tt][e]);
-            }
-            ks[tt][e] = mfma(ka[0], hi[e], ks[tt][e]);
-            qs[tt][e] = mfma(qa[0], hi[e], qs[tt][e]);
+            ka[tt][p] = *reinterpret_cast<const h8*>(op + p * O::piece + at);
+            qa[tt][p] = *reinterpret_cast<const h8*>(op + O::kq + p * O::piece + at);
           }
         }
+        // eight results by turns: a product does not wait for the one before it
+        auto all = [&](int p, const h8 (&x)[PT]) {
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int e = 0; e < PT; ++e) {
+              ks[tt][e] = mfma(ka[tt][p], x[e], ks[tt][e]);
+              qs[tt][e] = mfma(qa[tt][p], x[e], qs[tt][e]);
+            }
+        };
+        all(0, lo);
+        if constexpr (KP == 2) all(1, hi);
+        all(0, hi);
       }
       // ---- R = b (v - e^G k S); q S to its size
       if (cnt < kQ) {
@@ -1016,7 +1084,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int e = 0; e < PT; ++e) vr[kb][j][e] = 32 * kb + 8 * q4 + j < cnt ? vr[kb][j][e] : 0.0f;
+            for (int e = 0; e < RV; ++e) vr[kb][j][e] = 32 * kb + 8 * q4 + j < cnt ? vr[kb][j][e] : 0;
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
@@ -1027,7 +1095,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
         for (int e = 0; e < PT; ++e)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            ks[tt][e][r] = be[r] * fmaf(-(s1[r] * fi[e]), ks[tt][e][r], vr[tt >> 1][4 * (tt & 1) + r][e]);
+            ks[tt][e][r] = be[r] * fmaf(-(s1[r] * fi[e]), ks[tt][e][r], value(tt >> 1, 4 * (tt & 1) + r, e));
             qs[tt][e][r] *= s2[r] * fi[e];
           }
       }
@@ -1068,19 +1136,9 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb) pair_pieces(ks[2 * kb][e], ks[2 * kb + 1][e], f[e], hi[kb][e], lo[kb][e]);
         }
+        triangle(hop + O::t, hi, lo, u);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-          for (int kb = 0; kb <= tt / 2; ++kb) {
-            const char* at = hop + O::t + (tri(tt, kb) * 64 + lane) * 16;
-            const h8 th = *reinterpret_cast<const h8*>(at), tl = *reinterpret_cast<const h8*>(at + O::tri_piece);
-#pragma unroll
-            for (int e = 0; e < PT; ++e) {
-              u[tt][e] = mfma(tl, hi[kb][e], u[tt][e]);
-              u[tt][e] = mfma(th, lo[kb][e], u[tt][e]);
-              u[tt][e] = mfma(th, hi[kb][e], u[tt][e]);
-            }
-          }
           const f4 ft = *reinterpret_cast<const f4*>(sc + 64 * kFT + place_of(tt, 4 * q4));
 #pragma unroll
           for (int e = 0; e < PT; ++e)
@@ -1102,45 +1160,53 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb) pair_pieces(u[2 * kb][e], u[2 * kb + 1][e], f[e], hi[kb][e], lo[kb][e]);
         }
+        f4 y[4][PT] = {};
+        triangle(hop + O::m, hi, lo, y);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
-          f4 y[PT] = {};
+          const f4 fm = *reinterpret_cast<const f4*>(sc + 64 * kFM + place_of(tt, 4 * q4));
 #pragma unroll
-          for (int kb = 0; kb <= tt / 2; ++kb) {
-            const char* at = hop + O::m + (tri(tt, kb) * 64 + lane) * 16;
-            const h8 mh = *reinterpret_cast<const h8*>(at), ml = *reinterpret_cast<const h8*>(at + O::tri_piece);
+          for (int e = 0; e < PT; ++e)
 #pragma unroll
-            for (int e = 0; e < PT; ++e) {
-              y[e] = mfma(ml, hi[kb][e], y[e]);
-              y[e] = mfma(mh, lo[kb][e], y[e]);
-              y[e] = mfma(mh, hi[kb][e], y[e]);
-            }
+            for (int r = 0; r < 4; ++r) y[tt][e][r] = fmaf(y[tt][e][r], fm[r] * fi[e], qs[tt][e][r]);
+        }
+        if (bad) {
+          rarely();
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int e = 0; e < PT; ++e)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (place_of(tt, 4 * q4 + r) >= first[e]) y[tt][e][r] = __builtin_nanf("");
+        }
+        auto write = [&](char* at, int tt, int r) {
+          if constexpr (PAIR) {
+            typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+            *reinterpret_cast<b2*>(at) = __builtin_convertvector((f2){y[tt][0][r], y[tt][PT - 1][r]}, b2);
+          } else {
+#pragma unroll
+            for (int e = 0; e < PT; ++e)
+              if (FAST || p0 + PT * i16 + e < P) st<IO>(at, e, y[tt][e][r]);
           }
-          const int t = place_of(tt, 4 * q4);
-          const f4 fm = *reinterpret_cast<const f4*>(sc + 64 * kFM + t);
+        };
+        if (FAST && cnt == kQ) {
+          if (p0 + PT * i16 < P) {
+            char* row = static_cast<char*>(a.y) + (int64_t)r0 * a.ys * sizeof(IO);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float o[PT];
+            for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-            for (int e = 0; e < PT; ++e) {
-              o[e] = fmaf(y[e][r], fm[r] * fi[e], qs[tt][e][r]);
-              if (bad) o[e] = t + r >= first[e] ? __builtin_nanf("") : o[e];
-            }
-            if (t + r < cnt) {
-              const int64_t at = (int64_t)(r0 + t + r) * a.ys;
-              if constexpr (FAST && PT == 2 && sizeof(IO) == 2) {
-                if (p0 + PT * i16 < P) {
-                  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-                  *reinterpret_cast<b2*>(static_cast<uint16_t*>(a.y) + at + col[0]) =
-                      __builtin_convertvector((f2){o[0], o[PT - 1]}, b2);
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < PT; ++e)
-                  if (p0 + PT * i16 + e < P) st<IO>(a.y, at + col[e], o[e]);
-              }
-            }
+              for (int r = 0; r < 4; ++r)
+                write(row + (32 * (tt >> 1) + 4 * (tt & 1) + r) * a.ys * (int64_t)sizeof(IO) + y_own, tt, r);
           }
+        } else if (p0 + PT * i16 < P) {
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int t = place_of(tt, 4 * q4 + r);
+              if (t < cnt) write(static_cast<char*>(a.y) + ((r0 + t) * a.ys + col[0]) * (int64_t)sizeof(IO), tt, r);
+            }
         }
       }
       // ---- S = e^G64 S + sum_j k_j (e^(G64 - G_j) U_j)
@@ -1164,28 +1230,38 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
         }
         const float ec = sc[64 * kEC];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          f4 d[PT] = {};
+        for (int n0 = 0; n0 < NT; n0 += 2) {
+          f4 d[2][PT] = {};
+          h8 kt[2][2][KP];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+              // rows 32 kb + 8 q + i16 / 4 (and four on), states 16 n0 + 8 (i16 % 4) + 4 i + {0 .. 3}
+              const int r = 32 * kb + 8 * q4 + (i16 >> 2), pt = 2 * n0 + (i16 & 3);
+#pragma unroll
+              for (int p = 0; p < KP; ++p)
+                kt[i][kb][p] = joined_tr(read_tr(op + p * O::piece + O::part(r, pt) + 8 * i),
+                                         read_tr(op + p * O::piece + O::part(r + 4, pt) + 8 * i));
+            }
+          auto all = [&](int kb, int p, const h8 (&x)[PT]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < PT; ++e) d[i][e] = mfma(kt[i][kb][p], x[e], d[i][e]);
+          };
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb) {
-            // rows 32 kb + 8 q + i / 4 (and four on), states 32 (nt / 2) + 8 (i % 4) + 4 (nt % 2) + {0 .. 3}
-            const int r = 32 * kb + 8 * q4 + (i16 >> 2), pt = 4 * (nt >> 1) + (i16 & 3), lowhalf = 8 * (nt & 1);
-            h8 kt[KP];
-#pragma unroll
-            for (int p = 0; p < KP; ++p)
-              kt[p] = joined_tr(read_tr(op + p * O::piece + O::part(r, pt) + lowhalf),
-                                read_tr(op + p * O::piece + O::part(r + 4, pt) + lowhalf));
-#pragma unroll
-            for (int e = 0; e < PT; ++e) {
-              d[e] = mfma(kt[0], lo[kb][e], d[e]);
-              if constexpr (KP == 2) d[e] = mfma(kt[1], hi[kb][e], d[e]);
-              d[e] = mfma(kt[0], hi[kb][e], d[e]);
-            }
+            all(kb, 0, lo[kb]);
+            if constexpr (KP == 2) all(kb, 1, hi[kb]);
+            all(kb, 0, hi[kb]);
           }
 #pragma unroll
-          for (int e = 0; e < PT; ++e)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[nt][e][r] = fmaf(d[e][r], fi[e], S[nt][e][r] * ec);
+            for (int e = 0; e < PT; ++e)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) S[n0 + i][e][r] = fmaf(d[i][e][r], fi[e], S[n0 + i][e][r] * ec);
         }
       }
     }
@@ -1434,8 +1510,7 @@ template <typename IO, int NT>
 void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, hipStream_t s) {
   static_assert(Ops<IO, NT>::group == 2 * kQ * NT * 32 * Ops<IO, NT>::KP && Ops<IO, NT>::head == 4 * kTri * 1024 + 2048, "as in delta_layout");
   delta_plan_kernel<<<1, 1024, 0, s>>>(a);
-  const unsigned split = l.nchunk * a.G < 2 * kCUs ? a.per : 1;
-  const dim3 grid((unsigned)l.nchunk, a.G, split);
+  const dim3 grid((unsigned)l.nchunk, a.H);
   if (vec) delta_ops_kernel<IO, NT, true><<<grid, 256, 0, s>>>(a);
   else delta_ops_kernel<IO, NT, false><<<grid, 256, 0, s>>>(a);
   auto walk = [&](auto pt, auto fa) {
@@ -1466,7 +1541,8 @@ void launch_delta_io(const DeltaArgs& a, const DeltaLayout& l, hipStream_t s) {
     return ((uintptr_t)p | (uintptr_t)(stride * es) | (uintptr_t)(width * es)) % bytes == 0;
   };
   const bool vec = on(a.q, a.qs, a.N, 16) && on(a.k, a.ks, a.N, 16);
-  const bool fast = a.N % 4 == 0 && aligned16(a.state) && on(a.v, a.vs, a.P, 2 * es) && on(a.y, a.ys, a.P, 2 * es);
+  const bool fast = a.N % 4 == 0 && aligned16(a.state) && on(a.v, a.vs, a.P, 2 * es) && on(a.y, a.ys, a.P, 2 * es) &&
+                    a.vs < (1 << 24) && a.ys < (1 << 24);  // a lane's offset to its rows in 32 bits
   switch (l.nt) {
     case 2: launch_delta<IO, 2>(a, l, vec, fast, s); break;
     case 4: launch_delta<IO, 4>(a, l, vec, fast, s); break;
