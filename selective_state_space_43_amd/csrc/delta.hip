@@ -74,14 +74,10 @@ struct DeltaArgs {
   DeltaHead* head;
   DeltaChunk* chunks;
   DeltaSeq* seqs;
-  float *qh, *kh;        // [block, group][64][N] normalised rows
-  float *T, *M;          // [block, head][64][64]
-  double* cum;           // [block, head][64] G
-  float* b;              // [block, head][64]
   char *gops, *hops;     // operands of a (block, group), of a (block, head)
   // backward
-  float *S, *dS;         // [block, head][N][P] the state entering, its gradient behind
-  float *U, *dR;         // [block, head][64][P]
+  char* keep;            // Keep::block for every 32 channels of a (block, head)
+  int* shifts;           // [block, head][kKinds][padded P]
   float *dqh, *dkh;      // [block, head][64][N]
   float *part;           // [block, head][2] sums of dA, ddt_bias
 };
@@ -142,402 +138,6 @@ __device__ __forceinline__ void row_scalars(const DeltaArgs& a, int64_t r, int h
   b = a.sigmoid ? sigmoid(braw) : braw;
 }
 
-// one workgroup per block and group: the normalised rows
-template <typename IO>
-__global__ void __launch_bounds__(256) delta_rows_kernel(const DeltaArgs a) {
-  const int c = blockIdx.x, g = blockIdx.y, N = a.N;
-  if (c >= a.head->nchunk) return;
-  const DeltaChunk ck = a.chunks[c];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int i = wave; i < kQ; i += 4) {
-    const bool in = ck.r0 + i < ck.r1;
-    const int64_t r = in ? ck.r0 + i : ck.r0;
-    for (int which = 0; which < 2; ++which) {
-      const void* p = which ? a.k : a.q;
-      const int64_t at = r * (which ? a.ks : a.qs) + (int64_t)g * N;
-      float x[4], ss = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = in && lane + 64 * j < N ? ld<IO>(p, at + lane + 64 * j) : 0.0f;
-        ss = fmaf(x[j], x[j], ss);
-      }
-      ss = lane_sum<64>(ss);
-      const float f = (a.norm ? rsqrtf(ss + a.eps) : 1.0f) * (which ? 1.0f : a.scale);
-      float* out = (which ? a.kh : a.qh) + (((int64_t)c * a.G + g) * kQ + i) * N;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (lane + 64 * j < N) out[lane + 64 * j] = x[j] * f;
-    }
-  }
-}
-
-// one workgroup per block and head: T, M, the running sum
-template <typename IO>
-__global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs a) {
-  __shared__ float s_x[kQ][kQ + 1], s_l[kQ][kQ + 1], s_b[kQ];
-  __shared__ double s_g[kQ];
-  const int c = blockIdx.x, h = blockIdx.y, N = a.N, g = h / a.per;
-  if (c >= a.head->nchunk) return;
-  const DeltaChunk ck = a.chunks[c];
-  const int tid = threadIdx.x;
-  const int64_t at = (int64_t)c * a.H + h;
-  if (tid < kQ) {
-    float gr = 0.0f, b = 0.0f;
-    if (ck.r0 + tid < ck.r1) row_scalars<IO>(a, ck.r0 + tid, h, gr, b);
-    const double cum = wave_scan((double)gr);
-    s_g[tid] = cum;
-    s_b[tid] = b;
-    a.cum[at * kQ + tid] = cum;
-    a.b[at * kQ + tid] = b;
-  }
-  __syncthreads();
-  const float* kh = a.kh + ((int64_t)c * a.G + g) * kQ * N;
-  const float* qh = a.qh + ((int64_t)c * a.G + g) * kQ * N;
-  for (int u = tid; u < kQ * kQ; u += 256) {
-    const int i = u >> 6, j = u & 63;
-    float kk = 0.0f, qk = 0.0f;
-    if (j <= i)
-      for (int n = 0; n < N; ++n) {
-        kk = fmaf(kh[i * N + n], kh[j * N + n], kk);
-        qk = fmaf(qh[i * N + n], kh[j * N + n], qk);
-      }
-    const float D = j <= i ? ex2((float)(s_g[i] - s_g[j])) : 0.0f;
-    s_l[i][j] = j < i ? s_b[i] * D * kk : 0.0f;
-    a.M[at * kQ * kQ + u] = j <= i ? D * qk : 0.0f;
-  }
-  __syncthreads();
-  if (tid < kQ) {  // column tid of the inverse, row by row
-    for (int i = 0; i < kQ; ++i) {
-      float x = i == tid ? 1.0f : 0.0f;
-      for (int m = tid; m < i; ++m) x = fmaf(-s_l[i][m], s_x[m][tid], x);
-      s_x[i][tid] = i < tid ? 0.0f : x;
-    }
-  }
-  __syncthreads();
-  for (int u = tid; u < kQ * kQ; u += 256) a.T[at * kQ * kQ + u] = s_x[u >> 6][u & 63];
-}
-
-// ---------------------------------------------------------------- from block to block
-
-// One workgroup per sequence, head and 32 channels.  KEEP: for the backward, which keeps
-// S and U of every block and no y.
-template <typename IO, bool KEEP>
-__global__ void __launch_bounds__(256) delta_scan_kernel(const DeltaArgs a) {
-  __shared__ float s_S[kMaxN][33], s_r[kQ][33];
-  const DeltaSeq sq = a.seqs[blockIdx.x];
-  if (sq.slot < 0) return;
-  const int h = blockIdx.y, N = a.N, P = a.P, g = h / a.per;
-  const int cl = threadIdx.x & 31, rg = threadIdx.x >> 5, p = blockIdx.z * 32 + cl;
-  const bool on = p < P;
-  const int64_t own = KEEP ? blockIdx.x : sq.slot;
-  const float* src = KEEP ? a.h0 : sq.resume ? a.state : nullptr;
-  for (int n = rg; n < N; n += 8)
-    s_S[n][cl] = src && on ? src[((own * a.H + h) * P + p) * N + n] : 0.0f;
-  __syncthreads();
-  const int nc = (sq.t1 - sq.t0 + kQ - 1) / kQ;
-  for (int b = 0; b < nc; ++b) {
-    const int c = sq.c0 + b, r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
-    const int64_t at = (int64_t)c * a.H + h, ag = ((int64_t)c * a.G + g) * kQ;
-    const double* cum = a.cum + at * kQ;
-    const float *T = a.T + at * kQ * kQ, *M = a.M + at * kQ * kQ, *bb = a.b + at * kQ;
-    if (KEEP && on)
-      for (int n = rg; n < N; n += 8) a.S[(at * N + n) * P + p] = s_S[n][cl];
-    float u[8];
-    for (int ii = 0; ii < 8; ++ii) {
-      const int i = rg + 8 * ii;
-      float kS = 0.0f;
-      for (int n = 0; n < N; ++n) kS = fmaf(a.kh[(ag + i) * N + n], s_S[n][cl], kS);
-      const float v = on && i < cnt ? ld<IO>(a.v, (int64_t)(r0 + i) * a.vs + h * P + p) : 0.0f;
-      s_r[i][cl] = bb[i] * (v - ex2((float)cum[i]) * kS);
-    }
-    __syncthreads();
-    for (int ii = 0; ii < 8; ++ii) {
-      const int i = rg + 8 * ii;
-      u[ii] = 0.0f;
-      for (int j = 0; j <= i; ++j) u[ii] = fmaf(T[i * kQ + j], s_r[j][cl], u[ii]);
-    }
-    __syncthreads();
-    for (int ii = 0; ii < 8; ++ii) {
-      s_r[rg + 8 * ii][cl] = u[ii];
-      if (KEEP && on) a.U[(at * kQ + rg + 8 * ii) * P + p] = u[ii];
-    }
-    __syncthreads();
-    if constexpr (!KEEP) {
-      for (int ii = 0; ii < 8; ++ii) {
-        const int i = rg + 8 * ii;
-        float qS = 0.0f;
-        for (int n = 0; n < N; ++n) qS = fmaf(a.qh[(ag + i) * N + n], s_S[n][cl], qS);
-        float y = ex2((float)cum[i]) * qS;
-        for (int j = 0; j <= i; ++j) y = fmaf(M[i * kQ + j], s_r[j][cl], y);
-        if (on && i < cnt) st<IO>(a.y, (int64_t)(r0 + i) * a.ys + h * P + p, y);
-      }
-      __syncthreads();
-    }
-    const double last = cum[kQ - 1];
-    for (int n = rg; n < N; n += 8) {
-      float s = ex2((float)last) * s_S[n][cl];
-      for (int j = 0; j < cnt; ++j)
-        s = fmaf(a.kh[(ag + j) * N + n] * ex2((float)(last - cum[j])), s_r[j][cl], s);
-      s_S[n][cl] = s;
-    }
-    __syncthreads();
-  }
-  if (!KEEP && a.state && on)
-    for (int n = rg; n < N; n += 8) a.state[((own * a.H + h) * P + p) * N + n] = s_S[n][cl];
-}
-
-// against the blocks' order
-template <typename IO>
-__global__ void __launch_bounds__(256) delta_scan_bwd_kernel(const DeltaArgs a) {
-  __shared__ float s_S[kMaxN][33], s_r[kQ][33], s_y[kQ][33];
-  const DeltaSeq sq = a.seqs[blockIdx.x];
-  const int h = blockIdx.y, N = a.N, P = a.P, g = h / a.per;
-  const int cl = threadIdx.x & 31, rg = threadIdx.x >> 5, p = blockIdx.z * 32 + cl;
-  const bool on = p < P;
-  const int64_t own = ((int64_t)blockIdx.x * a.H + h) * P + p;
-  for (int n = rg; n < N; n += 8) s_S[n][cl] = a.dfinal && on ? a.dfinal[own * N + n] : 0.0f;
-  __syncthreads();
-  const int nc = (sq.t1 - sq.t0 + kQ - 1) / kQ;
-  for (int b = nc - 1; b >= 0; --b) {
-    const int c = sq.c0 + b, r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
-    const int64_t at = (int64_t)c * a.H + h, ag = ((int64_t)c * a.G + g) * kQ;
-    const double* cum = a.cum + at * kQ;
-    const double last = cum[kQ - 1];
-    const float *T = a.T + at * kQ * kQ, *M = a.M + at * kQ * kQ, *bb = a.b + at * kQ;
-    if (on)
-      for (int n = rg; n < N; n += 8) a.dS[(at * N + n) * P + p] = s_S[n][cl];
-    for (int i = rg; i < kQ; i += 8)
-      s_y[i][cl] = on && i < cnt ? ld<IO>(a.dy, (int64_t)(r0 + i) * a.gs + h * P + p) : 0.0f;
-    __syncthreads();
-    for (int j = rg; j < kQ; j += 8) {
-      float u = 0.0f;
-      for (int n = 0; n < N; ++n) u = fmaf(a.kh[(ag + j) * N + n], s_S[n][cl], u);
-      u *= ex2((float)(last - cum[j]));
-      for (int i = j; i < cnt; ++i) u = fmaf(M[i * kQ + j], s_y[i][cl], u);
-      s_r[j][cl] = u;
-    }
-    __syncthreads();
-    float dr[8];
-    for (int ii = 0; ii < 8; ++ii) {
-      const int j = rg + 8 * ii;
-      dr[ii] = 0.0f;
-      for (int i = j; i < cnt; ++i) dr[ii] = fmaf(T[i * kQ + j], s_r[i][cl], dr[ii]);
-    }
-    __syncthreads();
-    for (int ii = 0; ii < 8; ++ii) {
-      const int j = rg + 8 * ii;
-      s_r[j][cl] = dr[ii];
-      if (on) a.dR[(at * kQ + j) * P + p] = dr[ii];
-      if (on && j < cnt) st<IO>(a.dv, (int64_t)(r0 + j) * a.dvs + h * P + p, bb[j] * dr[ii]);
-    }
-    __syncthreads();
-    for (int n = rg; n < N; n += 8) {
-      float s = ex2((float)last) * s_S[n][cl];
-      for (int i = 0; i < cnt; ++i) {
-        const float e = ex2((float)cum[i]);
-        s = fmaf(e * a.qh[(ag + i) * N + n], s_y[i][cl], s);
-        s = fmaf(-e * bb[i] * a.kh[(ag + i) * N + n], s_r[i][cl], s);
-      }
-      s_S[n][cl] = s;
-    }
-    __syncthreads();
-  }
-  if (a.dh0 && on)
-    for (int n = rg; n < N; n += 8) a.dh0[own * N + n] = s_S[n][cl];
-}
-
-// ---------------------------------------------------------------- gradients of a block's rows and scalars
-
-// one workgroup per block and head
-template <typename IO>
-__global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaArgs a) {
-  __shared__ float s_m[kQ][kQ + 1], s_l[kQ][kQ + 1], s_mm[kQ][kQ + 1], s_b[kQ], s_db[kQ], s_tail[kQ], s_red[256];
-  __shared__ double s_g[kQ], s_dg[kQ];
-  const int c = blockIdx.x, h = blockIdx.y, N = a.N, P = a.P, g = h / a.per;
-  if (c >= a.head->nchunk) return;
-  const DeltaChunk ck = a.chunks[c];
-  const int tid = threadIdx.x, cnt = ck.r1 - ck.r0;
-  const int64_t at = (int64_t)c * a.H + h, ag = ((int64_t)c * a.G + g) * kQ;
-  const float *kh = a.kh + ag * N, *qh = a.qh + ag * N, *U = a.U + at * kQ * P, *dR = a.dR + at * kQ * P;
-  const float *S = a.S + at * N * P, *dS = a.dS + at * N * P;
-  if (tid < kQ) s_g[tid] = a.cum[at * kQ + tid], s_b[tid] = a.b[at * kQ + tid];
-  __syncthreads();
-  for (int u = tid; u < kQ * kQ; u += 256) {
-    const int i = u >> 6, j = u & 63;
-    float m = 0.0f, l = 0.0f, mm = 0.0f;
-    if (j <= i && i < cnt) {
-      float kk = 0.0f, qk = 0.0f;
-      for (int p = 0; p < P; ++p) {
-        m = fmaf(ld<IO>(a.dy, (int64_t)(ck.r0 + i) * a.gs + h * P + p), U[j * P + p], m);
-        l = fmaf(-dR[i * P + p], U[j * P + p], l);
-      }
-      for (int n = 0; n < N; ++n) {
-        kk = fmaf(kh[i * N + n], kh[j * N + n], kk);
-        qk = fmaf(qh[i * N + n], kh[j * N + n], qk);
-      }
-      const float D = ex2((float)(s_g[i] - s_g[j]));
-      m *= D;
-      l = j < i ? l * D : 0.0f;
-      // what the running sum's gradient takes from here; the diagonal's cancels
-      mm = j < i ? fmaf(m, qk, l * kk * s_b[i]) : 0.0f;
-      s_l[i][j] = l;
-      s_mm[i][j] = mm;
-      s_m[i][j] = m;
-    } else {
-      s_l[i][j] = s_m[i][j] = s_mm[i][j] = 0.0f;
-    }
-  }
-  __syncthreads();
-  const double last = s_g[kQ - 1];
-  // row i, four lanes a row
-  const int i = tid >> 2, ln = tid & 3;
-  const float e = ex2((float)s_g[i]), et = ex2((float)(last - s_g[i])), bi = s_b[i];
-  float qq = 0.0f, rk = 0.0f, tail = 0.0f, db = 0.0f, SdS = 0.0f;
-  for (int n = ln; n < N; n += 4) {
-    float yS = 0.0f, rS = 0.0f, uS = 0.0f;
-    if (i < cnt)
-      for (int p = 0; p < P; ++p) {
-        const float s = S[(int64_t)n * P + p];
-        yS = fmaf(ld<IO>(a.dy, (int64_t)(ck.r0 + i) * a.gs + h * P + p), s, yS);
-        rS = fmaf(dR[i * P + p], s, rS);
-        uS = fmaf(U[i * P + p], dS[(int64_t)n * P + p], uS);
-      }
-    yS *= e; rS *= e; uS *= et;
-    const float kn = kh[i * N + n], qn = qh[i * N + n];
-    qq = fmaf(yS, qn, qq);
-    rk = fmaf(rS, kn, rk);
-    tail = fmaf(uS, kn, tail);
-    float dq = yS, dk = uS - bi * rS;
-    for (int j = 0; j < kQ; ++j) {
-      if (j <= i) dq = fmaf(s_m[i][j], kh[j * N + n], dq);
-      if (j < i) dk = fmaf(s_l[i][j] * bi, kh[j * N + n], dk);
-      if (j >= i) dk = fmaf(s_m[j][i], qh[j * N + n], dk);
-      if (j > i) dk = fmaf(s_l[j][i] * s_b[j], kh[j * N + n], dk);
-    }
-    a.dqh[(at * kQ + i) * N + n] = dq;
-    a.dkh[(at * kQ + i) * N + n] = dk;
-  }
-  // S . dS over the whole block
-  for (int64_t u = tid; u < (int64_t)N * P; u += 256) SdS = fmaf(S[u], dS[u], SdS);
-  if (i < cnt) {
-    for (int p = ln; p < P; p += 4)
-      db = fmaf(dR[i * P + p], ld<IO>(a.v, (int64_t)(ck.r0 + i) * a.vs + h * P + p), db);
-    for (int j = ln; j < i; j += 4) {
-      float kk = 0.0f;
-      for (int n = 0; n < N; ++n) kk = fmaf(kh[i * N + n], kh[j * N + n], kk);
-      db = fmaf(s_l[i][j], kk, db);
-    }
-  }
-  qq = lane_sum<4>(qq); rk = lane_sum<4>(rk); tail = lane_sum<4>(tail); db = lane_sum<4>(db);
-  if (ln == 0) {
-    double d = (double)qq - (double)(bi * rk) - (double)tail;
-    for (int j = 0; j < kQ; ++j) d += (double)s_mm[i][j] - (double)s_mm[j][i];
-    s_dg[i] = d;
-    s_db[i] = db - rk;
-    s_tail[i] = tail;
-  }
-  s_red[tid] = SdS;
-  __syncthreads();
-  if (tid == 0) {
-    double sum = 0.0;
-    for (int t = 0; t < 256; ++t) sum += (double)s_red[t];
-    sum *= (double)ex2((float)last);
-    for (int j = 0; j < kQ; ++j) sum += (double)s_tail[j];
-    double run = sum;
-    float dA = 0.0f, dbias = 0.0f;
-    for (int j = kQ - 1; j >= 0; --j) {
-      run += s_dg[j];
-      if (j >= cnt) continue;
-      const int64_t r = ck.r0 + j;
-      const float raw = ld<IO>(a.dt, r * a.ds + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
-      const float dg = (float)run, dt = a.softplus ? softplus(raw) : raw;
-      const float ddt = dg * a.A[h] * (a.softplus ? sigmoid(raw) : 1.0f);
-      dA = fmaf(dg, dt, dA);
-      dbias += ddt;
-      st<IO>(a.ddt, r * a.dds + h, ddt);
-      const float b = s_b[j];
-      st<IO>(a.dbeta, r * a.dbs + h, s_db[j] * (a.sigmoid ? b * (1.0f - b) : 1.0f));
-    }
-    a.part[at * 2] = dA;
-    a.part[at * 2 + 1] = dbias;
-  }
-}
-
-// the heads of a group together, and the normalisation: one wave a row
-template <typename IO>
-__global__ void __launch_bounds__(256) delta_qk_grad_kernel(const DeltaArgs a) {
-  const int c = blockIdx.x, g = blockIdx.y, N = a.N;
-  if (c >= a.head->nchunk) return;
-  const DeltaChunk ck = a.chunks[c];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int i = wave; i < ck.r1 - ck.r0; i += 4) {
-    const int64_t r = ck.r0 + i;
-    for (int which = 0; which < 2; ++which) {
-      const void* p = which ? a.k : a.q;
-      const int64_t at = r * (which ? a.ks : a.qs) + (int64_t)g * N;
-      float x[4], d[4], ss = 0.0f, xd = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = lane + 64 * j;
-        x[j] = n < N ? ld<IO>(p, at + n) : 0.0f;
-        d[j] = 0.0f;
-        if (n < N)
-          for (int m = 0; m < a.per; ++m)
-            d[j] += (which ? a.dkh : a.dqh)[(((int64_t)c * a.H + g * a.per + m) * kQ + i) * N + n];
-        ss = fmaf(x[j], x[j], ss);
-      }
-      const float f = a.norm ? rsqrtf(lane_sum<64>(ss) + a.eps) : 1.0f, sc = which ? 1.0f : a.scale;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] *= f, xd = fmaf(x[j], d[j], xd);
-      xd = a.norm ? lane_sum<64>(xd) : 0.0f;
-      const int64_t to = r * (which ? a.dks : a.dqs) + (int64_t)g * N;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (lane + 64 * j < N) st<IO>(which ? a.dk : a.dq, to + lane + 64 * j, (d[j] - x[j] * xd) * f * sc);
-    }
-  }
-}
-
-// dA and ddt_bias: one workgroup a head, blocks in runs of a fixed order
-__global__ void __launch_bounds__(256) delta_sum_kernel(const DeltaArgs a) {
-  __shared__ double red[2][256];
-  const int h = blockIdx.x, t = threadIdx.x, nc = a.head->nchunk;
-  double s0 = 0.0, s1 = 0.0;
-  for (int c = t; c < nc; c += 256) {
-    s0 += a.part[((int64_t)c * a.H + h) * 2];
-    s1 += a.part[((int64_t)c * a.H + h) * 2 + 1];
-  }
-  red[0][t] = s0;
-  red[1][t] = s1;
-  __syncthreads();
-  if (t < 2) {
-    double s = 0.0;
-    for (int k = 0; k < 256; ++k) s += red[t][k];
-    float* out = t ? a.ddt_bias : a.dA;
-    if (out) out[h] = (float)s;
-  }
-}
-
-// rows of no sequence have no gradients
-template <typename IO>
-__global__ void __launch_bounds__(256) delta_zero_kernel(const DeltaArgs a) {
-  const int first = a.head->first, last = a.head->last;
-  const int64_t gn = (int64_t)a.G * a.N, hp = (int64_t)a.H * a.P, wide = 2 * gn + hp + 2 * a.H;
-  const int64_t rows = a.tokens - (last - first);
-  for (int64_t u = blockIdx.x * 256ll + threadIdx.x; u < rows * wide; u += gridDim.x * 256ll) {
-    int64_t r = u / wide, c = u % wide;
-    if (r >= first) r += last - first;
-    if (c < gn) { st<IO>(a.dq, r * a.dqs + c, 0.0f); continue; }
-    c -= gn;
-    if (c < gn) { st<IO>(a.dk, r * a.dks + c, 0.0f); continue; }
-    c -= gn;
-    if (c < hp) { st<IO>(a.dv, r * a.dvs + c, 0.0f); continue; }
-    c -= hp;
-    if (c < a.H) st<IO>(a.ddt, r * a.dds + c, 0.0f);
-    else st<IO>(a.dbeta, r * a.dbs + c - a.H, 0.0f);
-  }
-}
-
 // ---------------------------------------------------------------- a block's operands
 //
 // The products run on the matrix cores in fp16 pieces.  A row of k or q is scaled by a
@@ -556,8 +156,16 @@ __global__ void __launch_bounds__(256) delta_zero_kernel(const DeltaArgs a) {
 
 __device__ __forceinline__ int place_of(int tile, int r) { return 32 * (tile >> 1) + 8 * (r >> 2) + 4 * (tile & 1) + (r & 3); }
 
-constexpr int kTri = 6;  // 16 x 32 tiles of T and M on or below the diagonal
-__device__ __forceinline__ int tri(int tt, int kb) { return tt < 2 ? tt : 2 * tt - 2 + kb; }
+// T and M: columns 0 .. 31 of all rows, then columns 32 .. 63 of rows 32 .. 63, rows of 64
+// bytes; where 16-byte part c of row r of column block kb lies (as Ops::part()).
+constexpr int kTri = 6 * 1024;
+__device__ __forceinline__ int tri(int r, int kb, int c) {
+  return (kb ? 4096 + (r - 32) * 64 : r * 64) + ((c ^ (r >> 3 & 3)) << 4);
+}
+
+// a head's scalars: places of 64 floats each
+enum { kS1, kBeta, kS2, kS3, kFT, kFM, kEC, kGH, kGL, kLK, kLQ };
+constexpr int kScalars = 3072;
 
 // Bytes of the operands of a (block, group): k and q, rows of 2 NP bytes a piece, a row's
 // 16-byte parts in an order of its own (part()); and of a (block, head): T, M, scalars.
@@ -566,8 +174,7 @@ struct Ops {
   static constexpr int KP = sizeof(IO) == 4 ? 2 : 1, NP = 16 * NT, RB = 2 * NP;
   static constexpr int piece = kQ * RB, kq = KP * piece;  // one piece; all of k or q
   static constexpr int group = 2 * kq;
-  static constexpr int tri_piece = kTri * 1024;
-  static constexpr int t = 0, m = 2 * tri_piece, sc = 4 * tri_piece, head = sc + 2048;
+  static constexpr int t = 0, sc = 2 * kTri, m = sc + kScalars, head = m + 2 * kTri;
   // where 16-byte part c of row r lies: rows that are read together are in different banks
   __device__ static __forceinline__ int part(int r, int c) {
     constexpr int rows = RB >= 256 ? 1 : 256 / RB;  // rows in one round of the banks
@@ -575,8 +182,6 @@ struct Ops {
     return r * RB + ((c ^ f) << 4);
   }
 };
-// a head's scalars: places of 64 floats each
-enum { kS1, kBeta, kS2, kS3, kFT, kFM, kEC };
 
 __device__ __forceinline__ float max_nan(float a, float b) { return max3_nan(0.0f, a, b); }
 // 2^x of a running sum: what float32 leaves off it goes in to first order
@@ -714,6 +319,10 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
       sc[64 * kS2 + lane] = e * lq;
       sc[64 * kS3 + lane] = ex2(tot - cum) * lk;
       sc[64 * kEC + lane] = ex2(tot);
+      sc[64 * kGH + lane] = (float)cum;
+      sc[64 * kGL + lane] = (float)(cum - (double)(float)cum);
+      sc[64 * kLK + lane] = lk;
+      sc[64 * kLQ + lane] = lq;
       if (lane == 0) s_bad = kQ;
     }
     __syncthreads();  // k and q have been read, too
@@ -753,9 +362,9 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
         for (int e = 0; e < 8; ++e) mv[kb][e] *= f;
         h8 hi, lo;
         pieces(mv[kb], hi, lo);
-        char* to = out + O::m + (tri(tt, kb) * 64 + lane) * 16;
+        char* to = out + O::m + tri(row, kb, q4);
         *reinterpret_cast<h8*>(to) = hi;
-        *reinterpret_cast<h8*>(to + O::tri_piece) = lo;
+        *reinterpret_cast<h8*>(to + kTri) = lo;
       }
     }
     __syncthreads();
@@ -831,9 +440,9 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
         for (int e = 0; e < 8; ++e) t[kb][e] *= f;
         h8 hi, lo;
         pieces(t[kb], hi, lo);
-        char* to = out + O::t + (tri(tt, kb) * 64 + lane) * 16;
+        char* to = out + O::t + tri(row, kb, q4);
         *reinterpret_cast<h8*>(to) = hi;
-        *reinterpret_cast<h8*>(to + O::tri_piece) = lo;
+        *reinterpret_cast<h8*>(to + kTri) = lo;
       }
     }
   }
@@ -872,6 +481,7 @@ __device__ __forceinline__ void landed() {
   asm volatile("" ::: "memory");
 }
 
+constexpr int kNothing = 111;  // the shift of a column of zeros: that of the smallest values
 // The power of two for a column: its largest finite value over the four lanes that share it;
 // bad: whether one of the wave's columns has a value that is not finite.
 template <int PT, int NV>
@@ -901,7 +511,10 @@ __device__ __forceinline__ bool column_shifts(const f4 (&v)[NV][PT], int (&sh)[P
     }
   }
 #pragma unroll
-  for (int e = 0; e < PT; ++e) sh[e] = shift_for(row_max(mx[e]));
+  for (int e = 0; e < PT; ++e) {
+    mx[e] = row_max(mx[e]);
+    sh[e] = mx[e] == 0.0f ? kNothing : shift_for(mx[e]);
+  }
   return bad;
 }
 // the pieces of a pair of tiles of a column, scaled
@@ -912,13 +525,110 @@ __device__ __forceinline__ void pair_pieces(const f4& x, const f4& y, float f, h
   pieces(v, hi, lo);
 }
 
+// T or M (or, TR, its transpose) times a column's rows; XP pieces of these.  Products go by
+// turns over the results: none waits for the one before it.
+template <int PT, int XP, bool TR = false>
+__device__ __forceinline__ void triangle(const char* op, const h8 (&hi)[2][PT], const h8 (&lo)[2][PT], f4 (&out)[4][PT]) {
+  const int lane = threadIdx.x & 63, i16 = lane & 15, q4 = lane >> 4;
+  h8 x[4][2][2];  // [tile][block of the contraction][piece]
+#pragma unroll
+  for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const char* m = op + p * kTri;
+        if constexpr (TR) {
+          // rows of T 32 kb + 8 q + i16 / 4 (and four on), columns 32 (tt / 2) + 8 (i16 % 4) + 4 (tt % 2) + {0 .. 3}
+          const int r = 32 * kb + 8 * q4 + (i16 >> 2);
+          if (kb >= tt / 2)
+            x[tt][kb][p] = joined_tr(read_tr(m + tri(r, tt / 2, i16 & 3) + 8 * (tt & 1)),
+                                     read_tr(m + tri(r + 4, tt / 2, i16 & 3) + 8 * (tt & 1)));
+        } else {
+          if (kb <= tt / 2) x[tt][kb][p] = *reinterpret_cast<const h8*>(m + tri(place_of(tt, i16), kb, q4));
+        }
+      }
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        if (TR ? kb < tt / 2 : kb > tt / 2) continue;
+        if (XP == 1 && p == 1) continue;
+#pragma unroll
+        for (int e = 0; e < PT; ++e)
+          out[tt][e] = mfma(x[tt][kb][p == 0], p == 1 ? lo[kb][e] : hi[kb][e], out[tt][e]);
+      }
+}
+// k or q times a column's states: the pieces of S[2 m], S[2 m + 1] are made once for both
+// operands X, Y (Y may be left out).  part: of Ops.
+template <typename O, int PT, int NT, bool BOTH, typename EACH>
+__device__ __forceinline__ void times_state(const char* x, const char* y, const f4 (&S)[NT][PT], const float (&f)[PT],
+                                            f4 (&xs)[4][PT], f4 (&ys)[4][PT], EACH each) {
+  const int lane = threadIdx.x & 63, i16 = lane & 15, q4 = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < NT / 2; ++m) {
+    h8 hi[PT], lo[PT];
+#pragma unroll
+    for (int e = 0; e < PT; ++e) {
+      pair_pieces(S[2 * m][e], S[2 * m + 1][e], f[e], hi[e], lo[e]);
+      each(m, e, hi[e], lo[e]);
+    }
+    h8 xa[4][O::KP], ya[4][O::KP];
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      const int at = O::part(place_of(tt, i16), 4 * m + q4);
+#pragma unroll
+      for (int p = 0; p < O::KP; ++p) {
+        xa[tt][p] = *reinterpret_cast<const h8*>(x + p * O::piece + at);
+        if constexpr (BOTH) ya[tt][p] = *reinterpret_cast<const h8*>(y + p * O::piece + at);
+      }
+    }
+    auto all = [&](int p, const h8 (&v)[PT]) {
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          xs[tt][e] = mfma(xa[tt][p], v[e], xs[tt][e]);
+          if constexpr (BOTH) ys[tt][e] = mfma(ya[tt][p], v[e], ys[tt][e]);
+        }
+    };
+    all(0, lo);
+    if constexpr (O::KP == 2) all(1, hi);
+    all(0, hi);
+  }
+}
+// k or q transposed: the operand of state tiles 2 m, 2 m + 1 over rows 32 kb ..
+template <typename O>
+__device__ __forceinline__ h8 rows_tr(const char* x, int kb, int m, int i) {
+  const int lane = threadIdx.x & 63, i16 = lane & 15, q4 = lane >> 4;
+  // rows 32 kb + 8 q + i16 / 4 (and four on), states 32 m + 8 (i16 % 4) + 4 i + {0 .. 3}
+  const int r = 32 * kb + 8 * q4 + (i16 >> 2), pt = 4 * m + (i16 & 3);
+  return joined_tr(read_tr(x + O::part(r, pt) + 8 * i), read_tr(x + O::part(r + 4, pt) + 8 * i));
+}
+
+// What a backward keeps of a (block, head): the state S entering the block, the gradient dS
+// behind it, U and dR as pieces, a row a channel (S, dS: states; U, dR: the block's
+// tokens), 32 channels together with all four; a channel's shifts apart.
+enum { kKS, kKdS, kKU, kKdR, kKdY, kKinds };
+template <typename IO, int NT>
+struct Keep {
+  static constexpr int sp = 32 * Ops<IO, NT>::RB, tp = 32 * 128;  // a piece of 32 channels
+  static constexpr int s = 0, ds = 2 * sp, u = 4 * sp, dr = u + 2 * tp, block = dr + 2 * tp;
+  __device__ static __forceinline__ int part(int r, int c) {  // of U, dR: eight tokens
+    return r * 128 + ((c ^ ((r >> 1 & 1) | (r >> 3 & 3) << 1)) << 4);
+  }
+};
+__device__ __forceinline__ int padded(int P) { return (P + 31) & ~31; }
+
 // A workgroup walks a sequence's blocks with WV waves of 16 PT channels of one head each, the
 // states of a wave's channels in its accumulators.  DB: the next block's operands
 // come while this block's are used.
-template <typename IO, int NT, int PT, int WV, bool FAST>
+template <typename IO, int NT, int PT, int WV, bool FAST, bool KEEP>
 __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, int units) {
   using O = Ops<IO, NT>;
-  constexpr int KP = O::KP, B = O::group + O::head, PB = 16 * PT;
+  constexpr int KP = O::KP, GB = KEEP ? O::kq : O::group, HB = KEEP ? O::m : O::head, B = GB + HB, PB = 16 * PT;
   constexpr bool DB = 2 * B <= 160 * 1024;
   __shared__ __align__(16) char s_op[(DB ? 2 : 1) * B];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -931,25 +641,25 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
   const DeltaSeq sq = a.seqs[s];
   if (sq.slot < 0) return;
   const int N = a.N, P = a.P, p0 = (unit * WV + wave) * PB;
-  const bool on = p0 < P;  // else the wave only helps to stage
+  const bool on = p0 < (KEEP ? padded(P) : P);  // else the wave only helps to stage
   int col[PT];
 #pragma unroll
   for (int e = 0; e < PT; ++e) {
     const int p = p0 + PT * i16 + e;
-    col[e] = h * P + (p < P ? p : FAST ? (on ? p0 : 0) + e : 0);
+    col[e] = h * P + (p < P ? p : FAST ? (p0 < P ? p0 : 0) + e : 0);
   }
   const int nc = (sq.t1 - sq.t0 + kQ - 1) / kQ;
   auto stage_block = [&](int b) {
     const int64_t c = sq.c0 + b;
     char* to = s_op + (DB ? (b & 1) * B : 0);
-    send<WV, O::group>(a.gops + (c * a.G + g) * O::group, to);
-    send<WV, O::head>(a.hops + (c * a.H + h) * O::head, to + O::group);
+    send<WV, GB>(a.gops + (c * a.G + g) * O::group, to);
+    send<WV, HB>(a.hops + (c * a.H + h) * O::head, to + GB);
   };
   if (nc > 0) stage_block(0);
 
   // lane (i, q) holds the states 32 m + 8 q + {0 .. 3} of its channels in tile 2 m, {4 .. 7} in 2 m + 1
   f4 S[NT][PT];
-  const float* src = sq.resume ? a.state : nullptr;
+  const float* src = KEEP ? a.h0 : sq.resume ? a.state : nullptr;
 #pragma unroll
   for (int e = 0; e < PT; ++e)
 #pragma unroll
@@ -957,7 +667,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
       const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
       f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
       if (src) {
-        const float* at = src + ((int64_t)sq.slot * a.H * P + col[e]) * N + n;
+        const float* at = src + ((int64_t)(KEEP ? s : sq.slot) * a.H * P + col[e]) * N + n;
         if constexpr (FAST) {
           if (n < N) v = *reinterpret_cast<const f4*>(at);
         } else {
@@ -1005,25 +715,6 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
   };
   if (nc > 0 && on) fetch(0);
 
-  // T or M times the pieces of a column's rows
-  auto triangle = [&](const char* op, const h8 (&hi)[2][PT], const h8 (&lo)[2][PT], f4 (&out)[4][PT]) {
-    h8 xh[kTri], xl[kTri];
-#pragma unroll
-    for (int i = 0; i < kTri; ++i) {
-      xh[i] = *reinterpret_cast<const h8*>(op + (i * 64 + lane) * 16);
-      xl[i] = *reinterpret_cast<const h8*>(op + O::tri_piece + (i * 64 + lane) * 16);
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int tt = 2 * kb; tt < 4; ++tt)
-#pragma unroll
-          for (int e = 0; e < PT; ++e)
-            out[tt][e] = mfma(p == 0 ? xl[tri(tt, kb)] : xh[tri(tt, kb)], p == 1 ? lo[kb][e] : hi[kb][e], out[tt][e]);
-  };
-
   for (int b = 0; b < nc; ++b) {
     const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
     landed();
@@ -1037,7 +728,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
         for (int e = 0; e < RV; ++e) asm volatile("" : "+v"(vr[kb][j][e]));
     if (DB && b + 1 < nc) stage_block(b + 1);
     const char* op = s_op + (DB ? (b & 1) * B : 0);
-    const char* hop = op + O::group;
+    const char* hop = op + GB;
     const float* sc = reinterpret_cast<const float*>(hop + O::sc);
     if (on) {
       // ---- k S and q S
@@ -1047,35 +738,28 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
       float f[PT], fi[PT];
 #pragma unroll
       for (int e = 0; e < PT; ++e) f[e] = two(sh[e]), fi[e] = two(-sh[e]);
-#pragma unroll
-      for (int m = 0; m < NT / 2; ++m) {
-        h8 hi[PT], lo[PT];
-#pragma unroll
-        for (int e = 0; e < PT; ++e) pair_pieces(S[2 * m][e], S[2 * m + 1][e], f[e], hi[e], lo[e]);
-        h8 ka[4][KP], qa[4][KP];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const int at = O::part(place_of(tt, i16), 4 * m + q4);
-#pragma unroll
-          for (int p = 0; p < KP; ++p) {
-            ka[tt][p] = *reinterpret_cast<const h8*>(op + p * O::piece + at);
-            qa[tt][p] = *reinterpret_cast<const h8*>(op + O::kq + p * O::piece + at);
-          }
-        }
-        // eight results by turns: a product does not wait for the one before it
-        auto all = [&](int p, const h8 (&x)[PT]) {
-#pragma unroll
-          for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-            for (int e = 0; e < PT; ++e) {
-              ks[tt][e] = mfma(ka[tt][p], x[e], ks[tt][e]);
-              qs[tt][e] = mfma(qa[tt][p], x[e], qs[tt][e]);
-            }
-        };
-        all(0, lo);
-        if constexpr (KP == 2) all(1, hi);
-        all(0, hi);
+      using KL = Keep<IO, NT>;
+      char* kept = nullptr;  // of the wave's channels
+      int* kept_sh = nullptr;
+      if constexpr (KEEP) {
+        const int64_t at = (int64_t)(sq.c0 + b) * a.H + h;
+        kept = a.keep + (at * (padded(P) / 32) + p0 / 32) * KL::block;
+        kept_sh = a.shifts + at * kKinds * padded(P) + p0 + PT * i16;
       }
+      const int kr = p0 % 32 + PT * i16;
+      // pieces of a column into their place; channels past the last one are zeros
+      auto keep = [&](int off, int lo_off, int e, h8 hi, h8 lo) {
+        if (p0 + PT * i16 + e >= P) hi = h8{}, lo = h8{};
+        *reinterpret_cast<h8*>(kept + off) = hi;
+        *reinterpret_cast<h8*>(kept + off + lo_off) = lo;
+      };
+      if constexpr (KEEP)
+        if (q4 == 0)
+#pragma unroll
+          for (int e = 0; e < PT; ++e) kept_sh[kKS * padded(P) + e] = p0 + PT * i16 + e < P ? sh[e] : kNothing;
+      times_state<O, PT, NT, !KEEP>(op, op + O::kq, S, f, ks, qs, [&](int m, int e, const h8& hi, const h8& lo) {
+        if constexpr (KEEP) keep(KL::s + O::part(kr + e, 4 * m + q4), KL::sp, e, hi, lo);
+      });
       // ---- R = b (v - e^G k S); q S to its size
       if (cnt < kQ) {
         rarely();
@@ -1090,13 +774,14 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
       for (int tt = 0; tt < 4; ++tt) {
         const int t = place_of(tt, 4 * q4);
         const f4 s1 = *reinterpret_cast<const f4*>(sc + 64 * kS1 + t), be = *reinterpret_cast<const f4*>(sc + 64 * kBeta + t);
-        const f4 s2 = *reinterpret_cast<const f4*>(sc + 64 * kS2 + t);
+        f4 s2;
+        if constexpr (!KEEP) s2 = *reinterpret_cast<const f4*>(sc + 64 * kS2 + t);
 #pragma unroll
         for (int e = 0; e < PT; ++e)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             ks[tt][e][r] = be[r] * fmaf(-(s1[r] * fi[e]), ks[tt][e][r], value(tt >> 1, 4 * (tt & 1) + r, e));
-            qs[tt][e][r] *= s2[r] * fi[e];
+            if constexpr (!KEEP) qs[tt][e][r] *= s2[r] * fi[e];
           }
       }
       if (b + 1 < nc) fetch(b + 1);
@@ -1136,7 +821,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb) pair_pieces(ks[2 * kb][e], ks[2 * kb + 1][e], f[e], hi[kb][e], lo[kb][e]);
         }
-        triangle(hop + O::t, hi, lo, u);
+        triangle<PT, 2>(hop + O::t, hi, lo, u);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           const f4 ft = *reinterpret_cast<const f4*>(sc + 64 * kFT + place_of(tt, 4 * q4));
@@ -1160,8 +845,24 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb) pair_pieces(u[2 * kb][e], u[2 * kb + 1][e], f[e], hi[kb][e], lo[kb][e]);
         }
+        if constexpr (KEEP) {
+#pragma unroll
+          for (int e = 0; e < PT; ++e) {
+            if (q4 == 0) kept_sh[kKU * padded(P) + e] = p0 + PT * i16 + e < P ? sh[e] : kNothing;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+              if (bad) {
+                rarely();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (32 * kb + 8 * q4 + j >= first[e]) hi[kb][e][j] = (_Float16)__builtin_nanf("");
+              }
+              keep(KL::u + KL::part(kr + e, 4 * kb + q4), KL::tp, e, hi[kb][e], lo[kb][e]);
+            }
+          }
+        } else {
         f4 y[4][PT] = {};
-        triangle(hop + O::m, hi, lo, y);
+        triangle<PT, 2>(hop + O::m, hi, lo, y);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
           const f4 fm = *reinterpret_cast<const f4*>(sc + 64 * kFM + place_of(tt, 4 * q4));
@@ -1208,6 +909,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
               if (t < cnt) write(static_cast<char*>(a.y) + ((r0 + t) * a.ys + col[0]) * (int64_t)sizeof(IO), tt, r);
             }
         }
+        }
       }
       // ---- S = e^G64 S + sum_j k_j (e^(G64 - G_j) U_j)
 #pragma unroll
@@ -1236,14 +938,9 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-              // rows 32 kb + 8 q + i16 / 4 (and four on), states 16 n0 + 8 (i16 % 4) + 4 i + {0 .. 3}
-              const int r = 32 * kb + 8 * q4 + (i16 >> 2), pt = 2 * n0 + (i16 & 3);
+            for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-              for (int p = 0; p < KP; ++p)
-                kt[i][kb][p] = joined_tr(read_tr(op + p * O::piece + O::part(r, pt) + 8 * i),
-                                         read_tr(op + p * O::piece + O::part(r + 4, pt) + 8 * i));
-            }
+              for (int p = 0; p < KP; ++p) kt[i][kb][p] = rows_tr<O>(op + p * O::piece, kb, n0 / 2, i);
           auto all = [&](int kb, int p, const h8 (&x)[PT]) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -1270,7 +967,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
       stage_block(b + 1);
     }
   }
-  if (!a.state || !on) return;
+  if (KEEP || !a.state || !on) return;
 #pragma unroll
   for (int e = 0; e < PT; ++e)
     if (p0 + PT * i16 + e < P)
@@ -1286,6 +983,721 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
             if (n + r < N) at[r] = S[nt][e][r];
         }
       }
+}
+
+// The blocks against their order: the gradient dS behind a block from that behind the next
+// one, dR and dv, with what delta_rows_grad_kernel takes from here.  Waves, channels and places
+// as in delta_walk_kernel.
+template <typename IO, int NT, bool FAST>
+__global__ void __launch_bounds__(256) delta_back_kernel(const DeltaArgs a, int units) {
+  using O = Ops<IO, NT>;
+  using KL = Keep<IO, NT>;
+  constexpr int KP = O::KP, B = O::group + O::head, WV = 4;
+  constexpr bool DB = 2 * B <= 160 * 1024;
+  __shared__ __align__(16) char s_op[(DB ? 2 : 1) * B];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int i16 = lane & 15, q4 = lane >> 4;
+  const int item = blockIdx.x / (8 * units) * 8 + blockIdx.x % 8, unit = blockIdx.x / 8 % units;
+  if (item >= a.nseq * a.H) return;
+  const int s = item / a.H, g = item % a.G, h = g * a.per + item % a.H / a.G;
+  const DeltaSeq sq = a.seqs[s];
+  const int N = a.N, P = a.P, PP = padded(P), p0 = (unit * WV + wave) * 16, p = p0 + i16;
+  const bool on = p0 < PP, mine = p < P;
+  const int col = h * P + (mine ? p : 0);
+  const int nc = (sq.t1 - sq.t0 + kQ - 1) / kQ;
+  auto stage_block = [&](int b) {
+    const int64_t c = sq.c0 + b;
+    char* to = s_op + (DB ? (b & 1) * B : 0);
+    send<WV, O::group>(a.gops + (c * a.G + g) * O::group, to);
+    send<WV, O::head>(a.hops + (c * a.H + h) * O::head, to + O::group);
+  };
+  if (nc > 0) stage_block(nc - 1);
+  f4 S[NT][1];
+  const int64_t own = ((int64_t)s * a.H * P + col) * N;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
+    f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.dfinal) {
+      if constexpr (FAST) {
+        if (n < N) v = *reinterpret_cast<const f4*>(a.dfinal + own + n);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < N) v[r] = a.dfinal[own + n + r];
+      }
+    }
+    S[nt][0] = v;
+  }
+  IO raw[2][8];
+  const uint32_t y_own = (uint32_t)((8 * q4 * a.gs + col) * sizeof(IO)), v_own = (uint32_t)((8 * q4 * a.dvs + col) * sizeof(IO));
+  auto fetch = [&](int b) {
+    const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
+    if (FAST && cnt == kQ) {
+      const char* row = static_cast<const char*>(a.dy) + (int64_t)r0 * a.gs * sizeof(IO);
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          raw[kb][j] = *reinterpret_cast<const IO*>(row + (32 * kb + j) * a.gs * (int64_t)sizeof(IO) + y_own);
+    } else {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          raw[kb][j] = static_cast<const IO*>(a.dy)[(r0 + min(32 * kb + 8 * q4 + j, cnt - 1)) * a.gs + col];
+    }
+  };
+  if (nc > 0 && on) fetch(nc - 1);
+  for (int b = nc - 1; b >= 0; --b) {
+    const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
+    landed();
+    meet();
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(raw[kb][j]));
+    if (DB && b > 0) stage_block(b - 1);
+    const char* op = s_op + (DB ? (b & 1) * B : 0);
+    const char* hop = op + O::group;
+    const float* sc = reinterpret_cast<const float*>(hop + O::sc);
+    if (on) {
+      const int64_t at = (int64_t)(sq.c0 + b) * a.H + h;
+      char* kept = a.keep + (at * (PP / 32) + p0 / 32) * KL::block;
+      int* kept_sh = a.shifts + at * kKinds * PP + p;
+      const int kr = p0 % 32 + i16;
+      auto keep = [&](int off, int lo_off, h8 hi, h8 lo) {
+        if (!mine) hi = h8{}, lo = h8{};
+        *reinterpret_cast<h8*>(kept + off) = hi;
+        *reinterpret_cast<h8*>(kept + off + lo_off) = lo;
+      };
+      auto keep_shift = [&](int kind, int sh) {
+        if (q4 == 0) kept_sh[kind * PP] = mine ? sh : kNothing;
+      };
+      // ---- k dS
+      f4 ks[4][1] = {}, none[4][1];
+      int sh[1];
+      column_shifts<1, NT>(S, sh);
+      keep_shift(kKdS, sh[0]);
+      const float fs[1] = {two(sh[0])}, fsi = two(-sh[0]);
+      times_state<O, 1, NT, false>(op, op, S, fs, ks, none, [&](int m, int, const h8& hi, const h8& lo) {
+        keep(KL::ds + O::part(kr, 4 * m + q4), KL::sp, hi, lo);
+      });
+      // ---- dY; dU = M^T dY + e^(G64 - G) k dS
+      f4 dy[4][1];
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const IO w = raw[tt >> 1][4 * (tt & 1) + r];
+          if constexpr (sizeof(IO) == 2) dy[tt][0][r] = __uint_as_float((uint32_t)w << 16);
+          else dy[tt][0][r] = w;
+        }
+      if (cnt < kQ) {
+        rarely();
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) dy[tt][0][r] = place_of(tt, 4 * q4 + r) < cnt ? dy[tt][0][r] : 0.0f;
+      }
+      if (b > 0) fetch(b - 1);
+      column_shifts<1, 4>(dy, sh);
+      keep_shift(kKdY, sh[0]);
+      // rows times a scalar of theirs
+      auto rows = [&](const f4 (&v)[4][1], int kind, f4 (&o)[4][1]) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const f4 x = *reinterpret_cast<const f4*>(sc + 64 * kind + place_of(tt, 4 * q4));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[tt][0][r] = v[tt][0][r] * x[r];
+        }
+      };
+      h8 hi[2][1], lo[2][1];
+      float fi;
+      auto split = [&](const f4 (&v)[4][1]) {
+        column_shifts<1, 4>(v, sh);
+        const float f = two(sh[0]);
+        fi = two(-sh[0]);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) pair_pieces(v[2 * kb][0], v[2 * kb + 1][0], f, hi[kb][0], lo[kb][0]);
+      };
+      f4 w[4][1], du[4][1] = {};
+      rows(dy, kFM, w);
+      split(w);
+      triangle<1, KP, true>(hop + O::m, hi, lo, du);  // bf16 values times powers of two: one piece
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const f4 s3 = *reinterpret_cast<const f4*>(sc + 64 * kS3 + place_of(tt, 4 * q4));
+        const f4 ft = *reinterpret_cast<const f4*>(sc + 64 * kFT + place_of(tt, 4 * q4));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) du[tt][0][r] = fmaf(ks[tt][0][r], s3[r] * fsi, du[tt][0][r] * fi) * ft[r];
+      }
+      // ---- dR = T^T dU, dv = b dR
+      split(du);
+      f4 dr[4][1] = {};
+      triangle<1, 2, true>(hop + O::t, hi, lo, dr);
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dr[tt][0][r] *= fi;
+      split(dr);
+      keep_shift(kKdR, sh[0]);
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) keep(KL::dr + KL::part(kr, 4 * kb + q4), KL::tp, hi[kb][0], lo[kb][0]);
+      rows(dr, kBeta, dr);
+      if (mine) {
+        if (FAST && cnt == kQ) {
+          char* row = static_cast<char*>(a.dv) + (int64_t)r0 * a.dvs * sizeof(IO);
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              st<IO>(row + (32 * (tt >> 1) + 4 * (tt & 1) + r) * a.dvs * (int64_t)sizeof(IO) + v_own, 0, dr[tt][0][r]);
+        } else {
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int tk = place_of(tt, 4 * q4 + r);
+              if (tk < cnt) st<IO>(a.dv, (r0 + tk) * a.dvs + col, dr[tt][0][r]);
+            }
+        }
+      }
+      // ---- dS = e^G64 dS + (e^G q)^T dY - (b e^G k)^T dR
+      rows(dy, kS2, dy);
+      split(dy);
+      h8 yh[2], yl[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) yh[kb] = hi[kb][0], yl[kb] = lo[kb][0];
+      const float fy = fi;
+      rows(dr, kS1, dr);
+      split(dr);
+      const float ec = sc[64 * kEC];
+#pragma unroll
+      for (int m = 0; m < NT / 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f4 d0 = {}, d1 = {};
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            h8 qt[KP], kt[KP];
+#pragma unroll
+            for (int pc = 0; pc < KP; ++pc) {
+              qt[pc] = rows_tr<O>(op + O::kq + pc * O::piece, kb, m, i);
+              kt[pc] = rows_tr<O>(op + pc * O::piece, kb, m, i);
+            }
+            d0 = mfma(qt[0], yl[kb], d0);
+            d1 = mfma(kt[0], lo[kb][0], d1);
+            if constexpr (KP == 2) {
+              d0 = mfma(qt[KP - 1], yh[kb], d0);
+              d1 = mfma(kt[KP - 1], hi[kb][0], d1);
+            }
+            d0 = mfma(qt[0], yh[kb], d0);
+            d1 = mfma(kt[0], hi[kb][0], d1);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            S[2 * m + i][0][r] = fmaf(d1[r], -fi, fmaf(d0[r], fy, S[2 * m + i][0][r] * ec));
+        }
+    }
+    if (!DB && b > 0) {
+      meet();
+      stage_block(b - 1);
+    }
+  }
+  if (!a.dh0 || !mine) return;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
+    if constexpr (FAST) {
+      if (n < N) *reinterpret_cast<f4*>(a.dh0 + own + n) = S[nt][0];
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < N) a.dh0[own + n + r] = S[nt][0][r];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- gradients of a block's rows and scalars
+
+// fp16 pieces times weights of their contraction index
+__device__ __forceinline__ h8 weighted(h8 v, h8 w) { return v * w; }
+// Sum of four lanes' rows: the sixteen lanes that share q.
+__device__ __forceinline__ float sum16(float v) { return lane_sum<16>(v); }
+
+// One workgroup per block and head, eight waves: wave (tt, nh) has tile tt of the tokens and half
+// the states, or columns 32 nh .. of the 64 x 64 matrices.  First the products over the
+// channels, 32 at a time from what the walks kept: dY S^T, dR S^T, U dS^T, and dY U^T,
+// dR U^T.  Both factors are scaled by channel, so the left one is weighted with what both
+// scales leave, by the largest one.  Then the products over the block's tokens.
+template <typename IO, int NT, bool VEC>
+__global__ void __launch_bounds__(512) delta_rows_grad_kernel(const DeltaArgs a) {
+  using O = Ops<IO, NT>;
+  using KL = Keep<IO, NT>;
+  constexpr int KP = O::KP, NH = NT / 2;            // state tiles of a wave
+  constexpr bool DB = 2 * KL::block <= 100 * 1024;
+  constexpr int zp = 64 * 128;                      // a piece of a 64 x 64 matrix
+  constexpr bool ROOM = 2 * O::kq + 8 * zp <= 140 * 1024;  // for k and q at once
+  constexpr int zat = (ROOM ? 2 : 1) * O::kq, qat = ROOM ? O::kq : 0, post = zat + 8 * zp;
+  constexpr int lds = (DB ? 2 : 1) * KL::block > post ? (DB ? 2 : 1) * KL::block : post;
+  __shared__ __align__(16) char s_buf[lds];
+  __shared__ __align__(16) float s_sc[kScalars / 4];
+  __shared__ __align__(16) _Float16 s_w[5][256];
+  __shared__ __align__(16) float s_fy[256], s_fr[256];
+  __shared__ int s_e[5];
+  __shared__ float s_rmax[2][2][kQ], s_cmax[2][4][kQ];
+  __shared__ float s_row[2][kQ], s_col[4][kQ], s_db[2][kQ], s_qq[2][kQ], s_rk[2][kQ], s_tail[2][kQ], s_dot[8];
+  const int c = blockIdx.x, h = blockIdx.y, g = h / a.per, N = a.N, P = a.P, PP = padded(P);
+  if (c >= a.head->nchunk) return;
+  const DeltaChunk ck = a.chunks[c];
+  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, q4 = lane >> 4, cnt = ck.r1 - ck.r0;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), tt = wave & 3, nh = wave >> 2;
+  const int64_t at = (int64_t)c * a.H + h;
+  const char* kept = a.keep + at * (PP / 32) * KL::block;
+  const int* shifts = a.shifts + at * kKinds * PP;
+  const char* hop = a.hops + at * O::head;
+  auto stage_block = [&](int pb) { send<8, KL::block>(kept + (int64_t)pb * KL::block, s_buf + (DB ? (pb & 1) * KL::block : 0)); };
+  stage_block(0);
+  for (int u = tid; u < kScalars / 4; u += 512) s_sc[u] = reinterpret_cast<const float*>(hop + O::sc)[u];
+  for (int p = tid; p < PP; p += 512) {
+    s_fy[p] = two(shifts[kKdY * PP + p]);
+    s_fr[p] = two(-shifts[kKdR * PP + p]);
+  }
+  if (wave < 5) {
+    const int x = wave == 0 || wave == 3 ? kKdY : wave == 2 ? kKU : kKdR, y = wave == 2 ? kKdS : wave < 2 ? kKS : kKU;
+    int e[4], top = -1000;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int p = lane + 64 * k;
+      e[k] = p < PP ? -(shifts[x * PP + p] + shifts[y * PP + p]) : -1000;
+      top = max(top, e[k]);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = max(top, __shfl_xor(top, d, 64));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s_w[wave][lane + 64 * k] = (_Float16)two(max(e[k] - top, -100));
+    if (lane == 0) s_e[wave] = top;
+  }
+  const int row = place_of(tt, i16);  // as a lane of an operand
+  f4 yS[NH] = {}, rS[NH] = {}, uS[NH] = {}, dm[2] = {}, dl[2] = {};
+  float db = 0.0f;
+  const bool low = nh <= (tt >> 1);  // columns on or below the diagonal
+  for (int pb = 0; pb < PP / 32; ++pb) {
+    // the rows of dY (and v) come from where they lie
+    float y[8], v[8];
+    const int p = 32 * pb + 8 * q4;
+    const int64_t tok = ck.r0 + min(row, cnt - 1);
+    load8<IO, VEC>(a.dy, tok * a.gs + (int64_t)h * P + p, row < cnt ? P - p : 0, y);
+    if (nh == 0) load8<IO, VEC>(a.v, tok * a.vs + (int64_t)h * P + p, row < cnt ? P - p : 0, v);
+    landed();
+    __syncthreads();
+    if (DB && pb + 1 < PP / 32) stage_block(pb + 1);
+    const char* k = s_buf + (DB ? (pb & 1) * KL::block : 0);
+    h8 w[5], yh, yl, rp[2], up[2];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = *reinterpret_cast<const h8*>(&s_w[i][p]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] *= s_fy[p + j];
+    pieces(y, yh, yl);
+    // a token tile of U or dR: rows (channels) 8 q + i16 / 4 (and four on), tokens as place_of()
+    auto tokens = [&](int off, int tile) {
+      const int r = 8 * q4 + (i16 >> 2), pt = 4 * (tile >> 1) + (i16 & 3), half = 8 * (tile & 1);
+      return joined_tr(read_tr(k + off + KL::part(r, pt) + half), read_tr(k + off + KL::part(r + 4, pt) + half));
+    };
+    // a tile of 16 states of S or dS
+    auto states = [&](int off, int nt) {
+      const int r = 8 * q4 + (i16 >> 2), pt = 2 * nt + ((i16 & 3) >> 1), half = 8 * (i16 & 1);
+      return joined_tr(read_tr(k + off + O::part(r, pt) + half), read_tr(k + off + O::part(r + 4, pt) + half));
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      rp[i] = tokens(KL::dr + i * KL::tp, tt);
+      up[i] = tokens(KL::u + i * KL::tp, tt);
+    }
+    if (nh == 0) {
+      float x[8];
+      joined(rp[0], rp[1], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) db = fmaf(x[j] * s_fr[p + j], v[j], db);
+    }
+    const h8 y0h = weighted(yh, w[0]), r1h = weighted(rp[0], w[1]), r1l = weighted(rp[1], w[1]);
+    const h8 u2h = weighted(up[0], w[2]), u2l = weighted(up[1], w[2]);
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      const int nt = nh * NH + i;
+      const h8 sh = states(KL::s, nt), sl = states(KL::s + KL::sp, nt);
+      const h8 dh = states(KL::ds, nt), dlo = states(KL::ds + KL::sp, nt);
+      yS[i] = mfma(y0h, sl, yS[i]);
+      rS[i] = mfma(r1l, sh, rS[i]);
+      uS[i] = mfma(u2l, dh, uS[i]);
+      rS[i] = mfma(r1h, sl, rS[i]);
+      uS[i] = mfma(u2h, dlo, uS[i]);
+      if constexpr (KP == 2) yS[i] = mfma(weighted(yl, w[0]), sh, yS[i]);
+      rS[i] = mfma(r1h, sh, rS[i]);
+      uS[i] = mfma(u2h, dh, uS[i]);
+      yS[i] = mfma(y0h, sh, yS[i]);
+    }
+    if (low) {
+      const h8 y3h = weighted(yh, w[3]), r4h = weighted(rp[0], w[4]), r4l = weighted(rp[1], w[4]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const h8 uh = tokens(KL::u, 2 * nh + e), ul = tokens(KL::u + KL::tp, 2 * nh + e);
+        dm[e] = mfma(ul, y3h, dm[e]);
+        dl[e] = mfma(ul, r4h, dl[e]);
+        if constexpr (KP == 2) dm[e] = mfma(uh, weighted(yl, w[3]), dm[e]);
+        dl[e] = mfma(uh, r4l, dl[e]);
+        dm[e] = mfma(uh, y3h, dm[e]);
+        dl[e] = mfma(uh, r4h, dl[e]);
+      }
+    }
+    __syncthreads();  // the waves are done with this buffer
+    if (!DB && pb + 1 < PP / 32) stage_block(pb + 1);
+  }
+  if (nh == 0) {
+    db += __shfl_xor(db, 16, 64);
+    db += __shfl_xor(db, 32, 64);
+  }
+  // ---- k and q; the state's part of the last running sum's gradient meanwhile
+  const char* gop = a.gops + ((int64_t)c * a.G + g) * O::group;
+  send<8, O::kq>(gop, s_buf);
+  if constexpr (ROOM) send<8, O::kq>(gop + O::kq, s_buf + qat);
+  {
+    float dot = 0.0f;
+    for (int u = tid; u < PP * (O::RB / 16); u += 512) {
+      const int p = u / (O::RB / 16), at16 = u % (O::RB / 16) * 16;
+      const char* s = kept + (int64_t)(p >> 5) * KL::block + (p & 31) * O::RB + at16;
+      float x[8], y[8], part = 0.0f;
+      joined(*reinterpret_cast<const h8*>(s + KL::s), *reinterpret_cast<const h8*>(s + KL::s + KL::sp), x);
+      joined(*reinterpret_cast<const h8*>(s + KL::ds), *reinterpret_cast<const h8*>(s + KL::ds + KL::sp), y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part = fmaf(x[j], y[j], part);
+      dot += __builtin_amdgcn_ldexpf(part, -(shifts[kKS * PP + p] + shifts[kKdS * PP + p]));
+    }
+    dot = lane_sum<64>(dot);
+    if (lane == 0) s_dot[wave] = dot;
+  }
+  // ---- the accumulators to their size; rows 4 q + r of the tile
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int t = place_of(tt, 4 * q4 + r);
+    const float e = ex2(s_sc[64 * kGH + t]) * fmaf(s_sc[64 * kGL + t], kLn2, 1.0f);
+    const float gh = s_sc[64 * kGH + kQ - 1] - s_sc[64 * kGH + t], gl = s_sc[64 * kGL + kQ - 1] - s_sc[64 * kGL + t];
+    const float et = ex2(gh) * fmaf(gl, kLn2, 1.0f);
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      yS[i][r] = __builtin_amdgcn_ldexpf(yS[i][r], s_e[0]) * e;
+      rS[i][r] = __builtin_amdgcn_ldexpf(rS[i][r], s_e[1]) * e;
+      uS[i][r] = __builtin_amdgcn_ldexpf(uS[i][r], s_e[2]) * et;
+    }
+  }
+  landed();
+  __syncthreads();
+  // ---- the 64 x 64 matrices: lane (row, q) has columns 32 nh + 8 q + {0 .. 7}
+  float zr[2][8] = {}, zc[2][8] = {};  // for the products over columns and over rows: (dM D), (b dL D)
+  {
+    f4 kk[2] = {};
+    if (low) {
+#pragma unroll
+      for (int m = 0; m < NT / 2; ++m) {
+        h8 kb[KP];
+#pragma unroll
+        for (int pc = 0; pc < KP; ++pc) kb[pc] = *reinterpret_cast<const h8*>(s_buf + pc * O::piece + O::part(row, 4 * m + q4));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          h8 ka[KP];
+#pragma unroll
+          for (int pc = 0; pc < KP; ++pc)
+            ka[pc] = *reinterpret_cast<const h8*>(s_buf + pc * O::piece + O::part(place_of(2 * nh + e, i16), 4 * m + q4));
+          if constexpr (KP == 2) {
+            kk[e] = mfma(ka[KP - 1], kb[0], kk[e]);
+            kk[e] = mfma(ka[0], kb[KP - 1], kk[e]);
+          }
+          kk[e] = mfma(ka[0], kb[0], kk[e]);
+        }
+      }
+    }
+    float mr[8] = {};  // M of these columns
+    if (low) {
+      const char* m = hop + O::m + tri(row, nh, q4);
+      joined(*reinterpret_cast<const h8*>(m), *reinterpret_cast<const h8*>(m + kTri), mr);
+    }
+    const float gi = s_sc[64 * kGH + row], gil = s_sc[64 * kGL + row], bi = s_sc[64 * kBeta + row];
+    const float lki = s_sc[64 * kLK + row], lqi = s_sc[64 * kLQ + row], fm = s_sc[64 * kFM + row];
+    float rowsum = 0.0f, dbl = 0.0f, colsum[8], rmax[2] = {}, cmax[2][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int cj = 32 * nh + 8 * q4 + j;
+      const float D = ex2(gi - s_sc[64 * kGH + cj]) * fmaf(gil - s_sc[64 * kGL + cj], kLn2, 1.0f);
+      const float lkj = s_sc[64 * kLK + cj];
+      const float m0 = __builtin_amdgcn_ldexpf(dm[j >> 2][j & 3], s_e[3]);
+      const float l0 = __builtin_amdgcn_ldexpf(dl[j >> 2][j & 3], s_e[4]);
+      const float m = low && cj <= row ? m0 * D : 0.0f, l = low && cj < row ? -l0 * D : 0.0f;
+      const float kkh = lki * lkj * kk[j >> 2][j & 3], lb = l * bi;
+      // what the running sum's gradient takes from here; the diagonal's cancels
+      const float mm = low && cj < row ? fmaf(m0, mr[j] * fm, lb * kkh) : 0.0f;
+      dbl = fmaf(l, kkh, dbl);
+      rowsum += mm;
+      colsum[j] = sum16(mm);
+      zr[0][j] = m * lkj;
+      zr[1][j] = lb * lkj;
+      zc[0][j] = m * lqi;
+      zc[1][j] = lb * lki;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        rmax[i] = finite(zr[i][j]) ? fmaxf(rmax[i], fabsf(zr[i][j])) : rmax[i];
+        cmax[i][j] = lane_max<16>(finite(zc[i][j]) ? fabsf(zc[i][j]) : 0.0f);
+      }
+    }
+    rowsum += __shfl_xor(rowsum, 16, 64);
+    rowsum += __shfl_xor(rowsum, 32, 64);
+    dbl += __shfl_xor(dbl, 16, 64);
+    dbl += __shfl_xor(dbl, 32, 64);
+    db = nh == 0 ? db + dbl : dbl;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rmax[i] = row_max(rmax[i]);
+    if (q4 == 0) {
+      s_row[nh][row] = rowsum;
+      s_rmax[0][nh][row] = rmax[0];
+      s_rmax[1][nh][row] = rmax[1];
+    }
+    if (i16 == 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int cj = 32 * nh + 8 * q4 + j;
+        s_col[tt][cj] = colsum[j];
+        s_cmax[0][tt][cj] = cmax[0][j];
+        s_cmax[1][tt][cj] = cmax[1][j];
+      }
+  }
+  __syncthreads();
+  auto row_shift = [&](int i, int r) { return shift_for(fmaxf(s_rmax[i][0][r], s_rmax[i][1][r])); };
+  auto col_shift = [&](int i, int cj) {
+    return shift_for(fmaxf(fmaxf(s_cmax[i][0][cj], s_cmax[i][1][cj]), fmaxf(s_cmax[i][2][cj], s_cmax[i][3][cj])));
+  };
+  char* z = s_buf + zat;  // by row: dM D, b dL D; by column: the same
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float f = two(row_shift(i, row));
+    h8 hi, lo;
+    const int to = KL::part(row, 4 * nh + q4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) zr[i][j] *= f;
+    pieces(zr[i], hi, lo);
+    *reinterpret_cast<h8*>(z + 2 * i * zp + to) = hi;
+    *reinterpret_cast<h8*>(z + (2 * i + 1) * zp + to) = lo;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) zc[i][j] *= two(col_shift(i, 32 * nh + 8 * q4 + j));
+    pieces(zc[i], hi, lo);
+    *reinterpret_cast<h8*>(z + (4 + 2 * i) * zp + to) = hi;
+    *reinterpret_cast<h8*>(z + (5 + 2 * i) * zp + to) = lo;
+  }
+  __syncthreads();
+  // ---- the products over the block's tokens
+  auto z_rows = [&](int i, int kb) {
+    return *reinterpret_cast<const h8*>(z + i * zp + KL::part(row, 4 * kb + q4));
+  };
+  auto z_cols = [&](int i, int kb) {
+    const int r = 32 * kb + 8 * q4 + (i16 >> 2), pt = 4 * (tt >> 1) + (i16 & 3), half = 8 * (tt & 1);
+    return joined_tr(read_tr(z + i * zp + KL::part(r, pt) + half), read_tr(z + i * zp + KL::part(r + 4, pt) + half));
+  };
+  // rows 32 kb .. of k or q, 16 states
+  auto x_states = [&](const char* x, int kb, int nt) {
+    const int r = 32 * kb + 8 * q4 + (i16 >> 2), pt = 2 * nt + ((i16 & 3) >> 1), half = 8 * (i16 & 1);
+    return joined_tr(read_tr(x + O::part(r, pt) + half), read_tr(x + O::part(r + 4, pt) + half));
+  };
+  f4 fq[NH] = {};
+  float qq[4] = {}, rk[4] = {}, tail[4] = {};
+  float fr0[4], fr1[4], fc0[4], fc1[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int t = place_of(tt, 4 * q4 + r);
+    fr0[r] = two(-row_shift(0, t)); fr1[r] = two(-row_shift(1, t));
+    fc0[r] = two(-col_shift(0, t)); fc1[r] = two(-col_shift(1, t));
+  }
+  auto element = [&](const char* x, int t, int n) {
+    const char* e = x + O::part(t, n >> 3) + (n & 7) * 2;
+    float v = (float)*reinterpret_cast<const _Float16*>(e);
+    if constexpr (KP == 2) v += (float)*reinterpret_cast<const _Float16*>(e + O::piece);
+    return v;
+  };
+#pragma unroll
+  for (int i = 0; i < NH; ++i) {
+    const int nt = nh * NH + i;
+    f4 h1 = {}, h2 = {};
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      h8 x[KP];
+#pragma unroll
+      for (int pc = 0; pc < KP; ++pc) x[pc] = x_states(s_buf + pc * O::piece, kb, nt);
+      if (kb <= (tt >> 1)) {
+        fq[i] = mfma(z_rows(1, kb), x[0], fq[i]);
+        h1 = mfma(z_rows(3, kb), x[0], h1);
+        if constexpr (KP == 2) {
+          fq[i] = mfma(z_rows(0, kb), x[KP - 1], fq[i]);
+          h1 = mfma(z_rows(2, kb), x[KP - 1], h1);
+        }
+        fq[i] = mfma(z_rows(0, kb), x[0], fq[i]);
+        h1 = mfma(z_rows(2, kb), x[0], h1);
+      }
+      if (kb >= (tt >> 1)) {
+        h2 = mfma(z_cols(7, kb), x[0], h2);
+        if constexpr (KP == 2) h2 = mfma(z_cols(6, kb), x[KP - 1], h2);
+        h2 = mfma(z_cols(6, kb), x[0], h2);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = place_of(tt, 4 * q4 + r), n = 16 * nt + i16;
+      const float kh = element(s_buf, t, n) * s_sc[64 * kLK + t];
+      rk[r] = fmaf(rS[i][r], kh, rk[r]);
+      tail[r] = fmaf(uS[i][r], kh, tail[r]);
+      uS[i][r] = fmaf(-s_sc[64 * kBeta + t], rS[i][r], uS[i][r]) + fmaf(h1[r], fr1[r], h2[r] * fc1[r]);
+    }
+  }
+  if constexpr (!ROOM) {
+    __syncthreads();
+    send<8, O::kq>(gop + O::kq, s_buf);
+    landed();
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < NH; ++i) {
+    const int nt = nh * NH + i;
+    f4 gk = {};
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if (kb < (tt >> 1)) continue;
+      h8 x[KP];
+#pragma unroll
+      for (int pc = 0; pc < KP; ++pc) x[pc] = x_states(s_buf + qat + pc * O::piece, kb, nt);
+      gk = mfma(z_cols(5, kb), x[0], gk);
+      if constexpr (KP == 2) gk = mfma(z_cols(4, kb), x[KP - 1], gk);
+      gk = mfma(z_cols(4, kb), x[0], gk);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = place_of(tt, 4 * q4 + r), n = 16 * nt + i16;
+      qq[r] = fmaf(yS[i][r], element(s_buf + qat, t, n) * s_sc[64 * kLQ + t], qq[r]);
+      if (n < N) {
+        a.dqh[(at * kQ + t) * N + n] = fmaf(fq[i][r], fr0[r], yS[i][r]);
+        a.dkh[(at * kQ + t) * N + n] = fmaf(gk[r], fc0[r], uS[i][r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    qq[r] = sum16(qq[r]); rk[r] = sum16(rk[r]); tail[r] = sum16(tail[r]);
+    if (i16 == 0) {
+      const int t = place_of(tt, 4 * q4 + r);
+      s_qq[nh][t] = qq[r]; s_rk[nh][t] = rk[r]; s_tail[nh][t] = tail[r];
+    }
+  }
+  if (q4 == 0) s_db[nh][row] = db;
+  __syncthreads();
+  // ---- the scalars: lane t
+  if (wave == 0) {
+    const int t = lane;
+    const float b = s_sc[64 * kBeta + t], rkt = s_rk[0][t] + s_rk[1][t];
+    const double tl = (double)s_tail[0][t] + (double)s_tail[1][t];
+    double x = (double)s_qq[0][t] + (double)s_qq[1][t] - (double)(b * rkt) - tl + (double)s_row[0][t] + (double)s_row[1][t];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x -= (double)s_col[k][t];
+    double dot = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dot += (double)s_dot[k];
+    const double last = (double)s_sc[64 * kEC] * dot + lane63(wave_scan(tl));
+    const double pre = wave_scan(x);
+    const float dg = (float)(lane63(pre) - pre + x + last);
+    float dA = 0.0f, ddt = 0.0f;
+    if (t < cnt) {
+      const int64_t r = ck.r0 + t;
+      const float raw = ld<IO>(a.dt, r * a.ds + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
+      ddt = dg * a.A[h] * (a.softplus ? sigmoid(raw) : 1.0f);
+      dA = dg * (a.softplus ? softplus(raw) : raw);
+      st<IO>(a.ddt, r * a.dds + h, ddt);
+      const float d = s_db[0][t] + s_db[1][t] - rkt;
+      st<IO>(a.dbeta, r * a.dbs + h, d * (a.sigmoid ? b * (1.0f - b) : 1.0f));
+    }
+    dA = lane_sum<64>(dA);
+    ddt = lane_sum<64>(ddt);
+    if (lane == 0) a.part[at * 2] = dA, a.part[at * 2 + 1] = ddt;
+  }
+}
+
+// the heads of a group together, and the normalisation: one wave a row
+template <typename IO>
+__global__ void __launch_bounds__(256) delta_qk_grad_kernel(const DeltaArgs a) {
+  const int c = blockIdx.x, g = blockIdx.y, N = a.N;
+  if (c >= a.head->nchunk) return;
+  const DeltaChunk ck = a.chunks[c];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int i = wave; i < ck.r1 - ck.r0; i += 4) {
+    const int64_t r = ck.r0 + i;
+    for (int which = 0; which < 2; ++which) {
+      const void* p = which ? a.k : a.q;
+      const int64_t at = r * (which ? a.ks : a.qs) + (int64_t)g * N;
+      float x[4], d[4], ss = 0.0f, xd = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = lane + 64 * j;
+        x[j] = n < N ? ld<IO>(p, at + n) : 0.0f;
+        d[j] = 0.0f;
+        if (n < N)
+          for (int m = 0; m < a.per; ++m)
+            d[j] += (which ? a.dkh : a.dqh)[(((int64_t)c * a.H + g * a.per + m) * kQ + i) * N + n];
+        ss = fmaf(x[j], x[j], ss);
+      }
+      const float f = a.norm ? rsqrtf(lane_sum<64>(ss) + a.eps) : 1.0f, sc = which ? 1.0f : a.scale;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] *= f, xd = fmaf(x[j], d[j], xd);
+      xd = a.norm ? lane_sum<64>(xd) : 0.0f;
+      const int64_t to = r * (which ? a.dks : a.dqs) + (int64_t)g * N;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (lane + 64 * j < N) st<IO>(which ? a.dk : a.dq, to + lane + 64 * j, (d[j] - x[j] * xd) * f * sc);
+    }
+  }
+}
+
+// dA and ddt_bias: one workgroup a head, blocks in runs of a fixed order
+__global__ void __launch_bounds__(256) delta_sum_kernel(const DeltaArgs a) {
+  __shared__ double red[2][256];
+  const int h = blockIdx.x, t = threadIdx.x, nc = a.head->nchunk;
+  double s0 = 0.0, s1 = 0.0;
+  for (int c = t; c < nc; c += 256) {
+    s0 += a.part[((int64_t)c * a.H + h) * 2];
+    s1 += a.part[((int64_t)c * a.H + h) * 2 + 1];
+  }
+  red[0][t] = s0;
+  red[1][t] = s1;
+  __syncthreads();
+  if (t < 2) {
+    double s = 0.0;
+    for (int k = 0; k < 256; ++k) s += red[t][k];
+    float* out = t ? a.ddt_bias : a.dA;
+    if (out) out[h] = (float)s;
+  }
+}
+
+// rows of no sequence have no gradients
+template <typename IO>
+__global__ void __launch_bounds__(256) delta_zero_kernel(const DeltaArgs a) {
+  const int first = a.head->first, last = a.head->last;
+  const int64_t gn = (int64_t)a.G * a.N, hp = (int64_t)a.H * a.P, wide = 2 * gn + hp + 2 * a.H;
+  const int64_t rows = a.tokens - (last - first);
+  for (int64_t u = blockIdx.x * 256ll + threadIdx.x; u < rows * wide; u += gridDim.x * 256ll) {
+    int64_t r = u / wide, c = u % wide;
+    if (r >= first) r += last - first;
+    if (c < gn) { st<IO>(a.dq, r * a.dqs + c, 0.0f); continue; }
+    c -= gn;
+    if (c < gn) { st<IO>(a.dk, r * a.dks + c, 0.0f); continue; }
+    c -= gn;
+    if (c < hp) { st<IO>(a.dv, r * a.dvs + c, 0.0f); continue; }
+    c -= hp;
+    if (c < a.H) st<IO>(a.ddt, r * a.dds + c, 0.0f);
+    else st<IO>(a.dbeta, r * a.dbs + c - a.H, 0.0f);
+  }
 }
 
 // ---------------------------------------------------------------- one token a sequence
@@ -1435,7 +1847,7 @@ int check_state(const DeltaArgs& a, const DeltaCall& c) {
 struct DeltaLayout {
   int nt;  // tiles of 16 states
   int64_t nchunk;
-  int64_t chunks, seqs, gops, hops, qh, kh, T, M, cum, b, S, dS, U, dR, dqh, dkh, part, bytes;
+  int64_t chunks, seqs, gops, hops, keep, shifts, dqh, dkh, part, bytes;
 };
 
 DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N, int io_dtype, bool bwd) {
@@ -1453,21 +1865,12 @@ DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int
   take(sizeof(DeltaHead));
   l.chunks = take(l.nchunk * sizeof(DeltaChunk));
   l.seqs = take(nseq * sizeof(DeltaSeq));
-  if (!bwd) {
-    l.gops = take(l.nchunk * G * 2 * kQ * l.nt * 32 * (io_dtype == SSM_DTYPE_BF16 ? 1 : 2));
-    l.hops = take(ch * (4 * kTri * 1024 + 2048));
-  }
+  l.gops = take(l.nchunk * G * 2 * kQ * l.nt * 32 * (io_dtype == SSM_DTYPE_BF16 ? 1 : 2));
+  l.hops = take(ch * (4 * kTri + kScalars));
   if (bwd) {
-    l.qh = take(l.nchunk * G * kQ * N * 4);
-    l.kh = take(l.nchunk * G * kQ * N * 4);
-    l.T = take(ch * kQ * kQ * 4);
-    l.M = take(ch * kQ * kQ * 4);
-    l.cum = take(ch * kQ * 8);
-    l.b = take(ch * kQ * 4);
-    l.S = take(ch * N * P * 4);
-    l.dS = take(ch * N * P * 4);
-    l.U = take(ch * kQ * P * 4);
-    l.dR = take(ch * kQ * P * 4);
+    const int64_t pb = (P + 31) / 32;
+    l.keep = take(ch * pb * (128 * l.nt * 32 + 4 * 32 * 128));
+    l.shifts = take(ch * kKinds * pb * 32 * 4);
     l.dqh = take(ch * kQ * N * 4);
     l.dkh = take(ch * kQ * N * 4);
     l.part = take(ch * 8);
@@ -1488,79 +1891,88 @@ void place(DeltaArgs& a, const DeltaLayout& l, void* workspace) {
   a.head = reinterpret_cast<DeltaHead*>(w);
   a.chunks = reinterpret_cast<DeltaChunk*>(w + l.chunks);
   a.seqs = reinterpret_cast<DeltaSeq*>(w + l.seqs);
-  auto f = [&](int64_t o) { return reinterpret_cast<float*>(w + o); };
-  a.qh = f(l.qh); a.kh = f(l.kh); a.T = f(l.T); a.M = f(l.M); a.b = f(l.b);
-  a.cum = reinterpret_cast<double*>(w + l.cum);
-  a.S = f(l.S); a.dS = f(l.dS); a.U = f(l.U); a.dR = f(l.dR); a.dqh = f(l.dqh); a.dkh = f(l.dkh);
-  a.part = f(l.part);
-  a.gops = w + l.gops; a.hops = w + l.hops;
-}
-
-template <typename IO>
-void launch_delta_prep(const DeltaArgs& a, const DeltaLayout& l, hipStream_t s) {
-  delta_plan_kernel<<<1, 1024, 0, s>>>(a);
-  delta_rows_kernel<IO><<<dim3((unsigned)l.nchunk, a.G), 256, 0, s>>>(a);
-  delta_prep_kernel<IO><<<dim3((unsigned)l.nchunk, a.H), 256, 0, s>>>(a);
+  a.gops = w + l.gops; a.hops = w + l.hops; a.keep = w + l.keep;
+  a.shifts = reinterpret_cast<int*>(w + l.shifts);
+  a.dqh = reinterpret_cast<float*>(w + l.dqh);
+  a.dkh = reinterpret_cast<float*>(w + l.dkh);
+  a.part = reinterpret_cast<float*>(w + l.part);
 }
 
 // 128 channels a workgroup where that gives every CU one, else 64.
 constexpr int64_t kCUs = 256;
 
 template <typename IO, int NT>
-void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, hipStream_t s) {
-  static_assert(Ops<IO, NT>::group == 2 * kQ * NT * 32 * Ops<IO, NT>::KP && Ops<IO, NT>::head == 4 * kTri * 1024 + 2048, "as in delta_layout");
+void launch_delta_ops(const DeltaArgs& a, const DeltaLayout& l, bool vec, hipStream_t s) {
+  static_assert(Ops<IO, NT>::group == 2 * kQ * NT * 32 * Ops<IO, NT>::KP && Ops<IO, NT>::head == 4 * kTri + kScalars &&
+                Keep<IO, NT>::block == 128 * NT * 32 + 4 * 32 * 128, "as in delta_layout");
   delta_plan_kernel<<<1, 1024, 0, s>>>(a);
   const dim3 grid((unsigned)l.nchunk, a.H);
   if (vec) delta_ops_kernel<IO, NT, true><<<grid, 256, 0, s>>>(a);
   else delta_ops_kernel<IO, NT, false><<<grid, 256, 0, s>>>(a);
-  auto walk = [&](auto pt, auto fa) {
-    constexpr int PT = decltype(pt)::value;
-    const int units = (a.P + 64 * PT - 1) / (64 * PT);
-    const int64_t items = (a.nseq * a.H + 7) / 8 * 8;
-    delta_walk_kernel<IO, NT, PT, 4, decltype(fa)::value><<<(unsigned)(items * units), 256, 0, s>>>(a, units);
-  };
-  using One = std::integral_constant<int, 1>;
-  using Two = std::integral_constant<int, 2>;
-  bool wide = false;
-  if constexpr (NT < 16) wide = a.nseq * a.H * ((a.P + 127) / 128) >= kCUs;
-  if constexpr (NT < 16) {
-    if (wide) {
-      if (fast) walk(Two{}, std::true_type{});
-      else walk(Two{}, std::false_type{});
-      return;
-    }
+}
+
+template <typename IO, int NT, int PT, bool FAST, bool KEEP>
+void launch_delta_walk(const DeltaArgs& a, hipStream_t s) {
+  const int units = (a.P + 64 * PT - 1) / (64 * PT);
+  const int64_t items = (a.nseq * a.H + 7) / 8 * 8;
+  delta_walk_kernel<IO, NT, PT, 4, FAST, KEEP><<<(unsigned)(items * units), 256, 0, s>>>(a, units);
+}
+
+template <typename IO, int NT>
+void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, hipStream_t s) {
+  launch_delta_ops<IO, NT>(a, l, vec, s);
+  if constexpr (NT < 16)
+    if (a.nseq * a.H * ((a.P + 127) / 128) >= kCUs)
+      return fast ? launch_delta_walk<IO, NT, 2, true, false>(a, s) : launch_delta_walk<IO, NT, 2, false, false>(a, s);
+  if (fast) launch_delta_walk<IO, NT, 1, true, false>(a, s);
+  else launch_delta_walk<IO, NT, 1, false, false>(a, s);
+}
+
+template <typename IO, int NT>
+void launch_delta_bwd(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, hipStream_t s) {
+  launch_delta_ops<IO, NT>(a, l, vec, s);
+  const int units = (a.P + 63) / 64;
+  const unsigned walk = (unsigned)((a.nseq * a.H + 7) / 8 * 8 * units);
+  const dim3 blocks((unsigned)l.nchunk, a.H);
+  if (fast) {
+    launch_delta_walk<IO, NT, 1, true, true>(a, s);
+    delta_back_kernel<IO, NT, true><<<walk, 256, 0, s>>>(a, units);
+    delta_rows_grad_kernel<IO, NT, true><<<blocks, 512, 0, s>>>(a);
+  } else {
+    launch_delta_walk<IO, NT, 1, false, true>(a, s);
+    delta_back_kernel<IO, NT, false><<<walk, 256, 0, s>>>(a, units);
+    delta_rows_grad_kernel<IO, NT, false><<<blocks, 512, 0, s>>>(a);
   }
-  if (fast) walk(One{}, std::true_type{});
-  else walk(One{}, std::false_type{});
+  delta_qk_grad_kernel<IO><<<dim3((unsigned)l.nchunk, a.G), 256, 0, s>>>(a);
+  delta_zero_kernel<IO><<<1024, 256, 0, s>>>(a);
+  if (a.dA || a.ddt_bias) delta_sum_kernel<<<a.H, 256, 0, s>>>(a);
 }
 
 template <typename IO>
-void launch_delta_io(const DeltaArgs& a, const DeltaLayout& l, hipStream_t s) {
+void launch_delta_io(const DeltaArgs& a, const DeltaLayout& l, bool bwd, hipStream_t s) {
   constexpr int es = sizeof(IO);
   auto on = [&](const void* p, int64_t stride, int64_t width, int bytes) {
     return ((uintptr_t)p | (uintptr_t)(stride * es) | (uintptr_t)(width * es)) % bytes == 0;
   };
+  // rows in 16-byte accesses; states and a lane's pair of channels in whole accesses, a
+  // lane's offset to its rows in 32 bits
   const bool vec = on(a.q, a.qs, a.N, 16) && on(a.k, a.ks, a.N, 16);
-  const bool fast = a.N % 4 == 0 && aligned16(a.state) && on(a.v, a.vs, a.P, 2 * es) && on(a.y, a.ys, a.P, 2 * es) &&
-                    a.vs < (1 << 24) && a.ys < (1 << 24);  // a lane's offset to its rows in 32 bits
+  const int64_t far = (int64_t)1 << 24;
+  const bool fast = bwd ? a.N % 4 == 0 && aligned16(a.dfinal) && aligned16(a.dh0) && aligned16(a.h0) &&
+                              on(a.v, a.vs, a.P, 16) && on(a.dy, a.gs, a.P, 16) && a.vs < far && a.gs < far && a.dvs < far
+                        : a.N % 4 == 0 && aligned16(a.state) && on(a.v, a.vs, a.P, 2 * es) && on(a.y, a.ys, a.P, 2 * es) &&
+                              a.vs < far && a.ys < far;
+  auto go = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    if (bwd) launch_delta_bwd<IO, NT>(a, l, vec, fast, s);
+    else launch_delta<IO, NT>(a, l, vec, fast, s);
+  };
   switch (l.nt) {
-    case 2: launch_delta<IO, 2>(a, l, vec, fast, s); break;
-    case 4: launch_delta<IO, 4>(a, l, vec, fast, s); break;
-    case 8: launch_delta<IO, 8>(a, l, vec, fast, s); break;
-    default: launch_delta<IO, 16>(a, l, vec, fast, s); break;
+    case 2: go(std::integral_constant<int, 2>{}); break;
+    case 4: go(std::integral_constant<int, 4>{}); break;
+    case 8: go(std::integral_constant<int, 8>{}); break;
+    default: go(std::integral_constant<int, 16>{}); break;
   }
-}
-
-template <typename IO>
-void launch_delta_bwd(const DeltaArgs& a, const DeltaLayout& l, hipStream_t s) {
-  launch_delta_prep<IO>(a, l, s);
-  const dim3 walk((unsigned)a.nseq, a.H, (a.P + 31) / 32);
-  delta_scan_kernel<IO, true><<<walk, 256, 0, s>>>(a);
-  delta_scan_bwd_kernel<IO><<<walk, 256, 0, s>>>(a);
-  delta_grad_kernel<IO><<<dim3((unsigned)l.nchunk, a.H), 256, 0, s>>>(a);
-  delta_qk_grad_kernel<IO><<<dim3((unsigned)l.nchunk, a.G), 256, 0, s>>>(a);
-  delta_zero_kernel<IO><<<1024, 256, 0, s>>>(a);
-  if (a.dA || a.ddt_bias) delta_sum_kernel<<<a.H, 256, 0, s>>>(a);
 }
 
 template <typename IO, int LN, bool VEC>
@@ -1637,8 +2049,8 @@ int ssm_gated_delta_fwd(const void* q, int64_t q_stride, const void* k, int64_t 
   if ((st = check_workspace(workspace, workspace_bytes, l.bytes))) return st;
   place(a, l, workspace);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (io_dtype == SSM_DTYPE_BF16) launch_delta_io<uint16_t>(a, l, s);
-  else launch_delta_io<float>(a, l, s);
+  if (io_dtype == SSM_DTYPE_BF16) launch_delta_io<uint16_t>(a, l, false, s);
+  else launch_delta_io<float>(a, l, false, s);
   return launch_status("ssm_gated_delta_fwd launch");
 }
 
@@ -1720,8 +2132,8 @@ int ssm_gated_delta_bwd(const void* dy, int64_t dy_stride, const void* q, int64_
   if ((st = check_workspace(workspace, workspace_bytes, l.bytes))) return st;
   place(a, l, workspace);
   hipStream_t s = static_cast<hipStream_t>(hip_stream);
-  if (io_dtype == SSM_DTYPE_BF16) launch_delta_bwd<uint16_t>(a, l, s);
-  else launch_delta_bwd<float>(a, l, s);
+  if (io_dtype == SSM_DTYPE_BF16) launch_delta_io<uint16_t>(a, l, true, s);
+  else launch_delta_io<float>(a, l, true, s);
   return launch_status("ssm_gated_delta_bwd launch");
 }
 
