@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(team_threads(TL)) add_norm_kernel(const AddNor
     params<VE>(a.w, c, 1.0f, w);
 #pragma unroll
     for (int j = 0; j < VE; ++j) {
-      v[k][j] = v[k][j] * rs * w[j];
+      // for 8 bits the row's factor rs is left out: it is in the scale as in the value
+      v[k][j] = QUANT ? v[k][j] * w[j] : v[k][j] * rs * w[j];
       m = fmaxf(m, fabsf(v[k][j]));
     }
     if constexpr (QUANT) {
@@ -141,7 +142,8 @@ __global__ void __launch_bounds__(team_threads(TL)) add_norm_kernel(const AddNor
       if (k * TL >= nv) break;
       const int c = (i + k * TL) * VE;
       if (on && i + k * TL < nv) {
-        const float scale = fmaxf(__uint_as_float(s_max[tw][c >> a.lb]), 0x1p-100f) * (1.0f / 448.0f), f = 1.0f / scale;
+        const float m = __uint_as_float(s_max[tw][c >> a.lb]);
+        const float f = m * rs >= 0x1p-100f ? 448.0f / m : rs / (0x1p-100f / 448.0f);
 #pragma unroll
         for (int j = 0; j < VE; ++j) v[k][j] *= f;
         put_e4m3<VE>(a.y, r * a.ys + c, v[k]);
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(team_threads(TL)) add_norm_kernel(const AddNor
     }
     if (on)
       for (int u = i; u < a.nb; u += TL)
-        a.scales[r * a.nb + u] = fmaxf(__uint_as_float(s_max[tw][u]), 0x1p-100f) * (1.0f / 448.0f);
+        a.scales[r * a.nb + u] = fmaxf(__uint_as_float(s_max[tw][u]) * rs, 0x1p-100f) / 448.0f;
   }
 }
 
