@@ -43,13 +43,21 @@ constexpr int kQ = 64;  // tokens of a block
 struct DeltaChunk {
   int r0, r1;
 };
-struct DeltaSeq {
-  int slot, t0, t1;  // slot -1: padding
+// consecutive blocks of one sequence
+struct DeltaSeg {
+  int slot, t0, t1;  // the sequence's slot; rows of the segment
   int c0;            // its first block
-  int resume;
+  int resume;        // the sequence starts from its slot
+  int split;         // segments before this one among those of cut sequences; -1: not cut
+  int last;          // the sequence ends here
+};
+// A cut sequence: its segments' places among those of cut sequences.
+struct DeltaCut {
+  int slot, split, nseg, resume;
 };
 struct DeltaHead {
-  int nchunk, first, last, pad;  // blocks in use; rows [first, last) belong to sequences
+  int nchunk, nseg, ncut;  // in use
+  int first, last;         // rows [first, last) belong to sequences
 };
 
 struct DeltaArgs {
@@ -66,14 +74,18 @@ struct DeltaArgs {
   float *dA, *ddt_bias;
   int64_t qs, ks, vs, ds, bs, ys, gs;        // row strides
   int64_t dqs, dks, dvs, dds, dbs;
-  int64_t tokens, nseq, nslots;
+  int64_t tokens, nseq, nslots, nseg;         // nseg: at most
   int H, P, G, N, per;                       // per: heads of a group
   int softplus, sigmoid, norm;
   float eps, scale;
   // workspace
   DeltaHead* head;
   DeltaChunk* chunks;
-  DeltaSeq* seqs;
+  DeltaSeg* segs;        // the backward's are whole sequences
+  DeltaCut* cuts;
+  int seg_len;           // blocks of a segment; a sequence of more than two is cut
+  float* local;          // [split][head]: X [P][N], the state behind a segment from zero (then the one
+                         // entering it), and Y [N][N], the images of the unit vectors
   char *gops, *hops;     // operands of a (block, group), of a (block, head)
   // backward
   char* keep;            // Keep::block for every 32 channels of a (block, head)
@@ -89,8 +101,8 @@ constexpr int64_t kMaxN = 256;
 __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaArgs a) {
   __shared__ int red[16];
   __shared__ i4 red4[16];
-  __shared__ int s_t0[1024], s_t1[1024], s_chunk[1024];
-  int nchunk = 0;
+  __shared__ int s_t0[1024], s_t1[1024], s_slot[1024], s_chunk[1024], s_seg[1024], s_split[1024], s_n[1024];
+  int nchunk = 0, nseg = 0, nsplit = 0, ncut = 0;
   const int i = threadIdx.x, tokens = (int)a.tokens;
   const int start = max(0, min(a.cu[0], tokens));
   int reached = start;  // the largest offset so far
@@ -100,6 +112,7 @@ __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaArgs a) {
     const int64_t s = base + i;
     const bool in = s < a.nseq;
     const int64_t slot = in && a.slots ? a.slots[s] : s;
+    const bool resume = in && a.has && a.has[s];
     int end = in ? max(reached, min(a.cu[s + 1], tokens)) : reached;
     end = block_scan_max(end, red);
     s_t1[i] = end;
@@ -107,20 +120,38 @@ __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaArgs a) {
     const int begin = i ? s_t1[i - 1] : reached;
     reached = s_t1[1023];
     s_t0[i] = begin;
-    const bool use = in && (!a.state || (slot >= 0 && slot < a.nslots));
-    i4 n = {use ? (end - begin + kQ - 1) / kQ : 0, 0, 0, 0}, all;
+    i4 n = {0, 0, 0, 0}, all;  // blocks, segments, segments of cut sequences, cut sequences
+    if (in && (!a.state || (slot >= 0 && slot < a.nslots))) {  // else padding
+      n[0] = (end - begin + kQ - 1) / kQ;
+      n[1] = n[0] > 2 * a.seg_len ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
+      n[2] = n[1] > 1 ? n[1] : 0;
+      n[3] = n[1] > 1;
+    }
     const i4 at = block_scan(n, red4, all);
+    s_slot[i] = (int)slot | (resume ? (int)0x80000000 : 0);
     s_chunk[i] = at[0];
-    if (in) a.seqs[s] = {use ? (int)slot : -1, begin, end, nchunk + at[0], a.has ? a.has[s] != 0 : 0};
+    s_seg[i] = at[1];
+    s_split[i] = nsplit + at[2];
+    s_n[i] = n[1];
+    if (n[3]) a.cuts[ncut + at[3]] = {(int)slot, nsplit + at[2], n[1], resume};
     __syncthreads();
     for (int c = i; c < all[0]; c += 1024) {
       const int k = find(s_chunk, c), r0 = s_t0[k] + (c - s_chunk[k]) * kQ;
       a.chunks[nchunk + c] = {r0, min(s_t1[k], r0 + kQ)};
     }
+    for (int g = i; g < all[1]; g += 1024) {
+      const int k = find(s_seg, g), nb = (s_t1[k] - s_t0[k] + kQ - 1) / kQ, of = s_n[k], j = g - s_seg[k];
+      const int lo = (int)((int64_t)nb * j / of), hi = (int)((int64_t)nb * (j + 1) / of);
+      a.segs[nseg + g] = {s_slot[k] & 0x7fffffff, s_t0[k] + lo * kQ, min(s_t1[k], s_t0[k] + hi * kQ),
+                          nchunk + s_chunk[k] + lo, s_slot[k] < 0, of > 1 ? s_split[k] + j : -1, j == of - 1};
+    }
     nchunk += all[0];
+    nseg += all[1];
+    nsplit += all[2];
+    ncut += all[3];
     __syncthreads();
   }
-  if (i == 0) *a.head = {nchunk, start, reached, 0};
+  if (i == 0) *a.head = {nchunk, nseg, ncut, start, reached};
 }
 
 // ---------------------------------------------------------------- a block's matrices
@@ -664,13 +695,22 @@ struct Keep {
 };
 __device__ __forceinline__ int padded(int P) { return (P + 31) & ~31; }
 
+// WALK: to y.  KEEP: for the backward, which keeps S and U of every block.  SUM: the state behind a
+// segment from zero, and, in further units, from each unit vector without v: with X and Y
+// of that, a state s entering the segment leaves it as X + s Y.
+enum { kWalk, kKeepBlocks, kSum };
+
+// Floats of `local` for one segment.
+__device__ __forceinline__ int64_t local_size(const DeltaArgs& a) { return (int64_t)a.H * a.N * (a.N + a.P); }
+
 // A workgroup walks a sequence's blocks with WV waves of 16 PT channels of one head each, the
 // states of a wave's channels in its accumulators.  DB: the next block's operands
 // come while this block's are used.
-template <typename IO, int NT, int PT, int WV, bool FAST, bool KEEP>
+template <typename IO, int NT, int PT, int WV, bool FAST, int MODE>
 __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, int units) {
   using O = Ops<IO, NT>;
-  constexpr int KP = O::KP, GB = KEEP ? O::kq : O::group, HB = KEEP ? O::m : O::head, B = GB + HB, PB = 16 * PT;
+  constexpr bool KEEP = MODE == kKeepBlocks, YES = MODE == kWalk;  // YES: y is asked for
+  constexpr int KP = O::KP, GB = !YES ? O::kq : O::group, HB = !YES ? O::m : O::head, B = GB + HB, PB = 16 * PT;
   constexpr bool DB = 2 * B <= 160 * 1024;
   __shared__ __align__(16) char s_op[(DB ? 2 : 1) * B];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -678,11 +718,14 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
   // eight dies take the workgroups by turns: the units of a head, and the heads of a
   // group where there are eight groups, share a die's cache
   const int item = blockIdx.x / (8 * units) * 8 + blockIdx.x % 8, unit = blockIdx.x / 8 % units;
-  if (item >= a.nseq * a.H) return;
+  if (item >= a.nseg * a.H) return;
   const int s = item / a.H, g = item % a.G, h = g * a.per + item % a.H / a.G;
-  const DeltaSeq sq = a.seqs[s];
-  if (sq.slot < 0) return;
-  const int N = a.N, P = a.P, p0 = (unit * WV + wave) * PB;
+  const DeltaSeg sq = a.segs[s];  // garbage past the last one, which ends here
+  if (s >= a.head->nseg) return;
+  if (MODE == kSum && (sq.split < 0 || sq.last)) return;  // no state asked
+  const int uv = (a.P + 16 * PT * WV - 1) / (16 * PT * WV);
+  const bool image = MODE == kSum && unit >= uv;  // of the unit vectors
+  const int N = a.N, P = image ? a.N : a.P, p0 = ((image ? unit - uv : unit) * WV + wave) * PB;
   const bool on = p0 < (KEEP ? padded(P) : P);  // else the wave only helps to stage
   int col[PT];
 #pragma unroll
@@ -701,7 +744,10 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
 
   // lane (i, q) holds the states 32 m + 8 q + {0 .. 3} of its channels in tile 2 m, {4 .. 7} in 2 m + 1
   f4 S[NT][PT];
-  const float* src = KEEP ? a.h0 : sq.resume ? a.state : nullptr;
+  const float* src = nullptr;
+  if (KEEP && a.h0) src = a.h0 + (int64_t)s * a.H * P * N;
+  if (YES && sq.split >= 0) src = a.local + sq.split * local_size(a) + (int64_t)h * N * (N + P) - (int64_t)h * P * N;
+  else if (YES && sq.resume) src = a.state + (int64_t)sq.slot * a.H * P * N;
 #pragma unroll
   for (int e = 0; e < PT; ++e)
 #pragma unroll
@@ -709,7 +755,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
       const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
       f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
       if (src) {
-        const float* at = src + ((int64_t)(KEEP ? s : sq.slot) * a.H * P + col[e]) * N + n;
+        const float* at = src + (int64_t)col[e] * N + n;
         if constexpr (FAST) {
           if (n < N) v = *reinterpret_cast<const f4*>(at);
         } else {
@@ -718,6 +764,9 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
             if (n + r < N) v[r] = at[r];
         }
       }
+      if (image)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = n + r == p0 + PT * i16 + e ? 1.0f : 0.0f;
       S[nt][e] = v;
     }
   // v of a block's rows 32 kb + 8 q + j.  Whole blocks go by an address of the row, the
@@ -729,7 +778,14 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
   const uint32_t v_own = (uint32_t)((8 * q4 * a.vs + col[0]) * sizeof(IO)), y_own = (uint32_t)((8 * q4 * a.ys + col[0]) * sizeof(IO));
   auto fetch = [&](int b) {
     const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
-    if (FAST && cnt == kQ) {
+    if (image) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < RV; ++e) vr[kb][j][e] = 0;
+    } else if (FAST && cnt == kQ) {
       const char* row = static_cast<const char*>(a.v) + (int64_t)r0 * a.vs * sizeof(IO);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -760,7 +816,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
   for (int b = 0; b < nc; ++b) {
     const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
     // the last block's y may still be on its way: a whole block's stores come behind all loads
-    if (!KEEP && FAST && b > 0 && on) landed<16 * (PAIR ? 1 : PT)>();
+    if (YES && FAST && b > 0 && on) landed<16 * (PAIR ? 1 : PT)>();
     else landed();
     meet();  // this block's operands are there; the waves are done with the last block's
     // v has come too: else the compiler would wait for it behind what is sent next
@@ -801,7 +857,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
         if (q4 == 0)
 #pragma unroll
           for (int e = 0; e < PT; ++e) kept_sh[kKS * padded(P) + e] = p0 + PT * i16 + e < P ? sh[e] : kNothing;
-      times_state<O, PT, NT, !KEEP>(op, op + O::kq, S, f, ks, qs, [&](int m, int e, const h8& hi, const h8& lo) {
+      times_state<O, PT, NT, YES>(op, op + O::kq, S, f, ks, qs, [&](int m, int e, const h8& hi, const h8& lo) {
         if constexpr (KEEP) keep(KL::s + O::part(kr + e, 4 * m + q4), KL::sp, e, hi, lo);
       });
       // ---- R = b (v - e^G k S); q S to its size
@@ -819,13 +875,13 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
         const int t = place_of(tt, 4 * q4);
         const f4 s1 = *reinterpret_cast<const f4*>(sc + 64 * kS1 + t), be = *reinterpret_cast<const f4*>(sc + 64 * kBeta + t);
         f4 s2;
-        if constexpr (!KEEP) s2 = *reinterpret_cast<const f4*>(sc + 64 * kS2 + t);
+        if constexpr (YES) s2 = *reinterpret_cast<const f4*>(sc + 64 * kS2 + t);
 #pragma unroll
         for (int e = 0; e < PT; ++e)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             ks[tt][e][r] = be[r] * fmaf(-(s1[r] * fi[e]), ks[tt][e][r], value(tt >> 1, 4 * (tt & 1) + r, e));
-            if constexpr (!KEEP) qs[tt][e][r] *= s2[r] * fi[e];
+            if constexpr (YES) qs[tt][e][r] *= s2[r] * fi[e];
           }
       }
       if (b + 1 < nc) fetch(b + 1);
@@ -887,7 +943,7 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
               keep(KL::u + KL::part(kr + e, 4 * kb + q4), KL::tp, e, hi[kb][e], lo[kb][e]);
             }
           }
-        } else {
+        } else if constexpr (YES) {
         f4 y[4][PT] = {};
         triangle<PT, 2>(hop + O::m, hi, lo, y);
 #pragma unroll
@@ -994,14 +1050,17 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
       stage_block(b + 1);
     }
   }
-  if (KEEP || !a.state || !on) return;
+  float* out = nullptr;
+  if (YES && a.state && sq.last) out = a.state + (int64_t)sq.slot * a.H * P * N;
+  if (MODE == kSum) out = a.local + sq.split * local_size(a) + (int64_t)h * a.N * (a.N + a.P) + (image ? (int64_t)a.P * N : 0) - (int64_t)h * P * N;
+  if (!out || !on) return;
 #pragma unroll
   for (int e = 0; e < PT; ++e)
     if (p0 + PT * i16 + e < P)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
-        float* at = a.state + ((int64_t)sq.slot * a.H * P + col[e]) * N + n;
+        float* at = out + (int64_t)col[e] * N + n;
         if constexpr (FAST) {
           if (n < N) *reinterpret_cast<f4*>(at) = S[nt][e];
         } else {
@@ -1039,10 +1098,10 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
   // eight dies take the workgroups by turns: the units of a head, and the heads of a
   // group where there are eight groups, share a die's cache
   const int item = blockIdx.x / (8 * units) * 8 + blockIdx.x % 8, unit = blockIdx.x / 8 % units;
-  if (item >= a.nseq * a.H) return;
+  if (item >= a.nseg * a.H) return;
   const int s = item / a.H, g = item % a.G, h = g * a.per + item % a.H / a.G;
-  const DeltaSeq sq = a.seqs[s];
-  if (sq.slot < 0) return;
+  const DeltaSeg sq = a.segs[s];  // garbage past the last one, which ends here
+  if (s >= a.head->nseg) return;
   const int N = a.N, P = a.P, p0 = (unit * 4 + pw) * 16, p = p0 + i16;
   const bool on = p0 < P, mine = p < P;  // else the wave only helps to stage
   const int col = h * P + (mine ? p : 0);
@@ -1152,18 +1211,22 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
 
   // ---- the states: lane (i, q) holds the states 32 m + 8 q + {0 .. 3} of its channel in tile 2 m, {4 .. 7} in 2 m + 1
   f4 S[NT][1];
-  float* const own = a.state ? a.state + ((int64_t)sq.slot * a.H * P + col) * N : nullptr;
+  const int64_t at_p = (int64_t)(mine ? p : 0) * N;
+  const float* src = nullptr;
+  // a cut sequence's first segment too has its start in `local`: the last one writes the slot in this same launch
+  if (sq.split >= 0) src = a.local + sq.split * local_size(a) + (int64_t)h * N * (N + P) + at_p;
+  else if (sq.resume) src = a.state + ((int64_t)sq.slot * a.H + h) * P * N + at_p;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
     f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (sq.resume && own) {
+    if (src) {
       if constexpr (FAST) {
-        if (n < N) v = *reinterpret_cast<const f4*>(own + n);
+        if (n < N) v = *reinterpret_cast<const f4*>(src + n);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (n + r < N) v[r] = own[n + r];
+          if (n + r < N) v[r] = src[n + r];
       }
     }
     S[nt][0] = v;
@@ -1327,7 +1390,8 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
         for (int r = 0; r < 4; ++r) S[2 * m + i][0][r] = fmaf(d[i][r], wi, S[2 * m + i][0][r] * ec);
     }
   }
-  if (!own || !mine) return;
+  if (!a.state || !sq.last || !mine) return;
+  float* const own = a.state + ((int64_t)sq.slot * a.H + h) * P * N + at_p;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int n = 32 * (nt >> 1) + 8 * q4 + 4 * (nt & 1);
@@ -1338,6 +1402,47 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
       for (int r = 0; r < 4; ++r)
         if (n + r < N) own[n + r] = S[nt][0][r];
     }
+  }
+}
+
+// The states entering the segments of a cut sequence, s <- X + s Y one after another: eight
+// rows (channels) of a head a workgroup, a thread a state.
+__global__ void __launch_bounds__(256) delta_join_kernel(const DeltaArgs a) {
+  constexpr int R = 8;
+  __shared__ __align__(16) float s_s[kMaxN][R];
+  if ((int)blockIdx.z >= a.head->ncut) return;
+  const DeltaCut ct = a.cuts[blockIdx.z];
+  const int h = blockIdx.y, N = a.N, P = a.P, n = threadIdx.x, p0 = blockIdx.x * R;
+  const bool on = n < N;
+  float s[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    s[r] = ct.resume && on && p0 + r < P ? a.state[(((int64_t)ct.slot * a.H + h) * P + p0 + r) * N + n] : 0.0f;
+  for (int k = 0; k < ct.nseg; ++k) {
+    float* l = a.local + (ct.split + k) * local_size(a) + (int64_t)h * N * (N + P);
+    float x[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool in = on && p0 + r < P;
+      x[r] = in && k + 1 < ct.nseg ? l[(int64_t)(p0 + r) * N + n] : 0.0f;
+      if (in) l[(int64_t)(p0 + r) * N + n] = s[r];
+    }
+    if (k + 1 == ct.nseg) break;
+    __syncthreads();
+    if (on)
+#pragma unroll
+      for (int r = 0; r < R; ++r) s_s[n][r] = s[r];
+    __syncthreads();
+    const float* y = l + (int64_t)P * N + (on ? n : 0);
+#pragma unroll 16
+    for (int j = 0; j < N; ++j) {
+      const float m = y[(int64_t)j * N];
+      const f4 lo = *reinterpret_cast<const f4*>(s_s[j]), hi = *reinterpret_cast<const f4*>(s_s[j] + 4);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = fmaf(lo[r], m, x[r]), x[r + 4] = fmaf(hi[r], m, x[r + 4]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = x[r];
   }
 }
 
@@ -1354,9 +1459,10 @@ __global__ void __launch_bounds__(256) delta_back_kernel(const DeltaArgs a, int 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i16 = lane & 15, q4 = lane >> 4;
   const int item = blockIdx.x / (8 * units) * 8 + blockIdx.x % 8, unit = blockIdx.x / 8 % units;
-  if (item >= a.nseq * a.H) return;
+  if (item >= a.nseg * a.H) return;
   const int s = item / a.H, g = item % a.G, h = g * a.per + item % a.H / a.G;
-  const DeltaSeq sq = a.seqs[s];
+  const DeltaSeg sq = a.segs[s];
+  if (s >= a.head->nseg) return;
   const int N = a.N, P = a.P, PP = padded(P), p0 = (unit * WV + wave) * 16, p = p0 + i16;
   const bool on = p0 < PP, mine = p < P;
   const int col = h * P + (mine ? p : 0);
@@ -2202,8 +2308,8 @@ int check_delta_extents(int64_t tokens, int64_t nseq, int64_t nheads, int64_t he
   if (nseq > 0xfffff || tokens / kQ + nseq >= ((int64_t)1 << 22))
     return fail(SSM_E_SHAPE, "tokens = %lld, nseq = %lld: nseq is at most 2^20 - 1, tokens / 64 + nseq 2^22 - 1",
                 (long long)tokens, (long long)nseq);
-  // a workgroup for every block or sequence and head
-  if (!grid_ok((tokens / kQ + nseq) * nheads, 1024))
+  // the walks have up to four workgroups of 512 threads a sequence and head
+  if (!grid_ok((tokens / kQ + nseq) * nheads, 2048))
     return fail(SSM_E_SHAPE, "too many blocks and heads for one call");
   return SSM_OK;
 }
@@ -2260,10 +2366,16 @@ int check_state(const DeltaArgs& a, const DeltaCall& c) {
   return SSM_OK;
 }
 
+constexpr int64_t kCUs = 256;
+// A cut sequence is walked twice, once for twice as many columns: cut where that leaves at
+// least four segments a sequence, of eight blocks at least.
+constexpr int64_t kMinCut = 4, kMinSeg = 8;
+
 struct DeltaLayout {
   int nt;  // tiles of 16 states
-  int64_t nchunk;
-  int64_t chunks, seqs, gops, hops, keep, shifts, dqh, dkh, part, bytes;
+  int64_t nchunk, nseg, nsplit, ncut;  // at most
+  int seg_len;
+  int64_t chunks, segs, cuts, local, gops, hops, keep, shifts, dqh, dkh, part, bytes;
 };
 
 DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int64_t G, int64_t N, int io_dtype, bool bwd) {
@@ -2280,7 +2392,21 @@ DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int
   const int64_t ch = l.nchunk * H;
   take(sizeof(DeltaHead));
   l.chunks = take(l.nchunk * sizeof(DeltaChunk));
-  l.seqs = take(nseq * sizeof(DeltaSeq));
+  // a walk's workgroups are 64 channels of a head: segments for as many as the card has CUs
+  const int64_t at_once = kCUs / (H * ((P + 63) / 64)), blocks = (tokens + kQ - 1) / kQ;
+  int64_t len = (int64_t)1 << 24;
+  if (!bwd && at_once >= kMinCut) {
+    len = (blocks + at_once - 1) / at_once;
+    if (len < kMinSeg) len = kMinSeg;
+  }
+  l.seg_len = (int)len;
+  // a sequence of more than 2 len blocks has one for every len of them, rounded up
+  l.ncut = blocks / (2 * len);
+  l.nsplit = l.ncut ? blocks / len + l.ncut : 0;
+  l.nseg = nseq + l.nsplit;
+  l.segs = take(l.nseg * sizeof(DeltaSeg));
+  l.cuts = take(l.ncut * sizeof(DeltaCut));
+  l.local = take(l.nsplit * H * N * (N + P) * 4);
   l.gops = take(l.nchunk * G * 2 * kQ * l.nt * 32 * (io_dtype == SSM_DTYPE_BF16 ? 1 : 2));
   l.hops = take(ch * (4 * kTri + kScalars));
   if (bwd) {
@@ -2306,7 +2432,11 @@ void place(DeltaArgs& a, const DeltaLayout& l, void* workspace) {
   char* w = static_cast<char*>(workspace);
   a.head = reinterpret_cast<DeltaHead*>(w);
   a.chunks = reinterpret_cast<DeltaChunk*>(w + l.chunks);
-  a.seqs = reinterpret_cast<DeltaSeq*>(w + l.seqs);
+  a.segs = reinterpret_cast<DeltaSeg*>(w + l.segs);
+  a.cuts = reinterpret_cast<DeltaCut*>(w + l.cuts);
+  a.local = reinterpret_cast<float*>(w + l.local);
+  a.seg_len = l.seg_len;
+  a.nseg = l.nseg;
   a.gops = w + l.gops; a.hops = w + l.hops; a.keep = w + l.keep;
   a.shifts = reinterpret_cast<int*>(w + l.shifts);
   a.dqh = reinterpret_cast<float*>(w + l.dqh);
@@ -2324,39 +2454,47 @@ void launch_delta_ops(const DeltaArgs& a, const DeltaLayout& l, bool vec, hipStr
   else delta_ops_kernel<IO, NT, false><<<grid, 256, 0, s>>>(a);
 }
 
-template <typename IO, int NT, int PT, bool FAST, bool KEEP>
+// Workgroups of a walk over units of 64 channels.
+unsigned walk_grid(const DeltaArgs& a, int units) { return (unsigned)((a.nseg * a.H + 7) / 8 * 8 * units); }
+
+template <typename IO, int NT, bool FAST, int MODE>
 void launch_delta_walk(const DeltaArgs& a, hipStream_t s) {
-  const int units = (a.P + 64 * PT - 1) / (64 * PT);
-  const int64_t items = (a.nseq * a.H + 7) / 8 * 8;
-  delta_walk_kernel<IO, NT, PT, 4, FAST, KEEP><<<(unsigned)(items * units), 256, 0, s>>>(a, units);
+  const int units = (a.P + 63) / 64 + (MODE == kSum ? (a.N + 63) / 64 : 0);
+  delta_walk_kernel<IO, NT, 1, 4, FAST, MODE><<<walk_grid(a, units), 256, 0, s>>>(a, units);
 }
 
 template <typename IO, int NT>
 void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, hipStream_t s) {
   launch_delta_ops<IO, NT>(a, l, vec, s);
-  if constexpr (Pair<IO, NT>::fits) {
-    const int units = (a.P + 63) / 64;
-    const unsigned grid = (unsigned)((a.nseq * a.H + 7) / 8 * 8 * units);
-    if (fast) delta_pair_kernel<IO, NT, true><<<grid, 512, 0, s>>>(a, units);
-    else delta_pair_kernel<IO, NT, false><<<grid, 512, 0, s>>>(a, units);
-  } else {
-    if (fast) launch_delta_walk<IO, NT, 1, true, false>(a, s);
-    else launch_delta_walk<IO, NT, 1, false, false>(a, s);
-  }
+  auto go = [&](auto f) {
+    constexpr bool FAST = decltype(f)::value;
+    if (l.nsplit) {
+      launch_delta_walk<IO, NT, FAST, kSum>(a, s);
+      delta_join_kernel<<<dim3((a.P + 7) / 8, a.H, (unsigned)l.ncut), 256, 0, s>>>(a);
+    }
+    if constexpr (Pair<IO, NT>::fits) {
+      const int units = (a.P + 63) / 64;
+      delta_pair_kernel<IO, NT, FAST><<<walk_grid(a, units), 512, 0, s>>>(a, units);
+    } else {
+      launch_delta_walk<IO, NT, FAST, kWalk>(a, s);
+    }
+  };
+  if (fast) go(std::true_type{});
+  else go(std::false_type{});
 }
 
 template <typename IO, int NT>
 void launch_delta_bwd(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, bool out16, hipStream_t s) {
   launch_delta_ops<IO, NT>(a, l, vec, s);
   const int units = (a.P + 63) / 64;
-  const unsigned walk = (unsigned)((a.nseq * a.H + 7) / 8 * 8 * units);
+  const unsigned walk = walk_grid(a, units);
   const dim3 blocks((unsigned)l.nchunk, a.H);
   if (fast) {
-    launch_delta_walk<IO, NT, 1, true, true>(a, s);
+    launch_delta_walk<IO, NT, true, kKeepBlocks>(a, s);
     delta_back_kernel<IO, NT, true><<<walk, 256, 0, s>>>(a, units);
     delta_rows_grad_kernel<IO, NT, true><<<blocks, 512, 0, s>>>(a);
   } else {
-    launch_delta_walk<IO, NT, 1, false, true>(a, s);
+    launch_delta_walk<IO, NT, false, kKeepBlocks>(a, s);
     delta_back_kernel<IO, NT, false><<<walk, 256, 0, s>>>(a, units);
     delta_rows_grad_kernel<IO, NT, false><<<blocks, 512, 0, s>>>(a);
   }

@@ -130,6 +130,15 @@ CASES = [  # lens, H, G, P, N, dtype, options
     ((1,) * 40, 2, 1, 64, 128, "bf16", {}),
     ((1100, 1, 300), 2, 2, 64, 128, "bf16", dict(has=True)),
     ((900,), 1, 1, 64, 64, "f32", dict(has=True)),
+    # few heads: sequences of more than 16 blocks are cut into segments of eight at least
+    ((1024, 1025), 2, 1, 64, 128, "bf16", dict(has=True)),
+    ((1700, 40, 0, 1300, 64), 2, 1, 128, 128, "bf16", dict(behind=3)),
+    ((1200, 1), 1, 1, 17, 9, "bf16", dict(has=True, lead=1)),
+    ((1300,), 2, 1, 96, 192, "f32", dict(has=True)),
+    ((1100, 600), 1, 1, 256, 256, "bf16", dict(has=False)),
+    ((1111,), 3, 3, 80, 256, "f32", dict(has=True, lead=2)),
+    ((2900,), 1, 1, 32, 32, "f32", dict(state=False)),
+    ((1500, 1200), 2, 2, 64, 64, "bf16", dict(skip=((0, -1),), how=ref.How(norm=False), kstd=0.1)),
 ]
 
 
@@ -260,6 +269,27 @@ def test_non_finite_rows_stay_behind(ssm, dev, where, value):  # noqa: F811
     else:
         assert not torch.isfinite(head0).any() and not torch.isfinite(p.state[mine, 0]).any()
         assert torch.equal(p.y[:150, 64:], clean[:150, 64:])  # the other head has a group of its own
+
+
+@pytest.mark.parametrize("where", ["k", "v", "dt"])
+def test_non_finite_rows_in_a_cut_sequence(ssm, dev, where):  # noqa: F811
+    """The same where the sequence is walked in segments: what lies before the token, and
+    in other sequences, is as without it."""
+    p = Delta(dev, (1500, 1100), 2, 2, 64, 64, "bf16", seed=19, has=True, spare=0)
+    p.run(ssm)
+    clean, end = p.y.clone(), p.state.clone()
+    p.load()
+    hit = 700
+    p.t[where][hit, 0] = float("nan")
+    p.run(ssm)
+    mine, other = int(p.slots[0]), int(p.slots[1])
+    assert torch.equal(p.y[:hit], clean[:hit]) and torch.equal(p.y[1500:], clean[1500:])
+    assert torch.equal(p.state[other], end[other])
+    if where == "v":
+        assert not torch.isfinite(p.y[hit:1500, 0]).any() and torch.equal(p.y[:1500, 1:], clean[:1500, 1:])
+    else:
+        assert not torch.isfinite(p.y[hit:1500, :64]).any() and torch.equal(p.y[:1500, 64:], clean[:1500, 64:])
+        assert not torch.isfinite(p.state[mine, 0]).any()
 
 
 def test_outliers_keep_their_neighbours(ssm, dev):  # noqa: F811
