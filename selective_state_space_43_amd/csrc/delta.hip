@@ -156,6 +156,51 @@ __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaArgs a) {
 
 // ---------------------------------------------------------------- a block's matrices
 
+// The same for up to 64 sequences by one wave, which has nobody to meet.
+__global__ void __launch_bounds__(64) delta_plan_few_kernel(const DeltaArgs a) {
+  const int i = threadIdx.x, tokens = (int)a.tokens, nseq = (int)a.nseq;
+  const bool in = i < nseq;
+  const int start = max(0, min(a.cu[0], tokens));
+  const int64_t slot = in && a.slots ? a.slots[i] : i;
+  const bool resume = in && a.has && a.has[i];
+  int end = in ? max(start, min(a.cu[i + 1], tokens)) : start;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(end, d, 64);
+    if (i >= d) end = max(end, o);
+  }
+  const int before = __shfl_up(end, 1, 64), begin = i ? before : start;
+  int n[4] = {0, 0, 0, 0}, at[4];  // blocks, segments, segments of cut sequences, cut sequences
+  if (in && (!a.state || (slot >= 0 && slot < a.nslots))) {  // else padding
+    n[0] = (end - begin + kQ - 1) / kQ;
+    n[1] = n[0] > 2 * a.seg_len ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
+    n[2] = n[1] > 1 ? n[1] : 0;
+    n[3] = n[1] > 1;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    int x = n[k];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(x, d, 64);
+      if (i >= d) x += o;
+    }
+    at[k] = x - n[k];
+  }
+  if (n[3]) a.cuts[at[3]] = {(int)slot, at[2], n[1], resume};
+  if (i == 63) *a.head = {at[0] + n[0], at[1] + n[1], at[3] + n[3], start, end};
+  for (int k = 0; k < nseq; ++k) {
+    const int nb = __shfl(n[0], k, 64), of = __shfl(n[1], k, 64), t0 = __shfl(begin, k, 64), t1 = __shfl(end, k, 64);
+    const int c0 = __shfl(at[0], k, 64), s0 = __shfl(at[1], k, 64), split = __shfl(at[2], k, 64);
+    const int sl = __shfl((int)slot, k, 64), re = __shfl((int)resume, k, 64);
+    for (int c = i; c < nb; c += 64) a.chunks[c0 + c] = {t0 + c * kQ, min(t1, t0 + (c + 1) * kQ)};
+    for (int j = i; j < of; j += 64) {
+      const int lo = (int)((int64_t)nb * j / of), hi = (int)((int64_t)nb * (j + 1) / of);
+      a.segs[s0 + j] = {sl, t0 + lo * kQ, min(t1, t0 + hi * kQ), c0 + lo, re, of > 1 ? split + j : -1, j == of - 1};
+    }
+  }
+}
+
 // log(1 + e^x) and 1 / (1 + e^-x) as exactly as float32 has them: a step's rounding goes into
 // the decays of all tokens behind it, and the sums dA, ddt_bias cancel
 __device__ __forceinline__ float exact_softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
@@ -227,10 +272,18 @@ __device__ __forceinline__ float ex2(double x) {
   const float hi = (float)x;
   return ex2(hi) * fmaf((float)(x - (double)hi), kLn2, 1.0f);
 }
+// The largest of LN lanes' values, none of them negative.
 template <int LN>
 __device__ __forceinline__ float lane_max(float v) {
-#pragma unroll
-  for (int d = 1; d < LN; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  auto take = [&](int o) { v = fmaxf(v, __int_as_float(o)); };
+  take(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
+  take(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));
+  if constexpr (LN >= 8) take(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
+  if constexpr (LN >= 16) take(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
+  if constexpr (LN >= 32) {
+    const u2 w = __builtin_bit_cast(u2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+    v = fmaxf(__uint_as_float(w.x), __uint_as_float(w.y));
+  }
   return v;
 }
 __device__ __forceinline__ f4 mfma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
@@ -266,8 +319,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
   constexpr int lds = O::group > 2 * kQ * LD * 4 ? O::group : 2 * kQ * LD * 4;
   __shared__ __align__(16) char s_buf[lds];
   __shared__ float s_len[2][kQ];
-  __shared__ __align__(16) double s_cum[kQ];
-  __shared__ float s_b[kQ];
+  __shared__ float s_g[kQ], s_wc[kQ], s_wl[kQ], s_wm[kQ];  // G; the columns' and the rows' factors of L, M
   __shared__ int s_bad;
   const int c = blockIdx.x, h = blockIdx.y, g = h / a.per, N = a.N;
   if (c >= a.head->nchunk) return;
@@ -277,30 +329,56 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
   double gr = 0.0;
   float b = 0.0f;
   if (tt == 0 && lane < cnt) row_scalars<IO>(a, ck.r0 + lane, h, gr, b);
-  // ---- rows of k and q: scaled, their lengths
+  // ---- rows of k and q, all on their way at once: scaled, their lengths
+  constexpr int E = 16 / sizeof(IO), IT = kQ / RW, PV = 8 / E;
+  Vec<IO, E> in[VEC ? 2 : 1][VEC ? IT : 1][PV];
+  const int part = tid % LN;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int64_t r = ck.r0 + min(i * RW + tid / LN, cnt - 1);
+        const int64_t at = r * (which ? a.qs : a.ks) + (int64_t)g * N;
+#pragma unroll
+        for (int v = 0; v < PV; ++v) in[which][i][v].load(which ? a.q : a.k, at + min(8 * part + E * v, N - E));
+      }
+  }
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-#pragma unroll 4
-    for (int i0 = 0; i0 < kQ; i0 += RW) {
-      const int i = i0 + tid / LN, p = tid % LN;
-      float x[8], m = 0.0f, ss = 0.0f;
-      load8<IO, VEC>(which ? a.q : a.k, (int64_t)(ck.r0 + min(i, cnt - 1)) * (which ? a.qs : a.ks) + (int64_t)g * N + 8 * p,
-                     i < cnt ? N - 8 * p : 0, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, finite(x[j]) ? fabsf(x[j]) : 0.0f);
+    for (int ii = 0; ii < IT; ++ii) {
+      const int i = ii * RW + tid / LN;
+      float x[8], ss = 0.0f;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x[j] = i < cnt && 8 * part + j / E * E < N ? in[which][ii][j / E].get(j % E) : 0.0f;
+      } else {
+        load8<IO, false>(which ? a.q : a.k, (int64_t)(ck.r0 + min(i, cnt - 1)) * (which ? a.qs : a.ks) + (int64_t)g * N + 8 * part,
+                         i < cnt ? N - 8 * part : 0, x);
+      }
+      float m = max3_nan(max3_nan(max3_nan(max3_nan(0.0f, x[0], x[1]), x[2], x[3]), x[4], x[5]), x[6], x[7]);
+      if (!finite(m)) {
+        rarely();
+        m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, finite(x[j]) ? fabsf(x[j]) : 0.0f);
+      }
       const int e = shift_for(lane_max<LN>(m));
+      const float f = two(e);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = __builtin_amdgcn_ldexpf(x[j], e);
+        x[j] *= f;
         ss = fmaf(x[j], x[j], ss);
       }
       ss = lane_sum<LN>(ss);
       // x / sqrt(|x|^2 + eps) from the scaled row
-      if (p == 0)
+      if (part == 0)
         s_len[which][i] = (a.norm ? rsqrtf(ss + __builtin_amdgcn_ldexpf(a.eps, 2 * e)) : two(-e)) * (which ? a.scale : 1.0f);
       h8 hi, lo;
       pieces(x, hi, lo);
-      char* to = s_buf + which * O::kq + O::part(i, p);
+      char* to = s_buf + which * O::kq + O::part(i, part);
       *reinterpret_cast<h8*>(to) = hi;
       if constexpr (KP == 2) *reinterpret_cast<h8*>(to + O::piece) = lo;
     }
@@ -350,9 +428,13 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
     float* sc = reinterpret_cast<float*>(out + O::sc);
     if (tt == 0) {
       const double cum = wave_scan(gr), tot = lane63(cum);
-      s_cum[lane] = cum;
-      s_b[lane] = b;
       const float e = ex2(cum), lk = s_len[0][lane], lq = s_len[1][lane];
+      // what float32 leaves off the running sum goes with the rows and columns, to first order
+      const float gh = (float)cum, gl = (float)(cum - (double)gh) * kLn2;
+      s_g[lane] = gh;
+      s_wc[lane] = lk * (1.0f - gl);
+      s_wl[lane] = b * lk * (1.0f + gl);
+      s_wm[lane] = lq * (1.0f + gl);
       sc[64 * kS1 + lane] = e * lk;
       sc[64 * kBeta + lane] = b;
       sc[64 * kS2 + lane] = e * lq;
@@ -366,24 +448,31 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
     }
     __syncthreads();  // k and q have been read, too
     // ---- L into LDS, M out
-    const double ci = s_cum[row];
-    const float bi = s_b[row], lki = s_len[0][row], lqi = s_len[1][row];
+    const float gi = s_g[row], wl = s_wl[row], wm = s_wm[row];
     float mv[2][8], mx = 0.0f;
     bool bad = false;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       if (kb > (tt >> 1)) break;
-      float lv[8];
+      float lv[8], ml = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int col = 32 * kb + 8 * q4 + e;
-        const float w = ex2((float)(ci - s_cum[col])) * s_len[0][col];
-        const float l = bi * lki * (w * kk[kb][e >> 2][e & 3]);
-        const float m = lqi * (w * qk[kb][e >> 2][e & 3]);
-        lv[e] = col < row ? l : 0.0f;
-        mv[kb][e] = col <= row ? m : 0.0f;
-        if (!finite(lv[e])) bad = true, lv[e] = 0.0f;
-        mx = finite(mv[kb][e]) ? fmaxf(mx, fabsf(mv[kb][e])) : mx;
+        const float w = ex2(gi - s_g[col]) * s_wc[col];
+        const float l = wl * (w * kk[kb][e >> 2][e & 3]), m = wm * (w * qk[kb][e >> 2][e & 3]);
+        lv[e] = kb < (tt >> 1) || col < row ? l : 0.0f;
+        mv[kb][e] = kb < (tt >> 1) || col <= row ? m : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        ml = max3_nan(ml, lv[e], lv[e + 1]);
+        mx = max3_nan(mx, mv[kb][e], mv[kb][e + 1]);
+      }
+      if (!finite(ml)) {
+        rarely();
+        bad = true;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) lv[e] = finite(lv[e]) ? lv[e] : 0.0f;
       }
       f4* to = reinterpret_cast<f4*>(s_l + row * LD + 32 * kb + 8 * q4);
       to[0] = *reinterpret_cast<const f4*>(lv);
@@ -391,6 +480,15 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
     }
     if (bad) atomicMin(&s_bad, row);
     {
+      if (!finite(mx)) {
+        rarely();
+        mx = 0.0f;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+          if (kb <= (tt >> 1))
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = finite(mv[kb][e]) ? fmaxf(mx, fabsf(mv[kb][e])) : mx;
+      }
       const int sh = shift_for(row_max(mx));
       const float f = two(sh);
       if (q4 == 0) sc[64 * kFM + row] = two(-sh);
@@ -1406,43 +1504,71 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
 }
 
 // The states entering the segments of a cut sequence, s <- X + s Y one after another: eight
-// rows (channels) of a head a workgroup, a thread a state.
-__global__ void __launch_bounds__(256) delta_join_kernel(const DeltaArgs a) {
-  constexpr int R = 8;
-  __shared__ __align__(16) float s_s[kMaxN][R];
+// rows (channels) of a head a workgroup.  Thread (j, n) has state n and a run of the rows of Y,
+// whose next segment's come while this one's are used; the runs are added in order.
+template <int NT>
+__global__ void __launch_bounds__(1024) delta_join_kernel(const DeltaArgs a) {
+  constexpr int R = 8, NP = 16 * NT, JG = 1024 / NP, JN = NP / JG, AH = JN < 16 ? JN : 16;
+  __shared__ __align__(16) float s_s[NP][R], s_p[JG][R][NP];
   if ((int)blockIdx.z >= a.head->ncut) return;
   const DeltaCut ct = a.cuts[blockIdx.z];
-  const int h = blockIdx.y, N = a.N, P = a.P, n = threadIdx.x, p0 = blockIdx.x * R;
-  const bool on = n < N;
-  float s[R];
+  const int h = blockIdx.y, N = a.N, P = a.P, n = threadIdx.x % NP, jg = threadIdx.x / NP, p0 = blockIdx.x * R;
+  const int64_t step = local_size(a);
+  float* l = a.local + ct.split * step + (int64_t)h * N * (N + P);
+  // thread (r, n) keeps row r of the state where JG > r, else it has more than one
+  constexpr int RK = JG >= R ? 1 : R / JG;
+  float s[RK], m[AH];
+  auto fetch = [&](const float* y, int j0) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    s[r] = ct.resume && on && p0 + r < P ? a.state[(((int64_t)ct.slot * a.H + h) * P + p0 + r) * N + n] : 0.0f;
-  for (int k = 0; k < ct.nseg; ++k) {
-    float* l = a.local + (ct.split + k) * local_size(a) + (int64_t)h * N * (N + P);
-    float x[R];
+    for (int j = 0; j < AH; ++j) m[j] = y[(int64_t)min(jg * JN + j0 + j, N - 1) * N + min(n, N - 1)];
+  };
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool in = on && p0 + r < P;
-      x[r] = in && k + 1 < ct.nseg ? l[(int64_t)(p0 + r) * N + n] : 0.0f;
-      if (in) l[(int64_t)(p0 + r) * N + n] = s[r];
+  for (int k = 0; k < RK; ++k) {
+    const int r = jg + k * JG;
+    s[k] = ct.resume && r < R && n < N && p0 + r < P ? a.state[(((int64_t)ct.slot * a.H + h) * P + p0 + r) * N + n] : 0.0f;
+  }
+  fetch(l + (int64_t)P * N, 0);
+  for (int k = 0; k < ct.nseg; ++k, l += step) {
+    const bool more = k + 1 < ct.nseg;
+    float x[RK];
+#pragma unroll
+    for (int i = 0; i < RK; ++i) {
+      const int r = jg + i * JG;
+      const bool in = r < R && n < N && p0 + r < P;
+      x[i] = in && more ? l[(int64_t)(p0 + r) * N + n] : 0.0f;
+      if (in) l[(int64_t)(p0 + r) * N + n] = s[i];
+      if (r < R) s_s[n][r] = s[i];
     }
-    if (k + 1 == ct.nseg) break;
+    if (!more) break;
     __syncthreads();
-    if (on)
+    float acc[R] = {};
+    const float* y = l + (int64_t)P * N;
 #pragma unroll
-      for (int r = 0; r < R; ++r) s_s[n][r] = s[r];
-    __syncthreads();
-    const float* y = l + (int64_t)P * N + (on ? n : 0);
-#pragma unroll 16
-    for (int j = 0; j < N; ++j) {
-      const float m = y[(int64_t)j * N];
-      const f4 lo = *reinterpret_cast<const f4*>(s_s[j]), hi = *reinterpret_cast<const f4*>(s_s[j] + 4);
+    for (int j0 = 0; j0 < JN; j0 += AH) {
+      float v[AH];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = fmaf(lo[r], m, x[r]), x[r + 4] = fmaf(hi[r], m, x[r + 4]);
+      for (int j = 0; j < AH; ++j) v[j] = m[j];
+      if (j0 + AH < JN) fetch(y, j0 + AH);
+      else if (k + 2 < ct.nseg) fetch(y + step, 0);
+#pragma unroll
+      for (int j = 0; j < AH; ++j) {
+        const int at = jg * JN + j0 + j;  // past the last state: zeros in s
+        const f4 lo = *reinterpret_cast<const f4*>(s_s[at]), hi = *reinterpret_cast<const f4*>(s_s[at] + 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] = fmaf(lo[r], v[j], acc[r]), acc[r + 4] = fmaf(hi[r], v[j], acc[r + 4]);
+      }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = x[r];
+    for (int r = 0; r < R; ++r) s_p[jg][r][n] = acc[r];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RK; ++i) {
+      const int r = jg + i * JG;
+      if (r < R)
+#pragma unroll
+        for (int q = 0; q < JG; ++q) x[i] += s_p[q][r][n];
+      s[i] = n < N ? x[i] : 0.0f;
+    }
   }
 }
 
@@ -2367,8 +2493,8 @@ int check_state(const DeltaArgs& a, const DeltaCall& c) {
 }
 
 constexpr int64_t kCUs = 256;
-// A cut sequence is walked twice, once for twice as many columns: cut where that leaves at
-// least four segments a sequence, of eight blocks at least.
+// A cut sequence is walked twice, once for twice as many columns: cut where the card takes four
+// segments at once at least, and more than there are sequences, of eight blocks at least.
 constexpr int64_t kMinCut = 4, kMinSeg = 8;
 
 struct DeltaLayout {
@@ -2395,7 +2521,7 @@ DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int
   // a walk's workgroups are 64 channels of a head: segments for as many as the card has CUs
   const int64_t at_once = kCUs / (H * ((P + 63) / 64)), blocks = (tokens + kQ - 1) / kQ;
   int64_t len = (int64_t)1 << 24;
-  if (!bwd && at_once >= kMinCut) {
+  if (!bwd && at_once >= kMinCut && at_once > nseq) {
     len = (blocks + at_once - 1) / at_once;
     if (len < kMinSeg) len = kMinSeg;
   }
@@ -2448,7 +2574,8 @@ template <typename IO, int NT>
 void launch_delta_ops(const DeltaArgs& a, const DeltaLayout& l, bool vec, hipStream_t s) {
   static_assert(Ops<IO, NT>::group == 2 * kQ * NT * 32 * Ops<IO, NT>::KP && Ops<IO, NT>::head == 4 * kTri + kScalars &&
                 Keep<IO, NT>::block == 128 * NT * 32 + 4 * 32 * 128, "as in delta_layout");
-  delta_plan_kernel<<<1, 1024, 0, s>>>(a);
+  if (a.nseq <= 64) delta_plan_few_kernel<<<1, 64, 0, s>>>(a);
+  else delta_plan_kernel<<<1, 1024, 0, s>>>(a);
   const dim3 grid((unsigned)l.nchunk, a.H);
   if (vec) delta_ops_kernel<IO, NT, true><<<grid, 256, 0, s>>>(a);
   else delta_ops_kernel<IO, NT, false><<<grid, 256, 0, s>>>(a);
@@ -2470,7 +2597,7 @@ void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast,
     constexpr bool FAST = decltype(f)::value;
     if (l.nsplit) {
       launch_delta_walk<IO, NT, FAST, kSum>(a, s);
-      delta_join_kernel<<<dim3((a.P + 7) / 8, a.H, (unsigned)l.ncut), 256, 0, s>>>(a);
+      delta_join_kernel<NT><<<dim3((a.P + 7) / 8, a.H, (unsigned)l.ncut), 1024, 0, s>>>(a);
     }
     if constexpr (Pair<IO, NT>::fits) {
       const int units = (a.P + 63) / 64;

@@ -130,6 +130,8 @@ CASES = [  # lens, H, G, P, N, dtype, options
     ((1,) * 40, 2, 1, 64, 128, "bf16", {}),
     ((1100, 1, 300), 2, 2, 64, 128, "bf16", dict(has=True)),
     ((900,), 1, 1, 64, 64, "f32", dict(has=True)),
+    ((3, 0, 70) * 30, 2, 1, 32, 32, "bf16", dict(behind=2)),  # more sequences than one wave plans
+    ((2,) * 1030 + (100,), 1, 1, 16, 16, "f32", dict(skip=((5, -1),))),
     # few heads: sequences of more than 16 blocks are cut into segments of eight at least
     ((1024, 1025), 2, 1, 64, 128, "bf16", dict(has=True)),
     ((1700, 40, 0, 1300, 64), 2, 1, 128, 128, "bf16", dict(behind=3)),
