@@ -611,6 +611,12 @@ __device__ __forceinline__ void send(const char* from, char* to, int first = 0) 
                    "s"(from + i * WV * 1024)
                    : "memory");  // the compiler sets m0 itself before each of its own uses
 }
+// 16 bytes a lane from the lane's own address, one behind the other from `to` on.
+__device__ __forceinline__ void send_lane(const void* from, char* to) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::
+                   "s"((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)to), "v"(from)
+               : "memory");
+}
 // All of this wave's memory accesses but the last LEFT have ended (a wait that the compiler sees).
 template <int LEFT = 0>
 __device__ __forceinline__ void landed() {
@@ -629,11 +635,13 @@ __device__ __forceinline__ bool column_shifts(const f4 (&v)[NV][PT], int (&sh)[P
   bool bad = false;
 #pragma unroll
   for (int e = 0; e < PT; ++e) {
-    mx[e] = 0.0f;
+    float m0 = 0.0f, m1 = 0.0f;  // by turns: a largest value does not wait for the one before it
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int r = 0; r < 4; r += 2) mx[e] = max3_nan(mx[e], v[k][e][r], v[k][e][r + 1]);
+    for (int k = 0; k < NV; ++k) {
+      m0 = max3_nan(m0, v[k][e][0], v[k][e][1]);
+      m1 = max3_nan(m1, v[k][e][2], v[k][e][3]);
+    }
+    mx[e] = max3_nan(0.0f, m0, m1);
     bad = bad || !finite(mx[e]);
   }
   bad = __any(bad);
@@ -1170,10 +1178,11 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
 }
 
 // The same walk by pairs of waves of 16 channels: one holds the states and goes k S, R, U, next
-// state; the other, a step behind, takes the state's pieces and U from LDS and makes y. What
-// one wave did one after another (860 vector instructions a block, 3.7 us) two do side by side.
-// k, T, M and the scalars of the next block come while this block's are used; q has one place,
-// free from the second meeting on.
+// state; the other, a step behind, takes the state's pieces and U from LDS and makes y, and
+// sends what the next block needs: k, T, M and the scalars while this block's are used; q and v,
+// which have one place each, from the second meeting on. What one wave did one after another
+// (860 vector instructions a block, 3.7 us) two do side by side.
+// VL: v comes through LDS, rows of 64 channels (bf16, rows on 16 bytes), else lane by lane.
 template <typename IO, int NT>
 struct Pair {
   using O = Ops<IO, NT>;
@@ -1181,11 +1190,15 @@ struct Pair {
   static constexpr int q = 2 * kb, s = q + O::kq;          // q; the states' pieces of four waves
   static constexpr int sw = 2 * (NT / 2) * 1024;           // of one wave
   static constexpr int u = s + 4 * sw, f = u + 4 * 4096;   // U; the states' shifts
-  static constexpr int bytes = f + 4 * 64;
+  static constexpr int v = f + 4 * 64, bytes = v + (sizeof(IO) == 2 ? kQ * 128 : 0);
   static constexpr bool fits = bytes <= 160 * 1024;
 };
 
-template <typename IO, int NT, bool FAST>
+// where 16-byte part c of row r of v lies (and which part lies at c): rows that are read
+// together are in different banks
+__device__ __forceinline__ int v_turn(int r, int c) { return c ^ ((r >> 1 & 1) | (r >> 3 & 3) << 1); }
+
+template <typename IO, int NT, bool FAST, bool VL>
 __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int units) {
   using O = Ops<IO, NT>;
   using L = Pair<IO, NT>;
@@ -1207,17 +1220,28 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
   auto stage_block = [&](int b) {
     const int64_t c = sq.c0 + b;
     char* to = s_op + (b & 1) * L::kb;
-    send<8, O::kq>(a.gops + (c * a.G + g) * O::group, to);
-    send<8, O::head>(a.hops + (c * a.H + h) * O::head, to + O::kq);
+    send<4, O::kq>(a.gops + (c * a.G + g) * O::group, to, 4);
+    send<4, O::head>(a.hops + (c * a.H + h) * O::head, to + O::kq, 4);
   };
   char* const s_s = s_op + L::s + pw * L::sw + lane * 16;
   f4* const s_u = reinterpret_cast<f4*>(s_op + L::u + pw * 4096) + lane;
   float* const s_f = reinterpret_cast<float*>(s_op + L::f) + 16 * pw;
-  if (nc > 0) stage_block(0);
-
   if (wave >= 4) {
     // ---- y
-    auto stage_q = [&](int b) { send<4, O::kq>(a.gops + ((sq.c0 + (int64_t)b) * a.G + g) * O::group + O::kq, s_op + L::q, 4); };
+    if (nc > 0) stage_block(0);
+    // q, and v: eight rows of the 64 channels an access, 16-byte parts of a row in turned places
+    auto stage_q = [&](int b) {
+      send<4, O::kq>(a.gops + ((sq.c0 + (int64_t)b) * a.G + g) * O::group + O::kq, s_op + L::q, 4);
+      if constexpr (VL) {
+        const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 32 * i + 8 * pw + (lane >> 3), ch = 64 * unit + 8 * v_turn(r, lane & 7);
+          const IO* from = static_cast<const IO*>(a.v) + (int64_t)(r0 + min(r, cnt - 1)) * a.vs + h * P + min(ch, P - 8);
+          send_lane(from, s_op + L::v + (32 * i + 8 * pw) * 128);
+        }
+      }
+    };
     if (nc > 0) stage_q(0);
     const uint32_t y_own = (uint32_t)((8 * q4 * a.ys + col) * sizeof(IO));
     for (int b = 0; b < nc; ++b) {
@@ -1329,8 +1353,8 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
     }
     S[nt][0] = v;
   }
-  // v of a block's rows 32 kb + 8 q + j.  Whole blocks go by an address of the row, the
-  // same in all lanes, and the lane's own offset
+  // v of a block's rows 32 kb + 8 q + j, lane by lane.  Whole blocks go by an address of the
+  // row, the same in all lanes, and the lane's own offset
   IO raw[2][8];
   const uint32_t v_own = (uint32_t)((8 * q4 * a.vs + col) * sizeof(IO));
   auto fetch = [&](int b) {
@@ -1350,7 +1374,7 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
           raw[kb][j] = static_cast<const IO*>(a.v)[(r0 + min(32 * kb + 8 * q4 + j, cnt - 1)) * a.vs + col];
     }
   };
-  if (nc > 0 && on) fetch(0);
+  if (!VL && nc > 0 && on) fetch(0);
   for (int b = 0; b < nc; ++b) {
     const int cnt = min(sq.t1 - sq.t0 - b * kQ, kQ);
     const char* op = s_op + (b & 1) * L::kb;
@@ -1371,14 +1395,14 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
       }
       if (q4 == 0) s_f[i16] = fi;
     }
-    landed();
-    // v has come too: else the compiler would wait for it behind what is sent next
+    if constexpr (!VL) {
+      landed();
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(raw[kb][j]));
+        for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(raw[kb][j]));
+    }
     meet();  // this block's operands are there, and the state's pieces
-    if (b + 1 < nc) stage_block(b + 1);
     f4 u[4][1] = {};
     if (on) {
       // ---- R = b (v - e^G k S)
@@ -1398,6 +1422,18 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
           for (int tt = 0; tt < 4; ++tt) ks[tt][0] = mfma(ka[tt][KP - 1], shi[m], ks[tt][0]);
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) ks[tt][0] = mfma(ka[tt][0], shi[m], ks[tt][0]);
+      }
+      if constexpr (VL) {
+        // rows 32 kb + 8 q + {0 .. 3} and four on of the wave's 16 channels, transposed
+        const int r = 8 * q4 + (i16 >> 2), pt = 2 * pw + ((i16 & 3) >> 1), half = 8 * (i16 & 1);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const u2 x = read_tr(s_op + L::v + (32 * kb + r + 4 * k) * 128 + v_turn(32 * kb + r + 4 * k, pt) * 16 + half);
+            raw[kb][4 * k] = (IO)(x.x & 0xffff); raw[kb][4 * k + 1] = (IO)(x.x >> 16);
+            raw[kb][4 * k + 2] = (IO)(x.y & 0xffff); raw[kb][4 * k + 3] = (IO)(x.y >> 16);
+          }
       }
       if (cnt < kQ) {
         rarely();
@@ -1419,7 +1455,7 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
           ks[tt][0][r] = be[r] * fmaf(-(s1[r] * fi), ks[tt][0][r], v);
         }
       }
-      if (b + 1 < nc) fetch(b + 1);
+      if (!VL && b + 1 < nc) fetch(b + 1);
       // ---- U = T R.  What is not finite stays behind the first such row of its column:
       // 0 x Inf is not 0, so the products leave those rows out
       int first[1] = {kQ};
@@ -2591,7 +2627,7 @@ void launch_delta_walk(const DeltaArgs& a, hipStream_t s) {
 }
 
 template <typename IO, int NT>
-void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, hipStream_t s) {
+void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast, bool rows16, hipStream_t s) {
   launch_delta_ops<IO, NT>(a, l, vec, s);
   auto go = [&](auto f) {
     constexpr bool FAST = decltype(f)::value;
@@ -2601,7 +2637,13 @@ void launch_delta(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool fast,
     }
     if constexpr (Pair<IO, NT>::fits) {
       const int units = (a.P + 63) / 64;
-      delta_pair_kernel<IO, NT, FAST><<<walk_grid(a, units), 512, 0, s>>>(a, units);
+      if constexpr (FAST && sizeof(IO) == 2) {
+        if (rows16) {
+          delta_pair_kernel<IO, NT, FAST, true><<<walk_grid(a, units), 512, 0, s>>>(a, units);
+          return;
+        }
+      }
+      delta_pair_kernel<IO, NT, FAST, false><<<walk_grid(a, units), 512, 0, s>>>(a, units);
     } else {
       launch_delta_walk<IO, NT, FAST, kWalk>(a, s);
     }
@@ -2651,7 +2693,7 @@ void launch_delta_io(const DeltaArgs& a, const DeltaLayout& l, bool bwd, hipStre
   auto go = [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
     if (bwd) launch_delta_bwd<IO, NT>(a, l, vec, fast, on(a.dq, a.dqs, a.N, 16) && on(a.dk, a.dks, a.N, 16), s);
-    else launch_delta<IO, NT>(a, l, vec, fast, s);
+    else launch_delta<IO, NT>(a, l, vec, fast, on(a.v, a.vs, a.P, 16), s);
   };
   switch (l.nt) {
     case 2: go(std::integral_constant<int, 2>{}); break;
