@@ -239,11 +239,17 @@ __device__ __forceinline__ void row_scalars(const DeltaArgs& a, int64_t r, int h
 
 __device__ __forceinline__ int place_of(int tile, int r) { return 32 * (tile >> 1) + 8 * (r >> 2) + 4 * (tile & 1) + (r & 3); }
 
+// 16-byte parts of rows lie in an order of their own, so that what lanes read together is in
+// different banks: eight rows a part each (16 bytes a lane; the hardware takes lanes 0-3, 12-15,
+// 20-23, 24-27 together, so part q of rows 8 a and part q + 1 of other ones meet), and four rows of
+// four parts (transposed on the way).  0, 2, 3, 1 for row / 8 = 0, 1, 2, 3 keeps both apart.
+__device__ __forceinline__ int turn(int r) { return ((r >> 3 ^ r >> 4) & 1) << 1 | (r >> 4 & 1); }
+
 // T and M: columns 0 .. 31 of all rows, then columns 32 .. 63 of rows 32 .. 63, rows of 64
 // bytes; where 16-byte part c of row r of column block kb lies (as Ops::part()).
 constexpr int kTri = 6 * 1024;
 __device__ __forceinline__ int tri(int r, int kb, int c) {
-  return (kb ? 4096 + (r - 32) * 64 : r * 64) + ((c ^ (r >> 3 & 3)) << 4);
+  return (kb ? 4096 + (r - 32) * 64 : r * 64) + ((c ^ turn(r)) << 4);
 }
 
 // a head's scalars: places of 64 floats each
@@ -258,10 +264,10 @@ struct Ops {
   static constexpr int piece = kQ * RB, kq = KP * piece;  // one piece; all of k or q
   static constexpr int group = 2 * kq;
   static constexpr int t = 0, sc = 2 * kTri, m = sc + kScalars, head = m + 2 * kTri;
-  // where 16-byte part c of row r lies: rows that are read together are in different banks
+  // where 16-byte part c of row r lies
   __device__ static __forceinline__ int part(int r, int c) {
     constexpr int rows = RB >= 256 ? 1 : 256 / RB;  // rows in one round of the banks
-    const int f = rows == 1 ? (r & 3) | (r >> 3 & 3) << 2 : rows == 2 ? (r >> 1 & 1) | (r >> 3 & 3) << 1 : r >> 3 & 3;
+    const int f = rows == 1 ? (r & 3) << 2 | turn(r) : rows == 2 ? (r >> 1 & 1) << 2 | turn(r) : turn(r);
     return r * RB + ((c ^ f) << 4);
   }
 };
@@ -796,7 +802,7 @@ struct Keep {
   static constexpr int sp = 32 * Ops<IO, NT>::RB, tp = 32 * 128;  // a piece of 32 channels
   static constexpr int s = 0, ds = 2 * sp, u = 4 * sp, dr = u + 2 * tp, block = dr + 2 * tp;
   __device__ static __forceinline__ int part(int r, int c) {  // of U, dR: eight tokens
-    return r * 128 + ((c ^ ((r >> 1 & 1) | (r >> 3 & 3) << 1)) << 4);
+    return r * 128 + ((c ^ ((r >> 1 & 1) << 2 | turn(r))) << 4);
   }
 };
 __device__ __forceinline__ int padded(int P) { return (P + 31) & ~31; }
@@ -1194,9 +1200,8 @@ struct Pair {
   static constexpr bool fits = bytes <= 160 * 1024;
 };
 
-// where 16-byte part c of row r of v lies (and which part lies at c): rows that are read
-// together are in different banks
-__device__ __forceinline__ int v_turn(int r, int c) { return c ^ ((r >> 1 & 1) | (r >> 3 & 3) << 1); }
+// where 16-byte part c of row r of v lies (and which part lies at c)
+__device__ __forceinline__ int v_turn(int r, int c) { return c ^ ((r >> 1 & 1) << 2 | turn(r)); }
 
 template <typename IO, int NT, bool FAST, bool VL>
 __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int units) {
