@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
   constexpr int E = 16 / sizeof(IO), IT = kQ / RW, PV = 8 / E;
   Vec<IO, E> in[VEC ? 2 : 1][VEC ? IT : 1][PV];
   const int part = tid % LN;
+  const bool whole = cnt == kQ && N == 16 * NT;
   if constexpr (VEC) {
 #pragma unroll
     for (int which = 0; which < 2; ++which)
@@ -358,8 +359,10 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
       float x[8], ss = 0.0f;
       if constexpr (VEC) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[j] = i < cnt && 8 * part + j / E * E < N ? in[which][ii][j / E].get(j % E) : 0.0f;
+        for (int j = 0; j < 8; ++j) x[j] = in[which][ii][j / E].get(j % E);
+        if (!whole)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = i < cnt && 8 * part + j / E * E < N ? x[j] : 0.0f;
       } else {
         load8<IO, false>(which ? a.q : a.k, (int64_t)(ck.r0 + min(i, cnt - 1)) * (which ? a.qs : a.ks) + (int64_t)g * N + 8 * part,
                          i < cnt ? N - 8 * part : 0, x);
@@ -818,18 +821,27 @@ __device__ __forceinline__ int64_t local_size(const DeltaArgs& a) { return (int6
 // A workgroup walks a sequence's blocks with WV waves of 16 PT channels of one head each, the
 // states of a wave's channels in its accumulators.  DB: the next block's operands
 // come while this block's are used.
+template <typename IO, int NT, int MODE>
+struct WalkLds {
+  using O = Ops<IO, NT>;
+  static constexpr bool y = MODE == kWalk;
+  static constexpr int block = y ? O::group + O::head : O::kq + O::m;  // without y no q and no M
+  static constexpr bool twice = 2 * block <= 160 * 1024;               // the next block's operands beside
+  static constexpr int bytes = (twice ? 2 : 1) * block;
+};
+
 template <typename IO, int NT, int PT, int WV, bool FAST, int MODE>
-__global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, int units) {
+__device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int blk, char* s_op) {
   using O = Ops<IO, NT>;
   constexpr bool KEEP = MODE == kKeepBlocks, YES = MODE == kWalk;  // YES: y is asked for
   constexpr int KP = O::KP, GB = !YES ? O::kq : O::group, HB = !YES ? O::m : O::head, B = GB + HB, PB = 16 * PT;
-  constexpr bool DB = 2 * B <= 160 * 1024;
-  __shared__ __align__(16) char s_op[(DB ? 2 : 1) * B];
+  constexpr bool DB = WalkLds<IO, NT, MODE>::twice;
+  static_assert(B == WalkLds<IO, NT, MODE>::block, "one block");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i16 = lane & 15, q4 = lane >> 4;
   // eight dies take the workgroups by turns: the units of a head, and the heads of a
   // group where there are eight groups, share a die's cache
-  const int item = blockIdx.x / (8 * units) * 8 + blockIdx.x % 8, unit = blockIdx.x / 8 % units;
+  const int item = blk / (8 * units) * 8 + blk % 8, unit = blk / 8 % units;
   if (item >= a.nseg * a.H) return;
   const int s = item / a.H, g = item % a.G, h = g * a.per + item % a.H / a.G;
   const DeltaSeg sq = a.segs[s];  // garbage past the last one, which ends here
@@ -1181,6 +1193,12 @@ __global__ void __launch_bounds__(64 * WV) delta_walk_kernel(const DeltaArgs a, 
             if (n + r < N) at[r] = S[nt][e][r];
         }
       }
+}
+
+template <typename IO, int NT, bool FAST, int MODE>
+__global__ void __launch_bounds__(256) delta_walk_kernel(const DeltaArgs a, int units) {
+  __shared__ __align__(16) char s_op[WalkLds<IO, NT, MODE>::bytes];
+  delta_walk<IO, NT, 1, 4, FAST, MODE>(a, units, blockIdx.x, s_op);
 }
 
 // The same walk by pairs of waves of 16 channels: one holds the states and goes k S, R, U, next
@@ -1617,15 +1635,14 @@ __global__ void __launch_bounds__(1024) delta_join_kernel(const DeltaArgs a) {
 // one, dR and dv, with what delta_rows_grad_kernel takes from here.  Waves, channels and places
 // as in delta_walk_kernel.
 template <typename IO, int NT, bool FAST>
-__global__ void __launch_bounds__(256) delta_back_kernel(const DeltaArgs a, int units) {
+__device__ __forceinline__ void delta_back(const DeltaArgs& a, int units, int blk, char* s_op) {
   using O = Ops<IO, NT>;
   using KL = Keep<IO, NT>;
-  constexpr int KP = O::KP, B = O::group + O::head, WV = 4;
-  constexpr bool DB = 2 * B <= 160 * 1024;
-  __shared__ __align__(16) char s_op[(DB ? 2 : 1) * B];
+  constexpr int KP = O::KP, WV = 4, B = WalkLds<IO, NT, kWalk>::block;
+  constexpr bool DB = WalkLds<IO, NT, kWalk>::twice;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int i16 = lane & 15, q4 = lane >> 4;
-  const int item = blockIdx.x / (8 * units) * 8 + blockIdx.x % 8, unit = blockIdx.x / 8 % units;
+  const int item = blk / (8 * units) * 8 + blk % 8, unit = blk / 8 % units;
   if (item >= a.nseg * a.H) return;
   const int s = item / a.H, g = item % a.G, h = g * a.per + item % a.H / a.G;
   const DeltaSeg sq = a.segs[s];
@@ -1846,6 +1863,17 @@ __global__ void __launch_bounds__(256) delta_back_kernel(const DeltaArgs a, int 
         if (n + r < N) a.dh0[own + n + r] = S[nt][0][r];
     }
   }
+}
+
+// Both walks of a backward, which do not need each other: the first half of the grid goes
+// against the blocks' order, which takes longer (16 heads, four sequences: half the card each).
+template <typename IO, int NT, bool FAST>
+__global__ void __launch_bounds__(256) delta_both_kernel(const DeltaArgs a, int units) {
+  constexpr int back = WalkLds<IO, NT, kWalk>::bytes, keep = WalkLds<IO, NT, kKeepBlocks>::bytes;
+  __shared__ __align__(16) char s_op[back > keep ? back : keep];
+  const int half = gridDim.x / 2;
+  if ((int)blockIdx.x < half) delta_back<IO, NT, FAST>(a, units, blockIdx.x, s_op);
+  else delta_walk<IO, NT, 1, 4, FAST, kKeepBlocks>(a, units, blockIdx.x - half, s_op);
 }
 
 // ---------------------------------------------------------------- gradients of a block's rows and scalars
@@ -2628,7 +2656,7 @@ unsigned walk_grid(const DeltaArgs& a, int units) { return (unsigned)((a.nseg * 
 template <typename IO, int NT, bool FAST, int MODE>
 void launch_delta_walk(const DeltaArgs& a, hipStream_t s) {
   const int units = (a.P + 63) / 64 + (MODE == kSum ? (a.N + 63) / 64 : 0);
-  delta_walk_kernel<IO, NT, 1, 4, FAST, MODE><<<walk_grid(a, units), 256, 0, s>>>(a, units);
+  delta_walk_kernel<IO, NT, FAST, MODE><<<walk_grid(a, units), 256, 0, s>>>(a, units);
 }
 
 template <typename IO, int NT>
@@ -2664,12 +2692,10 @@ void launch_delta_bwd(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool f
   const unsigned walk = walk_grid(a, units);
   const dim3 blocks((unsigned)l.nchunk, a.H);
   if (fast) {
-    launch_delta_walk<IO, NT, true, kKeepBlocks>(a, s);
-    delta_back_kernel<IO, NT, true><<<walk, 256, 0, s>>>(a, units);
+    delta_both_kernel<IO, NT, true><<<2 * walk, 256, 0, s>>>(a, units);
     delta_rows_grad_kernel<IO, NT, true><<<blocks, 512, 0, s>>>(a);
   } else {
-    launch_delta_walk<IO, NT, false, kKeepBlocks>(a, s);
-    delta_back_kernel<IO, NT, false><<<walk, 256, 0, s>>>(a, units);
+    delta_both_kernel<IO, NT, false><<<2 * walk, 256, 0, s>>>(a, units);
     delta_rows_grad_kernel<IO, NT, false><<<blocks, 512, 0, s>>>(a);
   }
   // whole rows in 16-byte accesses, the states of the float32 sums too
