@@ -156,50 +156,72 @@ __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaArgs a) {
 
 // ---------------------------------------------------------------- a block's matrices
 
-// The same for up to 64 sequences by one wave, which has nobody to meet.
-__global__ void __launch_bounds__(64) delta_plan_few_kernel(const DeltaArgs a) {
-  const int i = threadIdx.x, tokens = (int)a.tokens, nseq = (int)a.nseq;
-  const bool in = i < nseq;
-  const int start = max(0, min(a.cu[0], tokens));
-  const int64_t slot = in && a.slots ? a.slots[i] : i;
-  const bool resume = in && a.has && a.has[i];
-  int end = in ? max(start, min(a.cu[i + 1], tokens)) : start;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(end, d, 64);
-    if (i >= d) end = max(end, o);
+// Inclusive sum or, of values that are not negative, largest so far over the wave's lanes.
+template <bool MAX>
+__device__ __forceinline__ int wave_scan_int(int v) {
+#define DELTA_STEP(ctrl, rows)                                                     \
+  {                                                                                \
+    const int o = __builtin_amdgcn_update_dpp(0, v, ctrl, rows, 0xf, rows == 0xf); \
+    v = MAX ? max(v, o) : v + o;                                                   \
   }
-  const int before = __shfl_up(end, 1, 64), begin = i ? before : start;
-  int n[4] = {0, 0, 0, 0}, at[4];  // blocks, segments, segments of cut sequences, cut sequences
-  if (in && (!a.state || (slot >= 0 && slot < a.nslots))) {  // else padding
-    n[0] = (end - begin + kQ - 1) / kQ;
-    n[1] = n[0] > 2 * a.seg_len ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
-    n[2] = n[1] > 1 ? n[1] : 0;
-    n[3] = n[1] > 1;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    int x = n[k];
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(x, d, 64);
-      if (i >= d) x += o;
-    }
-    at[k] = x - n[k];
-  }
-  if (n[3]) a.cuts[at[3]] = {(int)slot, at[2], n[1], resume};
-  if (i == 63) *a.head = {at[0] + n[0], at[1] + n[1], at[3] + n[3], start, end};
-  for (int k = 0; k < nseq; ++k) {
-    const int nb = __shfl(n[0], k, 64), of = __shfl(n[1], k, 64), t0 = __shfl(begin, k, 64), t1 = __shfl(end, k, 64);
-    const int c0 = __shfl(at[0], k, 64), s0 = __shfl(at[1], k, 64), split = __shfl(at[2], k, 64);
-    const int sl = __shfl((int)slot, k, 64), re = __shfl((int)resume, k, 64);
-    for (int c = i; c < nb; c += 64) a.chunks[c0 + c] = {t0 + c * kQ, min(t1, t0 + (c + 1) * kQ)};
-    for (int j = i; j < of; j += 64) {
-      const int lo = (int)((int64_t)nb * j / of), hi = (int)((int64_t)nb * (j + 1) / of);
-      a.segs[s0 + j] = {sl, t0 + lo * kQ, min(t1, t0 + hi * kQ), c0 + lo, re, of > 1 ? split + j : -1, j == of - 1};
-    }
-  }
+  DELTA_STEP(0x111, 0xf) DELTA_STEP(0x112, 0xf) DELTA_STEP(0x114, 0xf) DELTA_STEP(0x118, 0xf)
+  DELTA_STEP(0x142, 0xa) DELTA_STEP(0x143, 0xc)
+#undef DELTA_STEP
+  return v;
 }
+
+// The plan of up to 64 sequences, lane s sequence s: a launch of its own would take a fifth of
+// a short prompt's time.  Every wave that asks has it for itself; one writes the tables for
+// the kernels behind.
+constexpr int kFew = 64;
+struct FewPlan {
+  int start, begin, end, n[4], at[4];  // n, at: blocks, segments, segments of cut sequences, cut sequences, and those before
+  int slot;
+  bool resume;
+  __device__ __forceinline__ explicit FewPlan(const DeltaArgs& a) {
+    const int i = threadIdx.x & 63, tokens = (int)a.tokens;
+    const bool in = i < (int)a.nseq;
+    start = max(0, min(a.cu[0], tokens));
+    const int64_t sl = in && a.slots ? a.slots[i] : i;
+    slot = (int)sl;
+    resume = in && a.has && a.has[i];
+    end = wave_scan_int<true>(in ? max(start, min(a.cu[i + 1], tokens)) : start);
+    begin = __shfl_up(end, 1, 64);
+    begin = i ? begin : start;
+    n[0] = n[1] = n[2] = n[3] = 0;
+    if (in && (!a.state || (sl >= 0 && sl < a.nslots))) {  // else padding
+      n[0] = (end - begin + kQ - 1) / kQ;
+      n[1] = n[0] > 2 * a.seg_len ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
+      n[2] = n[1] > 1 ? n[1] : 0;
+      n[3] = n[1] > 1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) at[k] = wave_scan_int<false>(n[k]) - n[k];
+  }
+  // block c of all; no rows where there is none
+  __device__ __forceinline__ DeltaChunk chunk(int c) const {
+    const uint64_t mine = __ballot(c >= at[0] && c < at[0] + n[0]);
+    if (!mine) return {0, 0};
+    const int k = __ffsll((unsigned long long)mine) - 1;
+    const int r0 = __builtin_amdgcn_readlane(begin, k) + (c - __builtin_amdgcn_readlane(at[0], k)) * kQ;
+    return {r0, min(__builtin_amdgcn_readlane(end, k), r0 + kQ)};
+  }
+  __device__ __forceinline__ void write(const DeltaArgs& a) const {
+    const int i = threadIdx.x & 63;
+    if (n[3]) a.cuts[at[3]] = {slot, at[2], n[1], resume};
+    if (i == 63) *a.head = {at[0] + n[0], at[1] + n[1], at[3] + n[3], start, end};
+    for (int k = 0; k < (int)a.nseq; ++k) {
+      auto of_k = [&](int v) { return __builtin_amdgcn_readlane(v, k); };
+      const int nb = of_k(n[0]), of = of_k(n[1]), t0 = of_k(begin), t1 = of_k(end), c0 = of_k(at[0]), s0 = of_k(at[1]);
+      const int split = of_k(at[2]), sl = of_k(slot), re = of_k((int)resume);
+      for (int c = i; c < nb; c += 64) a.chunks[c0 + c] = {t0 + c * kQ, min(t1, t0 + (c + 1) * kQ)};
+      for (int j = i; j < of; j += 64) {
+        const int lo = (int)((int64_t)nb * j / of), hi = (int)((int64_t)nb * (j + 1) / of);
+        a.segs[s0 + j] = {sl, t0 + lo * kQ, min(t1, t0 + hi * kQ), c0 + lo, re, of > 1 ? split + j : -1, j == of - 1};
+      }
+    }
+  }
+};
 
 // log(1 + e^x) and 1 / (1 + e^-x) as exactly as float32 has them: a step's rounding goes into
 // the decays of all tokens behind it, and the sums dA, ddt_bias cancel
@@ -328,10 +350,19 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) d
   __shared__ float s_g[kQ], s_wc[kQ], s_wl[kQ], s_wm[kQ];  // G; the columns' and the rows' factors of L, M
   __shared__ int s_bad;
   const int c = blockIdx.x, h = blockIdx.y, g = h / a.per, N = a.N;
-  if (c >= a.head->nchunk) return;
-  const DeltaChunk ck = a.chunks[c];
-  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, q4 = lane >> 4, cnt = ck.r1 - ck.r0;
+  const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, q4 = lane >> 4;
   const int tt = __builtin_amdgcn_readfirstlane(tid >> 6);
+  DeltaChunk ck;
+  if (a.nseq <= kFew) {
+    const FewPlan plan(a);
+    if (c == 0 && h == 0 && tt == 3) plan.write(a);
+    ck = plan.chunk(c);
+    if (ck.r1 == ck.r0) return;
+  } else {
+    if (c >= a.head->nchunk) return;
+    ck = a.chunks[c];
+  }
+  const int cnt = ck.r1 - ck.r0;
   double gr = 0.0;
   float b = 0.0f;
   if (tt == 0 && lane < cnt) row_scalars<IO>(a, ck.r0 + lane, h, gr, b);
@@ -2346,33 +2377,36 @@ __global__ void __launch_bounds__(256) delta_qk_grad_kernel(const DeltaArgs a) {
   }
 }
 
-// dA and ddt_bias: one workgroup a head, blocks in runs of a fixed order
-__global__ void __launch_bounds__(256) delta_sum_kernel(const DeltaArgs a) {
-  __shared__ double red[2][256];
-  const int h = blockIdx.x, t = threadIdx.x, nc = a.head->nchunk;
-  double s0 = 0.0, s1 = 0.0;
-  for (int c = t; c < nc; c += 256) {
-    s0 += a.part[((int64_t)c * a.H + h) * 2];
-    s1 += a.part[((int64_t)c * a.H + h) * 2 + 1];
-  }
-  red[0][t] = s0;
-  red[1][t] = s1;
-  __syncthreads();
-  if (t < 2) {
-    double s = 0.0;
-    for (int k = 0; k < 256; ++k) s += red[t][k];
-    float* out = t ? a.ddt_bias : a.dA;
-    if (out) out[h] = (float)s;
-  }
-}
-
-// rows of no sequence have no gradients
+// dA and ddt_bias, one workgroup a head, blocks in runs of a fixed order; behind these
+// workgroups, zeros for the rows of no sequence.
 template <typename IO>
-__global__ void __launch_bounds__(256) delta_zero_kernel(const DeltaArgs a) {
+__global__ void __launch_bounds__(256) delta_rest_kernel(const DeltaArgs a) {
+  __shared__ double red[2][4];
+  const int h = blockIdx.x, t = threadIdx.x, nc = a.head->nchunk;
+  if (h < a.H) {
+    if (!a.dA && !a.ddt_bias) return;
+    double s[2] = {0.0, 0.0};
+    for (int c = t; c < nc; c += 256) {
+      const f2 p = *reinterpret_cast<const f2*>(a.part + ((int64_t)c * a.H + h) * 2);
+      s[0] += (double)p.x;
+      s[1] += (double)p.y;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      s[k] = lane63(wave_scan(s[k]));
+      if ((t & 63) == 0) red[k][t >> 6] = s[k];
+    }
+    __syncthreads();
+    if (t < 2) {
+      float* out = t ? a.ddt_bias : a.dA;
+      if (out) out[h] = (float)(red[t][0] + red[t][1] + red[t][2] + red[t][3]);
+    }
+    return;
+  }
   const int first = a.head->first, last = a.head->last;
   const int64_t gn = (int64_t)a.G * a.N, hp = (int64_t)a.H * a.P, wide = 2 * gn + hp + 2 * a.H;
-  const int64_t rows = a.tokens - (last - first);
-  for (int64_t u = blockIdx.x * 256ll + threadIdx.x; u < rows * wide; u += gridDim.x * 256ll) {
+  const int64_t rows = a.tokens - (last - first), step = (gridDim.x - a.H) * 256ll;
+  for (int64_t u = (h - a.H) * 256ll + t; u < rows * wide; u += step) {
     int64_t r = u / wide, c = u % wide;
     if (r >= first) r += last - first;
     if (c < gn) { st<IO>(a.dq, r * a.dqs + c, 0.0f); continue; }
@@ -2643,8 +2677,7 @@ template <typename IO, int NT>
 void launch_delta_ops(const DeltaArgs& a, const DeltaLayout& l, bool vec, hipStream_t s) {
   static_assert(Ops<IO, NT>::group == 2 * kQ * NT * 32 * Ops<IO, NT>::KP && Ops<IO, NT>::head == 4 * kTri + kScalars &&
                 Keep<IO, NT>::block == 128 * NT * 32 + 4 * 32 * 128, "as in delta_layout");
-  if (a.nseq <= 64) delta_plan_few_kernel<<<1, 64, 0, s>>>(a);
-  else delta_plan_kernel<<<1, 1024, 0, s>>>(a);
+  if (a.nseq > kFew) delta_plan_kernel<<<1, 1024, 0, s>>>(a);
   const dim3 grid((unsigned)l.nchunk, a.H);
   if (vec) delta_ops_kernel<IO, NT, true><<<grid, 256, 0, s>>>(a);
   else delta_ops_kernel<IO, NT, false><<<grid, 256, 0, s>>>(a);
@@ -2703,8 +2736,7 @@ void launch_delta_bwd(const DeltaArgs& a, const DeltaLayout& l, bool vec, bool f
   const auto blk = [&](int lanes) { return dim3((unsigned)l.nchunk, a.G, kQ * lanes / 256); };
   if (vec && a.N % 4 == 0 && (sizeof(IO) == 4 || a.N % 8 == 0) && out16) delta_qk_grad_kernel<IO, LN, true><<<blk(LN), 256, 0, s>>>(a);
   else delta_qk_grad_kernel<IO, 64, false><<<blk(64), 256, 0, s>>>(a);
-  delta_zero_kernel<IO><<<1024, 256, 0, s>>>(a);
-  if (a.dA || a.ddt_bias) delta_sum_kernel<<<a.H, 256, 0, s>>>(a);
+  delta_rest_kernel<IO><<<a.H + 256, 256, 0, s>>>(a);
 }
 
 template <typename IO>
