@@ -341,7 +341,7 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int n, float (&
 
 // One workgroup per block and head; the first head of a group writes its k and q.
 template <typename IO, int NT, bool VEC>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) delta_ops_kernel(const DeltaArgs a) {
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NT * sizeof(IO) <= 16 ? 3 : 1))) delta_ops_kernel(const DeltaArgs a) {
   using O = Ops<IO, NT>;
   constexpr int KP = O::KP, LN = 2 * NT, RW = 256 / LN, LD = kQ + 4;
   constexpr int lds = O::group > 2 * kQ * LD * 4 ? O::group : 2 * kQ * LD * 4;
@@ -1913,6 +1913,17 @@ __global__ void __launch_bounds__(256) delta_both_kernel(const DeltaArgs a, int 
 __device__ __forceinline__ h8 weighted(h8 v, h8 w) { return v * w; }
 // Sum of four lanes' rows: the sixteen lanes that share q.
 __device__ __forceinline__ float sum16(float v) { return lane_sum<16>(v); }
+__device__ __forceinline__ double sum16(double v) {
+  auto add = [&](auto turned) {
+    const u2 w = __builtin_bit_cast(u2, v);
+    v += __builtin_bit_cast(double, (u2){turned(w.x), turned(w.y)});
+  };
+  add([](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xf, 0xf, true); });
+  add([](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xf, 0xf, true); });
+  add([](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xf, 0xf, true); });
+  add([](uint32_t x) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xf, 0xf, true); });
+  return v;
+}
 
 // One workgroup per block and head, eight waves: wave (tt, nh) has tile tt of the tokens and half
 // the states, or columns 32 nh .. of the 64 x 64 matrices.  First the products over the
@@ -1935,9 +1946,11 @@ __global__ void __launch_bounds__(512) delta_rows_grad_kernel(const DeltaArgs a)
   __shared__ __align__(16) float s_sc[kScalars / 4];
   __shared__ __align__(16) _Float16 s_w[5][256];
   __shared__ __align__(16) float s_fy[256], s_fr[256];
+  auto s_row = reinterpret_cast<double (*)[kQ]>(s_fy);  // [2], behind the loop
+  auto s_col = reinterpret_cast<double (*)[kQ]>(s_w);   // [4]
   __shared__ int s_e[5], s_sd[256];  // the products' largest weights; the shifts of S and dS
   __shared__ float s_rmax[2][2][kQ], s_cmax[2][4][kQ];
-  __shared__ float s_row[2][kQ], s_col[4][kQ], s_db[2][kQ], s_qq[2][kQ], s_rk[2][kQ], s_tail[2][kQ], s_dot[8];
+  __shared__ float s_db[2][kQ], s_qq[2][kQ], s_rk[2][kQ], s_tail[2][kQ], s_dot[8];
   const int c = blockIdx.x, h = blockIdx.y, g = h / a.per, N = a.N, P = a.P, PP = padded(P);
   if (c >= a.head->nchunk) return;
   const DeltaChunk ck = a.chunks[c];
@@ -2117,7 +2130,10 @@ __global__ void __launch_bounds__(512) delta_rows_grad_kernel(const DeltaArgs a)
     }
     const float gi = s_sc[64 * kGH + row], gil = s_sc[64 * kGL + row], bi = s_sc[64 * kBeta + row];
     const float lki = s_sc[64 * kLK + row], lqi = s_sc[64 * kLQ + row], fm = s_sc[64 * kFM + row];
-    float rowsum = 0.0f, dbl = 0.0f, colsum[8], rmax[2] = {}, cmax[2][8];
+    // A pair is in its row's sum and in its column's, and between them in the running sum's
+    // gradient of the tokens before both, where it cancels: in float64 it does
+    double rowsum = 0.0, colsum[8];
+    float dbl = 0.0f, rmax[2] = {}, cmax[2][8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int cj = 32 * nh + 8 * q4 + j;
@@ -2130,8 +2146,8 @@ __global__ void __launch_bounds__(512) delta_rows_grad_kernel(const DeltaArgs a)
       // what the running sum's gradient takes from here; the diagonal's cancels
       const float mm = low && cj < row ? fmaf(m0, mr[j] * fm, lb * kkh) : 0.0f;
       dbl = fmaf(l, kkh, dbl);
-      rowsum += mm;
-      colsum[j] = sum16(mm);
+      rowsum += (double)mm;
+      colsum[j] = sum16((double)mm);
       zr[0][j] = m * lkj;
       zr[1][j] = lb * lkj;
       zc[0][j] = m * lqi;
@@ -2293,9 +2309,9 @@ __global__ void __launch_bounds__(512) delta_rows_grad_kernel(const DeltaArgs a)
     const int t = lane;
     const float b = s_sc[64 * kBeta + t], rkt = s_rk[0][t] + s_rk[1][t];
     const double tl = (double)s_tail[0][t] + (double)s_tail[1][t];
-    double x = (double)s_qq[0][t] + (double)s_qq[1][t] - (double)(b * rkt) - tl + (double)s_row[0][t] + (double)s_row[1][t];
+    double x = (double)s_qq[0][t] + (double)s_qq[1][t] - (double)(b * rkt) - tl + s_row[0][t] + s_row[1][t];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x -= (double)s_col[k][t];
+    for (int k = 0; k < 4; ++k) x -= s_col[k][t];
     double dot = 0.0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) dot += (double)s_dot[k];
