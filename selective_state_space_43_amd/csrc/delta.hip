@@ -349,7 +349,9 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NT * s
   __shared__ float s_len[2][kQ];
   __shared__ float s_g[kQ], s_wc[kQ], s_wl[kQ], s_wm[kQ];  // G; the columns' and the rows' factors of L, M
   __shared__ int s_bad;
-  const int c = blockIdx.x, h = blockIdx.y, g = h / a.per, N = a.N;
+  // the heads of a group one after another on one die (they take the workgroups by turns of eight)
+  const int item = blockIdx.x / (8 * a.per) * 8 + blockIdx.x % 8, N = a.N;
+  const int c = item / a.G, g = item % a.G, h = g * a.per + blockIdx.x / 8 % a.per;
   const int tid = threadIdx.x, lane = tid & 63, i16 = lane & 15, q4 = lane >> 4;
   const int tt = __builtin_amdgcn_readfirstlane(tid >> 6);
   DeltaChunk ck;
@@ -2694,7 +2696,7 @@ void launch_delta_ops(const DeltaArgs& a, const DeltaLayout& l, bool vec, hipStr
   static_assert(Ops<IO, NT>::group == 2 * kQ * NT * 32 * Ops<IO, NT>::KP && Ops<IO, NT>::head == 4 * kTri + kScalars &&
                 Keep<IO, NT>::block == 128 * NT * 32 + 4 * 32 * 128, "as in delta_layout");
   if (a.nseq > kFew) delta_plan_kernel<<<1, 1024, 0, s>>>(a);
-  const dim3 grid((unsigned)l.nchunk, a.H);
+  const unsigned grid = (unsigned)((l.nchunk * a.G + 7) / 8 * 8 * a.per);
   if (vec) delta_ops_kernel<IO, NT, true><<<grid, 256, 0, s>>>(a);
   else delta_ops_kernel<IO, NT, false><<<grid, 256, 0, s>>>(a);
 }
