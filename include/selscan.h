@@ -494,6 +494,9 @@ int64_t ssm_group_norm_bwd_workspace_size(int64_t rows, int64_t channels, int64_
  * state grow, as the formula says.  A non-finite input makes what depends on it
  * non-finite (an infinity may become a NaN), and leaves earlier tokens and other
  * sequences as they are.
+ * Precision: log decays are summed in float64; the state and all sums are float32; operands of
+ * products are taken in two fp16 parts (22 bits, or 2^-39 of the largest value of their
+ * row or column) where bf16 values do not fit one, so float32 rows keep float32 results.
  */
 int ssm_gated_delta_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                         const void* v, int64_t v_stride, const void* dt, int64_t dt_stride,
@@ -537,8 +540,10 @@ int ssm_gated_delta_update(const void* q, int64_t q_stride, const void* k, int64
  *  dA, ddt_bias [nheads] float32 or NULL (not computed)
  *  dh0          [nseq, nheads, headdim, dstate] float32 or NULL (not computed)
  *  workspace    ssm_gated_delta_bwd_workspace_size(...) bytes, as above
- * Every sum has a fixed order: results do not vary from run to run.  Extents and
- * errors as for ssm_gated_delta_fwd.
+ * Every sum has a fixed order: results do not vary from run to run.  Extents,
+ * precision and errors as for ssm_gated_delta_fwd.  A non-finite input may make any
+ * gradient of its sequence non-finite, and dA, ddt_bias of its heads; other sequences'
+ * gradients are left as they are.
  */
 int ssm_gated_delta_bwd(const void* dy, int64_t dy_stride, const void* q, int64_t q_stride,
                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,

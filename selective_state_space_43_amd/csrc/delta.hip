@@ -83,7 +83,7 @@ struct DeltaArgs {
   DeltaChunk* chunks;
   DeltaSeg* segs;        // the backward's are whole sequences
   DeltaCut* cuts;
-  int seg_len;           // blocks of a segment; a sequence of more than two is cut
+  int seg_len, cut_over;  // blocks of a segment; a sequence of more than cut_over is cut
   float* local;          // [split][head]: X [P][N], the state behind a segment from zero (then the one
                          // entering it), and Y [N][N], the images of the unit vectors
   char *gops, *hops;     // operands of a (block, group), of a (block, head)
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(1024) delta_plan_kernel(const DeltaArgs a) {
     i4 n = {0, 0, 0, 0}, all;  // blocks, segments, segments of cut sequences, cut sequences
     if (in && (!a.state || (slot >= 0 && slot < a.nslots))) {  // else padding
       n[0] = (end - begin + kQ - 1) / kQ;
-      n[1] = n[0] > 2 * a.seg_len ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
+      n[1] = n[0] > a.cut_over ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
       n[2] = n[1] > 1 ? n[1] : 0;
       n[3] = n[1] > 1;
     }
@@ -191,7 +191,7 @@ struct FewPlan {
     n[0] = n[1] = n[2] = n[3] = 0;
     if (in && (!a.state || (sl >= 0 && sl < a.nslots))) {  // else padding
       n[0] = (end - begin + kQ - 1) / kQ;
-      n[1] = n[0] > 2 * a.seg_len ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
+      n[1] = n[0] > a.cut_over ? (n[0] + a.seg_len - 1) / a.seg_len : 1;
       n[2] = n[1] > 1 ? n[1] : 0;
       n[3] = n[1] > 1;
     }
@@ -339,7 +339,12 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int n, float (&
   }
 }
 
-// One workgroup per block and head; the first head of a group writes its k and q.
+// One workgroup per block and head, wave tt with rows 16 tt ..; the first head of a group writes
+// its k and q.  k.k and q.k are made for every head of a group again: a workgroup that went
+// through them would hold both matrices beside T (154 registers to scratch, 492 us against 300
+// for four prompts of 8192, 32 heads of 16 groups); with them one after another on one die the
+// rows come from its cache (0.69 -> 0.65 ms a call).  There it reads and writes about 1.2 GB, most
+// of it what the walk reads next, at 4 TB/s: memory, and 1520 vector instructions a wave.
 template <typename IO, int NT, bool VEC>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NT * sizeof(IO) <= 16 ? 3 : 1))) delta_ops_kernel(const DeltaArgs a) {
   using O = Ops<IO, NT>;
@@ -853,7 +858,10 @@ __device__ __forceinline__ int64_t local_size(const DeltaArgs& a) { return (int6
 
 // A workgroup walks a sequence's blocks with WV waves of 16 PT channels of one head each, the
 // states of a wave's channels in its accumulators.  DB: the next block's operands
-// come while this block's are used.
+// come while this block's are used.  kWalk is for what delta_pair_kernel's LDS does not hold;
+// kSum takes 131 us for one prompt of 32768 tokens (8 heads: 31 segments of 16 or 17 blocks but the
+// last, 128 channels and 128 unit vectors), kKeepBlocks is half of delta_both_kernel.  A block's
+// products wait for one another: it is the steps' latency that counts, not their number.
 template <typename IO, int NT, int MODE>
 struct WalkLds {
   using O = Ops<IO, NT>;
@@ -1238,8 +1246,12 @@ __global__ void __launch_bounds__(256) delta_walk_kernel(const DeltaArgs a, int 
 // state; the other, a step behind, takes the state's pieces and U from LDS and makes y, and
 // sends what the next block needs: k, T, M and the scalars while this block's are used; q and v,
 // which have one place each, from the second meeting on. What one wave did one after another
-// (860 vector instructions a block, 3.7 us) two do side by side.
-// VL: v comes through LDS, rows of 64 channels (bf16, rows on 16 bytes), else lane by lane.
+// (860 vector instructions a block, 3.7 us) two do side by side (2.9 us a block, 3.5 with every CU
+// at work): four prompts of 8192, 32 heads 350 to 400 us of 0.65 ms, 1.0 GB read and 0.28 written.
+// No unit is full (vector ALU about half, matrix cores a third of the cycles); what is left
+// is the chain from k S over R, U to the next state.
+// VL: v comes through LDS, rows of 64 channels (bf16, rows on 16 bytes), else lane by lane
+// (four prompts of 8192: 0.68 ms against 0.70).
 template <typename IO, int NT>
 struct Pair {
   using O = Ops<IO, NT>;
@@ -1597,7 +1609,8 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
 
 // The states entering the segments of a cut sequence, s <- X + s Y one after another: eight
 // rows (channels) of a head a workgroup.  Thread (j, n) has state n and a run of the rows of Y,
-// whose next segment's come while this one's are used; the runs are added in order.
+// whose next segment's come while this one's are used; the runs are added in order.  One prompt of
+// 32768 tokens, 8 heads: 34 us for 31 segments, about 1.1 us a segment for 16 KB of Y from cache.
 template <int NT>
 __global__ void __launch_bounds__(1024) delta_join_kernel(const DeltaArgs a) {
   constexpr int R = 8, NP = 16 * NT, JG = 1024 / NP, JN = NP / JG, AH = JN < 16 ? JN : 16;
@@ -1666,7 +1679,7 @@ __global__ void __launch_bounds__(1024) delta_join_kernel(const DeltaArgs a) {
 
 // The blocks against their order: the gradient dS behind a block from that behind the next
 // one, dR and dv, with what delta_rows_grad_kernel takes from here.  Waves, channels and places
-// as in delta_walk_kernel.
+// as in delta_walk.
 template <typename IO, int NT, bool FAST>
 __device__ __forceinline__ void delta_back(const DeltaArgs& a, int units, int blk, char* s_op) {
   using O = Ops<IO, NT>;
@@ -1900,6 +1913,8 @@ __device__ __forceinline__ void delta_back(const DeltaArgs& a, int units, int bl
 
 // Both walks of a backward, which do not need each other: the first half of the grid goes
 // against the blocks' order, which takes longer (16 heads, four sequences: half the card each).
+// Four sequences of 2048 tokens, 16 heads: 209 us, 32 blocks one after another at 6.5 us; one
+// launch after the other took 0.63 ms for the whole backward, this way 0.53.
 template <typename IO, int NT, bool FAST>
 __global__ void __launch_bounds__(256) delta_both_kernel(const DeltaArgs a, int units) {
   constexpr int back = WalkLds<IO, NT, kWalk>::bytes, keep = WalkLds<IO, NT, kKeepBlocks>::bytes;
@@ -1932,6 +1947,9 @@ __device__ __forceinline__ double sum16(double v) {
 // channels, 32 at a time from what the walks kept: dY S^T, dR S^T, U dS^T, and dY U^T,
 // dR U^T.  Both factors are scaled by channel, so the left one is weighted with what both
 // scales leave, by the largest one.  Then the products over the block's tokens.
+// Four sequences of 2048 tokens, 16 heads: 255 us for 2048 workgroups, one a CU (145 KB of LDS):
+// 0.63 GB read (192 KB a workgroup are what the walks kept), 0.14 written, 3 TB/s.  Half of the
+// waves' cycles are waits at the meetings between its parts, which nothing else on the CU fills.
 template <typename IO, int NT, bool VEC>
 __global__ void __launch_bounds__(512) delta_rows_grad_kernel(const DeltaArgs a) {
   using O = Ops<IO, NT>;
@@ -2337,7 +2355,8 @@ __global__ void __launch_bounds__(512) delta_rows_grad_kernel(const DeltaArgs a)
 }
 
 // The heads of a group together, and the normalisation: LN lanes a row of q or k, eight states
-// each (VEC; else 64 lanes, 64 apart).
+// each (VEC; else 64 lanes, 64 apart).  Bound by memory: 37 us for 8192 tokens of 16 heads and 8
+// groups (0.16 GB read, 34 MB written: 5 TB/s).
 template <typename IO, int LN, bool VEC>
 __global__ void __launch_bounds__(256) delta_qk_grad_kernel(const DeltaArgs a) {
   const int c = blockIdx.x, g = blockIdx.y, N = a.N;
@@ -2614,14 +2633,18 @@ int check_state(const DeltaArgs& a, const DeltaCall& c) {
 }
 
 constexpr int64_t kCUs = 256;
-// A cut sequence is walked twice, once for twice as many columns: cut where the card takes four
-// segments at once at least, and more than there are sequences, of eight blocks at least.
-constexpr int64_t kMinCut = 4, kMinSeg = 8;
+// A cut sequence is walked twice, once for twice as many columns: cut where the card takes
+// three segments at once at least, and more than there are sequences.  Cut and not cut, 128
+// channels and states, bf16: 8192 tokens, 40 heads (three at once) 371 and 411 us, 32 heads 315 and
+// 409, 16 heads 167 and 383; 32768 tokens, 8 heads 0.33 and 1.42 ms.  Segments of four blocks at
+// least: 2048 tokens, 8 heads 65 us (eight blocks 75, not cut 106), 1536 tokens, 4 heads 57 (70,
+// 83).  Up to twelve blocks stay whole: 768 tokens, 16 heads 48 us, cut 53.
+constexpr int64_t kMinCut = 3, kMinSeg = 4, kMinCutBlocks = 12;
 
 struct DeltaLayout {
   int nt;  // tiles of 16 states
   int64_t nchunk, nseg, nsplit, ncut;  // at most
-  int seg_len;
+  int seg_len, cut_over;
   int64_t chunks, segs, cuts, local, gops, hops, keep, shifts, dqh, dkh, part, bytes;
 };
 
@@ -2647,8 +2670,9 @@ DeltaLayout delta_layout(int64_t tokens, int64_t nseq, int64_t H, int64_t P, int
     if (len < kMinSeg) len = kMinSeg;
   }
   l.seg_len = (int)len;
-  // a sequence of more than 2 len blocks has one for every len of them, rounded up
-  l.ncut = blocks / (2 * len);
+  l.cut_over = (int)(2 * len > kMinCutBlocks ? 2 * len : kMinCutBlocks);
+  // a sequence of more than cut_over blocks has one for every len of them, rounded up
+  l.ncut = blocks ? (blocks - 1) / l.cut_over : 0;
   l.nsplit = l.ncut ? blocks / len + l.ncut : 0;
   l.nseg = nseq + l.nsplit;
   l.segs = take(l.nseg * sizeof(DeltaSeg));
@@ -2683,6 +2707,7 @@ void place(DeltaArgs& a, const DeltaLayout& l, void* workspace) {
   a.cuts = reinterpret_cast<DeltaCut*>(w + l.cuts);
   a.local = reinterpret_cast<float*>(w + l.local);
   a.seg_len = l.seg_len;
+  a.cut_over = l.cut_over;
   a.nseg = l.nseg;
   a.gops = w + l.gops; a.hops = w + l.hops; a.keep = w + l.keep;
   a.shifts = reinterpret_cast<int*>(w + l.shifts);
@@ -2784,7 +2809,8 @@ void launch_delta_io(const DeltaArgs& a, const DeltaLayout& l, bool bwd, hipStre
   }
 }
 
-// Two rows a lane: 207 us for 253 tokens of 32 heads of 128 channels and 128 states (5.2 TB/s),
+// Two rows a lane: 207 us for 253 tokens of 32 heads of 128 channels and 128 states (5.2 TB/s, where
+// a large copy reaches 4.7),
 // four take 217, eight 422.
 template <typename IO, int LN, bool VEC>
 int launch_step(const DeltaArgs& a, hipStream_t s) {
