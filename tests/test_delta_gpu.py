@@ -132,7 +132,7 @@ CASES = [  # lens, H, G, P, N, dtype, options
     ((900,), 1, 1, 64, 64, "f32", dict(has=True)),
     ((3, 0, 70) * 30, 2, 1, 32, 32, "bf16", dict(behind=2)),  # more sequences than one wave plans
     ((2,) * 1030 + (100,), 1, 1, 16, 16, "f32", dict(skip=((5, -1),))),
-    # few heads: sequences of more than 16 blocks are cut into segments of eight at least
+    # few heads: sequences of more than twelve blocks are cut into segments of four at least
     ((1024, 1025), 2, 1, 64, 128, "bf16", dict(has=True)),
     ((1700, 40, 0, 1300, 64), 2, 1, 128, 128, "bf16", dict(behind=3)),
     ((1200, 1), 1, 1, 17, 9, "bf16", dict(has=True, lead=1)),
@@ -141,6 +141,11 @@ CASES = [  # lens, H, G, P, N, dtype, options
     ((1111,), 3, 3, 80, 256, "f32", dict(has=True, lead=2)),
     ((2900,), 1, 1, 32, 32, "f32", dict(state=False)),
     ((1500, 1200), 2, 2, 64, 64, "bf16", dict(skip=((0, -1),), how=ref.How(norm=False), kstd=0.1)),
+    ((768, 769, 5), 2, 1, 32, 32, "bf16", dict(has=True)),  # twelve blocks and thirteen
+    ((833,), 1, 1, 64, 128, "bf16", dict(has=True)),
+    ((1100,), 80, 8, 16, 16, "bf16", dict(has=True)),  # three segments at once
+    ((1,) * 70 + (900,), 1, 1, 16, 16, "bf16", dict(has=True)),  # cut, and more than one wave plans
+    ((200, 65), 6, 2, 32, 64, "bf16", {}),  # three heads a group, items not a multiple of eight
 ]
 
 
@@ -431,3 +436,103 @@ def test_states_past_32_bits(ssm, dev):  # noqa: F811
     assert torch.equal(y, z)
     for s, a in zip(p.slots, at):
         assert torch.equal(big[a], p.state[int(s)])
+
+
+def test_rows_far_apart(ssm, dev):  # noqa: F811
+    """Row strides of 2^24 values and more: a lane's offset to its rows does not fit 32 bits."""
+    p = Delta(dev, (66, 3), 2, 2, 64, 64, "bf16", seed=19, has=True)
+    far = (1 << 24) + 8
+
+    def spread(t):
+        big = torch.empty(t.shape[0] * far, dtype=t.dtype, device=dev).as_strided(t.shape, (far, 1))
+        big.copy_(t)
+        return big
+
+    p.run(ssm)
+    near, end = p.y.clone(), p.state.clone()
+    g = p.bwd(ssm)
+    p.load()
+    p.t["v"], p.y = spread(p.t["v"]), spread(p.y)
+    p.run(ssm)
+    p.check("far v and y")
+    # another path of the same arithmetic
+    assert torch.equal(p.y, near) and torch.equal(p.state, end)
+    p.t["dy"] = spread(p.t["dy"])
+    far_g = p.bwd(ssm)
+    p.check_bwd(far_g, "far v and dy")
+    assert all(torch.equal(far_g[k], g[k]) for k in ("dq", "dk", "dv", "ddt", "dbeta", "dh0"))
+
+
+def test_calls_at_the_same_time(ssm, dev):  # noqa: F811
+    """Calls on several streams, each with a workspace and states of its own, and two captured
+    graphs that run beside each other: the same bits as one after another."""
+    ps = [Delta(dev, lens, 4, 2, 128, 128, "bf16", seed=20 + i, has=True)
+          for i, lens in enumerate([(700, 60), (1300,), (64,) * 9])]
+    starts = [p.state.clone() for p in ps]
+    carry = [dict(h0=up(p.h0, dev), dfinal_state=up(p.dfinal, dev)) for p in ps]
+    want = []
+    for p, c in zip(ps, carry):
+        p.run(ssm)
+        g = p.bwd(ssm, carry=False, **c)
+        want.append([p.y.clone(), p.state.clone()] + [v.clone() for v in g.values() if v is not None])
+    streams = [torch.cuda.Stream() for _ in ps]
+    sizes = [(int(p.cu[-1]), len(p.cu) - 1, 4, 128, 2, 128) for p in ps]
+    ws = [[torch.empty(f(*z), dtype=torch.uint8, device=dev)
+           for f in (ssm.ssm_gated_delta_workspace_size, ssm.ssm_gated_delta_bwd_workspace_size)] for z in sizes]
+    torch.cuda.synchronize()
+    got, graphs = [None] * 3, []
+
+    def work(i):
+        ps[i].run(ssm, workspace=ws[i][0])
+        got[i] = ps[i].bwd(ssm, carry=False, workspace=ws[i][1], **carry[i])
+
+    def same():
+        torch.cuda.synchronize()
+        for p, g, w in zip(ps, got, want):
+            have = [p.y, p.state] + [v for v in g.values() if v is not None]
+            assert all(torch.equal(a, b) for a, b in zip(have, w))
+
+    for _ in range(2):
+        for p, s in zip(ps, starts):
+            p.state.copy_(s)
+        torch.cuda.synchronize()
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                work(i)
+        same()
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            work(i)
+        graphs.append(graph)
+    for _ in range(3):
+        for p, s in zip(ps[:2], starts):
+            p.state.copy_(s)
+            p.y.fill_(0)
+        torch.cuda.synchronize()
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        same()
+
+
+def test_sums_of_heads_that_forget_at_once(ssm, dev):  # noqa: F811
+    """Decays of e^-1 and less a token: what a block's pairs give to dA and ddt_bias cancels
+    but for neighbours, and has to cancel to its last bits."""
+    p = Delta(dev, (900, 300), 4, 4, 64, 64, "f32", seed=23, state=False)
+    p.x["A"][:] = [-16.0, -14.0, -12.0, -10.0]
+    p.x["dt_bias"][:] = np.float32(-2.2)
+    p.load()
+    g = p.bwd(ssm, carry=False)
+    want, _ = ref.delta_bwd(p.x, p.cu, p.G, p.how, None, None)
+    for k in ("dA", "ddt_bias"):
+        # A token's share is off by 2^-22 of itself from products of parts of 22 bits and sums in
+        # float32, and by its step's rounding: dt + dt_bias is a float32 value of size 2 to 4, off by
+        # 2^-23, so its softplus (e^raw, where steps are small) by 2^-23 of itself and the decay, a
+        # factor of the share, by |log decay| 2^-23, where shares count that are not below e^-4 of the
+        # largest: 2^-22 + 5 2^-23.  These have signs of their own, and so have the shares: the sums'
+        # sizes are as theirs, and twice that is allowed.  Sums of rows and columns that did not
+        # cancel would add the roundings of all of a block's pairs to every token.
+        off = np.linalg.norm(f64(g[k]) - want[k]) / np.linalg.norm(want[k])
+        print(k, off, flush=True)
+        assert off <= 2 * 3.5 * 2.0 ** -22, (k, off)
