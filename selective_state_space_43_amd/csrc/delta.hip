@@ -276,7 +276,7 @@ __device__ __forceinline__ int tri(int r, int kb, int c) {
 
 // a head's scalars: places of 64 floats each
 enum { kS1, kBeta, kS2, kS3, kFT, kFM, kEC, kGH, kGL, kLK, kLQ };
-constexpr int kScalars = 3072;
+constexpr int kScalars = 12 * 64 * 4;  // bytes: eleven places, and room to a whole KB
 
 // Bytes of the operands of a (block, group): k and q, rows of 2 NP bytes a piece, a row's
 // 16-byte parts in an order of its own (part()); and of a (block, head): T, M, scalars.
