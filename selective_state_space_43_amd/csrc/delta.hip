@@ -859,8 +859,8 @@ __device__ __forceinline__ int64_t local_size(const DeltaArgs& a) { return (int6
 // A workgroup walks a sequence's blocks with WV waves of 16 PT channels of one head each, the
 // states of a wave's channels in its accumulators.  DB: the next block's operands
 // come while this block's are used.  kWalk is for what delta_pair_kernel's LDS does not hold;
-// kSum takes 131 us for one prompt of 32768 tokens (8 heads: 31 segments of 16 or 17 blocks but the
-// last, 128 channels and 128 unit vectors), kKeepBlocks is half of delta_both_kernel.  A block's
+// kSum takes 131 us for one prompt of 32768 tokens (8 heads: 15 segments of 32 blocks, the
+// last one has none to make; 128 channels and 128 unit vectors), kKeepBlocks is half of delta_both_kernel.  A block's
 // products wait for one another: it is the steps' latency that counts, not their number.
 template <typename IO, int NT, int MODE>
 struct WalkLds {
@@ -936,10 +936,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int bl
     }
   // v of a block's rows 32 kb + 8 q + j.  Whole blocks go by an address of the row, the
   // same in all lanes, and the lane's own offset
-  constexpr bool PAIR = FAST && PT == 2 && sizeof(IO) == 2;
-  using Raw = typename std::conditional<PAIR, uint32_t, IO>::type;
-  constexpr int RV = PAIR ? 1 : PT;
-  Raw vr[2][8][RV];
+  IO vr[2][8][PT];
   const uint32_t v_own = (uint32_t)((8 * q4 * a.vs + col[0]) * sizeof(IO)), y_own = (uint32_t)((8 * q4 * a.ys + col[0]) * sizeof(IO));
   auto fetch = [&](int b) {
     const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
@@ -949,7 +946,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int bl
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int e = 0; e < RV; ++e) vr[kb][j][e] = 0;
+          for (int e = 0; e < PT; ++e) vr[kb][j][e] = 0;
     } else if (FAST && cnt == kQ) {
       const char* row = static_cast<const char*>(a.v) + (int64_t)r0 * a.vs * sizeof(IO);
 #pragma unroll
@@ -958,7 +955,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int bl
         for (int j = 0; j < 8; ++j) {
           const char* at = row + (32 * kb + j) * a.vs * (int64_t)sizeof(IO);
 #pragma unroll
-          for (int e = 0; e < RV; ++e) vr[kb][j][e] = *reinterpret_cast<const Raw*>(at + (v_own + e * (uint32_t)sizeof(IO)));
+          for (int e = 0; e < PT; ++e) vr[kb][j][e] = *reinterpret_cast<const IO*>(at + (v_own + e * (uint32_t)sizeof(IO)));
         }
     } else {
 #pragma unroll
@@ -967,13 +964,12 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int bl
         for (int j = 0; j < 8; ++j) {
           const IO* at = static_cast<const IO*>(a.v) + (r0 + min(32 * kb + 8 * q4 + j, cnt - 1)) * a.vs;
 #pragma unroll
-          for (int e = 0; e < RV; ++e) vr[kb][j][e] = *reinterpret_cast<const Raw*>(at + col[e]);
+          for (int e = 0; e < PT; ++e) vr[kb][j][e] = *reinterpret_cast<const IO*>(at + col[e]);
         }
     }
   };
   auto value = [&](int kb, int j, int e) {
-    if constexpr (PAIR) return __uint_as_float(e ? vr[kb][j][0] & 0xffff0000u : vr[kb][j][0] << 16);
-    else if constexpr (sizeof(IO) == 2) return __uint_as_float((uint32_t)vr[kb][j][e] << 16);
+    if constexpr (sizeof(IO) == 2) return __uint_as_float((uint32_t)vr[kb][j][e] << 16);
     else return (float)vr[kb][j][e];
   };
   if (nc > 0 && on) fetch(0);
@@ -981,7 +977,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int bl
   for (int b = 0; b < nc; ++b) {
     const int r0 = sq.t0 + b * kQ, cnt = min(sq.t1 - r0, kQ);
     // the last block's y may still be on its way: a whole block's stores come behind all loads
-    if (YES && FAST && b > 0 && on) landed<16 * (PAIR ? 1 : PT)>();
+    if (YES && FAST && b > 0 && on) landed<16 * PT>();
     else landed();
     meet();  // this block's operands are there; the waves are done with the last block's
     // v has come too: else the compiler would wait for it behind what is sent next
@@ -990,7 +986,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int bl
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < RV; ++e) asm volatile("" : "+v"(vr[kb][j][e]));
+        for (int e = 0; e < PT; ++e) asm volatile("" : "+v"(vr[kb][j][e]));
     if (DB && b + 1 < nc) stage_block(b + 1);
     const char* op = s_op + (DB ? (b & 1) * B : 0);
     const char* hop = op + GB;
@@ -1033,7 +1029,7 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int bl
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int e = 0; e < RV; ++e) vr[kb][j][e] = 32 * kb + 8 * q4 + j < cnt ? vr[kb][j][e] : 0;
+            for (int e = 0; e < PT; ++e) vr[kb][j][e] = 32 * kb + 8 * q4 + j < cnt ? vr[kb][j][e] : 0;
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
@@ -1130,14 +1126,9 @@ __device__ __forceinline__ void delta_walk(const DeltaArgs& a, int units, int bl
                 if (place_of(tt, 4 * q4 + r) >= first[e]) y[tt][e][r] = __builtin_nanf("");
         }
         auto write = [&](char* at, int tt, int r) {
-          if constexpr (PAIR) {
-            typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-            *reinterpret_cast<b2*>(at) = __builtin_convertvector((f2){y[tt][0][r], y[tt][PT - 1][r]}, b2);
-          } else {
 #pragma unroll
-            for (int e = 0; e < PT; ++e)
-              if (FAST || p0 + PT * i16 + e < P) st<IO>(at, e, y[tt][e][r]);
-          }
+          for (int e = 0; e < PT; ++e)
+            if (FAST || p0 + PT * i16 + e < P) st<IO>(at, e, y[tt][e][r]);
         };
         if (FAST && cnt == kQ) {
           if (p0 + PT * i16 < P) {
@@ -1610,7 +1601,7 @@ __global__ void __launch_bounds__(512) delta_pair_kernel(const DeltaArgs a, int 
 // The states entering the segments of a cut sequence, s <- X + s Y one after another: eight
 // rows (channels) of a head a workgroup.  Thread (j, n) has state n and a run of the rows of Y,
 // whose next segment's come while this one's are used; the runs are added in order.  One prompt of
-// 32768 tokens, 8 heads: 34 us for 31 segments, about 1.1 us a segment for 16 KB of Y from cache.
+// 32768 tokens, 8 heads: 34 us for 15 segments, 2.3 us each for the 64 KB of a head's Y from cache.
 template <int NT>
 __global__ void __launch_bounds__(1024) delta_join_kernel(const DeltaArgs a) {
   constexpr int R = 8, NP = 16 * NT, JG = 1024 / NP, JN = NP / JG, AH = JN < 16 ? JN : 16;
