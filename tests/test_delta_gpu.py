@@ -536,3 +536,21 @@ def test_sums_of_heads_that_forget_at_once(ssm, dev):  # noqa: F811
         off = np.linalg.norm(f64(g[k]) - want[k]) / np.linalg.norm(want[k])
         print(k, off, flush=True)
         assert off <= 2 * 3.5 * 2.0 ** -22, (k, off)
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v", "dt", "beta", "dy"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_gradients_of_other_sequences_stay(ssm, dev, where, value):  # noqa: F811
+    """A value of one sequence that is not finite: the others' gradients keep their bits, and what
+    it belongs to does not come out as if nothing had been there."""
+    p = Delta(dev, (70, 100, 5), 2, 1, 64, 64, "bf16", seed=24, state=False, behind=3)
+    clean = p.bwd(ssm)
+    p.t[where][90, 1] = value
+    g = p.bwd(ssm)
+    for k in ("dq", "dk", "dv", "ddt", "dbeta"):
+        for lo, hi in ((0, 70), (170, 178)):
+            assert torch.equal(g[k][lo:hi], clean[k][lo:hi]), k
+    assert torch.equal(g["dh0"][0], clean["dh0"][0]) and torch.equal(g["dh0"][2], clean["dh0"][2])
+    if (where, value) == ("beta", float("inf")):
+        return  # sigmoid(inf) = 1: a strength like others, and its slope 0
+    assert not all(bool(torch.isfinite(g[k][70:170].float()).all()) for k in ("dq", "dk", "dv", "ddt", "dbeta"))
